@@ -9,9 +9,10 @@
  *   - paged decode attention: each sequence's few newest query tokens attend over all of its
  *     cached K/V, read indirectly through its block table, with GQA head groups;
  *   - sink + ring decode attention with RoPE applied at read time;
- * and around it: an FP8 (E4M3) form of the cache with its append and decode, verification of
- * speculative drafts (accept/reject, next token), and a host block pool that hands out the
- * block tables (prefix sharing, reference counts, copy-on-write pairs).
+ * and around it: an FP8 (E4M3) and a 4-bit form of the cache with their appends and decodes, the
+ * per-head norm and rotation of queries and keys before them, verification of speculative drafts
+ * (accept/reject, next token), block tables and slot maps kept on the device, and a host block
+ * pool that hands out the block tables (prefix sharing, reference counts, copy-on-write pairs).
  *
  * Sources (page title, section):
  *   [EDGE]   "端侧 SLM 显存保活术：在 4GB 内存板卡上实现轻量 PagedAttention 与 KV 缓存分块"
@@ -67,6 +68,7 @@ typedef void* pkv_stream_t;
 #define PKV_DEVERR_SEQ 16u       /* a sequence id outside [0, num_seqs) */
 #define PKV_DEVERR_POSITION 32u  /* a position past the sequence's block table */
 #define PKV_DEVERR_TOKEN 64u     /* a draft token id outside [0, vocab) (treated as rejected) */
+#define PKV_DEVERR_SPACE 128u    /* the free-block stack or the token arrays were too small */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int pkv_version(void);
@@ -129,8 +131,8 @@ int pkv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const int3
 size_t pkv_decode_workspace_bytes(int num_seqs, int q_len, int num_q_heads, int num_kv_heads,
                                   int head_dim);
 
-/* Turns the launch overlap of the fused-append calls (pkv_paged_attn_decode_append, its FP8
- * form and pkv_ring_attn_decode_append) on (enable != 0, the default) or off, for every call made afterwards in this process,
+/* Turns the launch overlap of the fused-append calls (pkv_paged_attn_decode_append, its FP8 and
+ * 4-bit forms and pkv_ring_attn_decode_append) on (enable != 0, the default) or off, for every call made afterwards in this process,
  * including calls captured into a CUDA graph afterwards. With it off a fused call starts only
  * after the kernel before it has completed, so it may follow a kernel that writes its pools,
  * block tables or context lengths. Returns the previous setting (0 or 1). Not part of the
@@ -315,6 +317,115 @@ int pkv_paged_attn_decode_append_fp8(void* out, const void* q, const void* k_new
                                      int num_q_heads, int num_kv_heads, int head_dim,
                                      int block_size, float scale, void* workspace,
                                      size_t workspace_bytes, pkv_stream_t stream);
+
+/* ---- 4-bit cache ----------------------------------------------------------------------------
+ * [VLLM] §工程权衡 (量化与 KV Cache 精度的权衡) names INT4 as the step below FP8. The page fixes no
+ * layout; here the pools hold rows of 80 bytes, [num_blocks][num_kv_heads][block_size][80], 3.2
+ * times less than fp16. A row (one token, one kv head, K or V) is 64 bytes of codes (element 2 j
+ * in the low half of byte j, element 2 j + 1 in the high half), then for each 32 elements an fp16
+ * scale s and an fp16 minimum z (bytes 64 + 4 g .. 67 + 4 g for elements 32 g .. 32 g + 31);
+ * element value = s * code + z. Nothing has to be calibrated. pkv_copy_blocks copies such blocks
+ * when it is called with head_dim 40 (a row of 80 bytes is 40 fp16 elements).
+ *
+ * pkv_kv_append_int4: pkv_kv_append's scatter, each row quantised: z = the group's minimum, s =
+ * (max - min) / 15 in binary32, rounded up to fp16 (down where 15 s + z would pass the largest fp16), code =
+ * (x - z) / s rounded to nearest, ties to even, in 0 .. 15 (0 where s is 0). A group with a NaN or
+ * an infinity gets s = z = NaN. Same slot rules and errors as pkv_kv_append; k, v fp16
+ * [num_tokens][num_kv_heads][head_dim]; all four 16-byte aligned. */
+int pkv_kv_append_int4(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
+                       void* k_cache, void* v_cache, int num_blocks, int num_kv_heads,
+                       int head_dim, int block_size, pkv_stream_t stream);
+
+/* Widens blocks: for every i < n, K and V, block dst[i] of the fp16 pools k_out, v_out
+ * ([num_blocks_out][num_kv_heads][block_size][head_dim]) := block src[i] of the 4-bit pools, every
+ * element fp16(s * code + z), rounded once. For readers of fp16 blocks: pkv_paged_prefill over a
+ * chunk's context, a check, a move to an fp16 cache. src, dst (device): int32 [n]; a pair with an
+ * id outside its pool is skipped and sets PKV_DEVERR_BLOCK_ID. A block may stand in src more than
+ * once, in dst only once. All pools 16-byte aligned. */
+int pkv_widen_blocks_int4(const void* k_cache, const void* v_cache, const int32_t* src,
+                          const int32_t* dst, int n, int num_blocks, void* k_out, void* v_out,
+                          int num_blocks_out, int num_kv_heads, int head_dim, int block_size,
+                          pkv_stream_t stream);
+
+/* pkv_paged_attn_decode over a 4-bit cache. Scores use the keys s * code + z as they are (the
+ * codes' products summed in fp32, then scaled); the values are widened to fp16(s * code + z).
+ * (num_q_heads / num_kv_heads) * q_len <= 32, as there; other arguments, workspace and errors as
+ * there too. */
+int pkv_paged_attn_decode_int4(void* out, const void* q, const void* k_cache,
+                               const void* v_cache, int num_blocks, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                               int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                               int block_size, float scale, void* workspace,
+                               size_t workspace_bytes, pkv_stream_t stream);
+
+/* pkv_paged_attn_decode_append over a 4-bit cache: the step's new rows k_new, v_new (fp16, as
+ * there) are stored as pkv_kv_append_int4 stores them (the same bytes) and attended over in that
+ * form. One launch per layer, with the early-start contract of pkv_paged_attn_decode_append. */
+int pkv_paged_attn_decode_append_int4(void* out, const void* q, const void* k_new,
+                                      const void* v_new, void* k_cache, void* v_cache,
+                                      int num_blocks, const int32_t* block_tables,
+                                      int max_blocks_per_seq, const int32_t* context_lens,
+                                      int num_seqs, int q_len, int num_q_heads, int num_kv_heads,
+                                      int head_dim, int block_size, float scale, void* workspace,
+                                      size_t workspace_bytes, pkv_stream_t stream);
+
+/* ---- per-head norm with the position rotation ------------------------------------------------
+ * What comes between a layer's projections and its cache, for every token t with positions[t] >= 0
+ * and every query and key head x (its 128 elements), in fp32 with one rounding to fp16:
+ *   y_d = x_d / sqrt(mean(x^2) + eps) * weight_d
+ *   out_d = y_d cos_d - y_{d+64} sin_d,  out_{d+64} = y_{d+64} cos_d + y_d sin_d    (d < 64)
+ * with (cos_d, sin_d) = row positions[t] of cos_sin, a pkv_rope_table on the device: float
+ * [n_index][64][2]. q_out fp16 [num_tokens][num_q_heads][128], k_out fp16 [num_tokens]
+ * [num_kv_heads][128] are what the append and the decode calls take. q, k: fp16, a token's heads
+ * next to each other, tokens q_stride and k_stride elements apart (multiples of 4, so that the
+ * parts of one packed projection can be passed as they lie). q_weight, k_weight: fp16 [128]. A
+ * token with a negative position is padding: its output rows stay as they are. So do those of a
+ * position >= n_index, which sets PKV_DEVERR_POSITION. q_out = q (k_out = k) is allowed when the
+ * stride is that of the output; other overlaps are not. q, k, the weights and the outputs 8-byte,
+ * cos_sin 16-byte aligned. eps >= 0. */
+int pkv_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, int64_t q_stride,
+                     int64_t k_stride, const void* q_weight, const void* k_weight, float eps,
+                     const int64_t* positions, const float* cos_sin, int n_index, int num_tokens,
+                     int num_q_heads, int num_kv_heads, int head_dim, pkv_stream_t stream);
+
+/* ---- block tables on the device ---------------------------------------------------------------
+ * For callers that keep the tables, the lengths and the free blocks on the GPU (no host round trip
+ * between steps; both calls can be captured into a graph). free_blocks (device): int32
+ * [num_blocks], a stack of which the first *free_count (device int32) entries are free block ids;
+ * the others are left as they are. Blocks are private to a sequence here: nothing is shared or
+ * reference-counted (that is the host pool's part). num_seqs <= 4096. block_tables, context_lens
+ * as for the decode, updated in place, like the stack.
+ *
+ * pkv_extend_tables: makes room for new_lens[b] more tokens of every sequence b and maps them.
+ * Sequence after sequence, the ceil((ctx + new) / block_size) - ceil(ctx / block_size) blocks it
+ * lacks come off the top of the stack into its table, context_lens[b] grows by new_lens[b], and
+ * the step's tokens, packed sequence after sequence, get
+ *   cu_new_lens[b] = where sequence b's tokens start (int32 [num_seqs + 1], the last the total)
+ *   seq_out[i] = b, position_out[i] = its position, slot_out[i] = the slot of pkv_slot_mapping
+ * (int32, int64, int64 [max_tokens]); entries behind the last token get -1, so that the arrays
+ * serve as they are as the padded inputs of pkv_kv_append and pkv_qk_norm_rope. A sequence that
+ * cannot be served keeps its table and length, its tokens get -1 in all three arrays but keep
+ * their places, and an error bit is set: new_lens < 0 or a context outside [0, max_blocks *
+ * block_size] PKV_DEVERR_CONTEXT (a negative count has no places), past the table
+ * PKV_DEVERR_POSITION, past max_tokens or the free blocks PKV_DEVERR_SPACE (every later sequence
+ * that needs blocks, or tokens, is then refused too). A free id outside [0, num_blocks) goes into
+ * the table as it is, its tokens get slot -1, and PKV_DEVERR_BLOCK_ID is set.
+ *
+ * pkv_truncate_tables: cuts every sequence with 0 <= keep_lens[b] < context_lens[b] back to
+ * keep_lens[b] tokens (rejected drafts; 0 to give a sequence up); a negative or larger value
+ * leaves it as it is. Blocks past ceil(keep / block_size) leave the table (entries become -1) for
+ * the top of the stack, in such an order that cutting off what an extend just added restores the
+ * stack. If more blocks came back than the stack holds (num_blocks), nothing is changed and
+ * PKV_DEVERR_SPACE set. keep_lens (device): int32 [num_seqs]. */
+int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* new_lens,
+                      int num_seqs, int max_blocks_per_seq, int block_size, int32_t* free_blocks,
+                      int32_t* free_count, int num_blocks, int64_t* slot_out, int32_t* seq_out,
+                      int64_t* position_out, int32_t* cu_new_lens, int max_tokens,
+                      pkv_stream_t stream);
+int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* keep_lens,
+                        int num_seqs, int max_blocks_per_seq, int block_size,
+                        int32_t* free_blocks, int32_t* free_count, int num_blocks,
+                        pkv_stream_t stream);
 
 /* ---- speculative verification ------------------------------------------------------------
  * [RING] deferred speculative decoding: draft token x is accepted with probability

@@ -1,0 +1,144 @@
+// pkv_cache_int4.cu -- the 4-bit cache's own edits: the append (quantise and scatter) and the
+// widening of whole blocks to fp16.
+//
+// Both move bytes: the append reads 256 and writes 80 per row, the widening the other way round.
+// 16 lanes take a row, 8 elements (16 fp16 bytes, 4 bytes of codes) each.
+#include <algorithm>
+
+#include "pkv_int4.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowLanes = 16;
+
+// Half-warp = one (token, kv head): its K row and its V row. The two half-warps of a warp take
+// neighbouring tokens of one head, which usually are neighbouring rows of a block.
+__global__ void __launch_bounds__(kThreads)
+kv_append_int4_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
+                      const int64_t* __restrict__ slots, int num_tokens,
+                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
+                      int64_t num_slots, int num_kv_heads, int block_size, unsigned int* err) {
+  const int lane = threadIdx.x & 31, c = lane & (kRowLanes - 1);
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int64_t pair = warp / num_kv_heads;
+  const int h = static_cast<int>(warp - pair * num_kv_heads);
+  const int64_t t = 2 * pair + (lane >> 4);
+  const bool in = t < num_tokens;
+  const int64_t slot = in ? slots[t] : -1;
+  if (in && slot >= num_slots && c == 0 && h == 0) atomicOr(err, PKV_DEVERR_SLOT);
+  const bool live = slot >= 0 && slot < num_slots;
+  const int64_t src = (t * num_kv_heads + h) * kRowLanes + c;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint4 x = live ? __ldg(k + src) : zero, y = live ? __ldg(v + src) : zero;
+  uint32_t kc, kp, vc, vp;
+  int4_quantise(x, kc, kp);
+  int4_quantise(y, vc, vp);
+  if (!live) return;
+  const int64_t blk = slot / block_size, off = slot - blk * block_size;
+  const int64_t row = ((blk * num_kv_heads + h) * block_size + off) * kInt4Row;
+  uint32_t* kd = reinterpret_cast<uint32_t*>(k_cache + row);
+  uint32_t* vd = reinterpret_cast<uint32_t*>(v_cache + row);
+  kd[c] = kc;
+  vd[c] = vc;
+  if ((c & 3) == 0) {
+    kd[kInt4Params / 4 + (c >> 2)] = kp;
+    vd[kInt4Params / 4 + (c >> 2)] = vp;
+  }
+}
+
+// The grid enumerates (pair, K|V) and, within it, `parts` CTAs that stride over the block's rows,
+// 16 lanes a row.
+__global__ void __launch_bounds__(kThreads)
+widen_blocks_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
+                         const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
+                         int num_blocks, int num_blocks_out, int parts, int block_rows,
+                         uint4* __restrict__ k_out, uint4* __restrict__ v_out,
+                         unsigned int* err) {
+  const int job = blockIdx.x / parts, part = blockIdx.x - job * parts;
+  const int which = job & 1;
+  const int32_t s = src[job >> 1], d = dst[job >> 1];
+  if (s < 0 || s >= num_blocks || d < 0 || d >= num_blocks_out) {
+    if (part == 0 && threadIdx.x == 0) atomicOr(err, PKV_DEVERR_BLOCK_ID);
+    return;
+  }
+  const uint8_t* from =
+      (which ? v_cache : k_cache) + static_cast<int64_t>(s) * block_rows * kInt4Row;
+  uint4* to = (which ? v_out : k_out) + static_cast<int64_t>(d) * block_rows * kRowLanes;
+  for (int i = part * kThreads + threadIdx.x; i < block_rows * kRowLanes; i += parts * kThreads) {
+    const int c = i & (kRowLanes - 1);
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(from + (i / kRowLanes) * kInt4Row);
+    const uint32_t w = __ldg(row + c);
+    const uint32_t sz = __ldg(row + kInt4Params / 4 + (c >> 2));
+    const __half2 p = *reinterpret_cast<const __half2*>(&sz);
+    const __half2 sc = __low2half2(p), mn = __high2half2(p);
+    // (elements 0, 4), (1, 5), (2, 6), (3, 7), each s * code + z rounded once
+    const uint32_t e04 = half2_bits(__hfma2(int4_lo(w), sc, mn));
+    const uint32_t e15 = half2_bits(__hfma2(int4_hi(w), sc, mn));
+    const uint32_t e26 = half2_bits(__hfma2(int4_lo(w >> 8), sc, mn));
+    const uint32_t e37 = half2_bits(__hfma2(int4_hi(w >> 8), sc, mn));
+    to[i] = make_uint4(__byte_perm(e04, e15, 0x5410), __byte_perm(e26, e37, 0x5410),
+                       __byte_perm(e04, e15, 0x7632), __byte_perm(e26, e37, 0x7632));
+  }
+}
+
+int launch_status() { return cuda_status(cudaGetLastError()); }
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_kv_append_int4(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
+                       void* k_cache, void* v_cache, int num_blocks, int num_kv_heads,
+                       int head_dim, int block_size, pkv_stream_t stream) {
+  if (num_tokens < 0 || num_blocks < 0 || num_kv_heads <= 0 || head_dim != 128 ||
+      !valid_block_size(block_size))
+    return PKV_EINVAL;
+  if (num_tokens == 0) return PKV_OK;
+  if (!k || !v || !slot_mapping || !k_cache || !v_cache) return PKV_EINVAL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PKV_EINVAL;
+  const int64_t warps = (static_cast<int64_t>(num_tokens) + 1) / 2 * num_kv_heads;
+  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 0x7fffffff) return PKV_EINVAL;
+  unsigned int* err = device_error_ptr();
+  if (!err) return launch_status();
+  kv_append_int4_kernel<<<static_cast<unsigned>(blocks), kThreads, 0,
+                          static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping, num_tokens,
+      static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
+      static_cast<int64_t>(num_blocks) * block_size, num_kv_heads, block_size, err);
+  return launch_status();
+}
+
+int pkv_widen_blocks_int4(const void* k_cache, const void* v_cache, const int32_t* src,
+                          const int32_t* dst, int n, int num_blocks, void* k_out, void* v_out,
+                          int num_blocks_out, int num_kv_heads, int head_dim, int block_size,
+                          pkv_stream_t stream) {
+  if (n < 0 || num_blocks < 0 || num_blocks_out < 0 || num_kv_heads <= 0 || head_dim != 128 ||
+      !valid_block_size(block_size))
+    return PKV_EINVAL;
+  if (n == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !src || !dst || !k_out || !v_out) return PKV_EINVAL;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+    return PKV_EINVAL;
+  const int64_t rows = static_cast<int64_t>(num_kv_heads) * block_size;
+  const int64_t parts =
+      std::min<int64_t>((rows * kRowLanes + kThreads * 4 - 1) / (kThreads * 4), 1024);
+  if (rows * kRowLanes > 0x3fffffff || 2LL * n * parts > 0x7fffffff) return PKV_EINVAL;
+  unsigned int* err = device_error_ptr();
+  if (!err) return launch_status();
+  widen_blocks_int4_kernel<<<static_cast<unsigned>(2LL * n * parts), kThreads, 0,
+                             static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), src, dst,
+      num_blocks, num_blocks_out, static_cast<int>(parts), static_cast<int>(rows),
+      static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), err);
+  return launch_status();
+}
+
+}  // extern "C"

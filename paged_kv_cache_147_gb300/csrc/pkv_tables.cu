@@ -1,0 +1,363 @@
+// pkv_tables.cu -- block tables and slot maps kept on the GPU: growing each sequence's table for
+// a step's new tokens out of a stack of free blocks (and mapping those tokens to their slots),
+// and cutting tables back.
+//
+// With old lengths n_b, new tokens m_b and block size s, sequence b needs
+// ceil((n_b + m_b) / s) - ceil(n_b / s) blocks. An exclusive prefix sum over the sequences says
+// which blocks of the stack it gets and where its tokens stand in the packed order; everything
+// else is independent per token and per block.
+//
+// There is next to nothing to move (20 bytes per token, 8 per block): a launch and a few dependent
+// round trips bound it. So one launch does it all: every CTA of one cluster scans all sequences
+// by itself (at most kMaxTableSeqs, in shared memory), then takes its share of the tokens and
+// blocks; the cluster barrier keeps the lengths and the stack's count, updated in place at the
+// end, from changing under a CTA that has not read them yet. Past kClusterTokens tokens one
+// cluster's 8 SMs no longer write fast enough, and a grid over the whole GPU does the tokens
+// first and a second launch the rest.
+#include <algorithm>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kMaxTableSeqs = 4096;
+constexpr int kMaxCluster = 8;
+constexpr int kClusterTokens = 65536;
+
+struct TableArgs {
+  int32_t* tables;
+  int32_t* lens;
+  const int32_t* arg;        // extend: new tokens per sequence; truncate: tokens to keep
+  int32_t* free_blocks;
+  int32_t* free_count;
+  int64_t* slots;
+  int32_t* seqs;
+  int64_t* positions;
+  int32_t* cu;
+  int num_seqs, max_blocks, block_size, num_blocks, max_tokens;
+  unsigned int* err;
+};
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// Exclusive sums of two 64-bit values over the CTA's threads, and their totals.
+__device__ __forceinline__ void cta_scan(int64_t& x, int64_t& y, int64_t& total_x,
+                                         int64_t& total_y, int64_t (*part)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t ix = x, iy = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t ux = __shfl_up_sync(0xffffffffu, ix, o);
+    const int64_t uy = __shfl_up_sync(0xffffffffu, iy, o);
+    if (lane >= o) { ix += ux; iy += uy; }
+  }
+  if (lane == 31) { part[warp][0] = ix; part[warp][1] = iy; }
+  __syncthreads();
+  int64_t bx = 0, by = 0;
+  total_x = total_y = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) { bx += part[w][0]; by += part[w][1]; }
+    total_x += part[w][0];
+    total_y += part[w][1];
+  }
+  x = bx + ix - x;
+  y = by + iy - y;
+}
+
+// Largest b in [0, n) with first[b] <= x (first[0] = 0 <= x).
+__device__ __forceinline__ int find(const int* first, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int blocks_of(int64_t tokens, int bs) {
+  return static_cast<int>((tokens + bs - 1) / bs);
+}
+
+// TOKENS: the token arrays and the new table entries; STATE: lengths, count and error bits.
+// Shared memory: tok[n + 1], blk[n + 1], len[n].
+template <bool TOKENS, bool STATE>
+__global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
+  extern __shared__ int smem[];
+  __shared__ int64_t part[kThreads / 32][2];
+  __shared__ int used_s;
+  int* tok = smem;                       // first packed token of each sequence
+  int* blk = tok + a.num_seqs + 1;       // first block (from the top of the stack)
+  int* len = blk + a.num_seqs + 1;       // old length; -1: refused
+  const int n = a.num_seqs, bs = a.block_size;
+  const int tid = threadIdx.x;
+  const int rank = TOKENS && STATE ? cluster_rank() : blockIdx.x;
+  const int ctas = TOKENS && STATE ? cluster_size() : gridDim.x;
+  const int64_t cap = static_cast<int64_t>(a.max_blocks) * bs;
+  unsigned int bad = 0;
+
+  int count = *a.free_count;
+  if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = 0; }
+  if (tid == 0) used_s = 0;
+
+  // ---- the scan: each thread takes `per` neighbouring sequences ----
+  const int per = (n + kThreads - 1) / kThreads;
+  const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
+  int64_t x = 0, y = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int ctx = a.lens[b], m = a.arg[b];
+    const bool ok = ctx >= 0 && ctx <= cap && m >= 0 && ctx + static_cast<int64_t>(m) <= cap;
+    x += max(m, 0);
+    if (ok) y += blocks_of(ctx + static_cast<int64_t>(m), bs) - blocks_of(ctx, bs);
+  }
+  int64_t total_x, total_y;
+  cta_scan(x, y, total_x, total_y, part);
+  int used = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int ctx = a.lens[b], m = a.arg[b];
+    bool ok = true;
+    int need = 0;
+    if (ctx < 0 || ctx > cap || m < 0) {
+      bad |= PKV_DEVERR_CONTEXT;
+      ok = false;
+    } else if (ctx + static_cast<int64_t>(m) > cap) {
+      bad |= PKV_DEVERR_POSITION;
+      ok = false;
+    } else {
+      need = blocks_of(ctx + static_cast<int64_t>(m), bs) - blocks_of(ctx, bs);
+    }
+    tok[b] = static_cast<int>(min(x, static_cast<int64_t>(a.max_tokens)));
+    blk[b] = static_cast<int>(min(y, static_cast<int64_t>(0x7fffffff)));
+    x += max(m, 0);
+    y += need;
+    if (ok && (x > a.max_tokens || (need > 0 && y > count))) {
+      bad |= PKV_DEVERR_SPACE;
+      ok = false;
+    }
+    if (ok && need > 0) used = static_cast<int>(y);
+    len[b] = ok ? ctx : -1;
+  }
+  if (used > 0) atomicMax(&used_s, used);
+  const int live = static_cast<int>(min(total_x, static_cast<int64_t>(a.max_tokens)));
+  if (tid == 0) {
+    tok[n] = live;
+    blk[n] = static_cast<int>(min(total_y, static_cast<int64_t>(count)));
+  }
+  __syncthreads();
+  used = used_s;
+  if (TOKENS && STATE) cluster_arrive();   // this CTA has read the lengths and the count
+
+  if (TOKENS) {
+    // ---- the new tokens, and the padding behind them ----
+    for (int64_t i = static_cast<int64_t>(rank) * kThreads + tid; i < a.max_tokens;
+         i += static_cast<int64_t>(ctas) * kThreads) {
+      int64_t slot = -1, pos = -1;
+      int seq = -1;
+      if (i < live) {
+        const int b = find(tok, n, static_cast<int>(i));
+        if (len[b] >= 0) {
+          seq = b;
+          pos = len[b] + (i - tok[b]);
+          const int lb = static_cast<int>(pos / bs), held = blocks_of(len[b], bs);
+          const int id = lb < held ? a.tables[static_cast<int64_t>(b) * a.max_blocks + lb]
+                                   : a.free_blocks[count - 1 - (blk[b] + lb - held)];
+          if (id >= 0 && id < a.num_blocks)
+            slot = static_cast<int64_t>(id) * bs + (pos - static_cast<int64_t>(lb) * bs);
+          else
+            bad |= PKV_DEVERR_BLOCK_ID;
+        }
+      }
+      a.slots[i] = slot;
+      a.seqs[i] = seq;
+      a.positions[i] = pos;
+    }
+    // ---- the new table entries ----
+    for (int k = rank * kThreads + tid; k < used; k += ctas * kThreads) {
+      const int b = find(blk, n, k);
+      if (len[b] < 0) continue;
+      const int id = a.free_blocks[count - 1 - k];
+      if (id < 0 || id >= a.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
+      a.tables[static_cast<int64_t>(b) * a.max_blocks + blocks_of(len[b], bs) + (k - blk[b])] = id;
+    }
+    for (int b = rank * kThreads + tid; b <= n; b += ctas * kThreads) a.cu[b] = tok[b];
+  }
+  if (bad) atomicOr(a.err, bad);
+  if (STATE) {
+    if (TOKENS) cluster_wait();
+    for (int b = rank * kThreads + tid; b < n; b += ctas * kThreads)
+      if (len[b] >= 0) a.lens[b] = len[b] + a.arg[b];
+    if (rank == 0 && tid == 0) *a.free_count = count - used;
+  }
+}
+
+// Shared memory: blk[n + 1], keep[n].
+__global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
+  extern __shared__ int smem[];
+  __shared__ int64_t part[kThreads / 32][2];
+  int* blk = smem;                       // first freed block of each sequence
+  int* keep = blk + a.num_seqs + 1;      // length kept; -1: as it is
+  const int n = a.num_seqs, bs = a.block_size;
+  const int tid = threadIdx.x;
+  const int rank = cluster_rank(), ctas = cluster_size();
+  const int64_t cap = static_cast<int64_t>(a.max_blocks) * bs;
+  unsigned int bad = 0;
+
+  int count = *a.free_count;
+  if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = a.num_blocks; }
+  const int per = (n + kThreads - 1) / kThreads;
+  const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
+  int64_t x = 0, unused = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int ctx = a.lens[b], m = a.arg[b];
+    if (ctx >= 0 && ctx <= cap && m >= 0 && m < ctx) x += blocks_of(ctx, bs) - blocks_of(m, bs);
+  }
+  int64_t total, total_unused;
+  cta_scan(x, unused, total, total_unused, part);
+  const bool fits = count + total <= a.num_blocks;
+  if (!fits) bad |= PKV_DEVERR_SPACE;
+  for (int b = b0; b < b1; ++b) {
+    const int ctx = a.lens[b], m = a.arg[b];
+    const bool known = ctx >= 0 && ctx <= cap;
+    if (!known) bad |= PKV_DEVERR_CONTEXT;
+    const bool cut = known && m >= 0 && m < ctx;
+    blk[b] = fits ? static_cast<int>(x) : 0;
+    if (cut) x += blocks_of(ctx, bs) - blocks_of(m, bs);
+    keep[b] = cut && fits ? m : -1;
+  }
+  const int freed = fits ? static_cast<int>(total) : 0;
+  if (tid == 0) blk[n] = freed;
+  __syncthreads();
+  cluster_arrive();   // this CTA has read the lengths and the count
+
+  for (int k = rank * kThreads + tid; k < freed; k += ctas * kThreads) {
+    const int b = find(blk, n, k);
+    int32_t* entry =
+        a.tables + static_cast<int64_t>(b) * a.max_blocks + blocks_of(keep[b], bs) + (k - blk[b]);
+    const int id = *entry;
+    if (id < 0 || id >= a.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
+    a.free_blocks[count + freed - 1 - k] = id;
+    *entry = -1;
+  }
+  if (bad) atomicOr(a.err, bad);
+  cluster_wait();
+  for (int b = rank * kThreads + tid; b < n; b += ctas * kThreads)
+    if (keep[b] >= 0) a.lens[b] = keep[b];
+  if (rank == 0 && tid == 0 && freed > 0) *a.free_count = count + freed;
+}
+
+int launch_status() { return cuda_status(cudaGetLastError()); }
+
+int launch_cluster(const void* fn, const TableArgs& a, size_t smem, int cluster,
+                   cudaStream_t stream) {
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+  if (e != cudaSuccess) return cuda_status(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* params[1] = {const_cast<TableArgs*>(&a)};
+  return cuda_status(cudaLaunchKernelExC(&cfg, fn, params));
+}
+
+int cluster_for(int64_t items, int per_cta) {
+  int c = 1;
+  while (c < kMaxCluster && static_cast<int64_t>(c) * per_cta < items) c *= 2;
+  return c;
+}
+
+bool valid_tables(int num_seqs, int max_blocks, int block_size, int num_blocks) {
+  return num_seqs >= 0 && num_seqs <= kMaxTableSeqs && max_blocks >= 0 && num_blocks >= 0 &&
+         valid_block_size(block_size) &&
+         static_cast<int64_t>(max_blocks) * block_size <= 0x7fffffff;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* new_lens,
+                      int num_seqs, int max_blocks_per_seq, int block_size, int32_t* free_blocks,
+                      int32_t* free_count, int num_blocks, int64_t* slot_out, int32_t* seq_out,
+                      int64_t* position_out, int32_t* cu_new_lens, int max_tokens,
+                      pkv_stream_t stream) {
+  if (!valid_tables(num_seqs, max_blocks_per_seq, block_size, num_blocks) || max_tokens < 0)
+    return PKV_EINVAL;
+  if (num_seqs == 0 && max_tokens == 0) return PKV_OK;
+  if ((num_seqs > 0 && (!context_lens || !new_lens || !block_tables)) || !free_blocks ||
+      !free_count || !cu_new_lens || (max_tokens > 0 && (!slot_out || !seq_out || !position_out)))
+    return PKV_EINVAL;
+  TableArgs a = {block_tables, context_lens, new_lens, free_blocks, free_count, slot_out, seq_out,
+                 position_out, cu_new_lens, num_seqs, max_blocks_per_seq, block_size, num_blocks,
+                 max_tokens, device_error_ptr()};
+  if (!a.err) return launch_status();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t smem = (3 * static_cast<size_t>(num_seqs) + 2) * sizeof(int);
+  if (max_tokens <= kClusterTokens)
+    return launch_cluster(reinterpret_cast<const void*>(&extend_kernel<true, true>), a, smem,
+                          cluster_for(max_tokens, 2 * kThreads), s);
+  const int ctas = std::min(2 * sm_count(), (max_tokens + kThreads - 1) / kThreads);
+  if (ctas < 1) return launch_status();
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(&extend_kernel<true, false>),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  extend_kernel<true, false><<<ctas, kThreads, smem, s>>>(a);
+  const int st = launch_status();
+  if (st != PKV_OK) return st;
+  return launch_cluster(reinterpret_cast<const void*>(&extend_kernel<false, true>), a, smem, 1, s);
+}
+
+int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* keep_lens,
+                        int num_seqs, int max_blocks_per_seq, int block_size,
+                        int32_t* free_blocks, int32_t* free_count, int num_blocks,
+                        pkv_stream_t stream) {
+  if (!valid_tables(num_seqs, max_blocks_per_seq, block_size, num_blocks)) return PKV_EINVAL;
+  if (num_seqs == 0) return PKV_OK;
+  if (!block_tables || !context_lens || !keep_lens || !free_blocks || !free_count)
+    return PKV_EINVAL;
+  TableArgs a = {block_tables, context_lens, keep_lens, free_blocks, free_count, nullptr, nullptr,
+                 nullptr, nullptr, num_seqs, max_blocks_per_seq, block_size, num_blocks, 0,
+                 device_error_ptr()};
+  if (!a.err) return launch_status();
+  const size_t smem = (2 * static_cast<size_t>(num_seqs) + 1) * sizeof(int);
+  return launch_cluster(reinterpret_cast<const void*>(&truncate_kernel), a, smem,
+                        cluster_for(static_cast<int64_t>(num_seqs) * max_blocks_per_seq,
+                                    16 * kThreads),
+                        static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

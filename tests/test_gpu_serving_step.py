@@ -1,0 +1,98 @@
+"""The operators of a serving step over a 4-bit cache, as they are used together: prompts are
+admitted (tables on the device, norm + rotation, append, prefill over widened blocks), then
+decode steps with drafts, some of which are taken back."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import int4, step
+from paged_kv_cache_147_gb300 import pkv
+
+from _util import f16_host
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _dev(a):
+    return torch.as_tensor(np.ascontiguousarray(a)).to(DEV)
+
+
+def test_prompts_then_drafts_with_rollback():
+    rng = np.random.default_rng(42)
+    B, hq, hkv, bs, nb, width, q_len = 5, 12, 2, 16, 90, 16, 3
+    scale, eps = 128 ** -0.5, 1e-6
+    table = pkv.rope_table(512)
+    table_h, table_d = table.numpy(), table.to(DEV)
+    w = (1 + 0.2 * rng.standard_normal((2, 128))).astype(np.float16)
+    wd = [_dev(x) for x in w]
+    tables, lens = np.full((B, width), -1, np.int32), np.zeros(B, np.int32)
+    free, count = rng.permutation(nb).astype(np.int32), nb
+    d = [_dev(x) for x in (tables, lens, free, np.array([count], np.int32))]
+    kd, vd = (torch.full((nb, hkv, bs, 80), 255, dtype=torch.uint8, device=DEV) for _ in range(2))
+    kp, vp = kd.cpu().numpy().copy(), vd.cpu().numpy().copy()
+
+    def layer(new, max_tokens):
+        """One step's tables, projections, norm and rotation on the GPU; tables by the oracle."""
+        nonlocal tables, lens, count
+        slots, seqs, pos, cu = pkv.extend_tables(d[0], d[1], _dev(new), bs, d[2], d[3], max_tokens)
+        tables, lens, count, s, q_, p, c, refused = step.extend(tables, lens, new, bs, free, count,
+                                                                max_tokens)
+        assert not refused and np.array_equal(slots.cpu().numpy(), s)
+        x = rng.standard_normal((max_tokens, (hq + 2 * hkv) * 128)).astype(np.float16)
+        xd = _dev(x)
+        q, k = pkv.qk_norm_rope(xd[:, :hq * 128].view(-1, hq, 128),
+                                xd[:, hq * 128:-hkv * 128].view(-1, hkv, 128), *wd, eps, pos, table_d)
+        v = xd[:, -hkv * 128:].view(-1, hkv, 128).contiguous()
+        real = p >= 0
+        for got, lo, hi, ww in ((q, 0, hq, w[0]), (k, hq, hq + hkv, w[1])):
+            want, tol = step.norm_rope(x[real, lo * 128:hi * 128].reshape(-1, hi - lo, 128), ww, eps,
+                                       p[real], table_h)
+            assert (np.abs(got.cpu().numpy()[real].astype(np.float64) - want) <= tol).all()
+        return q, k, v, slots, s
+
+    # ---- prompts of the same chunk length (the prefill's), padded token arrays ----
+    chunk = 37
+    q, k, v, slots, s = layer(np.full(B, chunk, np.int32), B * chunk + 4)
+    pkv.kv_append_int4(k, v, slots, kd, vd)
+    int4.append(f16_host(k), f16_host(v), s, kp, vp)
+    assert np.array_equal(kd.cpu().numpy(), kp) and np.array_equal(vd.cpu().numpy(), vp)
+    used = tables[tables >= 0]
+    wide = [torch.zeros(nb, hkv, bs, 128, dtype=torch.float16, device=DEV) for _ in range(2)]
+    pkv.widen_blocks_int4(kd, vd, _dev(used), _dev(used), *wide)
+    qp = q[:B * chunk].view(B, chunk, hq, 128)
+    out = torch.empty_like(qp)
+    pkv.paged_prefill(out, qp, *wide, d[0], d[1], scale)
+    ref = oracle.paged_attention(f16_host(qp), f16_host(wide[0]), f16_host(wide[1]), tables, lens,
+                                 bs, scale)
+    assert np.abs(out.float().cpu().numpy() - ref).max() <= 2e-3     # the prefill's own bar
+
+    # ---- decode steps: three drafts each, some rejected ----
+    ws = pkv.make_workspace(B, q_len, hq, hkv)
+    for i in range(8):
+        q, k, v, slots, s = layer(np.full(B, q_len, np.int32), B * q_len)
+        out = torch.empty(B, q_len, hq, 128, dtype=torch.float16, device=DEV)
+        qd = q.view(B, q_len, hq, 128)
+        if i % 2:
+            pkv.kv_append_int4(k, v, slots, kd, vd)
+            pkv.paged_attn_decode_int4(out, qd, kd, vd, d[0], d[1], scale, ws)
+        else:
+            pkv.paged_attn_decode_append_int4(out, qd, k, v, kd, vd, d[0], d[1], scale, ws)
+        int4.append(f16_host(k), f16_host(v), s, kp, vp)
+        assert np.array_equal(kd.cpu().numpy(), kp) and np.array_equal(vd.cpu().numpy(), vp)
+        want, tol = int4.attention(f16_host(qd), kp, vp, tables, lens, scale)
+        assert (np.abs(out.float().cpu().numpy() - want) <= tol).all()
+        keep = (lens - rng.integers(0, q_len, B)).astype(np.int32)
+        pkv.truncate_tables(d[0], d[1], _dev(keep), bs, d[2], d[3])
+        tables, lens, free, count = step.truncate(tables, lens, keep, bs, free, count)
+        for got, want in zip(d, (tables, lens, free, np.array([count]))):
+            assert np.array_equal(got.cpu().numpy(), want)
+
+    # ---- one sequence ends; its blocks serve the others ----
+    keep = np.full(B, -1, np.int32)
+    keep[2] = 0
+    pkv.truncate_tables(d[0], d[1], _dev(keep), bs, d[2], d[3])
+    tables, lens, free, count = step.truncate(tables, lens, keep, bs, free, count)
+    assert d[3].item() == count and d[1][2].item() == 0
+    assert pkv.device_error(clear=True) == 0

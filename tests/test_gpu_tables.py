@@ -1,0 +1,167 @@
+"""GPU parity of the block tables kept on the device (extend, truncate) with the step oracle:
+every entry of every array, refusals included."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import step
+from paged_kv_cache_147_gb300 import pkv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _dev(a):
+    return torch.as_tensor(np.ascontiguousarray(a)).to(DEV)
+
+
+def _state(rng, lens, bs, width, spare):
+    lens = np.asarray(lens, np.int32)
+    need = -(-lens // bs)
+    nb = int(need.sum()) + spare
+    perm = rng.permutation(nb).astype(np.int32)
+    tables = np.full((len(lens), width), -1, np.int32)
+    tables[np.arange(width)[None] < need[:, None]] = perm[:nb - spare]
+    free = rng.integers(0, 1000, nb).astype(np.int32)     # entries past the count: anything
+    free[:spare] = perm[nb - spare:]
+    return tables, lens, free, spare
+
+
+def _extend(tables, lens, new, bs, free, count, max_tokens, want_error=0):
+    d = [_dev(x) for x in (tables, lens, np.asarray(new, np.int32), free,
+                           np.array([count], np.int32))]
+    slots, seqs, pos, cu = pkv.extend_tables(d[0], d[1], d[2], bs, d[3], d[4], max_tokens)
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == want_error
+    wt, wl, wc, ws, wq, wp, wcu, _ = step.extend(tables, lens, np.asarray(new), bs, free, count,
+                                                 max_tokens)
+    for got, want in ((d[0], wt), (d[1], wl), (d[3], free), (d[4], np.array([wc])), (slots, ws),
+                      (seqs, wq), (pos, wp), (cu, wcu)):
+        assert np.array_equal(got.cpu().numpy(), want)
+    return d, wt, wl, wc
+
+
+@pytest.mark.parametrize("B,bs,hi,new", [
+    (1, 16, 0, 1), (1, 16, 40, 1), (3, 16, 40, 17), (64, 16, 2048, 1), (64, 64, 500, 5),
+    (700, 32, 100, 40), (4096, 16, 60, 3), (2, 256, 1000, 60000), (300, 16, 64, 1000),
+])
+def test_extend_and_back(B, bs, hi, new):
+    rng = np.random.default_rng(B + bs)
+    lens = rng.integers(0, hi, B, endpoint=True)
+    m = rng.integers(0, new, B, endpoint=True)
+    width = -(-(hi + new) // bs)
+    tables, lens, free, count = _state(rng, lens, bs, width, int((-(-(lens + m) // bs)).sum()) + 3)
+    d, wt, wl, wc = _extend(tables, lens, m, bs, free, count, int(m.sum()) + 7)
+    keep = lens.copy()
+    keep[::3] = -1
+    pkv.truncate_tables(d[0], d[1], _dev(keep), bs, d[3], d[4])
+    tt, tl, tf, tc = step.truncate(wt, wl, keep, bs, free, wc)
+    for got, want in zip((d[0], d[1], d[3], d[4]), (tt, tl, tf, np.array([tc]))):
+        assert np.array_equal(got.cpu().numpy(), want)
+    assert pkv.device_error(clear=True) == 0
+
+
+def test_no_sequences_and_no_tokens():
+    rng = np.random.default_rng(0)
+    tables, lens, free, count = _state(rng, [20, 3], 16, 4, 5)
+    _extend(tables, lens, [0, 0], 16, free, count, 0)
+    _extend(tables, lens, [0, 0], 16, free, count, 9)
+    z = torch.zeros(0, 4, dtype=torch.int32, device=DEV)
+    e = torch.zeros(0, dtype=torch.int32, device=DEV)
+    slots, seqs, pos, cu = pkv.extend_tables(z, e, e, 16, _dev(free),
+                                             _dev(np.array([5], np.int32)), 6)
+    assert (slots == -1).all() and (seqs == -1).all() and (pos == -1).all() and cu.tolist() == [0]
+
+
+def test_refusals_leave_a_sequence_as_it_is():
+    rng = np.random.default_rng(7)
+    bs = 16
+    tables, lens, free, count = _state(rng, [20, 16, 40, 5, 0, 31], bs, 6, 9)
+    # a negative count, one past the table (6 x 16 = 96), one served
+    _extend(tables, lens, [3, -2, 57, 4, 0, 1], bs, free, count, 80,
+            want_error=pkv.DEVERR_CONTEXT | pkv.DEVERR_POSITION)
+    # the third past the table (40 + 60 of 96), so that the 7 blocks of the others suffice
+    _extend(tables, lens, [50, 60, 60, 2, 0, 1], bs, free, count, 200,
+            want_error=pkv.DEVERR_POSITION)
+    # blocks run out at the third (3 + 4 + 3 of 9); the later ones that need none are served
+    _extend(tables, lens, [50, 60, 50, 2, 0, 1], bs, free, count, 200, want_error=pkv.DEVERR_SPACE)
+    # the token arrays are too small for the third
+    _extend(tables, lens, [10, 10, 10, 2, 0, 1], bs, free, count, 25, want_error=pkv.DEVERR_SPACE)
+    # a length outside the table
+    bad = lens.copy()
+    bad[1], bad[2] = 97, -1
+    _extend(tables, bad, [1, 1, 1, 1, 1, 1], bs, free, count, 6, want_error=pkv.DEVERR_CONTEXT)
+    # a free id outside the pool: in the table as it is, its tokens' slots -1
+    free2 = free.copy()
+    free2[count - 1] = len(free) + 4
+    _extend(tables, lens, [20, 1, 1, 1, 1, 1], bs, free2, count, 25, want_error=pkv.DEVERR_BLOCK_ID)
+    # counts no stack has
+    d = [_dev(x) for x in (tables, lens, np.full(6, 40, np.int32), free, np.array([999], np.int32))]
+    pkv.extend_tables(d[0], d[1], d[2], bs, d[3], d[4], 300)
+    assert pkv.device_error(clear=True) == pkv.DEVERR_SPACE
+    assert np.array_equal(d[0].cpu().numpy(), tables) and np.array_equal(d[1].cpu().numpy(), lens)
+
+
+def test_truncate_refuses_more_blocks_than_the_stack_holds():
+    rng = np.random.default_rng(9)
+    tables, lens, free, count = _state(rng, [64, 40], 16, 4, 3)
+    d = [_dev(x) for x in (tables, lens, np.array([0, 0], np.int32), free[:6],
+                           np.array([3], np.int32))]
+    pkv.truncate_tables(d[0], d[1], d[2], 16, d[3], d[4])
+    assert pkv.device_error(clear=True) == pkv.DEVERR_SPACE
+    assert np.array_equal(d[0].cpu().numpy(), tables) and np.array_equal(d[1].cpu().numpy(), lens)
+    assert d[4].item() == 3
+
+
+def test_many_tokens_take_the_wide_path_and_agree_with_the_narrow_one():
+    rng = np.random.default_rng(13)
+    B, bs = 200, 16
+    lens = rng.integers(0, 100, B)
+    m = rng.integers(0, 900, B)
+    tables, lens, free, count = _state(rng, lens, bs, 64, int((-(-(lens + m) // bs)).sum()))
+    assert m.sum() > 65536 > (m // 2).sum()
+    _extend(tables, lens, m, bs, free, count, 65536, want_error=pkv.DEVERR_SPACE)   # one launch
+    _extend(tables, lens, m // 2, bs, free, count, 65536)
+    _extend(tables, lens, m // 2, bs, free, count, 65537)                           # two
+    _extend(tables, lens, m, bs, free, count, 400001)
+    _extend(tables, lens, m, bs, free, count - 900, 400001, want_error=pkv.DEVERR_SPACE)
+
+
+def test_captured_in_a_graph_and_replayed():
+    rng = np.random.default_rng(17)
+    bs, B = 16, 12
+    tables, lens, free, count = _state(rng, rng.integers(0, 50, B), bs, 9, 60)
+    new = np.ones(B, np.int32)
+    d = [_dev(x) for x in (tables, lens, new, free, np.array([count], np.int32))]
+    out = pkv.extend_tables(d[0].clone(), d[1].clone(), d[2], bs, d[3].clone(), d[4].clone(), B + 2)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        pkv.extend_tables(d[0], d[1], d[2], bs, d[3], d[4], B + 2, out=out)
+    want = (tables, lens, count)
+    for _ in range(20):
+        graph.replay()
+        t, l, c, slots, seqs, pos, cu, _ = step.extend(want[0], want[1], new, bs, free, want[2], B + 2)
+        want = (t, l, c)
+        for got, w in zip((d[0], d[1], d[4]) + tuple(out), (t, l, np.array([c]), slots, seqs, pos, cu)):
+            assert np.array_equal(got.cpu().numpy(), w)
+    assert pkv.device_error(clear=True) == 0
+
+
+def test_binding_refuses_wrong_types_and_shapes():
+    z = torch.zeros(2, 4, dtype=torch.int32, device=DEV)
+    n, one = z[0, :2].clone(), z[0, :1].clone()
+    bad = [
+        lambda: pkv.extend_tables(z.long(), n, n, 16, n, one, 4),
+        lambda: pkv.extend_tables(z[:1], n, n, 16, n, one, 4),
+        lambda: pkv.extend_tables(z, n, n[:1], 16, n, one, 4),
+        lambda: pkv.extend_tables(z, n, n, 12, n, one, 4),
+        lambda: pkv.extend_tables(z.t(), z[0].clone(), z[0].clone(), 16, n, one, 4),
+        lambda: pkv.truncate_tables(z, n, n.float(), 16, n, one),
+        lambda: pkv.truncate_tables(z, n, n, 16, n.cpu(), one),
+    ]
+    for call in bad:
+        with pytest.raises(pkv.PkvError) as e:
+            call()
+        assert e.value.status == pkv.EINVAL
