@@ -86,6 +86,10 @@ def attention(q, k_pool, v_pool, tables, lens, scale):
     tol is how far a result may be off that rounds each value and each softmax weight once to
     fp16 (half a step, 2^-11 relative each; a weight below 2^-14 of a warp's largest by 2^-25
     of it), sums in fp32, and rounds the output once (2^-11 relative, 2^-25 for subnormals).
+    The fp32 sums of p s code and of p z may be kept apart: they nearly cancel where a value is
+    near zero, so their errors are relative to S = sum p (15 s + |z|). A tensor-core sum
+    truncates by less than 2^-23 of it, at most 64 times in a row here (64 steps of 16 keys a
+    warp): 2^-17 S.
     Scores: products of q with codes and with minima are summed separately, so their error is
     relative to sum |q| (15 s + |z|); at most 32 roundings of 2^-23 each (truncating tensor-core
     sums) on the way, 2^-18. A relative error e of the weights moves the output by at most
@@ -103,7 +107,9 @@ def attention(q, k_pool, v_pool, tables, lens, scale):
         ids = tables[b, :(n + bs - 1) // bs]
         for h in range(hkv):
             kc, ks, kz = parts(k_pool[ids, h].reshape(-1, ROW)[:n])
-            K, V = ks * kc + kz, values(v_pool[ids, h].reshape(-1, ROW)[:n])
+            vc, vs, vz = parts(v_pool[ids, h].reshape(-1, ROW)[:n])
+            K, V = ks * kc + kz, vs * vc + vz
+            reach_v = 15 * np.abs(vs) + np.abs(vz)
             reach = 15 * np.abs(ks) + np.abs(kz)
             for i in range(q_len):
                 m = n - q_len + i + 1
@@ -119,5 +125,6 @@ def attention(q, k_pool, v_pool, tables, lens, scale):
                 out[b, i, h * group:(h + 1) * group] = o
                 tol[b, i, h * group:(h + 1) * group] += (
                     (2 * 2.0 ** -11 + 2 * e) * avg + 2.0 ** -11 * np.abs(o) +
+                    2.0 ** -17 * ((p / L) @ reach_v[:m]) +
                     m * 2.0 ** -25 / L * np.abs(V[:m]).max())
     return out, tol

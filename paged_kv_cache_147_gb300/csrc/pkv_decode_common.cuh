@@ -443,20 +443,21 @@ struct LastSeg {
 
 // End of the slice: the consumers and the epilogue warp (kNE threads, dense index t) merge the
 // last segment, then any split unit whose last partial arrived from this CTA (the producer has
-// left). smem: the CTA's stage memory, stage_bytes of it; stO, stM, stL: the double-buffered
-// per-warp states; npend_s, fast_s: the CTA's pending merges and the outcome of the wait.
-template <int NCW, int SEG = kSegCost>
+// left). smem: the CTA's stage memory, stage_bytes of it; stO, stM, stL: the per-warp states, SB
+// buffers of NCW states; npend_s, fast_s: the CTA's pending merges and the outcome of the wait.
+// WARPS: consumer warps (more than NCW where several hold different rows of one state).
+template <int NCW, int SEG = kSegCost, int WARPS = NCW, int SB = 2>
 __device__ __forceinline__ void finish_slice(const DecodeArgs& a, const LastSeg& ls,
                                              const int* pre, int per, uint8_t* smem,
                                              int stage_bytes, float* stO, const float* stM,
                                              const float* stL, int* npend_s,
                                              volatile int* fast_s, int t) {
-  constexpr int kNE = (NCW + 1) * 32;
+  constexpr int kNE = (WARPS + 1) * 32;
   const int ua = unit_first<SEG>(pre, a.Hkv, ls.b, ls.h, ls.nb);
   const int parts = (ua + ls.nb - 1) / per - ua / per + 1;
   const MergeStage ms(smem, stage_bytes, a.R);
   named_barrier_sync(2, kNE);                  // last states written, earlier segments merged
-  const int sb = ls.k & 1;
+  const int sb = ls.k % SB;
   float* so_w = stO + sb * NCW * a.R * kSt;
   const float* sm_w = stM + sb * NCW * a.R;
   const float* sl_w = stL + sb * NCW * a.R;
@@ -531,16 +532,16 @@ __device__ __forceinline__ uint32_t u4_word(const uint4& v, int i) {
 }
 
 // Requests segment kk's queries (and, fused append, its new K/V rows) into query buffer kk & 1,
-// completing on that buffer's full barrier; waits first until the consumers have released the
-// buffer's previous use. One thread.
-template <class L, bool APPEND>
+// completing on that buffer's full barrier (bar_qfull, followed by the empty ones); waits first
+// until the consumers have released the buffer's previous use (WAIT; otherwise the caller has).
+// One thread.
+template <class L, bool APPEND, bool WAIT = true>
 __device__ __forceinline__ void issue_queries(const DecodeArgs& a, const CUtensorMap* tmQ,
-                                              uint32_t sbase, int B, const Seg& sg, int kk,
-                                              volatile int* abort) {
-  const uint32_t bar_qfull = sbase + L::kBars + 2 * L::kNST * 8;
+                                              uint32_t sbase, uint32_t bar_qfull, int B,
+                                              const Seg& sg, int kk, volatile int* abort) {
   const uint32_t bar_qempty = bar_qfull + 2 * 8;
   const int qs = kk & 1;
-  if (kk >= 2 && !mbar_wait(bar_qempty + qs * 8, ((kk >> 1) - 1) & 1, abort))
+  if (WAIT && kk >= 2 && !mbar_wait(bar_qempty + qs * 8, ((kk >> 1) - 1) & 1, abort))
     flag_timeout(a, abort);
   mbar_arrive_expect_tx(bar_qfull + qs * 8, a.R * 256 + (APPEND ? a.q_len * 512 : 0));
   const uint32_t qdst = sbase + L::kQ + qs * L::kQBuf;
@@ -613,13 +614,12 @@ inline WsLayout ws_layout(int num_seqs, int Hkv, int R) {
 
 inline int encode(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
                   const cuuint64_t* strides, const cuuint32_t* box,
-                  CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                  CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                  CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16) {
   auto fn = tensor_map_encoder();
   if (!fn) return PKV_ECUDA_BASE - static_cast<int>(cudaErrorNotSupported);
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, type, rank, const_cast<void*>(base), dims,
-                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PKV_OK : PKV_EINVAL;
 }

@@ -4,29 +4,44 @@
 // What it computes: pkv_paged_attn_decode's operation with K_t[d] = s_K code_K + z_K and
 // V_t[d] = s_V code_V + z_V, (s, z) of the 32 elements that d belongs to.
 //
-// What bounds it: 160 bytes per (token, kv head) against 512 of the fp16 cache, so the widening of
-// the codes, not the loads, is what the loop has to keep short. It is written so that a step of
-// 16 keys takes a warp about 300 issue slots for up to 8 query rows:
+// What bounds it: 160 bytes per (token, kv head) against 512 of the fp16 cache, so the work per
+// key, not the loads, is what the loop has to keep short: at the copy rate an SM has ~109 cycles
+// for 16 keys of one kv head. Codes go to the tensor cores as they stand; nothing is widened
+// per element:
 //  * Stream, slices, split units and their merge are those of pkv_decode.cu (shared in
-//    pkv_decode_common.cuh). A stage holds two 16-token chunks: K of both, V of both, four boxes
-//    of 16 rows x 80 bytes (rows 20 words apart: any 8 rows x 4 words touch all 32 banks, so
-//    the tiles need no swizzle).
-//  * Transposed tile: S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16, keys (and output dims)
-//    on the 16-row side, query rows in NT tiles of 8 columns. A code is widened once for all NT.
-//  * Keys: sum_d q_d (s c_d + z) = s sum_d q_d c_d + z sum_d q_d per group of 32 dims. The codes
-//    go to the tensor cores as they stand: four bits at bits 4-7 of a 16-bit half are the fp16
-//    (subnormal) number c 2^-20, exactly, and one AND of a shifted word makes two of them. The
-//    group's two products (32 dims) are scaled by s in fp32; 2^20 joins the score scale. z times
-//    the group's query sum is one more product per 16 keys: a row's four (s, z) pairs as they
-//    stand against (0, mean of q over the group), the mean split in two fp16 numbers (it is
-//    held as sum / 32 so that no sum of finite fp16 queries overflows).
-//  * Values: s varies with the key, the summed dimension, so V is widened: pairs of neighbouring
-//    keys' codes by byte permutes, code = (1024 + code) - 1024 in fp16, then s code + z by one
-//    fused multiply-add: rounded once to fp16 (2^-12 relative, as a cached fp16 V would be).
-//    A thread's 16 output dims lie in one group, so it needs one (s, z) pair per key.
-//  * Softmax as in pkv_decode.cu (fp32, exp2 domain, lazy running maximum); weights in fp16.
+//    pkv_decode_common.cuh). A stage is two 16-token chunks: K of both, V of both, four runs of
+//    1280 contiguous bytes. Rows are 20 words apart: any 8 rows x 16 bytes touch all 32 banks
+//    without a swizzle.
+//  * No producer: every consumer warp keeps a ring of its own stages in flight with cp.async (10
+//    copies of 512 bytes a stage), waits for its own copies and needs no barrier. One producer
+//    warp for all (tensor tiles or bulk copies, an mbarrier pair per stage) took ~450 ns a stage
+//    whatever its size, which bounded the kernel at 3 TB/s.
+//  * Transposed tile: S^T = K Q^T and O^T = V^T P^T, keys (and output dims) on the mma's 16-row
+//    side, query rows in tiles of 8 columns (NT of them a warp).
+//  * Four bits at bits 0-3 (4-7) of a 16-bit half are the fp16 subnormal c 2^-24 (c 2^-20),
+//    exactly, and the products' sums are fp32: one AND of a word or of the word shifted by 8
+//    makes an mma operand of two codes.
+//  * Keys: sum_d q_d (s c_d + z) = s sum_d q_d c_d + z sum_d q_d per group of 32 dims. The
+//    queries are scaled by a power of two that puts the row's largest between 128 and 256, those
+//    that meet codes at bits 0-3 by 16 more (both exact: what falls below fp16's smallest is
+//    under 2^-31 of the row's largest). The group's sum is scaled by s in fp32; z times the
+//    group's query sum is one more product per 16 keys, the (s, z) words as they stand against
+//    (0, sum), the sum split in two fp16 numbers.
+//  * Values: O[d] = sum_k (p_k s_k) c_kd + sum_k p_k z_k. ldmatrix.trans brings, per group, a
+//    register with four codes of two neighbouring keys. The weights take the group's scales as
+//    packed fp16 products, each with what its rounding left over as a second operand (s c and z
+//    nearly cancel for values near zero, so an error of 2^-11 of s c would show). The minima's
+//    sum is one product per 16 keys with the (s, z) halves as its rows; it is added when the
+//    segment ends.
+//  * Softmax as in pkv_decode.cu (fp32, exp2 domain, a reference that follows the running
+//    maximum lazily). p and p s are fp16: the reference stays kShift = 11 powers of two below
+//    the maximum while every scale is below 2 (p < 2^13, p s < 2^14, and values of 1e-6 still
+//    count); the first scale of 2 or more (values over a range of 30) moves it up to the maximum
+//    (p <= 4, p s <= 4 x 8736) for the rest of the segment.
 //  * Tokens past the context hold anything: their scores are masked and their (s, z) of V set
-//    to zero before the widening.
+//    to zero.
+//  * More than 16 rows: two warps take a stage, each with half of the row tiles (and its own
+//    copy, the second of which comes from L2).
 #include <cuda_fp16.h>
 
 #include "pkv_decode_common.cuh"
@@ -40,20 +55,23 @@ namespace {
 constexpr int kTile = kChunk * kInt4Row;     // one chunk's K (or V): 1280 bytes
 constexpr int kStage4 = 4 * kTile;           // K of two chunks, V of two chunks
 constexpr int kSeg4 = 4;                     // per-segment cost in chunks (see kSegCost)
+// How far the softmax's reference stays below the running maximum (see above), and how far a
+// weight may grow past the maximum it was taken at before the reference moves.
+constexpr float kShift = 11.f, kGrow = 2.f;
 
-// Shared-memory layout (offsets from a 1024-byte aligned base); the names are those the shared
-// helpers use.
-template <int NCW, int NST, int NT>
+// Shared-memory layout (offsets from a 1024-byte aligned base). NCS: warps that share the stages
+// among them, RS: warps that take one stage (row halves), ND: stages in flight per warp, SB:
+// buffers of segment states.
+template <int NCS, int RS, int ND, int NT, int SB>
 struct Smem4 {
-  static constexpr int kNST = NST;
-  static constexpr int kQHalf = NT * 1024;            // 8 NT rows x 128 B
+  static constexpr int kRows = 8 * RS * NT;
+  static constexpr int kQHalf = kRows * 128;
   static constexpr int kQBuf = 2 * kQHalf;
-  static constexpr int kQ = NST * kStage4;
-  static constexpr int kBars = kQ + 2 * kQBuf;        // full, empty, qfull, qempty, sdone, sfree
-  static constexpr int kFlags = kBars + (2 * NST + 8) * 8;
-  static constexpr int kSrow = kFlags + 64;           // TMA rows of each stage's two chunks
-  static constexpr int kState = kSrow + ((NST * 8 + 15) & ~15);
-  __host__ __device__ static int state_floats(int R) { return 2 * NCW * R * (kSt + 2); }
+  static constexpr int kQ = ((NCS * RS * ND * kStage4 + 1023) & ~1023);   // swizzle atoms
+  static constexpr int kBars = kQ + 2 * kQBuf;        // qfull[2], sdone[2], sfree[2]
+  static constexpr int kFlags = kBars + 6 * 8;
+  static constexpr int kState = (kFlags + 64 + 15) & ~15;
+  __host__ __device__ static int state_floats(int R) { return SB * NCS * R * (kSt + 2); }
   __host__ __device__ static int seq_off(int R) { return kState + state_floats(R) * 4; }
   __host__ __device__ static int newkv_off(int R, int B) {
     return (seq_off(R) + (2 * B + 1) * 4 + 127) & ~127;
@@ -61,44 +79,134 @@ struct Smem4 {
   __host__ static size_t bytes(int R, int B, int newkv_bytes) {
     return 1024 + static_cast<size_t>(newkv_off(R, B)) + static_cast<size_t>(newkv_bytes);
   }
-  static_assert(kStage4 % 1024 == 0 && kQHalf % 1024 == 0, "swizzle atoms of the query tiles");
   // the merge of split units stages at least two partials in the stage memory
-  static_assert(kQ >= 8 * NT * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
+  static_assert(kQ >= kRows * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
 };
 
-// (x & m), the four bits of each half at bits 4-7: c 2^-20 as fp16.
-__device__ __forceinline__ uint32_t nibs(uint32_t x) { return x & 0x00f000f0u; }
+// A warp's walk over the stages it loads: stage jp of a segment goes to warp (jp + stages before
+// the segment) mod NCS. Pool rows are fetched for up to 16 of the warp's stages at once (lane l:
+// chunk l & 1 of the (l / 2)-th), one group ahead of their use.
+template <int NCS>
+struct StageWalk {
+  Seg s;
+  int j, jp;        // stages of the slice before the segment; the warp's next stage in it
+  bool has;
+  int rows, n, i;   // current group: pool rows per lane, stages, position
+  int ids, at, nn;  // group ahead: block ids, (h << 16 | first row in the block) per lane, stages
 
-// Warp roles as in decode_kernel: warps 0..NCW-1 consume stages, warp NCW produces, warp NCW+1 is
-// the epilogue.
-template <int NCW, int NST, int NT, int MINB, bool APPEND>
-__global__ void __launch_bounds__((NCW + 2) * 32, MINB)
-decode_int4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                   const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) {
-  using L = Smem4<NCW, NST, NT>;
-  static_assert(NST % NCW == 0, "pipeline stages must be a multiple of the consumer warps");
-  // more than two row tiles: the query fragments do not fit the registers and are read from the
-  // (permuted) query tile, which then stays in use for the whole segment
-  constexpr bool kQSmem = NT > 2;
-  constexpr bool kHoldQ = APPEND || kQSmem;
-  constexpr int kNC = NCW * 32;
+  __device__ __forceinline__ static int npair(const Seg& s) { return (s.c1 - s.c0 + 1) >> 1; }
+  __device__ __forceinline__ void enter(int w) { jp = ((w - j) % NCS + NCS) % NCS; }
+
+  // requests the block ids of the next group
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, const CursorT<kSeg4>& cur, int w,
+                                        int lane) {
+    nn = 0;
+    ids = -1;
+    at = -1;
+    while (has && jp >= npair(s)) {
+      j += npair(s);
+      has = cur.next(s);
+      enter(w);
+    }
+    if (!has) return;
+    const int np = npair(s);
+    nn = min(16, (np - jp + NCS - 1) / NCS);
+    const int c = s.c0 + 2 * (jp + (lane >> 1) * NCS) + (lane & 1);
+    if ((lane >> 1) < nn && c < s.c1) {
+      ids = __ldg(a.block_tables + static_cast<int64_t>(s.b) * a.max_blocks + (c >> a.bs_shift));
+      at = (s.h << 8) | ((c & ((1 << a.bs_shift) - 1)) << 4);
+    }
+    jp += nn * NCS;
+  }
+  // makes it the current one: rows (-1: no chunk, -2: bad block id)
+  __device__ __forceinline__ void take(const DecodeArgs& a) {
+    rows = -1;
+    if (at >= 0) {
+      if (ids >= 0 && ids < a.num_blocks) {
+        rows = (ids * a.Hkv + (at >> 8)) * a.block_size + (at & 255);
+      } else {
+        atomicOr(a.err, PKV_DEVERR_BLOCK_ID);
+        rows = -2;
+      }
+    }
+    n = nn;
+    i = 0;
+  }
+  __device__ __forceinline__ void start(const DecodeArgs& a, const CursorT<kSeg4>& cur, int begin,
+                                        int w, int lane) {
+    j = 0;
+    has = cur.first(begin, s);
+    enter(w);
+    fetch(a, cur, w, lane);
+    take(a);
+    fetch(a, cur, w, lane);
+  }
+  // requests the warp's next stage into buffer `dst`, if there is one; one group of copies
+  __device__ __forceinline__ void load(const DecodeArgs& a, const CursorT<kSeg4>& cur, int w,
+                                       int lane, uint32_t dst, uint64_t policy) {
+    if (i == n) {
+      take(a);
+      fetch(a, cur, w, lane);
+    }
+    if (i < n) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = __shfl_sync(0xffffffffu, rows, 2 * i + h);
+        const uint32_t kd = dst + h * kTile, vd = kd + 2 * kTile;
+        if (r >= 0) {
+          // 80 pieces of 16 bytes each of K and V: 64 + 64, and the last 16 of both together
+          const int64_t off = static_cast<int64_t>(r) * kInt4Row + lane * 16;
+          const uint8_t* ks = reinterpret_cast<const uint8_t*>(a.k_pool) + off;
+          const uint8_t* vs = reinterpret_cast<const uint8_t*>(a.v_pool) + off;
+          cp_async_16_hint(kd + lane * 16, ks, policy);
+          cp_async_16_hint(kd + lane * 16 + 512, ks + 512, policy);
+          cp_async_16_hint(vd + lane * 16, vs, policy);
+          cp_async_16_hint(vd + lane * 16 + 512, vs + 512, policy);
+          const bool k16 = lane < 16;
+          cp_async_16_hint((k16 ? kd : vd - 256) + lane * 16 + 1024, (k16 ? ks : vs - 256) + 1024,
+                           policy);
+        } else if (r == -2) {   // a chunk behind a bad block id reads as zeros
+          for (int x = lane; x < kTile / 16; x += 32) {
+            st_shared_v4(kd + x * 16, make_uint4(0, 0, 0, 0));
+            st_shared_v4(vd + x * 16, make_uint4(0, 0, 0, 0));
+          }
+        }
+      }
+      ++i;
+    }
+    cp_async_commit();
+  }
+};
+
+// The products without `volatile`: the compiler may order them (pkv_device.cuh's keep theirs).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Warps 0 .. NCS RS - 1 consume; the last warp loads the queries and is the epilogue (merges
+// each segment's per-warp states, writes outputs and split units' partials).
+template <int NCS, int RS, int ND, int NT, int SB, int MINB, bool APPEND>
+__global__ void __launch_bounds__((NCS * RS + 1) * 32, MINB)
+decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) {
+  using L = Smem4<NCS, RS, ND, NT, SB>;
+  constexpr int NCW = NCS * RS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar_full = sbase + L::kBars;
-  const uint32_t bar_empty = bar_full + NST * 8;
-  const uint32_t bar_qfull = bar_empty + NST * 8;
-  const uint32_t bar_qempty = bar_qfull + 2 * 8;
-  const uint32_t bar_sdone = bar_qempty + 2 * 8;
+  const uint32_t bar_qfull = sbase + L::kBars;
+  const uint32_t bar_sdone = bar_qfull + 2 * 8;
   const uint32_t bar_sfree = bar_sdone + 2 * 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kFlags);
-  int* srow_s = reinterpret_cast<int*>(smem + L::kSrow);
   int* npend_s = reinterpret_cast<int*>(smem + L::kFlags) + 1;   // then 2 x (b, h, nb)
   volatile int* fast_s = reinterpret_cast<volatile int*>(smem + L::kFlags) + 8;
-  float* stO = reinterpret_cast<float*>(smem + L::kState);       // [2][NCW][R][kSt]
-  float* stM = stO + 2 * NCW * a.R * kSt;                         // [2][NCW][R]
-  float* stL = stM + 2 * NCW * a.R;                               // [2][NCW][R]
+  float* stO = reinterpret_cast<float*>(smem + L::kState);       // [SB][NCS][R][kSt]
+  float* stM = stO + SB * NCS * a.R * kSt;                        // [SB][NCS][R]
+  float* stL = stM + SB * NCS * a.R;                              // [SB][NCS][R]
   int* pre = reinterpret_cast<int*>(smem + L::seq_off(a.R));
   int* slen = pre + a.num_seqs + 1;
 
@@ -122,13 +230,8 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   for (int i = tid; i < L::kQBuf * 2 / 16; i += blockDim.x)
     reinterpret_cast<uint4*>(smem + L::kQ)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) {
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(bar_full + s * 8, 1);
-      mbar_init(bar_empty + s * 8, 1);
-    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_qfull + s * 8, 1);
-      mbar_init(bar_qempty + s * 8, NCW);
       mbar_init(bar_sdone + s * 8, NCW);
       mbar_init(bar_sfree + s * 8, 1);
     }
@@ -150,112 +253,32 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   // before it reads anything this kernel writes)
   if (tid == 0) griddep_launch_dependents();
 
-  if (warp == NCW) {
-    // =================================== producer ============================================
-    const int chunk_mask = (1 << a.bs_shift) - 1;
-    const uint64_t kv_policy = l2_policy_evict_first();
-    int j = 0, k = 0;
-    Seg s;
-    bool has = cur.first(begin, s);
-    auto load_ids = [&](const Seg& sg, int cb) -> int32_t {
-      const int cc = cb + lane;
-      return cc < sg.c1 ? __ldg(a.block_tables + static_cast<int64_t>(sg.b) * a.max_blocks +
-                                (cc >> a.bs_shift))
-                        : -1;
-    };
-    int32_t ids = has ? load_ids(s, s.c0) : -1;
-    if (lane == 0) {
-      prefetch_tensormap(&tmK);
-      prefetch_tensormap(&tmV);
-      prefetch_tensormap(&tmQ);
-    }
-    // An early-started launch (APPEND) requests its first stages at once and waits for the
-    // preceding kernel before the queries; the epilogue warp requests the first segment's.
-    bool waited = false;
-    while (has) {
-      if (!APPEND || k > 0) {
-        if (!waited) { griddep_wait(); waited = true; }
-        if (lane == 0) issue_queries<L, APPEND>(a, &tmQ, sbase, B, s, k, abort);
-      }
-      Seg nx = s;
-      const bool has_next = cur.next(nx);
-      for (int cb = s.c0; cb < s.c1; cb += 32) {
-        const int32_t cur_ids = ids;
-        if (cb + 32 < s.c1) ids = load_ids(s, cb + 32);
-        else if (has_next) ids = load_ids(nx, nx.c0);
-        const int cc = cb + lane;
-        int row = -kChunk;  // an out-of-range box: TMA fills it with zeros
-        if (cc < s.c1) {
-          if (cur_ids >= 0 && cur_ids < a.num_blocks)
-            row = (cur_ids * a.Hkv + s.h) * a.block_size + ((cc & chunk_mask) << 4);
-          else
-            atomicOr(a.err, PKV_DEVERR_BLOCK_ID);
-        }
-        const int n = min(32, s.c1 - cb);
-        for (int l = 0; l < n; l += 2, ++j) {
-          if (APPEND && !waited && j == NST) {
-            griddep_wait();   // every stage is requested; none frees before the dependency is met
-            waited = true;
-          }
-          const int r = __shfl_sync(0xffffffffu, row, l);
-          const int r2 = __shfl_sync(0xffffffffu, row, (l + 1) & 31);   // l + 1 < n, or out of range
-          const int st = j % NST;
-          const uint32_t fb = bar_full + st * 8;
-          if (lane == 0) {
-            if (j >= NST && !mbar_wait(bar_empty + st * 8, ((j / NST) - 1) & 1, abort))
-              flag_timeout(a, abort);
-            if (APPEND) {
-              srow_s[2 * st] = r;
-              srow_s[2 * st + 1] = r2;
-            }
-            mbar_arrive_expect_tx(fb, kStage4);
-          }
-          __syncwarp();
-          if (lane < 4)
-            tma_load_2d_hint(sbase + st * kStage4 + lane * kTile, (lane >> 1) ? &tmV : &tmK, 0,
-                             (lane & 1) ? r2 : r, fb, kv_policy);
-        }
-      }
-      ++k;
-      s = nx;
-      has = has_next;
-    }
-    if (!waited) griddep_wait();
-    // sequences without any chunk get zeros (their units are in no CTA's slice)
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-      if (pre[b + 1] != pre[b]) continue;
-      const int n = a.q_len * a.Hq * kD;
-      for (int i = lane; i < n; i += 32)
-        a.out[static_cast<int64_t>(b) * n + i] = __float2half_rn(0.f);
-    }
-    // no TMA write into this CTA's shared memory may be pending when it exits
-    if (lane == 0) {
-      for (int jj = max(0, j - NST); jj < j; ++jj)
-        if (!mbar_wait(bar_full + (jj % NST) * 8, (jj / NST) & 1, nullptr)) flag_timeout(a, abort);
-      for (int kk = max(0, k - 2); kk < k; ++kk)
-        if (!mbar_wait(bar_qfull + (kk & 1) * 8, (kk >> 1) & 1, nullptr)) flag_timeout(a, abort);
-    }
-    return;
-  }
-
   const LastSeg last = LastSeg::of(cur, begin);
 
-  if (warp == NCW + 1) {
-    // =================================== epilogue ============================================
-    int k = 0, npend = 0;
-    Seg s;
-    bool has = cur.first(begin, s);
-    if (APPEND && has) {
-      griddep_wait();
-      if (lane == 0) issue_queries<L, APPEND>(a, &tmQ, sbase, B, s, 0, abort);
-    }
-    while (has && k < last.k) {
-      const int sb = k & 1;
-      if (!mbar_wait(bar_sdone + sb * 8, (k >> 1) & 1, abort)) flag_timeout(a, abort);
+  if (warp == NCW) {
+    // ============================ queries and epilogue =======================================
+    if (lane == 0) prefetch_tensormap(&tmQ);
+    // An early-started launch (APPEND) has its first stages on the way already; queries, new
+    // rows, outputs and the workspace are touched only after the preceding kernel completed.
+    griddep_wait();
+    Seg q;                       // segment whose queries go out next
+    bool has_q = cur.first(begin, q);
+    auto load_queries = [&](int kk) {
+      if (lane == 0) issue_queries<L, APPEND, false>(a, &tmQ, sbase, bar_qfull, B, q, kk, abort);
+      has_q = cur.next(q);
+    };
+    Seg s = q;
+    if (has_q) load_queries(0);
+    if (has_q) load_queries(1);
+    int npend = 0;
+    for (int k = 0; k < last.k; ++k) {
+      const int sb = k % SB;
+      if (!mbar_wait(bar_sdone + sb * 8, (k / SB) & 1, abort)) flag_timeout(a, abort);
+      if (has_q) load_queries(k + 2);   // segment k's query buffer is free
       const bool complete = (s.c0 == 0 && s.c1 == s.nb);
       const int slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
-      merge_segment<NCW, 32>(a, stO + sb * NCW * a.R * kSt, stM + sb * NCW * a.R,
-                             stL + sb * NCW * a.R, s.b, s.h, complete,
+      merge_segment<NCS, 32>(a, stO + sb * NCS * a.R * kSt, stM + sb * NCS * a.R,
+                             stL + sb * NCS * a.R, s.b, s.h, complete,
                              a.part_o + static_cast<int64_t>(slot) * a.R * kD,
                              a.part_ml + static_cast<int64_t>(slot) * a.R * 4, lane);
       __syncwarp();
@@ -271,15 +294,35 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
           ++npend;
         }
       }
-      ++k;
-      has = cur.next(s);
+      cur.next(s);
     }
     if (lane == 0) *npend_s = npend;
+    // sequences without any chunk get zeros (their units are in no CTA's slice)
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+      if (pre[b + 1] != pre[b]) continue;
+      const int n = a.q_len * a.Hq * kD;
+      for (int i = lane; i < n; i += 32)
+        a.out[static_cast<int64_t>(b) * n + i] = __float2half_rn(0.f);
+    }
+    // no asynchronous write into this CTA's shared memory may be pending when it exits
+    if (lane == 0)
+      for (int kk = max(0, last.k - 1); kk <= last.k; ++kk)
+        if (!mbar_wait(bar_qfull + (kk & 1) * 8, (kk >> 1) & 1, nullptr)) flag_timeout(a, abort);
   } else {
     // =================================== consumers ===========================================
-    const int w = warp;
+    const int w = warp % NCS, rs = warp / NCS;   // share of the stages, half of the rows
     const int g = lane >> 2, t4 = lane & 3;
-    const float score_l2 = a.scale_log2 * 1048576.f;   // the codes come in as c 2^-20
+    // ldmatrix row addresses: matrices 0, 1 the two key octets of 16 bytes, 2, 3 of the next 16
+    // (codes), or the two octets of the next chunk (scales and minima)
+    const uint32_t lm_row = ((lane >> 3) & 1) * 8 * kInt4Row + (lane & 7) * kInt4Row;
+    const uint32_t lm_codes = lm_row + (lane >> 4) * 16;
+    const uint32_t lm_par = lm_row + (lane >> 4) * kTile + kInt4Params;
+    const uint64_t kv_policy = l2_policy_evict_first();
+    const uint32_t ring = sbase + warp * (ND * kStage4);
+    StageWalk<NCS> walk;
+    walk.start(a, cur, begin, w, lane);
+    for (int i = 0; i < ND; ++i) walk.load(a, cur, w, lane, ring + i * kStage4, kv_policy);
+    int slot = 0;   // ring position of the warp's next stage
     int j = 0, k = 0;
     Seg s;
     bool has = cur.first(begin, s);
@@ -290,89 +333,96 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
       const int Lc = slen[s.b];
 
       // ---- Q^T fragments (B operands): thread (g, t4) holds row g of each tile and, of group
-      // gr, dims d0 = 32 gr + 8 t4 .. d0 + 7, paired as the codes of a word come out of the
-      // masks: (d0 + i, d0 + i + 4) for i = 0 .. 3. And the group means, for the minima: t4's
-      // group, as two fp16 numbers in the upper halves (the lower ones meet the scales). ----
-      uint32_t qf[kQSmem ? 1 : NT][kQSmem ? 1 : 4][4], qzh[NT], qzl[NT];
+      // gr, dims d0 = 32 gr + 8 t4 .. d0 + 7 (the codes of its key words), paired as the masks
+      // pair them; and the sums of group t4 as two fp16 numbers in the upper halves (the lower
+      // ones meet the scales) ----
+      uint32_t qf[NT][4][4], qzh[NT], qzl[NT];
+      float rsc[NT][2];     // scores of rows 2 t4, 2 t4 + 1 from the products' units
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float mean_own = 0.f;
+        uint4 v[4];
+        __half2 big = as_half2(0u);
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr) {
           const int ch = 4 * gr + t4;
-          const uint4 v = ld_shared_v4(qb + (ch >> 3) * L::kQHalf + swz128(8 * nt + g, ch & 7));
+          v[gr] = ld_shared_v4(qb + (ch >> 3) * L::kQHalf + swz128(8 * (NT * rs + nt) + g, ch & 7));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            big = __hmax2_nan(big, __habs2(as_half2(u4_word(v[gr], i))));
+        }
+        big = __hmax2_nan(big, __lowhigh2highlow(big));
+        big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const float top = __low2float(big);
+        // 2^(7 - exponent of the row's largest): it comes to lie in [128, 256)
+        const int ex = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) : 127;
+        const float f = __uint_as_float(static_cast<uint32_t>(261 - ex) << 23);
+        // codes come in as c 2^-20; a NaN or an infinity among the queries makes the scores NaN
+        const float unit =
+            top <= 65504.f
+                ? a.scale_log2 * (1048576.f * __uint_as_float(static_cast<uint32_t>(ex - 7) << 23))
+                : __uint_as_float(0x7fffffffu);
+        float own = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
           float sum = 0.f;
+          float2 u[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t u = u4_word(v, i);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-            sum += f.x + f.y;
+            u[i] = __half22float2(as_half2(u4_word(v[gr], i)));
+            u[i].x *= f;
+            u[i].y *= f;
+            sum += u[i].x + u[i].y;
           }
+          qf[nt][gr][0] = pack_half2(u[0].x * 16.f, u[2].x * 16.f);   // dims 0, 4
+          qf[nt][gr][1] = pack_half2(u[1].x * 16.f, u[3].x * 16.f);   // dims 2, 6
+          qf[nt][gr][2] = pack_half2(u[0].y, u[2].y);                 // dims 1, 5
+          qf[nt][gr][3] = pack_half2(u[1].y, u[3].y);                 // dims 3, 7
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (gr == t4) mean_own = sum * 0.03125f;
-          if constexpr (!kQSmem) {
-            qf[nt][gr][0] = __byte_perm(v.x, v.z, 0x5410);
-            qf[nt][gr][1] = __byte_perm(v.x, v.z, 0x7632);
-            qf[nt][gr][2] = __byte_perm(v.y, v.w, 0x5410);
-            qf[nt][gr][3] = __byte_perm(v.y, v.w, 0x7632);
-          }
+          if (gr == t4) own = sum * 0x1p-3f;   // at most 1024
         }
-        const __half hi = __float2half_rn(mean_own);
-        const __half lo = __float2half_rn(mean_own - __half2float(hi));
+        const __half hi = __float2half_rn(own);
+        const __half lo = __float2half_rn(own - __half2float(hi));
         qzh[nt] = static_cast<uint32_t>(__half_as_ushort(hi)) << 16;
         qzl[nt] = static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
+        rsc[nt][0] = __shfl_sync(0xffffffffu, unit, 8 * t4);
+        rsc[nt][1] = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
       }
-      if constexpr (kQSmem) {
-        // every 16-byte piece of the tile into its fragment order, in place
-        named_barrier_sync(1, kNC);                   // all warps have read the plain tile
-        for (int i = tid; i < L::kQBuf / 16; i += kNC) {
-          const uint4 v = ld_shared_v4(qb + i * 16);
-          st_shared_v4(qb + i * 16, make_uint4(__byte_perm(v.x, v.z, 0x5410),
-                                               __byte_perm(v.x, v.z, 0x7632),
-                                               __byte_perm(v.y, v.w, 0x5410),
-                                               __byte_perm(v.y, v.w, 0x7632)));
-        }
-        named_barrier_sync(1, kNC);
-      }
-      if (!kHoldQ) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_qempty + qs * 8);
-      }
-
-      float tm[NT][2], tl[NT][2], ot[NT][8][4];
-      int tlim[NT][2];
+      float tm[NT][2], tl[NT][2], ot[NT][4][2][4], oz[NT][4];
+      int qis[NT];   // query tokens of rows 2 t4 (low half), 2 t4 + 1
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           tm[nt][e] = kNegInf;
           tl[nt][e] = 0.f;
-          const int r = 8 * nt + 2 * t4 + e;
-          const int qi = r < a.R ? r / a.G : a.q_len - 1;
-          tlim[nt][e] = Lc - a.q_len + qi + 1;
         }
+        const int r0 = 8 * (NT * rs + nt) + 2 * t4;
+        qis[nt] = min(r0 / a.G, a.q_len - 1) | (min((r0 + 1) / a.G, a.q_len - 1) << 16);
 #pragma unroll
-        for (int dt = 0; dt < 8; ++dt)
-          ot[nt][dt][0] = ot[nt][dt][1] = ot[nt][dt][2] = ot[nt][dt][3] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          oz[nt][i] = 0.f;
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) ot[nt][gr][0][i] = ot[nt][gr][1][i] = 0.f;
+        }
       }
+      float shift = kShift;   // the same for all lanes
 
       const int nchunk = s.c1 - s.c0;
       const int npair = (nchunk + 1) >> 1;
-      for (int jp = ((w - j) % NCW + NCW) % NCW; jp < npair; jp += NCW) {
-        const int gj = j + jp;
-        const int st = gj % NST;
-        if (!mbar_wait(bar_full + st * 8, (gj / NST) & 1, abort)) flag_timeout(a, abort);
-        const uint32_t stK = sbase + st * kStage4;
+      for (int jp = ((w - j) % NCS + NCS) % NCS; jp < npair; jp += NCS) {
+        cp_async_wait<ND - 1>();
+        __syncwarp();                        // every lane's copies of this stage are in
+        const uint32_t stK = ring + slot * kStage4;
         const uint32_t stV = stK + 2 * kTile;
         const int c = s.c0 + 2 * jp;
         const bool two = c + 1 < s.c1;
         const int nk = two ? 2 * kChunk : kChunk;
         const bool full = two && (c + 2) * kChunk <= Lc - a.q_len + 1;
-        bool patched = false;
         if (APPEND && (c * kChunk + nk > Lc - a.q_len)) {
           // new rows of these chunks: lanes 0-15 quantise the K row, 16-31 the V row, into the
-          // stage's tiles and into the pool
+          // stage's tiles and into the pool (warps that share a stage write the same bytes)
           const int first_new = Lc - a.q_len;
           const uint32_t nkv = sbase + L::newkv_off(a.R, B) + qs * a.q_len * 512;
           const int which = lane >> 4, p = lane & 15;
@@ -385,207 +435,188 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
             const uint32_t row = stK + which * 2 * kTile + tk * kInt4Row;
             st_shared_u32(row + 4 * p, codes);
             if ((p & 3) == 0) st_shared_u32(row + kInt4Params + p, params);
-            const int srow = srow_s[2 * st + (tk >> 4)];
-            if (srow >= 0) {
+            const int id =
+                __ldg(a.block_tables + static_cast<int64_t>(s.b) * a.max_blocks + pos / a.block_size);
+            if (id >= 0 && id < a.num_blocks) {
+              const int64_t prow = (static_cast<int64_t>(id) * a.Hkv + s.h) * a.block_size +
+                                   pos % a.block_size;
               uint32_t* pool = reinterpret_cast<uint32_t*>(
-                  reinterpret_cast<uint8_t*>(which ? a.v_pool : a.k_pool) +
-                  (static_cast<int64_t>(srow) + (tk & 15)) * kInt4Row);
+                  reinterpret_cast<uint8_t*>(which ? a.v_pool : a.k_pool) + prow * kInt4Row);
               pool[p] = codes;
               if ((p & 3) == 0) pool[(kInt4Params + p) / 4] = params;
             }
           }
           __syncwarp();
-          patched = true;
         }
 
-        // ---- S^T = K Q^T, 16 keys at a time ----
-        float x[NT][2][2][2];   // [tile][row e][chunk h][key g, g + 8]
+        // ---- S^T = K Q^T, 16 keys (g, g + 8) at a time ----
+        float x[NT][2][4];   // [tile][chunk h][key g: rows 2 t4, + 1; key g + 8: the same]
+        uint32_t kz[4];      // (s, z) of group t4: keys g, g + 8 of both chunks
+        ldsm_x4(stK + lm_par, kz[0], kz[1], kz[2], kz[3]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t kb0 = stK + h * kTile + g * kInt4Row, kb1 = kb0 + 8 * kInt4Row;
-          const uint4 p0 = ld_shared_v4(kb0 + kInt4Params), p1 = ld_shared_v4(kb1 + kInt4Params);
-          const uint32_t z0 = ld_shared_u32(kb0 + kInt4Params + 4 * t4);
-          const uint32_t z1 = ld_shared_u32(kb1 + kInt4Params + 4 * t4);
-          float acc[NT][4];
+          const uint32_t kb = stK + h * kTile;
+          uint32_t kw[4][2];
+          ldsm_x4(kb + lm_codes, kw[0][0], kw[0][1], kw[1][0], kw[1][1]);
+          ldsm_x4(kb + lm_codes + 32, kw[2][0], kw[2][1], kw[3][0], kw[3][1]);
+          const uint4 p0 = ld_shared_v4(kb + g * kInt4Row + kInt4Params);
+          const uint4 p1 = ld_shared_v4(kb + (g + 8) * kInt4Row + kInt4Params);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-            mma_16816(acc[nt], z0, z1, z0, z1, qzh[nt], qzl[nt]);
+            x[nt][h][0] = x[nt][h][1] = x[nt][h][2] = x[nt][h][3] = 0.f;
+            mma_f16(x[nt][h], kz[2 * h], kz[2 * h + 1], kz[2 * h], kz[2 * h + 1], qzh[nt], qzl[nt]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][i] *= 0x1p-15f;   // x 32, in units of 2^-20
+            for (int i = 0; i < 4; ++i) x[nt][h][i] *= 0x1p-17f;   // sums / 8, in units of 2^-20
           }
 #pragma unroll
           for (int gr = 0; gr < 4; ++gr) {
-            const uint32_t w0 = ld_shared_u32(kb0 + 16 * gr + 4 * t4);
-            const uint32_t w1 = ld_shared_u32(kb1 + 16 * gr + 4 * t4);
-            const uint32_t u0 = u4_word(p0, gr), u1 = u4_word(p1, gr);
-            const float s0 = __low2float(*reinterpret_cast<const __half2*>(&u0));
-            const float s1 = __low2float(*reinterpret_cast<const __half2*>(&u1));
+            const float s0 = __low2float(as_half2(u4_word(p0, gr)));
+            const float s1 = __low2float(as_half2(u4_word(p1, gr)));
+            const uint32_t w0 = kw[gr][0], w1 = kw[gr][1], u0 = w0 >> 8, u1 = w1 >> 8;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              uint32_t q0, q1, q2, q3;
-              if constexpr (kQSmem) {
-                const int ch = 4 * gr + t4;
-                const uint4 v =
-                    ld_shared_v4(qb + (ch >> 3) * L::kQHalf + swz128(8 * nt + g, ch & 7));
-                q0 = v.x; q1 = v.y; q2 = v.z; q3 = v.w;
-              } else {
-                q0 = qf[nt][gr][0]; q1 = qf[nt][gr][1]; q2 = qf[nt][gr][2]; q3 = qf[nt][gr][3];
-              }
               float t[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_16816(t, nibs(w0 << 4), nibs(w1 << 4), nibs(w0), nibs(w1), q0, q1);
-              mma_16816(t, nibs(w0 >> 4), nibs(w1 >> 4), nibs(w0 >> 8), nibs(w1 >> 8), q2, q3);
-              acc[nt][0] = fmaf(s0, t[0], acc[nt][0]);
-              acc[nt][1] = fmaf(s0, t[1], acc[nt][1]);
-              acc[nt][2] = fmaf(s1, t[2], acc[nt][2]);
-              acc[nt][3] = fmaf(s1, t[3], acc[nt][3]);
+              mma_f16(t, w0 & 0x000f000fu, w1 & 0x000f000fu, u0 & 0x000f000fu, u1 & 0x000f000fu,
+                      qf[nt][gr][0], qf[nt][gr][1]);
+              mma_f16(t, w0 & 0x00f000f0u, w1 & 0x00f000f0u, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
+                      qf[nt][gr][2], qf[nt][gr][3]);
+              x[nt][h][0] = fmaf(s0, t[0], x[nt][h][0]);
+              x[nt][h][1] = fmaf(s0, t[1], x[nt][h][1]);
+              x[nt][h][2] = fmaf(s1, t[2], x[nt][h][2]);
+              x[nt][h][3] = fmaf(s1, t[3], x[nt][h][3]);
             }
           }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              x[nt][e][h][0] = acc[nt][e] * score_l2;
-              x[nt][e][h][1] = acc[nt][2 + e] * score_l2;
-            }
         }
 
-        // ---- mask, online softmax (exp2 domain, lazy running maximum) ----
-        uint32_t pb[NT][2][2];   // P^T of chunk h as the B operand
-        bool grow = false;
+        // ---- V's scales and minima: half g of each key's eight, for keys 2 t4, 2 t4 + 1 of the
+        // two octets of both chunks ----
+        uint32_t vp[2][2];
+        ldsm_x4_trans(stV + lm_par, vp[0][0], vp[0][1], vp[1][0], vp[1][1]);
+        if (!full) {   // keys that no query may see may hold anything
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const int t0 = (c + h) * kChunk + 8 * o + 2 * t4;
+              const int lim = h == 0 || two ? Lc : 0;
+              vp[h][o] &= (t0 < lim ? 0x0000ffffu : 0u) | (t0 + 1 < lim ? 0xffff0000u : 0u);
+            }
+        }
+        // even g: scales; bit 14 says 2 or more
+        const bool wide = !(g & 1) && ((vp[0][0] | vp[0][1] | vp[1][0] | vp[1][1]) & 0x40004000u);
+
+        // ---- mask, softmax weights against the reference (exp2 domain) ----
+        bool move = wide && shift != 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (!full) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int p0 = (c + h) * kChunk + g;
-                const int lim = h == 0 || two ? tlim[nt][e] : 0;
-                if (p0 >= lim) x[nt][e][h][0] = kNegInf;
-                if (p0 + 8 >= lim) x[nt][e][h][1] = kNegInf;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int o = 0; o < 2; ++o) {
+                float& v = x[nt][h][2 * o + e];
+                v *= rsc[nt][e];
+                if (!full) {
+                  const int lim = Lc - a.q_len + 1 + ((qis[nt] >> (16 * e)) & 0xffff);
+                  if ((c + h) * kChunk + 8 * o + g >= lim || (h && !two)) v = kNegInf;
+                }
               }
-            }
-            const float lm = fmaxf(fmaxf(x[nt][e][0][0], x[nt][e][0][1]),
-                                   fmaxf(x[nt][e][1][0], x[nt][e][1][1]));
-            grow |= lm > tm[nt][e] + kLazyLog2;
+            move |= fmaxf(fmaxf(x[nt][0][e], x[nt][0][2 + e]), fmaxf(x[nt][1][e], x[nt][1][2 + e])) >
+                    tm[nt][e] + (shift + kGrow);
           }
-        if (__any_sync(0xffffffffu, grow)) {
+        if (__any_sync(0xffffffffu, move)) {
+          const float to = __any_sync(0xffffffffu, wide) ? 0.f : shift;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(fmaxf(x[nt][e][0][0], x[nt][e][0][1]),
-                               fmaxf(x[nt][e][1][0], x[nt][e][1][1]));
+              float mx = fmaxf(fmaxf(x[nt][0][e], x[nt][0][2 + e]),
+                               fmaxf(x[nt][1][e], x[nt][1][2 + e]));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float m_new = fmaxf(tm[nt][e], mx);
+              const float m_new = fmaxf(tm[nt][e] + (shift - to), mx - to);
               alpha[e] = fast_exp2(tm[nt][e] - (m_new == kNegInf ? 0.f : m_new));
               tm[nt][e] = m_new;
               tl[nt][e] *= alpha[e];
             }
 #pragma unroll
-            for (int dt = 0; dt < 8; ++dt) {
-              ot[nt][dt][0] *= alpha[0];
-              ot[nt][dt][1] *= alpha[1];
-              ot[nt][dt][2] *= alpha[0];
-              ot[nt][dt][3] *= alpha[1];
+            for (int i = 0; i < 4; ++i) {
+              oz[nt][i] *= alpha[i & 1];
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                ot[nt][gr][0][i] *= alpha[i & 1];
+                ot[nt][gr][1][i] *= alpha[i & 1];
+              }
             }
           }
+          shift = to;
         }
+        uint32_t pb[NT][2][2];   // P^T of chunk h as the B operand
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float pv[2][2][2];   // [chunk h][key half][row e]
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float m_use = tm[nt][e] == kNegInf ? 0.f : tm[nt][e];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) pv[h][i][e] = fast_exp2(x[nt][e][h][i] - m_use);
-            tl[nt][e] += (pv[0][0][e] + pv[0][1][e]) + (pv[1][0][e] + pv[1][1][e]);
+            for (int h = 0; h < 2; ++h) {
+              x[nt][h][e] = fast_exp2(x[nt][h][e] - m_use);
+              x[nt][h][2 + e] = fast_exp2(x[nt][h][2 + e] - m_use);
+            }
+            tl[nt][e] += (x[nt][0][e] + x[nt][0][2 + e]) + (x[nt][1][e] + x[nt][1][2 + e]);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              pb[nt][h][i] = movmatrix_trans(pack_half2(pv[h][i][0], pv[h][i][1]));
+            for (int o = 0; o < 2; ++o)
+              pb[nt][h][o] = movmatrix_trans(pack_half2(x[nt][h][2 * o], x[nt][h][2 * o + 1]));
         }
 
-        // ---- O^T += V^T P^T. Row g of tile dt is output dim 16 g + dt, row g + 8 dim
-        // 16 g + 8 + dt (undone at the hand-off): a thread's operands are its own 8 bytes of
-        // keys 2 t4, 2 t4 + 1, 2 t4 + 8 and 2 t4 + 9 ----
+        // ---- O^T += V^T (P s)^T and the minima's sums ----
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t vb = stV + h * kTile + 2 * t4 * kInt4Row;
-          uint2 v[4];
-          uint32_t p[4];
+          const uint32_t vb = stV + h * kTile;
+          uint32_t vw[4][2];
+          ldsm_x4_trans(vb + lm_codes, vw[0][0], vw[0][1], vw[1][0], vw[1][1]);
+          ldsm_x4_trans(vb + lm_codes + 32, vw[2][0], vw[2][1], vw[3][0], vw[3][1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t r = vb + ((i & 1) + 8 * (i >> 1)) * kInt4Row;
-            v[i] = ld_shared_v2(r + 8 * g);
-            p[i] = ld_shared_u32(r + kInt4Params + 4 * (g >> 1));
-          }
-          uint32_t sc[2], mn[2];   // scales, minima of the two key pairs
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(oz[nt], vp[h][0], 0u, vp[h][1], 0u, pb[nt][h][0], pb[nt][h][1]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            sc[i] = __byte_perm(p[2 * i], p[2 * i + 1], 0x5410);
-            mn[i] = __byte_perm(p[2 * i], p[2 * i + 1], 0x7632);
-            if (!full) {   // keys that no query may see may hold anything
-              const int t0 = (c + h) * kChunk + 2 * t4 + 8 * i;
-              const int lim = h == 0 || two ? Lc : 0;
-              const uint32_t m = (t0 < lim ? 0x0000ffffu : 0u) | (t0 + 1 < lim ? 0xffff0000u : 0u);
-              sc[i] &= m;
-              mn[i] &= m;
-            }
-          }
+          for (int gr = 0; gr < 4; ++gr) {
+            const uint32_t s0 = __shfl_sync(0xffffffffu, vp[h][0], 8 * gr + t4);
+            const uint32_t s1 = __shfl_sync(0xffffffffu, vp[h][1], 8 * gr + t4);
+            const uint32_t u0 = vw[gr][0] >> 8, u1 = vw[gr][1] >> 8;
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t sel = hf ? 0x7632u : 0x5410u;
-            uint32_t u[2][2];   // [word][key pair]: four codes of each of the pair's keys
+            for (int nt = 0; nt < NT; ++nt) {
+              const __half2 p0 = as_half2(pb[nt][h][0]), p1 = as_half2(pb[nt][h][1]);
+              const __half2 b0 = __hmul2(p0, as_half2(s0)), b1 = __hmul2(p1, as_half2(s1));
+              // what the products' rounding left over (exact)
+              const uint32_t r0 = half2_bits(__hfma2(p0, as_half2(s0), __hneg2(b0)));
+              const uint32_t r1 = half2_bits(__hfma2(p1, as_half2(s1), __hneg2(b1)));
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              u[0][i] = __byte_perm(v[2 * i].x, v[2 * i + 1].x, sel);
-              u[1][i] = __byte_perm(v[2 * i].y, v[2 * i + 1].y, sel);
-            }
-#pragma unroll
-            for (int jn = 0; jn < 4; ++jn) {
-              uint32_t f[2][2];
-#pragma unroll
-              for (int wd = 0; wd < 2; ++wd)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint32_t y = jn < 2 ? u[wd][i] : u[wd][i] >> 8;
-                  const __half2 code = (jn & 1) ? int4_hi(y) : int4_lo(y);
-                  f[wd][i] = half2_bits(__hfma2(code, *reinterpret_cast<const __half2*>(&sc[i]),
-                                                *reinterpret_cast<const __half2*>(&mn[i])));
-                }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_16816(ot[nt][4 * hf + jn], f[0][0], f[1][0], f[0][1], f[1][1], pb[nt][h][0],
-                          pb[nt][h][1]);
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t m = i ? 0x00f000f0u : 0x000f000fu;
+                mma_f16(ot[nt][gr][i], vw[gr][0] & m, u0 & m, vw[gr][1] & m, u1 & m,
+                        half2_bits(b0), half2_bits(b1));
+                mma_f16(ot[nt][gr][i], vw[gr][0] & m, u0 & m, vw[gr][1] & m, u1 & m, r0, r1);
+              }
             }
           }
         }
-        // a patched tile was written through the generic proxy; order that before the next TMA
-        // write into this stage
-        if (APPEND && patched) fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_empty + st * 8);
-      }
-      if (kHoldQ) {
-        if (kQSmem) fence_proxy_async_smem();   // the tile was permuted in place
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_qempty + qs * 8);
+        __syncwarp();                        // every lane has read the stage
+        walk.load(a, cur, w, lane, stK, kv_policy);
+        slot = slot + 1 == ND ? 0 : slot + 1;
       }
       j += npair;
 
-      // ---- hand this warp's state to the epilogue ----
-      const int sb = k & 1;
-      if (k >= 2 && !mbar_wait(bar_sfree + sb * 8, ((k >> 1) - 1) & 1, abort)) flag_timeout(a, abort);
-      float* o_d = stO + sb * NCW * a.R * kSt;
+      // ---- hand this warp's state to the epilogue: row g of tile (gr, i) is dim 32 gr + 4 g + i,
+      // row g + 8 dim 32 gr + 4 g + 2 + i ----
+      const int sb = k % SB;
+      if (k >= SB && !mbar_wait(bar_sfree + sb * 8, ((k / SB) - 1) & 1, abort)) flag_timeout(a, abort);
+      float* o_d = stO + sb * NCS * a.R * kSt;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -594,48 +625,49 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
           lv += __shfl_xor_sync(0xffffffffu, lv, 4);
           lv += __shfl_xor_sync(0xffffffffu, lv, 8);
           lv += __shfl_xor_sync(0xffffffffu, lv, 16);
-          const int r = 8 * nt + 2 * t4 + e;
+          float z[4];
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+            z[gr] = __shfl_sync(0xffffffffu, oz[nt][e], 8 * gr + 4 + t4);
+          const int r = 8 * (NT * rs + nt) + 2 * t4 + e;
           if (r < a.R) {
-            float4* dst = reinterpret_cast<float4*>(o_d + (w * a.R + r) * kSt + 16 * g);
-            dst[0] = make_float4(ot[nt][0][e], ot[nt][1][e], ot[nt][2][e], ot[nt][3][e]);
-            dst[1] = make_float4(ot[nt][4][e], ot[nt][5][e], ot[nt][6][e], ot[nt][7][e]);
-            dst[2] = make_float4(ot[nt][0][2 + e], ot[nt][1][2 + e], ot[nt][2][2 + e],
-                                 ot[nt][3][2 + e]);
-            dst[3] = make_float4(ot[nt][4][2 + e], ot[nt][5][2 + e], ot[nt][6][2 + e],
-                                 ot[nt][7][2 + e]);
+            float* row = o_d + (w * a.R + r) * kSt + 4 * g;
+#pragma unroll
+            for (int gr = 0; gr < 4; ++gr)
+              *reinterpret_cast<float4*>(row + 32 * gr) =
+                  make_float4(fmaf(ot[nt][gr][0][e], 0x1p24f, z[gr]),
+                              fmaf(ot[nt][gr][1][e], 0x1p20f, z[gr]),
+                              fmaf(ot[nt][gr][0][2 + e], 0x1p24f, z[gr]),
+                              fmaf(ot[nt][gr][1][2 + e], 0x1p20f, z[gr]));
             if (g == 0) {
-              stM[(sb * NCW + w) * a.R + r] = tm[nt][e];
-              stL[(sb * NCW + w) * a.R + r] = lv;
+              stM[(sb * NCS + w) * a.R + r] = tm[nt][e];
+              stL[(sb * NCS + w) * a.R + r] = lv;
             }
           }
         }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_sdone + (k & 1) * 8);
+      if (lane == 0) mbar_arrive(bar_sdone + sb * 8);
       ++k;
       has = cur.next(s);
     }
+    cp_async_wait<0>();
   }
 
-  // ---- end of the slice (the producer has left; t: dense index over consumers + epilogue)
-  if (warp != NCW && last.k >= 0)
-    finish_slice<NCW, kSeg4>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s, fast_s,
-                             warp < NCW ? tid : tid - 32);
+  // ---- end of the slice ----
+  if (last.k >= 0)
+    finish_slice<NCS, kSeg4, NCW, SB>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s,
+                                      fast_s, tid);
 }
 
 // ---------------------------------------------------------------------------------------------
 // Host side.
 
-template <int NCW, int NST, int NT>
-size_t smem4_of(int R, int B, int newkv_bytes) {
-  return Smem4<NCW, NST, NT>::bytes(R, B, newkv_bytes);
-}
-
-template <int NCW, int NST, int NT, int MINB>
+template <int NCS, int RS, int ND, int NT, int SB, int MINB>
 Variant variant4(bool append) {
   const void* fn =
-      append ? reinterpret_cast<const void*>(&decode_int4_kernel<NCW, NST, NT, MINB, true>)
-             : reinterpret_cast<const void*>(&decode_int4_kernel<NCW, NST, NT, MINB, false>);
-  return Variant{fn, NT, false, (NCW + 2) * 32, &smem4_of<NCW, NST, NT>};
+      append ? reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, MINB, true>)
+             : reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, MINB, false>);
+  return Variant{fn, NT, false, (NCS * RS + 1) * 32, &Smem4<NCS, RS, ND, NT, SB>::bytes};
 }
 
 int launch_decode_int4(void* out, const void* q, const void* k_new, const void* v_new,
@@ -658,7 +690,7 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PKV_EINVAL;
   if (append && (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))) return PKV_EINVAL;
-  // all chunk indices and TMA rows fit in int32
+  // all chunk indices and pool rows fit in int32
   const int64_t rows = static_cast<int64_t>(num_blocks) * Hkv * block_size;
   const int64_t max_ctx = static_cast<int64_t>(max_blocks) * block_size;
   if (rows >= (1ll << 31) || max_ctx >= (1ll << 31) ||
@@ -669,8 +701,18 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   const WsLayout ws = ws_layout(num_seqs, Hkv, R);
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
-  const Variant v = R <= 8 ? variant4<4, 8, 1, 2>(append)
-                    : R <= 16 ? variant4<4, 8, 2, 1>(append) : variant4<4, 12, 4, 1>(append);
+#ifndef V1
+#define V1 5, 1, 3, 1, 1, 2
+#endif
+#ifndef V2
+#define V2 7, 1, 3, 2, 1, 1
+#endif
+#ifndef V4
+#define V4 3, 2, 3, 2, 1, 1
+#endif
+  const Variant v = R <= 8    ? variant4<V1>(append)
+                    : R <= 16 ? variant4<V2>(append)
+                              : variant4<V4>(append);
   const int newkv_bytes = append ? 2 * q_len * 512 : 0;
   const size_t smem = v.smem(R, num_seqs, newkv_bytes);
   if (smem > 227 * 1024) return PKV_EINVAL;
@@ -678,20 +720,12 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   const int grid = grid_size(v, smem, &status);
   if (!grid) return status != PKV_OK ? status : PKV_EINVAL;
 
-  CUtensorMap tmK, tmV, tmQ;
-  const cuuint64_t kv_dims[2] = {kInt4Row, static_cast<cuuint64_t>(rows)};
-  const cuuint64_t kv_strides[1] = {kInt4Row};
-  const cuuint32_t kv_box[2] = {kInt4Row, kChunk};
-  int st = encode(&tmK, k_cache, 2, kv_dims, kv_strides, kv_box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                  CU_TENSOR_MAP_SWIZZLE_NONE);
-  if (st == PKV_OK)
-    st = encode(&tmV, v_cache, 2, kv_dims, kv_strides, kv_box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
-                CU_TENSOR_MAP_SWIZZLE_NONE);
+  CUtensorMap tmQ;
   const cuuint64_t q_dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(Hq),
                                 static_cast<cuuint64_t>(num_seqs) * q_len};
   const cuuint64_t q_strides[2] = {kD * 2, static_cast<cuuint64_t>(Hq) * kD * 2};
   const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(q_len)};
-  if (st == PKV_OK) st = encode(&tmQ, q, 3, q_dims, q_strides, q_box);
+  const int st = encode(&tmQ, q, 3, q_dims, q_strides, q_box);
   if (st != PKV_OK) return st;
 
   unsigned int* err = device_error_ptr();
@@ -723,7 +757,7 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   args.k_pool = static_cast<__half*>(const_cast<void*>(k_cache));
   args.v_pool = static_cast<__half*>(const_cast<void*>(v_cache));
 
-  void* params[4] = {&tmK, &tmV, &tmQ, &args};
+  void* params[2] = {&tmQ, &args};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(v.threads);

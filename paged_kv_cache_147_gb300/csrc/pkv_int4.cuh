@@ -90,5 +90,8 @@ __device__ __forceinline__ __half2 int4_hi(uint32_t x) {
 __device__ __forceinline__ uint32_t half2_bits(__half2 v) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ __half2 as_half2(uint32_t u) {
+  return *reinterpret_cast<const __half2*>(&u);
+}
 
 }  // namespace pkv
