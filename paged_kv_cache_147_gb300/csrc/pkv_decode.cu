@@ -340,7 +340,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     const bool early_kv = APPEND;
     bool waited = false;
     auto issue_q = [&](const Seg& sg, int kk) {
-      if (lane == 0) issue_queries<L, APPEND>(a, &tmQ, sbase, bar_qfull, B, sg, kk, abort);
+      if (lane == 0) issue_queries<L, APPEND>(a, &tmQ, sbase, B, sg, kk, abort);
     };
     while (has) {
       // with an early start the epilogue warp requests the first segment's queries (it is
@@ -447,7 +447,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     bool has = cur.first(begin, s);
     if (APPEND && has) {
       griddep_wait();
-      if (lane == 0) issue_queries<L, APPEND>(a, &tmQ, sbase, bar_qfull, B, s, 0, abort);
+      if (lane == 0) issue_queries<L, APPEND>(a, &tmQ, sbase, B, s, 0, abort);
     }
     while (has && k < last.k) {
       const int sb = k & 1;

@@ -532,16 +532,16 @@ __device__ __forceinline__ uint32_t u4_word(const uint4& v, int i) {
 }
 
 // Requests segment kk's queries (and, fused append, its new K/V rows) into query buffer kk & 1,
-// completing on that buffer's full barrier (bar_qfull, followed by the empty ones); waits first
-// until the consumers have released the buffer's previous use (WAIT; otherwise the caller has).
-// One thread.
-template <class L, bool APPEND, bool WAIT = true>
+// completing on that buffer's full barrier; waits first until the consumers have released the
+// buffer's previous use. One thread.
+template <class L, bool APPEND>
 __device__ __forceinline__ void issue_queries(const DecodeArgs& a, const CUtensorMap* tmQ,
-                                              uint32_t sbase, uint32_t bar_qfull, int B,
-                                              const Seg& sg, int kk, volatile int* abort) {
+                                              uint32_t sbase, int B, const Seg& sg, int kk,
+                                              volatile int* abort) {
+  const uint32_t bar_qfull = sbase + L::kBars + 2 * L::kNST * 8;
   const uint32_t bar_qempty = bar_qfull + 2 * 8;
   const int qs = kk & 1;
-  if (WAIT && kk >= 2 && !mbar_wait(bar_qempty + qs * 8, ((kk >> 1) - 1) & 1, abort))
+  if (kk >= 2 && !mbar_wait(bar_qempty + qs * 8, ((kk >> 1) - 1) & 1, abort))
     flag_timeout(a, abort);
   mbar_arrive_expect_tx(bar_qfull + qs * 8, a.R * 256 + (APPEND ? a.q_len * 512 : 0));
   const uint32_t qdst = sbase + L::kQ + qs * L::kQBuf;

@@ -22,9 +22,9 @@
 //    exactly, and the products' sums are fp32: one AND of a word or of the word shifted by 8
 //    makes an mma operand of two codes.
 //  * Keys: sum_d q_d (s c_d + z) = s sum_d q_d c_d + z sum_d q_d per group of 32 dims. The
-//    queries are scaled by a power of two that puts the row's largest between 128 and 256, those
+//    queries are scaled by a power of two that puts the row's largest between 2^10 and 2^11, those
 //    that meet codes at bits 0-3 by 16 more (both exact: what falls below fp16's smallest is
-//    under 2^-31 of the row's largest). The group's sum is scaled by s in fp32; z times the
+//    under 2^-34 of the row's largest). The group's sum is scaled by s in fp32; z times the
 //    group's query sum is one more product per 16 keys, the (s, z) words as they stand against
 //    (0, sum), the sum split in two fp16 numbers.
 //  * Values: O[d] = sum_k (p_k s_k) c_kd + sum_k p_k z_k. ldmatrix.trans brings, per group, a
@@ -65,9 +65,9 @@ constexpr float kShift = 11.f, kGrow = 2.f;
 template <int NCS, int RS, int ND, int NT, int SB>
 struct Smem4 {
   static constexpr int kRows = 8 * RS * NT;
-  static constexpr int kQHalf = kRows * 128;
-  static constexpr int kQBuf = 2 * kQHalf;
-  static constexpr int kQ = ((NCS * RS * ND * kStage4 + 1023) & ~1023);   // swizzle atoms
+  static constexpr int kQTile = 5 * 512;              // fragments of 4 groups, row constants
+  static constexpr int kQBuf = RS * NT * kQTile;
+  static constexpr int kQ = NCS * RS * ND * kStage4;
   static constexpr int kBars = kQ + 2 * kQBuf;        // qfull[2], sdone[2], sfree[2]
   static constexpr int kFlags = kBars + 6 * 8;
   static constexpr int kState = (kFlags + 64 + 15) & ~15;
@@ -77,7 +77,7 @@ struct Smem4 {
     return (seq_off(R) + (2 * B + 1) * 4 + 127) & ~127;
   }
   __host__ static size_t bytes(int R, int B, int newkv_bytes) {
-    return 1024 + static_cast<size_t>(newkv_off(R, B)) + static_cast<size_t>(newkv_bytes);
+    return 128 + static_cast<size_t>(newkv_off(R, B)) + static_cast<size_t>(newkv_bytes);
   }
   // the merge of split units stages at least two partials in the stage memory
   static_assert(kQ >= kRows * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
@@ -187,16 +187,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Warps 0 .. NCS RS - 1 consume; the last warp loads the queries and is the epilogue (merges
-// each segment's per-warp states, writes outputs and split units' partials).
-template <int NCS, int RS, int ND, int NT, int SB, int MINB, bool APPEND>
+// Warps 0 .. NCS RS - 1 consume; the last warp prepares the queries and is the epilogue (merges
+// each segment's per-warp states, writes outputs and split units' partials). QR: the query
+// fragments stay in the consumers' registers (else they are read from shared memory per stage,
+// which leaves registers for more warps).
+template <int NCS, int RS, int ND, int NT, int SB, int QR, int MINB, bool APPEND>
 __global__ void __launch_bounds__((NCS * RS + 1) * 32, MINB)
-decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) {
+decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
   using L = Smem4<NCS, RS, ND, NT, SB>;
   constexpr int NCW = NCS * RS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar_qfull = sbase + L::kBars;
   const uint32_t bar_sdone = bar_qfull + 2 * 8;
@@ -204,6 +206,7 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kFlags);
   int* npend_s = reinterpret_cast<int*>(smem + L::kFlags) + 1;   // then 2 x (b, h, nb)
   volatile int* fast_s = reinterpret_cast<volatile int*>(smem + L::kFlags) + 8;
+  int* longest_s = reinterpret_cast<int*>(smem + L::kFlags) + 9;
   float* stO = reinterpret_cast<float*>(smem + L::kState);       // [SB][NCS][R][kSt]
   float* stM = stO + SB * NCS * a.R * kSt;                        // [SB][NCS][R]
   float* stL = stM + SB * NCS * a.R;                              // [SB][NCS][R]
@@ -212,23 +215,10 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
   const int B = a.num_seqs;
 
   // ---- per-sequence lengths and chunk counts -------------------------------------------------
-  for (int b = tid; b < B; b += blockDim.x) {
-    int ctx = a.context_lens[b];
-    const int lim = a.max_blocks * a.block_size;
-    if (ctx < 0 || ctx > lim) {
-      atomicOr(a.err, PKV_DEVERR_CONTEXT);
-      ctx = ctx < 0 ? 0 : lim;
-    }
-    const int nchunks = (ctx + kChunk - 1) / kChunk;
-    slen[b] = ctx;
-    pre[b + 1] = nchunks > 0 ? nchunks + kSeg4 : 0;
-  }
-  // zero both Q buffers so rows past R are finite; TMA overwrites rows < R
-  for (int i = tid; i < L::kQBuf * 2 / 16; i += blockDim.x)
-    reinterpret_cast<uint4*>(smem + L::kQ)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_qfull + s * 8, 1);
@@ -237,131 +227,96 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
     }
     *abort = 0;
     *npend_s = 0;
+    *longest_s = 0;
     pre[0] = 0;
+  }
+  int longest = 0;
+  for (int b = tid; b < B; b += blockDim.x) {
+    int ctx = a.context_lens[b];
+    const int lim = a.max_blocks * a.block_size;
+    if (ctx < 0 || ctx > lim) {
+      atomicOr(a.err, PKV_DEVERR_CONTEXT);
+      ctx = ctx < 0 ? 0 : lim;
+    }
+    const int nchunks = (ctx + kChunk - 1) / kChunk;
+    longest = max(longest, nchunks);
+    slen[b] = ctx;
+    pre[b + 1] = nchunks > 0 ? nchunks + kSeg4 : 0;
   }
   fence_barrier_init();
   __syncthreads();
+  if (longest > 0) atomicMax(longest_s, longest);
   if (warp == 0) scan_chunks(pre, B, lane);
   __syncthreads();
 
+  // ---- this CTA's slice of the stream --------------------------------------------------------
   const int total = pre[B] * a.Hkv;
   const int per = (total + gridDim.x - 1) / gridDim.x;
-  const int begin = blockIdx.x * per;
-  const CursorT<kSeg4> cur{pre, B, a.Hkv, min(total, begin + per)};
+  int begin = blockIdx.x * per, end = min(total, begin + per);
+  // Few short units: a whole unit for each CTA. Its warps then take kAlone rounds of stages more
+  // than an equal share has, which costs less than writing partials and merging them (~4 us).
+  constexpr int kAlone = 3;
+  if (B * a.Hkv <= gridDim.x && *longest_s <= 2 * NCS * ((per + 2 * NCS - 1) / (2 * NCS) + kAlone)) {
+    const int b = blockIdx.x / a.Hkv;
+    const int len = b < B ? pre[b + 1] - pre[b] : 0;
+    begin = len > 0 ? pre[b] * a.Hkv + (blockIdx.x - b * a.Hkv) * len : 0;
+    end = begin + len;
+  }
+  const CursorT<kSeg4> cur{pre, B, a.Hkv, end};
 
   // let the next kernel on the stream launch as SM resources free up (it waits for this one
   // before it reads anything this kernel writes)
   if (tid == 0) griddep_launch_dependents();
 
-  const LastSeg last = LastSeg::of(cur, begin);
+  LastSeg last{-1, 0, 0, 0, 0, true, false};
+  auto set_last = [&](const Seg& s, int k) {
+    last = LastSeg{k, s.b, s.h, s.nb, 2 * static_cast<int>(blockIdx.x) + (k == 0 ? 0 : 1),
+                   s.c0 == 0 && s.c1 == s.nb, s.c0 == 0};
+  };
 
   if (warp == NCW) {
     // ============================ queries and epilogue =======================================
-    if (lane == 0) prefetch_tensormap(&tmQ);
     // An early-started launch (APPEND) has its first stages on the way already; queries, new
     // rows, outputs and the workspace are touched only after the preceding kernel completed.
     griddep_wait();
-    Seg q;                       // segment whose queries go out next
-    bool has_q = cur.first(begin, q);
-    auto load_queries = [&](int kk) {
-      if (lane == 0) issue_queries<L, APPEND, false>(a, &tmQ, sbase, bar_qfull, B, q, kk, abort);
-      has_q = cur.next(q);
-    };
-    Seg s = q;
-    if (has_q) load_queries(0);
-    if (has_q) load_queries(1);
-    int npend = 0;
-    for (int k = 0; k < last.k; ++k) {
-      const int sb = k % SB;
-      if (!mbar_wait(bar_sdone + sb * 8, (k / SB) & 1, abort)) flag_timeout(a, abort);
-      if (has_q) load_queries(k + 2);   // segment k's query buffer is free
-      const bool complete = (s.c0 == 0 && s.c1 == s.nb);
-      const int slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
-      merge_segment<NCS, 32>(a, stO + sb * NCS * a.R * kSt, stM + sb * NCS * a.R,
-                             stL + sb * NCS * a.R, s.b, s.h, complete,
-                             a.part_o + static_cast<int64_t>(slot) * a.R * kD,
-                             a.part_ml + static_cast<int64_t>(slot) * a.R * 4, lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_sfree + sb * 8);
-      if (!complete && lane == 0) {
-        // announce the partial (release) and see who else has arrived (acquire)
-        const int ua = unit_first<kSeg4>(pre, a.Hkv, s.b, s.h, s.nb);
-        const int parts = (ua + s.nb - 1) / per - ua / per + 1;
-        if (atomic_add_acq_rel(a.counters + s.b * a.Hkv + s.h, 1) == parts - 1) {
-          npend_s[1 + 3 * npend] = s.b;
-          npend_s[2 + 3 * npend] = s.h;
-          npend_s[3 + 3 * npend] = s.nb;
-          ++npend;
-        }
-      }
-      cur.next(s);
-    }
-    if (lane == 0) *npend_s = npend;
-    // sequences without any chunk get zeros (their units are in no CTA's slice)
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-      if (pre[b + 1] != pre[b]) continue;
-      const int n = a.q_len * a.Hq * kD;
-      for (int i = lane; i < n; i += 32)
-        a.out[static_cast<int64_t>(b) * n + i] = __float2half_rn(0.f);
-    }
-    // no asynchronous write into this CTA's shared memory may be pending when it exits
-    if (lane == 0)
-      for (int kk = max(0, last.k - 1); kk <= last.k; ++kk)
-        if (!mbar_wait(bar_qfull + (kk & 1) * 8, (kk >> 1) & 1, nullptr)) flag_timeout(a, abort);
-  } else {
-    // =================================== consumers ===========================================
-    const int w = warp % NCS, rs = warp / NCS;   // share of the stages, half of the rows
-    const int g = lane >> 2, t4 = lane & 3;
-    // ldmatrix row addresses: matrices 0, 1 the two key octets of 16 bytes, 2, 3 of the next 16
-    // (codes), or the two octets of the next chunk (scales and minima)
-    const uint32_t lm_row = ((lane >> 3) & 1) * 8 * kInt4Row + (lane & 7) * kInt4Row;
-    const uint32_t lm_codes = lm_row + (lane >> 4) * 16;
-    const uint32_t lm_par = lm_row + (lane >> 4) * kTile + kInt4Params;
-    const uint64_t kv_policy = l2_policy_evict_first();
-    const uint32_t ring = sbase + warp * (ND * kStage4);
-    StageWalk<NCS> walk;
-    walk.start(a, cur, begin, w, lane);
-    for (int i = 0; i < ND; ++i) walk.load(a, cur, w, lane, ring + i * kStage4, kv_policy);
-    int slot = 0;   // ring position of the warp's next stage
-    int j = 0, k = 0;
-    Seg s;
-    bool has = cur.first(begin, s);
-    while (has) {
-      const int qs = k & 1;
-      const uint32_t qb = sbase + L::kQ + qs * L::kQBuf;
-      if (!mbar_wait(bar_qfull + qs * 8, (k >> 1) & 1, abort)) flag_timeout(a, abort);
-      const int Lc = slen[s.b];
-
-      // ---- Q^T fragments (B operands): thread (g, t4) holds row g of each tile and, of group
-      // gr, dims d0 = 32 gr + 8 t4 .. d0 + 7 (the codes of its key words), paired as the masks
-      // pair them; and the sums of group t4 as two fp16 numbers in the upper halves (the lower
-      // ones meet the scales) ----
-      uint32_t qf[NT][4][4], qzh[NT], qzl[NT];
-      float rsc[NT][2];     // scores of rows 2 t4, 2 t4 + 1 from the products' units
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+    // Queries of segment kk into buffer kk & 1 as the products' B operands: for lane (g, t4), row
+    // g of each tile, the dims d0 = 32 gr + 8 t4 .. d0 + 7 of group gr (the codes of its key
+    // words), paired as the masks pair them. And per lane: the sum of group t4 as two fp16 numbers
+    // in the upper halves (the lower ones meet the scales), and what makes scores of rows 2 t4,
+    // 2 t4 + 1 from the products.
+    auto prepare = [&](const Seg& sg, int kk) {
+      const uint32_t qb = sbase + L::kQ + (kk & 1) * L::kQBuf;
+#pragma unroll 1
+      for (int tile = 0; 8 * tile < a.R; ++tile) {
+        const int row = 8 * tile + g;
         uint4 v[4];
         __half2 big = as_half2(0u);
+        const int qi = row / a.G;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            q_in + ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
 #pragma unroll
-        for (int gr = 0; gr < 4; ++gr) {
-          const int ch = 4 * gr + t4;
-          v[gr] = ld_shared_v4(qb + (ch >> 3) * L::kQHalf + swz128(8 * (NT * rs + nt) + g, ch & 7));
+        for (int gr = 0; gr < 4; ++gr)
+          v[gr] = row < a.R ? __ldg(src + 4 * gr + t4) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             big = __hmax2_nan(big, __habs2(as_half2(u4_word(v[gr], i))));
-        }
         big = __hmax2_nan(big, __lowhigh2highlow(big));
         big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
         const float top = __low2float(big);
-        // 2^(7 - exponent of the row's largest): it comes to lie in [128, 256)
+        // 2^(10 - exponent of the row's largest), which comes to lie in [2^10, 2^11); a negative
+        // score scale turns the queries' signs instead, so that a larger product is a larger score
         const int ex = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) : 127;
-        const float f = __uint_as_float(static_cast<uint32_t>(261 - ex) << 23);
+        float f = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
         // codes come in as c 2^-20; a NaN or an infinity among the queries makes the scores NaN
-        const float unit =
-            top <= 65504.f
-                ? a.scale_log2 * (1048576.f * __uint_as_float(static_cast<uint32_t>(ex - 7) << 23))
-                : __uint_as_float(0x7fffffffu);
+        float unit = top <= 65504.f
+                         ? fabsf(a.scale_log2) *
+                               (1048576.f * __uint_as_float(static_cast<uint32_t>(ex - 10) << 23))
+                         : __uint_as_float(0x7fffffffu);
+        if (a.scale_log2 < 0.f) f = -f;
+        if (unit == 0.f) unit = 0x1p-100f;   // so that masked scores stay -infinity
         float own = 0.f;
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr) {
@@ -374,29 +329,131 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
             u[i].y *= f;
             sum += u[i].x + u[i].y;
           }
-          qf[nt][gr][0] = pack_half2(u[0].x * 16.f, u[2].x * 16.f);   // dims 0, 4
-          qf[nt][gr][1] = pack_half2(u[1].x * 16.f, u[3].x * 16.f);   // dims 2, 6
-          qf[nt][gr][2] = pack_half2(u[0].y, u[2].y);                 // dims 1, 5
-          qf[nt][gr][3] = pack_half2(u[1].y, u[3].y);                 // dims 3, 7
+          st_shared_v4(qb + tile * L::kQTile + gr * 512 + lane * 16,
+                       make_uint4(pack_half2(u[0].x * 16.f, u[2].x * 16.f),    // dims 0, 4
+                                  pack_half2(u[1].x * 16.f, u[3].x * 16.f),    // dims 2, 6
+                                  pack_half2(u[0].y, u[2].y),                  // dims 1, 5
+                                  pack_half2(u[1].y, u[3].y)));                // dims 3, 7
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (gr == t4) own = sum * 0x1p-3f;   // at most 1024
+          if (gr == t4) own = sum * 0x1p-20f;   // in the products' units; at most 2^-4
         }
         const __half hi = __float2half_rn(own);
         const __half lo = __float2half_rn(own - __half2float(hi));
-        qzh[nt] = static_cast<uint32_t>(__half_as_ushort(hi)) << 16;
-        qzl[nt] = static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
-        rsc[nt][0] = __shfl_sync(0xffffffffu, unit, 8 * t4);
-        rsc[nt][1] = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
+        const float r0 = __shfl_sync(0xffffffffu, unit, 8 * t4);
+        const float r1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
+        st_shared_v4(qb + tile * L::kQTile + 2048 + lane * 16,
+                     make_uint4(static_cast<uint32_t>(__half_as_ushort(hi)) << 16,
+                                static_cast<uint32_t>(__half_as_ushort(lo)) << 16,
+                                __float_as_uint(r0), __float_as_uint(r1)));
       }
-      float tm[NT][2], tl[NT][2], ot[NT][4][2][4], oz[NT][4];
+      if (APPEND) {   // new rows: K in lanes 0-15, V in 16-31
+        const uint32_t nkv = sbase + L::newkv_off(a.R, B) + (kk & 1) * a.q_len * 512;
+        const __half* src = lane < 16 ? a.k_new : a.v_new;
+        for (int i = 0; i < a.q_len; ++i) {
+          const int64_t row = (static_cast<int64_t>(sg.b) * a.q_len + i) * a.Hkv + sg.h;
+          st_shared_v4(nkv + i * 512 + lane * 16,
+                       __ldg(reinterpret_cast<const uint4*>(src + row * kD) + (lane & 15)));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_qfull + (kk & 1) * 8);
+    };
+    Seg s;
+    if (cur.first(begin, s)) {
+      Seg q = s;   // segment whose queries were prepared last
+      prepare(q, 0);
+      bool has_q = cur.next(q);
+      if (has_q) prepare(q, 1);
+      int npend = 0, k = 0;
+      Seg nx = s;
+      while (cur.next(nx)) {
+        const int sb = k % SB;
+        if (!mbar_wait(bar_sdone + sb * 8, (k / SB) & 1, abort)) flag_timeout(a, abort);
+        const bool complete = (s.c0 == 0 && s.c1 == s.nb);
+        const int slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
+        merge_segment<NCS, 32>(a, stO + sb * NCS * a.R * kSt, stM + sb * NCS * a.R,
+                               stL + sb * NCS * a.R, s.b, s.h, complete,
+                               a.part_o + static_cast<int64_t>(slot) * a.R * kD,
+                               a.part_ml + static_cast<int64_t>(slot) * a.R * 4, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sfree + sb * 8);
+        if (!complete && lane == 0) {
+          // announce the partial (release) and see who else has arrived (acquire)
+          const int ua = unit_first<kSeg4>(pre, a.Hkv, s.b, s.h, s.nb);
+          const int parts = (ua + s.nb - 1) / per - ua / per + 1;
+          if (atomic_add_acq_rel(a.counters + s.b * a.Hkv + s.h, 1) == parts - 1) {
+            npend_s[1 + 3 * npend] = s.b;
+            npend_s[2 + 3 * npend] = s.h;
+            npend_s[3 + 3 * npend] = s.nb;
+            ++npend;
+          }
+        }
+        if (has_q) has_q = cur.next(q);
+        if (has_q) prepare(q, k + 2);   // the consumers are done with segment k's queries
+        s = nx;
+        ++k;
+      }
+      if (lane == 0) *npend_s = npend;
+      set_last(s, k);
+    }
+    // sequences without any chunk get zeros (their units are in no CTA's slice)
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+      if (pre[b + 1] != pre[b]) continue;
+      const int n = a.q_len * a.Hq * kD;
+      for (int i = lane; i < n; i += 32)
+        a.out[static_cast<int64_t>(b) * n + i] = __float2half_rn(0.f);
+    }
+  } else {
+    // =================================== consumers ===========================================
+    const int w = warp % NCS, rs = warp / NCS;   // share of the stages, half of the rows
+    // ldmatrix row addresses: matrices 0, 1 the two key octets of 16 bytes, 2, 3 of the next 16
+    // (codes), or the two octets of the next chunk (scales and minima)
+    const uint32_t lm_row = ((lane >> 3) & 1) * 8 * kInt4Row + (lane & 7) * kInt4Row;
+    const uint32_t lm_codes = lm_row + (lane >> 4) * 16;
+    const uint32_t lm_par = lm_row + (lane >> 4) * kTile + kInt4Params;
+    const uint64_t kv_policy = l2_policy_evict_first();
+    const uint32_t ring = sbase + warp * (ND * kStage4);
+    StageWalk<NCS> walk;
+    walk.start(a, cur, begin, w, lane);
+    for (int i = 0; i < ND; ++i) walk.load(a, cur, w, lane, ring + i * kStage4, kv_policy);
+    const uint32_t wide_mask = (g & 1) ? 0u : 0x40004000u;
+    int slot = 0;   // ring position of the warp's next stage
+    int j = 0, k = 0;
+    Seg s;
+    bool has = cur.first(begin, s);
+    while (has) {
+      const int qs = k & 1;
+      const uint32_t qb = sbase + L::kQ + qs * L::kQBuf + rs * NT * L::kQTile + lane * 16;
+      if (!mbar_wait(bar_qfull + qs * 8, (k >> 1) & 1, abort)) flag_timeout(a, abort);
+      const int Lc = slen[s.b];
+      uint4 qf[QR ? NT : 1][QR ? 4 : 1];
+      uint32_t qzh[NT], qzl[NT];
+      float rsc[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (QR != 0) {
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+            qf[nt][gr] = ld_shared_v4(qb + nt * L::kQTile + gr * 512);
+        }
+        const uint4 v = ld_shared_v4(qb + nt * L::kQTile + 2048);
+        qzh[nt] = v.x;
+        qzl[nt] = v.y;
+        rsc[nt][0] = __uint_as_float(v.z);
+        rsc[nt][1] = __uint_as_float(v.w);
+      }
+
+      // per row: the reference's negative (0 before the first score), the product above which it
+      // moves, the sum of the weights
+      float nm[NT][2], thr[NT][2], tl[NT][2], ot[NT][4][2][4], oz[NT][4];
       int qis[NT];   // query tokens of rows 2 t4 (low half), 2 t4 + 1
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          tm[nt][e] = kNegInf;
-          tl[nt][e] = 0.f;
+          nm[nt][e] = tl[nt][e] = 0.f;
+          thr[nt][e] = kNegInf;
         }
         const int r0 = 8 * (NT * rs + nt) + 2 * t4;
         qis[nt] = min(r0 / a.G, a.q_len - 1) | (min((r0 + 1) / a.G, a.q_len - 1) << 16);
@@ -465,8 +522,6 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
           for (int nt = 0; nt < NT; ++nt) {
             x[nt][h][0] = x[nt][h][1] = x[nt][h][2] = x[nt][h][3] = 0.f;
             mma_f16(x[nt][h], kz[2 * h], kz[2 * h + 1], kz[2 * h], kz[2 * h + 1], qzh[nt], qzl[nt]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[nt][h][i] *= 0x1p-17f;   // sums / 8, in units of 2^-20
           }
 #pragma unroll
           for (int gr = 0; gr < 4; ++gr) {
@@ -476,10 +531,12 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float t[4] = {0.f, 0.f, 0.f, 0.f};
+              const uint4 b = QR ? qf[QR ? nt : 0][QR ? gr : 0]
+                                 : ld_shared_v4(qb + nt * L::kQTile + gr * 512);
               mma_f16(t, w0 & 0x000f000fu, w1 & 0x000f000fu, u0 & 0x000f000fu, u1 & 0x000f000fu,
-                      qf[nt][gr][0], qf[nt][gr][1]);
+                      b.x, b.y);
               mma_f16(t, w0 & 0x00f000f0u, w1 & 0x00f000f0u, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
-                      qf[nt][gr][2], qf[nt][gr][3]);
+                      b.z, b.w);
               x[nt][h][0] = fmaf(s0, t[0], x[nt][h][0]);
               x[nt][h][1] = fmaf(s0, t[1], x[nt][h][1]);
               x[nt][h][2] = fmaf(s1, t[2], x[nt][h][2]);
@@ -497,34 +554,29 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
-              const int t0 = (c + h) * kChunk + 8 * o + 2 * t4;
+              const int t0 = (c + h) * kChunk + 8 * o;
               const int lim = h == 0 || two ? Lc : 0;
-              vp[h][o] &= (t0 < lim ? 0x0000ffffu : 0u) | (t0 + 1 < lim ? 0xffff0000u : 0u);
+              vp[h][o] &= (t0 + 2 * t4 < lim ? 0x0000ffffu : 0u) |
+                          (t0 + 2 * t4 + 1 < lim ? 0xffff0000u : 0u);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (t0 + g >= lim - a.q_len + 1 + ((qis[nt] >> (16 * e)) & 0xffff))
+                    x[nt][h][2 * o + e] = kNegInf;
             }
         }
         // even g: scales; bit 14 says 2 or more
-        const bool wide = !(g & 1) && ((vp[0][0] | vp[0][1] | vp[1][0] | vp[1][1]) & 0x40004000u);
+        const bool wide = ((vp[0][0] | vp[0][1] | vp[1][0] | vp[1][1]) & wide_mask) != 0;
 
-        // ---- mask, softmax weights against the reference (exp2 domain) ----
+        // ---- softmax weights against the reference (exp2 domain) ----
         bool move = wide && shift != 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int o = 0; o < 2; ++o) {
-                float& v = x[nt][h][2 * o + e];
-                v *= rsc[nt][e];
-                if (!full) {
-                  const int lim = Lc - a.q_len + 1 + ((qis[nt] >> (16 * e)) & 0xffff);
-                  if ((c + h) * kChunk + 8 * o + g >= lim || (h && !two)) v = kNegInf;
-                }
-              }
-            move |= fmaxf(fmaxf(x[nt][0][e], x[nt][0][2 + e]), fmaxf(x[nt][1][e], x[nt][1][2 + e])) >
-                    tm[nt][e] + (shift + kGrow);
-          }
+          for (int e = 0; e < 2; ++e)
+            move |= fmaxf(fmaxf(x[nt][0][e], x[nt][0][2 + e]),
+                          fmaxf(x[nt][1][e], x[nt][1][2 + e])) > thr[nt][e];
         if (__any_sync(0xffffffffu, move)) {
           const float to = __any_sync(0xffffffffu, wide) ? 0.f : shift;
 #pragma unroll
@@ -537,9 +589,13 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float m_new = fmaxf(tm[nt][e] + (shift - to), mx - to);
-              alpha[e] = fast_exp2(tm[nt][e] - (m_new == kNegInf ? 0.f : m_new));
-              tm[nt][e] = m_new;
+              const float m_old = thr[nt][e] == kNegInf ? kNegInf : -nm[nt][e];
+              const float m_new = fmaxf(m_old + (shift - to), mx * rsc[nt][e] - to);
+              alpha[e] = m_old == kNegInf ? 0.f : fast_exp2(m_old - m_new);
+              if (m_new != kNegInf) {
+                nm[nt][e] = -m_new;
+                thr[nt][e] = (m_new + (to + kGrow)) / rsc[nt][e];
+              }
               tl[nt][e] *= alpha[e];
             }
 #pragma unroll
@@ -559,11 +615,10 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float m_use = tm[nt][e] == kNegInf ? 0.f : tm[nt][e];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              x[nt][h][e] = fast_exp2(x[nt][h][e] - m_use);
-              x[nt][h][2 + e] = fast_exp2(x[nt][h][2 + e] - m_use);
+              x[nt][h][e] = fast_exp2(fmaf(x[nt][h][e], rsc[nt][e], nm[nt][e]));
+              x[nt][h][2 + e] = fast_exp2(fmaf(x[nt][h][2 + e], rsc[nt][e], nm[nt][e]));
             }
             tl[nt][e] += (x[nt][0][e] + x[nt][0][2 + e]) + (x[nt][1][e] + x[nt][1][2 + e]);
           }
@@ -640,13 +695,14 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
                               fmaf(ot[nt][gr][0][2 + e], 0x1p24f, z[gr]),
                               fmaf(ot[nt][gr][1][2 + e], 0x1p20f, z[gr]));
             if (g == 0) {
-              stM[(sb * NCS + w) * a.R + r] = tm[nt][e];
+              stM[(sb * NCS + w) * a.R + r] = thr[nt][e] == kNegInf ? kNegInf : -nm[nt][e];
               stL[(sb * NCS + w) * a.R + r] = lv;
             }
           }
         }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_sdone + sb * 8);
+      set_last(s, k);
       ++k;
       has = cur.next(s);
     }
@@ -662,11 +718,11 @@ decode_int4_kernel(const __grid_constant__ CUtensorMap tmQ, const DecodeArgs a) 
 // ---------------------------------------------------------------------------------------------
 // Host side.
 
-template <int NCS, int RS, int ND, int NT, int SB, int MINB>
+template <int NCS, int RS, int ND, int NT, int SB, int QR, int MINB>
 Variant variant4(bool append) {
   const void* fn =
-      append ? reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, MINB, true>)
-             : reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, MINB, false>);
+      append ? reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, QR, MINB, true>)
+             : reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, QR, MINB, false>);
   return Variant{fn, NT, false, (NCS * RS + 1) * 32, &Smem4<NCS, RS, ND, NT, SB>::bytes};
 }
 
@@ -702,13 +758,13 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
 #ifndef V1
-#define V1 5, 1, 3, 1, 1, 2
+#define V1 4, 1, 3, 1, 1, 1, 2
 #endif
 #ifndef V2
-#define V2 7, 1, 3, 2, 1, 1
+#define V2 7, 1, 3, 2, 1, 1, 1
 #endif
 #ifndef V4
-#define V4 3, 2, 3, 2, 1, 1
+#define V4 3, 2, 3, 2, 1, 1, 1
 #endif
   const Variant v = R <= 8    ? variant4<V1>(append)
                     : R <= 16 ? variant4<V2>(append)
@@ -719,14 +775,6 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   int status = PKV_OK;
   const int grid = grid_size(v, smem, &status);
   if (!grid) return status != PKV_OK ? status : PKV_EINVAL;
-
-  CUtensorMap tmQ;
-  const cuuint64_t q_dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(Hq),
-                                static_cast<cuuint64_t>(num_seqs) * q_len};
-  const cuuint64_t q_strides[2] = {kD * 2, static_cast<cuuint64_t>(Hq) * kD * 2};
-  const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(q_len)};
-  const int st = encode(&tmQ, q, 3, q_dims, q_strides, q_box);
-  if (st != PKV_OK) return st;
 
   unsigned int* err = device_error_ptr();
   if (!err) return cuda_status(cudaGetLastError());
@@ -757,7 +805,8 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   args.k_pool = static_cast<__half*>(const_cast<void*>(k_cache));
   args.v_pool = static_cast<__half*>(const_cast<void*>(v_cache));
 
-  void* params[2] = {&tmQ, &args};
+  const __half* q_in = static_cast<const __half*>(q);
+  void* params[2] = {&args, &q_in};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(v.threads);
