@@ -54,7 +54,10 @@ namespace {
 
 constexpr int kTile = kChunk * kInt4Row;     // one chunk's K (or V): 1280 bytes
 constexpr int kStage4 = 4 * kTile;           // K of two chunks, V of two chunks
-constexpr int kSeg4 = 4;                     // per-segment cost in chunks (see kSegCost)
+#ifndef SEG4
+#define SEG4 12
+#endif
+constexpr int kSeg4 = SEG4;                     // per-segment cost in chunks (see kSegCost)
 // How far the softmax's reference stays below the running maximum (see above), and how far a
 // weight may grow past the maximum it was taken at before the reference moves.
 constexpr float kShift = 11.f, kGrow = 2.f;
@@ -68,8 +71,8 @@ struct Smem4 {
   static constexpr int kQTile = 5 * 512;              // fragments of 4 groups, row constants
   static constexpr int kQBuf = RS * NT * kQTile;
   static constexpr int kQ = NCS * RS * ND * kStage4;
-  static constexpr int kBars = kQ + 2 * kQBuf;        // qfull[2], sdone[2], sfree[2]
-  static constexpr int kFlags = kBars + 6 * 8;
+  static constexpr int kBars = kQ + 2 * kQBuf;        // qfull, qempty, sdone, sfree: 2 each
+  static constexpr int kFlags = kBars + 8 * 8;
   static constexpr int kState = (kFlags + 64 + 15) & ~15;
   __host__ __device__ static int state_floats(int R) { return SB * NCS * R * (kSt + 2); }
   __host__ __device__ static int seq_off(int R) { return kState + state_floats(R) * 4; }
@@ -187,12 +190,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Warps 0 .. NCS RS - 1 consume; the last warp prepares the queries and is the epilogue (merges
-// each segment's per-warp states, writes outputs and split units' partials). QR: the query
+// Warps 0 .. NCS RS - 1 consume; the next one prepares the queries, the last one is the epilogue
+// (merges each segment's per-warp states, writes outputs and split units' partials). QR: the query
 // fragments stay in the consumers' registers (else they are read from shared memory per stage,
 // which leaves registers for more warps).
 template <int NCS, int RS, int ND, int NT, int SB, int QR, int MINB, bool APPEND>
-__global__ void __launch_bounds__((NCS * RS + 1) * 32, MINB)
+__global__ void __launch_bounds__((NCS * RS + 2) * 32, MINB)
 decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
   using L = Smem4<NCS, RS, ND, NT, SB>;
   constexpr int NCW = NCS * RS;
@@ -201,7 +204,8 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar_qfull = sbase + L::kBars;
-  const uint32_t bar_sdone = bar_qfull + 2 * 8;
+  const uint32_t bar_qempty = bar_qfull + 2 * 8;
+  const uint32_t bar_sdone = bar_qempty + 2 * 8;
   const uint32_t bar_sfree = bar_sdone + 2 * 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kFlags);
   int* npend_s = reinterpret_cast<int*>(smem + L::kFlags) + 1;   // then 2 x (b, h, nb)
@@ -222,6 +226,7 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_qfull + s * 8, 1);
+      mbar_init(bar_qempty + s * 8, NCW);
       mbar_init(bar_sdone + s * 8, NCW);
       mbar_init(bar_sfree + s * 8, 1);
     }
@@ -275,7 +280,7 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
   };
 
   if (warp == NCW) {
-    // ============================ queries and epilogue =======================================
+    // =================================== queries =============================================
     // An early-started launch (APPEND) has its first stages on the way already; queries, new
     // rows, outputs and the workspace are touched only after the preceding kernel completed.
     griddep_wait();
@@ -360,11 +365,27 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
       if (lane == 0) mbar_arrive(bar_qfull + (kk & 1) * 8);
     };
     Seg s;
+    bool has = cur.first(begin, s);
+    for (int k = 0; has; ++k) {
+      if (k >= 2 && !mbar_wait(bar_qempty + (k & 1) * 8, ((k >> 1) - 1) & 1, abort))
+        flag_timeout(a, abort);
+      prepare(s, k);
+      has = cur.next(s);
+    }
+    // sequences without any chunk get zeros (their units are in no CTA's slice)
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+      if (pre[b + 1] != pre[b]) continue;
+      const int n = a.q_len * a.Hq * kD;
+      for (int i = lane; i < n; i += 32)
+        a.out[static_cast<int64_t>(b) * n + i] = __float2half_rn(0.f);
+    }
+    return;
+  }
+  if (warp == NCW + 1) {
+    // =================================== epilogue ============================================
+    griddep_wait();
+    Seg s;
     if (cur.first(begin, s)) {
-      Seg q = s;   // segment whose queries were prepared last
-      prepare(q, 0);
-      bool has_q = cur.next(q);
-      if (has_q) prepare(q, 1);
       int npend = 0, k = 0;
       Seg nx = s;
       while (cur.next(nx)) {
@@ -389,20 +410,11 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
             ++npend;
           }
         }
-        if (has_q) has_q = cur.next(q);
-        if (has_q) prepare(q, k + 2);   // the consumers are done with segment k's queries
         s = nx;
         ++k;
       }
       if (lane == 0) *npend_s = npend;
       set_last(s, k);
-    }
-    // sequences without any chunk get zeros (their units are in no CTA's slice)
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-      if (pre[b + 1] != pre[b]) continue;
-      const int n = a.q_len * a.Hq * kD;
-      for (int i = lane; i < n; i += 32)
-        a.out[static_cast<int64_t>(b) * n + i] = __float2half_rn(0.f);
     }
   } else {
     // =================================== consumers ===========================================
@@ -667,6 +679,9 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
       }
       j += npair;
 
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_qempty + qs * 8);
+
       // ---- hand this warp's state to the epilogue: row g of tile (gr, i) is dim 32 gr + 4 g + i,
       // row g + 8 dim 32 gr + 4 g + 2 + i ----
       const int sb = k % SB;
@@ -712,7 +727,7 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
   // ---- end of the slice ----
   if (last.k >= 0)
     finish_slice<NCS, kSeg4, NCW, SB>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s,
-                                      fast_s, tid);
+                                      fast_s, warp < NCW ? tid : tid - 32);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -723,7 +738,7 @@ Variant variant4(bool append) {
   const void* fn =
       append ? reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, QR, MINB, true>)
              : reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, QR, MINB, false>);
-  return Variant{fn, NT, false, (NCS * RS + 1) * 32, &Smem4<NCS, RS, ND, NT, SB>::bytes};
+  return Variant{fn, NT, false, (NCS * RS + 2) * 32, &Smem4<NCS, RS, ND, NT, SB>::bytes};
 }
 
 int launch_decode_int4(void* out, const void* q, const void* k_new, const void* v_new,
@@ -758,10 +773,10 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
 #ifndef V1
-#define V1 4, 1, 3, 1, 1, 1, 2
+#define V1 4, 1, 3, 1, 1, 0, 2
 #endif
 #ifndef V2
-#define V2 7, 1, 3, 2, 1, 1, 1
+#define V2 6, 1, 3, 2, 1, 1, 1
 #endif
 #ifndef V4
 #define V4 3, 2, 3, 2, 1, 1, 1
