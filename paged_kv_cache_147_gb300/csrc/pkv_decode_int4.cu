@@ -535,24 +535,41 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
             x[nt][h][0] = x[nt][h][1] = x[nt][h][2] = x[nt][h][3] = 0.f;
             mma_f16(x[nt][h], kz[2 * h], kz[2 * h + 1], kz[2 * h], kz[2 * h + 1], qzh[nt], qzl[nt]);
           }
+          // two groups at a time: their products do not wait on each other
 #pragma unroll
-          for (int gr = 0; gr < 4; ++gr) {
-            const float s0 = __low2float(as_half2(u4_word(p0, gr)));
-            const float s1 = __low2float(as_half2(u4_word(p1, gr)));
-            const uint32_t w0 = kw[gr][0], w1 = kw[gr][1], u0 = w0 >> 8, u1 = w1 >> 8;
+          for (int gp = 0; gp < 4; gp += 2) {
+            float t[NT][2][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float t[4] = {0.f, 0.f, 0.f, 0.f};
-              const uint4 b = QR ? qf[QR ? nt : 0][QR ? gr : 0]
-                                 : ld_shared_v4(qb + nt * L::kQTile + gr * 512);
-              mma_f16(t, w0 & 0x000f000fu, w1 & 0x000f000fu, u0 & 0x000f000fu, u1 & 0x000f000fu,
-                      b.x, b.y);
-              mma_f16(t, w0 & 0x00f000f0u, w1 & 0x00f000f0u, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
-                      b.z, b.w);
-              x[nt][h][0] = fmaf(s0, t[0], x[nt][h][0]);
-              x[nt][h][1] = fmaf(s0, t[1], x[nt][h][1]);
-              x[nt][h][2] = fmaf(s1, t[2], x[nt][h][2]);
-              x[nt][h][3] = fmaf(s1, t[3], x[nt][h][3]);
+            for (int part = 0; part < 2; ++part) {
+              const uint32_t m = part ? 0x00f000f0u : 0x000f000fu;
+#pragma unroll
+              for (int j2 = 0; j2 < 2; ++j2) {
+                const uint32_t w0 = kw[gp + j2][0], w1 = kw[gp + j2][1];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  uint2 b;
+                  if constexpr (QR != 0) {
+                    const uint4 q4 = qf[nt][gp + j2];
+                    b = part ? make_uint2(q4.z, q4.w) : make_uint2(q4.x, q4.y);
+                  } else {
+                    b = ld_shared_v2(qb + nt * L::kQTile + (gp + j2) * 512 + part * 8);
+                  }
+                  if (part == 0) t[nt][j2][0] = t[nt][j2][1] = t[nt][j2][2] = t[nt][j2][3] = 0.f;
+                  mma_f16(t[nt][j2], w0 & m, w1 & m, (w0 >> 8) & m, (w1 >> 8) & m, b.x, b.y);
+                }
+              }
+            }
+#pragma unroll
+            for (int j2 = 0; j2 < 2; ++j2) {
+              const float s0 = __low2float(as_half2(u4_word(p0, gp + j2)));
+              const float s1 = __low2float(as_half2(u4_word(p1, gp + j2)));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                x[nt][h][0] = fmaf(s0, t[nt][j2][0], x[nt][h][0]);
+                x[nt][h][1] = fmaf(s0, t[nt][j2][1], x[nt][h][1]);
+                x[nt][h][2] = fmaf(s1, t[nt][j2][2], x[nt][h][2]);
+                x[nt][h][3] = fmaf(s1, t[nt][j2][3], x[nt][h][3]);
+              }
             }
           }
         }
@@ -664,12 +681,13 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
               const uint32_t r0 = half2_bits(__hfma2(p0, as_half2(s0), __hneg2(b0)));
               const uint32_t r1 = half2_bits(__hfma2(p1, as_half2(s1), __hneg2(b1)));
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t m = i ? 0x00f000f0u : 0x000f000fu;
-                mma_f16(ot[nt][gr][i], vw[gr][0] & m, u0 & m, vw[gr][1] & m, u1 & m,
-                        half2_bits(b0), half2_bits(b1));
-                mma_f16(ot[nt][gr][i], vw[gr][0] & m, u0 & m, vw[gr][1] & m, u1 & m, r0, r1);
-              }
+              for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t m = i ? 0x00f000f0u : 0x000f000fu;
+                  mma_f16(ot[nt][gr][i], vw[gr][0] & m, u0 & m, vw[gr][1] & m, u1 & m,
+                          part ? r0 : half2_bits(b0), part ? r1 : half2_bits(b1));
+                }
             }
           }
         }
