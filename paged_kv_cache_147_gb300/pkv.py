@@ -151,16 +151,22 @@ def _p(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _need(fn: str, dtype, *tensors, strided=False):
-    """Raises unless every tensor is of `dtype`, on the current device and contiguous (or only
-    checked by the caller): the library sees bare pointers."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t.dtype is not dtype or t.get_device() != dev or not (strided or t.is_contiguous()):
-            raise PkvError(fn, EINVAL)
+# The newer entry points check what the library cannot see through a bare pointer: element type,
+# device, layout, shape. The checks are written out for speed: a decode step's calls are short.
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_F16, _F32, _U8, _I32, _I64 = torch.float16, torch.float32, torch.uint8, torch.int32, torch.int64
 
 
-def _same(fn: str, ok: bool):
+def _is(t: torch.Tensor, dtype, dev: int) -> bool:
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+
+
+def _on(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _require(fn: str, ok: bool) -> None:
     if not ok:
         raise PkvError(fn, EINVAL)
 
@@ -372,80 +378,80 @@ def ring_attn_decode_append(out, q, k_new, v_new, k_cache, v_cache, block_tables
 INT4_ROW = 80   # bytes of one row (token, kv head) of a 4-bit pool
 
 
-def _pools_int4(fn, k_cache, v_cache):
-    _need(fn, torch.uint8, k_cache, v_cache)
-    _same(fn, k_cache.dim() == 4 and k_cache.shape[3] == INT4_ROW and
-          v_cache.shape == k_cache.shape)
-    return k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
-
-
 def kv_append_int4(k, v, slots, k_cache, v_cache, stream=None):
-    """k, v fp16 [T, Hkv, D]; k_cache, v_cache one layer of uint8 4-bit rows [NB, Hkv, bs, 80]."""
-    fn = "pkv_kv_append_int4"
-    nb, hkv, bs = _pools_int4(fn, k_cache, v_cache)
-    _need(fn, torch.float16, k, v)
-    _need(fn, torch.int64, slots)
-    T = slots.numel()
-    _same(fn, k.shape == (T, hkv, 128) and v.shape == k.shape)
-    _check(fn, load().pkv_kv_append_int4(
-        k.data_ptr(), v.data_ptr(), slots.data_ptr(), T, k_cache.data_ptr(), v_cache.data_ptr(),
-        nb, hkv, 128, bs, _stream(stream)))
+    """k, v fp16 [T, Hkv, 128]; slots int64 [T]; k_cache, v_cache one layer of uint8 4-bit rows
+    [NB, Hkv, bs, 80]."""
+    fn, dev = "pkv_kv_append_int4", _device()
+    _require(fn, _is(k, _F16, dev) and _is(v, _F16, dev) and _is(slots, _I64, dev) and
+             _is(k_cache, _U8, dev) and _is(v_cache, _U8, dev) and k_cache.dim() == 4)
+    nb, hkv, bs, row = shape = k_cache.shape
+    n = slots.numel()
+    _require(fn, row == INT4_ROW and v_cache.shape == shape and k.shape == (n, hkv, 128) and
+             v.shape == k.shape)
+    _check(fn, (_lib or load()).pkv_kv_append_int4(
+        k.data_ptr(), v.data_ptr(), slots.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(),
+        nb, hkv, 128, bs, _on(stream, dev)))
 
 
 def widen_blocks_int4(k_cache, v_cache, src, dst, k_out, v_out, stream=None):
     """Blocks src[i] of the 4-bit pools [NB, Hkv, bs, 80] -> blocks dst[i] of the fp16 pools k_out,
     v_out [NB', Hkv, bs, 128]; src, dst int32."""
-    fn = "pkv_widen_blocks_int4"
-    nb, hkv, bs = _pools_int4(fn, k_cache, v_cache)
-    _need(fn, torch.float16, k_out, v_out)
-    _need(fn, torch.int32, src, dst)
-    _same(fn, src.numel() == dst.numel() and k_out.dim() == 4 and
-          k_out.shape[1:] == (hkv, bs, 128) and v_out.shape == k_out.shape)
-    _check(fn, load().pkv_widen_blocks_int4(
-        k_cache.data_ptr(), v_cache.data_ptr(), src.data_ptr(), dst.data_ptr(), src.numel(), nb,
-        k_out.data_ptr(), v_out.data_ptr(), k_out.shape[0], hkv, 128, bs, _stream(stream)))
-
-
-def _decode_args_int4(fn, out, q, k_cache, v_cache, block_tables, context_lens):
-    nb, hkv, bs = _pools_int4(fn, k_cache, v_cache)
-    _need(fn, torch.float16, out, q)
-    _need(fn, torch.int32, block_tables, context_lens)
-    _same(fn, q.dim() == 4 and out.shape == q.shape and block_tables.dim() == 2 and
-          block_tables.shape[0] == q.shape[0] and context_lens.numel() == q.shape[0])
-    return nb, hkv, bs
+    fn, dev = "pkv_widen_blocks_int4", _device()
+    _require(fn, _is(k_cache, _U8, dev) and _is(v_cache, _U8, dev) and _is(k_out, _F16, dev) and
+             _is(v_out, _F16, dev) and _is(src, _I32, dev) and _is(dst, _I32, dev) and
+             k_cache.dim() == 4 and k_out.dim() == 4)
+    nb, hkv, bs, row = shape = k_cache.shape
+    n, nb_out = src.numel(), k_out.shape[0]
+    _require(fn, row == INT4_ROW and v_cache.shape == shape and dst.numel() == n and
+             k_out.shape == (nb_out, hkv, bs, 128) and v_out.shape == k_out.shape)
+    _check(fn, (_lib or load()).pkv_widen_blocks_int4(
+        k_cache.data_ptr(), v_cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, nb,
+        k_out.data_ptr(), v_out.data_ptr(), nb_out, hkv, 128, bs, _on(stream, dev)))
 
 
 def paged_attn_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, scale, workspace,
                            stream=None):
     """paged_attn_decode over a 4-bit cache: uint8 pools [NB, Hkv, bs, 80] (kv_append_int4's
     rows); everything else as there."""
-    fn = "pkv_paged_attn_decode_int4"
-    nb, hkv, bs = _decode_args_int4(fn, out, q, k_cache, v_cache, block_tables, context_lens)
+    fn, dev = "pkv_paged_attn_decode_int4", _device()
+    _require(fn, _is(q, _F16, dev) and _is(out, _F16, dev) and _is(k_cache, _U8, dev) and
+             _is(v_cache, _U8, dev) and _is(block_tables, _I32, dev) and
+             _is(context_lens, _I32, dev) and workspace.get_device() == dev and
+             workspace.is_contiguous() and q.dim() == 4 and k_cache.dim() == 4 and
+             block_tables.dim() == 2)
     B, q_len, hq, d = q.shape
-    _need(fn, workspace.dtype, workspace)
-    _check(fn, load().pkv_paged_attn_decode_int4(
+    nb, hkv, bs, row = shape = k_cache.shape
+    rows, width = block_tables.shape
+    _require(fn, row == INT4_ROW and v_cache.shape == shape and out.shape == q.shape and
+             rows == B and context_lens.numel() == B)
+    _check(fn, (_lib or load()).pkv_paged_attn_decode_int4(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb,
-        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, q_len, hq,
-        hkv, d, bs, float(scale), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        block_tables.data_ptr(), width, context_lens.data_ptr(), B, q_len, hq, hkv, d, bs,
+        scale, workspace.data_ptr(), workspace.nbytes, _on(stream, dev)))
     return out
 
 
 def paged_attn_decode_append_int4(out, q, k_new, v_new, k_cache, v_cache, block_tables,
                                   context_lens, scale, workspace, stream=None):
-    """paged_attn_decode_append over a 4-bit cache: the new fp16 rows are stored as kv_append_int4
-    stores them and attended over with the rest. Early-start caveat as there."""
-    fn = "pkv_paged_attn_decode_append_int4"
-    nb, hkv, bs = _decode_args_int4(fn, out, q, k_cache, v_cache, block_tables, context_lens)
+    """paged_attn_decode_append over a 4-bit cache: the new fp16 rows k_new, v_new
+    [B*q_len, Hkv, 128] are stored as kv_append_int4 stores them and attended over with the rest.
+    Early-start caveat as there."""
+    fn, dev = "pkv_paged_attn_decode_append_int4", _device()
+    _require(fn, _is(q, _F16, dev) and _is(out, _F16, dev) and _is(k_new, _F16, dev) and
+             _is(v_new, _F16, dev) and _is(k_cache, _U8, dev) and _is(v_cache, _U8, dev) and
+             _is(block_tables, _I32, dev) and _is(context_lens, _I32, dev) and
+             workspace.get_device() == dev and workspace.is_contiguous() and q.dim() == 4 and
+             k_cache.dim() == 4 and block_tables.dim() == 2)
     B, q_len, hq, d = q.shape
-    _need(fn, torch.float16, k_new, v_new)
-    _need(fn, workspace.dtype, workspace)
-    _same(fn, k_new.shape == (B * q_len, hkv, 128) and v_new.shape == k_new.shape)
-    _check(fn, load().pkv_paged_attn_decode_append_int4(
+    nb, hkv, bs, row = shape = k_cache.shape
+    rows, width = block_tables.shape
+    _require(fn, row == INT4_ROW and v_cache.shape == shape and out.shape == q.shape and
+             rows == B and context_lens.numel() == B and k_new.shape == (B * q_len, hkv, 128) and
+             v_new.shape == k_new.shape)
+    _check(fn, (_lib or load()).pkv_paged_attn_decode_append_int4(
         out.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), nb, block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), B, q_len, hq, hkv, d, bs, float(scale), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        v_cache.data_ptr(), nb, block_tables.data_ptr(), width, context_lens.data_ptr(), B, q_len,
+        hq, hkv, d, bs, scale, workspace.data_ptr(), workspace.nbytes, _on(stream, dev)))
     return out
 
 
@@ -456,34 +462,33 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps, positions, cos_sin, q_out=None, 
     heads contiguous, tokens any stride apart: slices of a packed projection do), weights fp16
     [128], positions int64 [T] (negative: padding, left as it is), cos_sin a rope_table on the
     device -> (q_out, k_out), contiguous."""
-    fn = "pkv_qk_norm_rope"
-    _need(fn, torch.float16, q, k, strided=True)
-    _need(fn, torch.float16, q_weight, k_weight)
-    _need(fn, torch.int64, positions)
-    _need(fn, torch.float32, cos_sin)
-    T = positions.numel()
-    _same(fn, q.dim() == 3 and k.dim() == 3)
-    hq, hkv = q.shape[1], k.shape[1]
+    fn, dev = "pkv_qk_norm_rope", _device()
+    _require(fn, q.dtype is _F16 and k.dtype is _F16 and q.get_device() == dev and
+             k.get_device() == dev and q.dim() == 3 and k.dim() == 3 and
+             _is(q_weight, _F16, dev) and _is(k_weight, _F16, dev) and
+             _is(positions, _I64, dev) and _is(cos_sin, _F32, dev) and cos_sin.dim() == 3)
+    T, hq, d = q.shape
+    _, hkv, _ = k.shape
     (qs, qh, qd), (ks, kh, kd) = q.stride(), k.stride()
-    _same(fn, q.shape == (T, hq, 128) and k.shape == (T, hkv, 128) and qd == 1 and kd == 1 and
-          (qh == 128 or hq == 1) and (kh == 128 or hkv == 1) and q_weight.numel() == 128 and
-          k_weight.numel() == 128 and cos_sin.dim() == 3 and cos_sin.shape[1:] == (64, 2))
+    n_index = cos_sin.shape[0]
+    _require(fn, d == 128 and k.shape == (T, hkv, 128) and positions.numel() == T and qd == 1 and
+             kd == 1 and (qh == 128 or hq == 1) and (kh == 128 or hkv == 1) and
+             q_weight.numel() == 128 and k_weight.numel() == 128 and
+             cos_sin.shape == (n_index, 64, 2))
     if T <= 1:   # the stride of a single token means nothing
         qs, ks = hq * 128, hkv * 128
     if q_out is None:
-        q_out = torch.empty((T, hq, 128), dtype=torch.float16, device=q.device)
+        q_out = torch.empty((T, hq, 128), dtype=_F16, device=q.device)
     else:
-        _need(fn, torch.float16, q_out)
-        _same(fn, q_out.shape == q.shape)
+        _require(fn, _is(q_out, _F16, dev) and q_out.shape == q.shape)
     if k_out is None:
-        k_out = torch.empty((T, hkv, 128), dtype=torch.float16, device=k.device)
+        k_out = torch.empty((T, hkv, 128), dtype=_F16, device=q.device)
     else:
-        _need(fn, torch.float16, k_out)
-        _same(fn, k_out.shape == k.shape)
-    _check(fn, load().pkv_qk_norm_rope(
+        _require(fn, _is(k_out, _F16, dev) and k_out.shape == k.shape)
+    _check(fn, (_lib or load()).pkv_qk_norm_rope(
         q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(), qs, ks,
-        q_weight.data_ptr(), k_weight.data_ptr(), float(eps), positions.data_ptr(),
-        cos_sin.data_ptr(), cos_sin.shape[0], T, hq, hkv, 128, _stream(stream)))
+        q_weight.data_ptr(), k_weight.data_ptr(), eps, positions.data_ptr(), cos_sin.data_ptr(),
+        n_index, T, hq, hkv, 128, _on(stream, dev)))
     return q_out, k_out
 
 
@@ -494,27 +499,29 @@ def extend_tables(block_tables, context_lens, new_lens, block_size, free_blocks,
     per sequence, blocks off the stack free_blocks (int32 [num_blocks], free_count of them free;
     all updated in place) -> (slots int64, seq_ids int32, positions int64 [max_tokens],
     cu_new_lens int32 [B + 1]); `out` gives the four to write into."""
-    fn = "pkv_extend_tables"
-    _need(fn, torch.int32, block_tables, context_lens, new_lens, free_blocks, free_count)
-    B = context_lens.numel()
-    _same(fn, block_tables.dim() == 2 and block_tables.shape[0] == B and new_lens.numel() == B and
-          free_count.numel() == 1)
+    fn, dev = "pkv_extend_tables", _device()
+    _require(fn, _is(block_tables, _I32, dev) and _is(context_lens, _I32, dev) and
+             _is(new_lens, _I32, dev) and _is(free_blocks, _I32, dev) and
+             _is(free_count, _I32, dev) and block_tables.dim() == 2)
+    B, width = block_tables.shape
+    _require(fn, context_lens.numel() == B and new_lens.numel() == B and free_count.numel() == 1)
     if out is None:
-        dev = block_tables.device
-        out = (torch.empty(max_tokens, dtype=torch.int64, device=dev),
-               torch.empty(max_tokens, dtype=torch.int32, device=dev),
-               torch.empty(max_tokens, dtype=torch.int64, device=dev),
-               torch.empty(B + 1, dtype=torch.int32, device=dev))
+        on = block_tables.device
+        out = (torch.empty(max_tokens, dtype=_I64, device=on),
+               torch.empty(max_tokens, dtype=_I32, device=on),
+               torch.empty(max_tokens, dtype=_I64, device=on),
+               torch.empty(B + 1, dtype=_I32, device=on))
+        slots, seqs, pos, cu = out
     else:
-        _need(fn, torch.int64, out[0], out[2])
-        _need(fn, torch.int32, out[1], out[3])
-        _same(fn, out[0].numel() == max_tokens and out[1].numel() == max_tokens and
-              out[2].numel() == max_tokens and out[3].numel() == B + 1)
-    _check(fn, load().pkv_extend_tables(
-        block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(), B,
-        block_tables.shape[1], block_size, free_blocks.data_ptr(), free_count.data_ptr(),
-        free_blocks.numel(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
-        out[3].data_ptr(), max_tokens, _stream(stream)))
+        slots, seqs, pos, cu = out
+        _require(fn, _is(slots, _I64, dev) and _is(seqs, _I32, dev) and _is(pos, _I64, dev) and
+                 _is(cu, _I32, dev) and slots.numel() == max_tokens and
+                 seqs.numel() == max_tokens and pos.numel() == max_tokens and cu.numel() == B + 1)
+    _check(fn, (_lib or load()).pkv_extend_tables(
+        block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(), B, width,
+        block_size, free_blocks.data_ptr(), free_count.data_ptr(), free_blocks.numel(),
+        slots.data_ptr(), seqs.data_ptr(), pos.data_ptr(), cu.data_ptr(), max_tokens,
+        _on(stream, dev)))
     return out
 
 
@@ -522,15 +529,16 @@ def truncate_tables(block_tables, context_lens, keep_lens, block_size, free_bloc
                     stream=None):
     """Cuts sequences back to keep_lens tokens (int32 [B]; negative or past the length: as it is);
     their blocks go back on the stack. All updated in place."""
-    fn = "pkv_truncate_tables"
-    _need(fn, torch.int32, block_tables, context_lens, keep_lens, free_blocks, free_count)
-    B = context_lens.numel()
-    _same(fn, block_tables.dim() == 2 and block_tables.shape[0] == B and keep_lens.numel() == B and
-          free_count.numel() == 1)
-    _check(fn, load().pkv_truncate_tables(
-        block_tables.data_ptr(), context_lens.data_ptr(), keep_lens.data_ptr(), B,
-        block_tables.shape[1], block_size, free_blocks.data_ptr(), free_count.data_ptr(),
-        free_blocks.numel(), _stream(stream)))
+    fn, dev = "pkv_truncate_tables", _device()
+    _require(fn, _is(block_tables, _I32, dev) and _is(context_lens, _I32, dev) and
+             _is(keep_lens, _I32, dev) and _is(free_blocks, _I32, dev) and
+             _is(free_count, _I32, dev) and block_tables.dim() == 2)
+    B, width = block_tables.shape
+    _require(fn, context_lens.numel() == B and keep_lens.numel() == B and free_count.numel() == 1)
+    _check(fn, (_lib or load()).pkv_truncate_tables(
+        block_tables.data_ptr(), context_lens.data_ptr(), keep_lens.data_ptr(), B, width,
+        block_size, free_blocks.data_ptr(), free_count.data_ptr(), free_blocks.numel(),
+        _on(stream, dev)))
 
 
 # ------------------------------------------------------------------------------ host checks
