@@ -25,14 +25,29 @@ constexpr int kInt4Params = 64;     // offset of the (s, z) pairs
 //   maximum, or rounded down where 15 s + z would pass the largest fp16; code = (x - z) / s
 //   rounded to nearest, ties to even (0 where s is 0).
 // A group with a NaN or an infinity gets s = z = NaN: all of it reads back as NaN.
-// The code comes from a product with 1 / s (off by at most 2^-22 relative, so by 4e-6 of a
-// step); one that lies nearer than 1e-5 to a border between two codes is decided by the exact
-// remainder, the rounding error of x - z included. A division per element instead made the
-// append compute-bound.
+// range / 15 is a product with RN(1 / 15) corrected by its exact remainder, which gives the
+// correctly rounded quotient (Markstein's theorem on division by a correctly rounded
+// reciprocal). The codes come from a product with an approximate 1 / s, rounded to an integer by
+// adding 1.5 2^23 in the same operation (conversions run at a sixteenth of its rate and made the
+// append compute-bound); products nearer than 1e-5 to a border between two codes, 20 times what
+// they can be off, send the lane through int4_exact_code.
+constexpr float kInt4Magic = 12582912.f;   // 1.5 * 2^23, bits 0x4b400000
+
+// The code of x in a group with minimum lo and scale s > 0, q its approximate (x - lo) / s: the
+// exact remainder decides, the rounding error of x - lo included.
+__device__ __forceinline__ uint32_t int4_exact_code(float x, float lo, float s, float q) {
+  const float k = fminf(floorf(q), 15.f);
+  const float d = x - lo, bb = d - x;              // x - lo = d + off exactly
+  const float off = (x - (d - bb)) + (-lo - bb);
+  const float rem = fmaf(-(k + 0.5f), s, d) + off;  // past the border if > 0
+  const uint32_t c = static_cast<uint32_t>(k);
+  return min(c + (rem > 0.f || (rem == 0.f && (c & 1u)) ? 1u : 0u), 15u);
+}
+
 __device__ __forceinline__ void int4_quantise(const uint4& h, uint32_t& codes, uint32_t& params) {
   const __half2* p = reinterpret_cast<const __half2*>(&h);
-  __half2 lo2 = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
-  __half2 hi2 = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+  const __half2 lo2 = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
+  const __half2 hi2 = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
   // (min, -max) in one register: one shuffle and one packed minimum per step
   __half2 mm = __halves2half2(__hmin_nan(__low2half(lo2), __high2half(lo2)),
                               __hneg(__hmax_nan(__low2half(hi2), __high2half(hi2))));
@@ -45,31 +60,40 @@ __device__ __forceinline__ void int4_quantise(const uint4& h, uint32_t& codes, u
     params = 0x7fff7fffu;
     return;
   }
-  const __half up = __float2half_ru(__fdiv_rn(range, 15.f));
-  const __half top = __float2half_rz(__fdiv_rn(65504.f - lo, 15.f));
-  const __half s = __hmin(up, top);
+  constexpr float kInv15 = 1.f / 15.f;
+  const float q15 = range * kInv15;
+  __half s = __float2half_ru(fmaf(fmaf(-15.f, q15, range), kInv15, q15));
+  float sf = __half2float(s);
+  if (fmaf(15.f, sf, lo) > 65504.f) {
+    s = __hmin(s, __float2half_rz(__fdiv_rn(65504.f - lo, 15.f)));
+    sf = __half2float(s);
+  }
   const __half2 sz = __halves2half2(s, __low2half(mm));
   params = *reinterpret_cast<const uint32_t*>(&sz);
-  const float sf = __half2float(s);
-  const float r = sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;   // at most 2^24: s is a multiple of 2^-24
-  codes = 0u;
+  const float r = sf > 0.f ? __fdividef(1.f, sf) : 0.f;   // s is a multiple of 2^-24
+  float x[8], off = 0.f;
+  uint32_t c = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(p[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float d = (e ? f.y : f.x) - lo;
-      const float q = d * r;
-      float k = rintf(q);
-      if (fabsf(q - k) > 0.5f - 1e-5f) {
-        k = floorf(q);
-        const float a = e ? f.y : f.x, bb = d - a;              // a - lo = d + off
-        const float off = (a - (d - bb)) + (-lo - bb);
-        const float rem = fmaf(-(k + 0.5f), sf, d) + off;       // over the border if > 0
-        if (rem > 0.f || (rem == 0.f && (static_cast<int>(k) & 1))) k += 1.f;
-      }
-      codes |= static_cast<uint32_t>(min(static_cast<int>(k), 15)) << (4 * (2 * i + e));
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float d = x[i] - lo;
+    const float m = fmaf(d, r, kInt4Magic);
+    off = fmaxf(off, fabsf(fmaf(d, r, kInt4Magic - m)));
+    c += __float_as_uint(m) << (4 * i);
+  }
+  // the magic number's own bits, shifted and summed
+  constexpr uint32_t kBias = 0x4b400000u + (0x4b400000u << 4) + (0x4b400000u << 8);
+  codes = c - kBias;
+  if (off > 0.5f - 1e-5f) {
+    codes = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      codes |= int4_exact_code(x[i], lo, sf, (x[i] - lo) * r) << (4 * i);
   }
 }
 
