@@ -11,9 +11,9 @@
 // round trips bound it. So one launch does it all: every CTA of one cluster scans all sequences
 // by itself (at most kMaxTableSeqs, in shared memory), then takes its share of the tokens and
 // blocks; the cluster barrier keeps the lengths and the stack's count, updated in place at the
-// end, from changing under a CTA that has not read them yet. Past kClusterTokens tokens one
-// cluster's 8 SMs no longer write fast enough, and a grid over the whole GPU does the tokens
-// first and a second launch the rest.
+// end, from changing under a CTA that has not read them yet. Past kClusterTokens tokens (or
+// kClusterBlocks table entries to cut) one cluster's 8 SMs no longer write fast enough: a grid
+// over the whole GPU does the tokens and blocks first and a second, one-CTA launch the rest.
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -25,7 +25,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kMaxTableSeqs = 4096;
 constexpr int kMaxCluster = 8;
-constexpr int kClusterTokens = 65536;
+constexpr int kClusterTokens = 32768;
+constexpr int kClusterBlocks = 16384;
 
 struct TableArgs {
   int32_t* tables;
@@ -37,7 +38,8 @@ struct TableArgs {
   int32_t* seqs;
   int64_t* positions;
   int32_t* cu;
-  int num_seqs, max_blocks, block_size, num_blocks, max_tokens;
+  int num_seqs, max_blocks, block_size, bs_shift, num_blocks, max_tokens;
+  bool vec;                  // the token arrays are 16-byte aligned
   unsigned int* err;
 };
 
@@ -61,6 +63,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // Exclusive sums of two 64-bit values over the CTA's threads, and their totals.
 __device__ __forceinline__ void cta_scan(int64_t& x, int64_t& y, int64_t& total_x,
                                          int64_t& total_y, int64_t (*part)[2]) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t ix = x, iy = y;
 #pragma unroll
@@ -71,16 +74,20 @@ __device__ __forceinline__ void cta_scan(int64_t& x, int64_t& y, int64_t& total_
   }
   if (lane == 31) { part[warp][0] = ix; part[warp][1] = iy; }
   __syncthreads();
-  int64_t bx = 0, by = 0;
-  total_x = total_y = 0;
+  // every warp scans the warps' sums by itself
+  int64_t px = lane < kWarps ? part[lane][0] : 0, py = lane < kWarps ? part[lane][1] : 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) { bx += part[w][0]; by += part[w][1]; }
-    total_x += part[w][0];
-    total_y += part[w][1];
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const int64_t ux = __shfl_up_sync(0xffffffffu, px, o);
+    const int64_t uy = __shfl_up_sync(0xffffffffu, py, o);
+    if (lane >= o) { px += ux; py += uy; }
   }
-  x = bx + ix - x;
-  y = by + iy - y;
+  total_x = __shfl_sync(0xffffffffu, px, kWarps - 1);
+  total_y = __shfl_sync(0xffffffffu, py, kWarps - 1);
+  const int64_t bx = __shfl_sync(0xffffffffu, px, max(warp - 1, 0));
+  const int64_t by = __shfl_sync(0xffffffffu, py, max(warp - 1, 0));
+  x = ix - x + (warp ? bx : 0);
+  y = iy - y + (warp ? by : 0);
 }
 
 // Largest b in [0, n) with first[b] <= x (first[0] = 0 <= x).
@@ -93,8 +100,8 @@ __device__ __forceinline__ int find(const int* first, int n, int x) {
   return lo;
 }
 
-__device__ __forceinline__ int blocks_of(int64_t tokens, int bs) {
-  return static_cast<int>((tokens + bs - 1) / bs);
+__device__ __forceinline__ int blocks_of(int64_t tokens, int shift) {
+  return static_cast<int>((tokens + (1 << shift) - 1) >> shift);
 }
 
 // TOKENS: the token arrays and the new table entries; STATE: lengths, count and error bits.
@@ -107,11 +114,11 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
   int* tok = smem;                       // first packed token of each sequence
   int* blk = tok + a.num_seqs + 1;       // first block (from the top of the stack)
   int* len = blk + a.num_seqs + 1;       // old length; -1: refused
-  const int n = a.num_seqs, bs = a.block_size;
+  const int n = a.num_seqs, sh = a.bs_shift;
   const int tid = threadIdx.x;
   const int rank = TOKENS && STATE ? cluster_rank() : blockIdx.x;
   const int ctas = TOKENS && STATE ? cluster_size() : gridDim.x;
-  const int64_t cap = static_cast<int64_t>(a.max_blocks) * bs;
+  const int64_t cap = static_cast<int64_t>(a.max_blocks) << sh;
   unsigned int bad = 0;
 
   int count = *a.free_count;
@@ -126,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
     const int ctx = a.lens[b], m = a.arg[b];
     const bool ok = ctx >= 0 && ctx <= cap && m >= 0 && ctx + static_cast<int64_t>(m) <= cap;
     x += max(m, 0);
-    if (ok) y += blocks_of(ctx + static_cast<int64_t>(m), bs) - blocks_of(ctx, bs);
+    if (ok) y += blocks_of(ctx + static_cast<int64_t>(m), sh) - blocks_of(ctx, sh);
   }
   int64_t total_x, total_y;
   cta_scan(x, y, total_x, total_y, part);
@@ -142,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
       bad |= PKV_DEVERR_POSITION;
       ok = false;
     } else {
-      need = blocks_of(ctx + static_cast<int64_t>(m), bs) - blocks_of(ctx, bs);
+      need = blocks_of(ctx + static_cast<int64_t>(m), sh) - blocks_of(ctx, sh);
     }
     tok[b] = static_cast<int>(min(x, static_cast<int64_t>(a.max_tokens)));
     blk[b] = static_cast<int>(min(y, static_cast<int64_t>(0x7fffffff)));
@@ -166,28 +173,46 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
   if (TOKENS && STATE) cluster_arrive();   // this CTA has read the lengths and the count
 
   if (TOKENS) {
-    // ---- the new tokens, and the padding behind them ----
-    for (int64_t i = static_cast<int64_t>(rank) * kThreads + tid; i < a.max_tokens;
-         i += static_cast<int64_t>(ctas) * kThreads) {
-      int64_t slot = -1, pos = -1;
-      int seq = -1;
-      if (i < live) {
-        const int b = find(tok, n, static_cast<int>(i));
-        if (len[b] >= 0) {
-          seq = b;
-          pos = len[b] + (i - tok[b]);
-          const int lb = static_cast<int>(pos / bs), held = blocks_of(len[b], bs);
-          const int id = lb < held ? a.tables[static_cast<int64_t>(b) * a.max_blocks + lb]
-                                   : a.free_blocks[count - 1 - (blk[b] + lb - held)];
-          if (id >= 0 && id < a.num_blocks)
-            slot = static_cast<int64_t>(id) * bs + (pos - static_cast<int64_t>(lb) * bs);
-          else
-            bad |= PKV_DEVERR_BLOCK_ID;
+    // ---- the new tokens, and the padding behind them, four neighbours a thread ----
+    for (int64_t i0 = 4 * (static_cast<int64_t>(rank) * kThreads + tid); i0 < a.max_tokens;
+         i0 += 4 * static_cast<int64_t>(ctas) * kThreads) {
+      int64_t slot[4], pos[4];
+      int seq[4];
+      int b = i0 < live ? find(tok, n, static_cast<int>(i0)) : n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t i = i0 + e;
+        slot[e] = pos[e] = -1;
+        seq[e] = -1;
+        if (i >= live) continue;
+        while (tok[b + 1] <= i) ++b;
+        const int ctx = len[b];
+        if (ctx < 0) continue;
+        seq[e] = b;
+        pos[e] = ctx + (i - tok[b]);
+        const int lb = static_cast<int>(pos[e] >> sh), held = blocks_of(ctx, sh);
+        const int id = lb < held ? a.tables[static_cast<int64_t>(b) * a.max_blocks + lb]
+                                 : a.free_blocks[count - 1 - (blk[b] + lb - held)];
+        if (id >= 0 && id < a.num_blocks)
+          slot[e] = (static_cast<int64_t>(id) << sh) + (pos[e] & ((1 << sh) - 1));
+        else
+          bad |= PKV_DEVERR_BLOCK_ID;
+      }
+      if (a.vec && i0 + 4 <= a.max_tokens) {
+        longlong2* s2 = reinterpret_cast<longlong2*>(a.slots + i0);
+        longlong2* p2 = reinterpret_cast<longlong2*>(a.positions + i0);
+        s2[0] = make_longlong2(slot[0], slot[1]);
+        s2[1] = make_longlong2(slot[2], slot[3]);
+        p2[0] = make_longlong2(pos[0], pos[1]);
+        p2[1] = make_longlong2(pos[2], pos[3]);
+        *reinterpret_cast<int4*>(a.seqs + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+      } else {
+        for (int e = 0; e < 4 && i0 + e < a.max_tokens; ++e) {
+          a.slots[i0 + e] = slot[e];
+          a.seqs[i0 + e] = seq[e];
+          a.positions[i0 + e] = pos[e];
         }
       }
-      a.slots[i] = slot;
-      a.seqs[i] = seq;
-      a.positions[i] = pos;
     }
     // ---- the new table entries ----
     for (int k = rank * kThreads + tid; k < used; k += ctas * kThreads) {
@@ -195,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
       if (len[b] < 0) continue;
       const int id = a.free_blocks[count - 1 - k];
       if (id < 0 || id >= a.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
-      a.tables[static_cast<int64_t>(b) * a.max_blocks + blocks_of(len[b], bs) + (k - blk[b])] = id;
+      a.tables[static_cast<int64_t>(b) * a.max_blocks + blocks_of(len[b], sh) + (k - blk[b])] = id;
     }
     for (int b = rank * kThreads + tid; b <= n; b += ctas * kThreads) a.cu[b] = tok[b];
   }
@@ -208,16 +233,19 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
   }
 }
 
-// Shared memory: blk[n + 1], keep[n].
+// BLOCKS: the table entries and the stack; STATE: lengths and count. Shared memory: blk[n + 1],
+// keep[n].
+template <bool BLOCKS, bool STATE>
 __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
   extern __shared__ int smem[];
   __shared__ int64_t part[kThreads / 32][2];
   int* blk = smem;                       // first freed block of each sequence
   int* keep = blk + a.num_seqs + 1;      // length kept; -1: as it is
-  const int n = a.num_seqs, bs = a.block_size;
+  const int n = a.num_seqs, sh = a.bs_shift;
   const int tid = threadIdx.x;
-  const int rank = cluster_rank(), ctas = cluster_size();
-  const int64_t cap = static_cast<int64_t>(a.max_blocks) * bs;
+  const int rank = BLOCKS && STATE ? cluster_rank() : blockIdx.x;
+  const int ctas = BLOCKS && STATE ? cluster_size() : gridDim.x;
+  const int64_t cap = static_cast<int64_t>(a.max_blocks) << sh;
   unsigned int bad = 0;
 
   int count = *a.free_count;
@@ -227,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
   int64_t x = 0, unused = 0;
   for (int b = b0; b < b1; ++b) {
     const int ctx = a.lens[b], m = a.arg[b];
-    if (ctx >= 0 && ctx <= cap && m >= 0 && m < ctx) x += blocks_of(ctx, bs) - blocks_of(m, bs);
+    if (ctx >= 0 && ctx <= cap && m >= 0 && m < ctx) x += blocks_of(ctx, sh) - blocks_of(m, sh);
   }
   int64_t total, total_unused;
   cta_scan(x, unused, total, total_unused, part);
@@ -239,41 +267,46 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
     if (!known) bad |= PKV_DEVERR_CONTEXT;
     const bool cut = known && m >= 0 && m < ctx;
     blk[b] = fits ? static_cast<int>(x) : 0;
-    if (cut) x += blocks_of(ctx, bs) - blocks_of(m, bs);
+    if (cut) x += blocks_of(ctx, sh) - blocks_of(m, sh);
     keep[b] = cut && fits ? m : -1;
   }
   const int freed = fits ? static_cast<int>(total) : 0;
   if (tid == 0) blk[n] = freed;
   __syncthreads();
-  cluster_arrive();   // this CTA has read the lengths and the count
+  if (BLOCKS && STATE) cluster_arrive();   // this CTA has read the lengths and the count
 
-  for (int k = rank * kThreads + tid; k < freed; k += ctas * kThreads) {
-    const int b = find(blk, n, k);
-    int32_t* entry =
-        a.tables + static_cast<int64_t>(b) * a.max_blocks + blocks_of(keep[b], bs) + (k - blk[b]);
-    const int id = *entry;
-    if (id < 0 || id >= a.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
-    a.free_blocks[count + freed - 1 - k] = id;
-    *entry = -1;
+  if (BLOCKS) {
+    for (int k = rank * kThreads + tid; k < freed; k += ctas * kThreads) {
+      const int b = find(blk, n, k);
+      int32_t* entry = a.tables + static_cast<int64_t>(b) * a.max_blocks +
+                       blocks_of(keep[b], sh) + (k - blk[b]);
+      const int id = *entry;
+      if (id < 0 || id >= a.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
+      a.free_blocks[count + freed - 1 - k] = id;
+      *entry = -1;
+    }
   }
   if (bad) atomicOr(a.err, bad);
-  cluster_wait();
-  for (int b = rank * kThreads + tid; b < n; b += ctas * kThreads)
-    if (keep[b] >= 0) a.lens[b] = keep[b];
-  if (rank == 0 && tid == 0 && freed > 0) *a.free_count = count + freed;
+  if (STATE) {
+    if (BLOCKS) cluster_wait();
+    for (int b = rank * kThreads + tid; b < n; b += ctas * kThreads)
+      if (keep[b] >= 0) a.lens[b] = keep[b];
+    if (rank == 0 && tid == 0 && freed > 0) *a.free_count = count + freed;
+  }
 }
 
 int launch_status() { return cuda_status(cudaGetLastError()); }
 
-int launch_cluster(const void* fn, const TableArgs& a, size_t smem, int cluster,
-                   cudaStream_t stream) {
+// `cluster` > 0: one cluster of that many CTAs; 0: `ctas` CTAs on their own.
+int launch(const void* fn, const TableArgs& a, size_t smem, int cluster, int ctas,
+           cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
+  if (smem > 47 * 1024)   // past the default limit, beside the kernels' own 300 bytes
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+                             static_cast<int>((3 * kMaxTableSeqs + 2) * sizeof(int)));
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster);
+  cfg.gridDim = dim3(cluster ? cluster : ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -283,9 +316,15 @@ int launch_cluster(const void* fn, const TableArgs& a, size_t smem, int cluster,
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster ? 1 : 0;
   void* params[1] = {const_cast<TableArgs*>(&a)};
   return cuda_status(cudaLaunchKernelExC(&cfg, fn, params));
+}
+
+int log2_of(int n) {
+  int s = 0;
+  while ((1 << s) < n) ++s;
+  return s;
 }
 
 int cluster_for(int64_t items, int per_cta) {
@@ -318,27 +357,23 @@ int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_
   if ((num_seqs > 0 && (!context_lens || !new_lens || !block_tables)) || !free_blocks ||
       !free_count || !cu_new_lens || (max_tokens > 0 && (!slot_out || !seq_out || !position_out)))
     return PKV_EINVAL;
+  const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
   TableArgs a = {block_tables, context_lens, new_lens, free_blocks, free_count, slot_out, seq_out,
-                 position_out, cu_new_lens, num_seqs, max_blocks_per_seq, block_size, num_blocks,
-                 max_tokens, device_error_ptr()};
+                 position_out, cu_new_lens, num_seqs, max_blocks_per_seq, block_size,
+                 log2_of(block_size), num_blocks, max_tokens,
+                 ((at(slot_out) | at(seq_out) | at(position_out)) & 15u) == 0, device_error_ptr()};
   if (!a.err) return launch_status();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t smem = (3 * static_cast<size_t>(num_seqs) + 2) * sizeof(int);
   if (max_tokens <= kClusterTokens)
-    return launch_cluster(reinterpret_cast<const void*>(&extend_kernel<true, true>), a, smem,
-                          cluster_for(max_tokens, 2 * kThreads), s);
-  const int ctas = std::min(2 * sm_count(), (max_tokens + kThreads - 1) / kThreads);
+    return launch(reinterpret_cast<const void*>(&extend_kernel<true, true>), a, smem,
+                  cluster_for(max_tokens, 4 * kThreads), 0, s);
+  const int ctas = std::min(2 * sm_count(), (max_tokens / 4 + kThreads) / kThreads);
   if (ctas < 1) return launch_status();
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(&extend_kernel<true, false>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return cuda_status(e);
-  }
-  extend_kernel<true, false><<<ctas, kThreads, smem, s>>>(a);
-  const int st = launch_status();
+  const int st =
+      launch(reinterpret_cast<const void*>(&extend_kernel<true, false>), a, smem, 0, ctas, s);
   if (st != PKV_OK) return st;
-  return launch_cluster(reinterpret_cast<const void*>(&extend_kernel<false, true>), a, smem, 1, s);
+  return launch(reinterpret_cast<const void*>(&extend_kernel<false, true>), a, smem, 0, 1, s);
 }
 
 int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* keep_lens,
@@ -350,14 +385,23 @@ int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int3
   if (!block_tables || !context_lens || !keep_lens || !free_blocks || !free_count)
     return PKV_EINVAL;
   TableArgs a = {block_tables, context_lens, keep_lens, free_blocks, free_count, nullptr, nullptr,
-                 nullptr, nullptr, num_seqs, max_blocks_per_seq, block_size, num_blocks, 0,
-                 device_error_ptr()};
+                 nullptr, nullptr, num_seqs, max_blocks_per_seq, block_size, log2_of(block_size),
+                 num_blocks, 0, false, device_error_ptr()};
   if (!a.err) return launch_status();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t smem = (2 * static_cast<size_t>(num_seqs) + 1) * sizeof(int);
-  return launch_cluster(reinterpret_cast<const void*>(&truncate_kernel), a, smem,
-                        cluster_for(static_cast<int64_t>(num_seqs) * max_blocks_per_seq,
-                                    16 * kThreads),
-                        static_cast<cudaStream_t>(stream));
+  // at most this many entries leave the tables
+  const int64_t most = std::min<int64_t>(static_cast<int64_t>(num_seqs) * max_blocks_per_seq,
+                                         num_blocks);
+  if (most <= kClusterBlocks)
+    return launch(reinterpret_cast<const void*>(&truncate_kernel<true, true>), a, smem,
+                  cluster_for(most, 4 * kThreads), 0, s);
+  const int ctas = std::min<int64_t>(sm_count(), (most + kThreads - 1) / kThreads);
+  if (ctas < 1) return launch_status();
+  const int st =
+      launch(reinterpret_cast<const void*>(&truncate_kernel<true, false>), a, smem, 0, ctas, s);
+  if (st != PKV_OK) return st;
+  return launch(reinterpret_cast<const void*>(&truncate_kernel<false, true>), a, smem, 0, 1, s);
 }
 
 }  // extern "C"

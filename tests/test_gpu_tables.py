@@ -44,6 +44,7 @@ def _extend(tables, lens, new, bs, free, count, max_tokens, want_error=0):
 @pytest.mark.parametrize("B,bs,hi,new", [
     (1, 16, 0, 1), (1, 16, 40, 1), (3, 16, 40, 17), (64, 16, 2048, 1), (64, 64, 500, 5),
     (700, 32, 100, 40), (4096, 16, 60, 3), (2, 256, 1000, 60000), (300, 16, 64, 1000),
+    (100, 16, 3000, 4000),      # more than 16384 blocks: the wide forms of both calls
 ])
 def test_extend_and_back(B, bs, hi, new):
     rng = np.random.default_rng(B + bs)
