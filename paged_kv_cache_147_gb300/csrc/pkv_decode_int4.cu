@@ -17,7 +17,7 @@
 //    warp for all (tensor tiles or bulk copies, an mbarrier pair per stage) took ~450 ns a stage
 //    whatever its size, which bounded the kernel at 3 TB/s.
 //  * Transposed tile: S^T = K Q^T and O^T = V^T P^T, keys (and output dims) on the mma's 16-row
-//    side, query rows in tiles of 8 columns (NT of them a warp).
+//    side, 8 query rows on its 8 columns.
 //  * Four bits at bits 0-3 (4-7) of a 16-bit half are the fp16 subnormal c 2^-24 (c 2^-20),
 //    exactly, and the products' sums are fp32: one AND of a word or of the word shifted by 8
 //    makes an mma operand of two codes.
@@ -40,8 +40,9 @@
 //    (p <= 4, p s <= 4 x 8736) for the rest of the segment.
 //  * Tokens past the context hold anything: their scores are masked and their (s, z) of V set
 //    to zero.
-//  * More than 16 rows: two warps take a stage, each with half of the row tiles (and its own
-//    copy, the second of which comes from L2).
+//  * More than 8 rows: two to four warps take a stage, 8 rows each (and a copy of their own; all
+//    but the first come from L2). Two row tiles in one warp save the second masking of the codes
+//    but not the registers: with two, four drafts of 6 heads took 36 us, with one 27.
 #include <cuda_fp16.h>
 
 #include "pkv_decode_common.cuh"
@@ -54,27 +55,29 @@ namespace {
 
 constexpr int kTile = kChunk * kInt4Row;     // one chunk's K (or V): 1280 bytes
 constexpr int kStage4 = 4 * kTile;           // K of two chunks, V of two chunks
-#ifndef SEG4
-#define SEG4 12
-#endif
-constexpr int kSeg4 = SEG4;                     // per-segment cost in chunks (see kSegCost)
+// Per-segment cost in chunks (see kSegCost): queries, hand-off and merge of a segment take a CTA
+// ~1.5 us, the time of a dozen chunks (70B mixed lengths: 62 us with 4, 55 with 8, 51 with 12).
+constexpr int kSeg4 = 12;
 // How far the softmax's reference stays below the running maximum (see above), and how far a
 // weight may grow past the maximum it was taken at before the reference moves.
 constexpr float kShift = 11.f, kGrow = 2.f;
+// Stages after which a warp's sums move to its state buffer. The tensor cores' fp32 sums truncate,
+// and the two large sums that make a value's (of p s c and of p z) do not lose alike: over 100
+// stages a warp (16384 tokens) their difference was off by 6.7e-4 relative, over 20 by 2.9e-4,
+// near what the rounded weights and output alone cost (2.6e-4); moving them costs 3 % of the time.
+constexpr int kFlush = 20;
 
-// Shared-memory layout (offsets from a 1024-byte aligned base). NCS: warps that share the stages
-// among them, RS: warps that take one stage (row halves), ND: stages in flight per warp, SB:
-// buffers of segment states.
-template <int NCS, int RS, int ND, int NT, int SB>
+// Shared-memory layout (offsets from a 128-byte aligned base). NCS: warps that share the stages
+// among them, RS: warps that take one stage, 8 query rows each, ND: stages in flight per warp.
+template <int NCS, int RS, int ND>
 struct Smem4 {
-  static constexpr int kRows = 8 * RS * NT;
-  static constexpr int kQTile = 5 * 512;              // fragments of 4 groups, row constants
-  static constexpr int kQBuf = RS * NT * kQTile;
+  static constexpr int kQTile = 5 * 512;              // 8 rows: fragments of 4 groups, constants
+  static constexpr int kQBuf = RS * kQTile;
   static constexpr int kQ = NCS * RS * ND * kStage4;
-  static constexpr int kBars = kQ + 2 * kQBuf;        // qfull, qempty, sdone, sfree: 2 each
-  static constexpr int kFlags = kBars + 8 * 8;
-  static constexpr int kState = (kFlags + 64 + 15) & ~15;
-  __host__ __device__ static int state_floats(int R) { return SB * NCS * R * (kSt + 2); }
+  static constexpr int kBars = kQ + 2 * kQBuf;        // qfull[2], qempty[2], sdone, sfree
+  static constexpr int kFlags = kBars + 6 * 8;
+  static constexpr int kState = (kFlags + 64 + 15) & ~15;   // [NCS] segment states
+  __host__ __device__ static int state_floats(int R) { return NCS * R * (kSt + 2); }
   __host__ __device__ static int seq_off(int R) { return kState + state_floats(R) * 4; }
   __host__ __device__ static int newkv_off(int R, int B) {
     return (seq_off(R) + (2 * B + 1) * 4 + 127) & ~127;
@@ -83,7 +86,7 @@ struct Smem4 {
     return 128 + static_cast<size_t>(newkv_off(R, B)) + static_cast<size_t>(newkv_bytes);
   }
   // the merge of split units stages at least two partials in the stage memory
-  static_assert(kQ >= kRows * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
+  static_assert(kQ >= 8 * RS * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
 };
 
 // A warp's walk over the stages it loads: stage jp of a segment goes to warp (jp + stages before
@@ -191,13 +194,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 
 // Warps 0 .. NCS RS - 1 consume; the next one prepares the queries, the last one is the epilogue
-// (merges each segment's per-warp states, writes outputs and split units' partials). QR: the query
-// fragments stay in the consumers' registers (else they are read from shared memory per stage,
-// which leaves registers for more warps).
-template <int NCS, int RS, int ND, int NT, int SB, int QR, int MINB, bool APPEND>
+// (merges each segment's per-warp states, writes outputs and split units' partials).
+template <int NCS, int RS, int ND, int MINB, bool APPEND>
 __global__ void __launch_bounds__((NCS * RS + 2) * 32, MINB)
 decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
-  using L = Smem4<NCS, RS, ND, NT, SB>;
+  using L = Smem4<NCS, RS, ND>;
   constexpr int NCW = NCS * RS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -206,14 +207,14 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
   const uint32_t bar_qfull = sbase + L::kBars;
   const uint32_t bar_qempty = bar_qfull + 2 * 8;
   const uint32_t bar_sdone = bar_qempty + 2 * 8;
-  const uint32_t bar_sfree = bar_sdone + 2 * 8;
+  const uint32_t bar_sfree = bar_sdone + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kFlags);
   int* npend_s = reinterpret_cast<int*>(smem + L::kFlags) + 1;   // then 2 x (b, h, nb)
   volatile int* fast_s = reinterpret_cast<volatile int*>(smem + L::kFlags) + 8;
   int* longest_s = reinterpret_cast<int*>(smem + L::kFlags) + 9;
-  float* stO = reinterpret_cast<float*>(smem + L::kState);       // [SB][NCS][R][kSt]
-  float* stM = stO + SB * NCS * a.R * kSt;                        // [SB][NCS][R]
-  float* stL = stM + SB * NCS * a.R;                              // [SB][NCS][R]
+  float* stO = reinterpret_cast<float*>(smem + L::kState);       // [NCS][R][kSt]
+  float* stM = stO + NCS * a.R * kSt;                             // [NCS][R]
+  float* stL = stM + NCS * a.R;                                   // [NCS][R]
   int* pre = reinterpret_cast<int*>(smem + L::seq_off(a.R));
   int* slen = pre + a.num_seqs + 1;
 
@@ -227,9 +228,9 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_qfull + s * 8, 1);
       mbar_init(bar_qempty + s * 8, NCW);
-      mbar_init(bar_sdone + s * 8, NCW);
-      mbar_init(bar_sfree + s * 8, 1);
     }
+    mbar_init(bar_sdone, NCW);
+    mbar_init(bar_sfree, 1);
     *abort = 0;
     *npend_s = 0;
     *longest_s = 0;
@@ -389,16 +390,14 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
       int npend = 0, k = 0;
       Seg nx = s;
       while (cur.next(nx)) {
-        const int sb = k % SB;
-        if (!mbar_wait(bar_sdone + sb * 8, (k / SB) & 1, abort)) flag_timeout(a, abort);
+        if (!mbar_wait(bar_sdone, k & 1, abort)) flag_timeout(a, abort);
         const bool complete = (s.c0 == 0 && s.c1 == s.nb);
         const int slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
-        merge_segment<NCS, 32>(a, stO + sb * NCS * a.R * kSt, stM + sb * NCS * a.R,
-                               stL + sb * NCS * a.R, s.b, s.h, complete,
+        merge_segment<NCS, 32>(a, stO, stM, stL, s.b, s.h, complete,
                                a.part_o + static_cast<int64_t>(slot) * a.R * kD,
                                a.part_ml + static_cast<int64_t>(slot) * a.R * 4, lane);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sfree + sb * 8);
+        if (lane == 0) mbar_arrive(bar_sfree);
         if (!complete && lane == 0) {
           // announce the partial (release) and see who else has arrived (acquire)
           const int ua = unit_first<kSeg4>(pre, a.Hkv, s.b, s.h, s.nb);
@@ -418,7 +417,7 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
     }
   } else {
     // =================================== consumers ===========================================
-    const int w = warp % NCS, rs = warp / NCS;   // share of the stages, half of the rows
+    const int w = warp % NCS, rs = warp / NCS;   // share of the stages, query rows 8 rs .. + 7
     // ldmatrix row addresses: matrices 0, 1 the two key octets of 16 bytes, 2, 3 of the next 16
     // (codes), or the two octets of the next chunk (scales and minima)
     const uint32_t lm_row = ((lane >> 3) & 1) * 8 * kInt4Row + (lane & 7) * kInt4Row;
@@ -436,305 +435,265 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
     bool has = cur.first(begin, s);
     while (has) {
       const int qs = k & 1;
-      const uint32_t qb = sbase + L::kQ + qs * L::kQBuf + rs * NT * L::kQTile + lane * 16;
+      const uint32_t qb = sbase + L::kQ + qs * L::kQBuf + rs * L::kQTile + lane * 16;
       if (!mbar_wait(bar_qfull + qs * 8, (k >> 1) & 1, abort)) flag_timeout(a, abort);
       const int Lc = slen[s.b];
-      uint4 qf[QR ? NT : 1][QR ? 4 : 1];
-      uint32_t qzh[NT], qzl[NT];
-      float rsc[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if constexpr (QR != 0) {
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr)
-            qf[nt][gr] = ld_shared_v4(qb + nt * L::kQTile + gr * 512);
-        }
-        const uint4 v = ld_shared_v4(qb + nt * L::kQTile + 2048);
-        qzh[nt] = v.x;
-        qzl[nt] = v.y;
-        rsc[nt][0] = __uint_as_float(v.z);
-        rsc[nt][1] = __uint_as_float(v.w);
-      }
+      // the sums of group t4; what makes scores of rows 2 t4, 2 t4 + 1 from the products
+      const uint4 qc = ld_shared_v4(qb + 2048);
+      const float rsc[2] = {__uint_as_float(qc.z), __uint_as_float(qc.w)};
 
       // per row: the reference's negative (0 before the first score), the product above which it
       // moves, the sum of the weights
-      float nm[NT][2], thr[NT][2], tl[NT][2], ot[NT][4][2][4], oz[NT][4];
-      int qis[NT];   // query tokens of rows 2 t4 (low half), 2 t4 + 1
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          nm[nt][e] = tl[nt][e] = 0.f;
-          thr[nt][e] = kNegInf;
-        }
-        const int r0 = 8 * (NT * rs + nt) + 2 * t4;
-        qis[nt] = min(r0 / a.G, a.q_len - 1) | (min((r0 + 1) / a.G, a.q_len - 1) << 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          oz[nt][i] = 0.f;
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr) ot[nt][gr][0][i] = ot[nt][gr][1][i] = 0.f;
-        }
-      }
+      float nm[2] = {0.f, 0.f}, thr[2] = {kNegInf, kNegInf}, tl[2] = {0.f, 0.f};
+      float ot[4][2][4], oz[4];
+      const int r0 = 8 * rs + 2 * t4;
+      // query tokens of rows 2 t4 (low half), 2 t4 + 1
+      const int qis = min(r0 / a.G, a.q_len - 1) | (min((r0 + 1) / a.G, a.q_len - 1) << 16);
       float shift = kShift;   // the same for all lanes
 
       const int nchunk = s.c1 - s.c0;
       const int npair = (nchunk + 1) >> 1;
-      for (int jp = ((w - j) % NCS + NCS) % NCS; jp < npair; jp += NCS) {
-        cp_async_wait<ND - 1>();
-        __syncwarp();                        // every lane's copies of this stage are in
-        const uint32_t stK = ring + slot * kStage4;
-        const uint32_t stV = stK + 2 * kTile;
-        const int c = s.c0 + 2 * jp;
-        const bool two = c + 1 < s.c1;
-        const int nk = two ? 2 * kChunk : kChunk;
-        const bool full = two && (c + 2) * kChunk <= Lc - a.q_len + 1;
-        if (APPEND && (c * kChunk + nk > Lc - a.q_len)) {
-          // new rows of these chunks: lanes 0-15 quantise the K row, 16-31 the V row, into the
-          // stage's tiles and into the pool (warps that share a stage write the same bytes)
-          const int first_new = Lc - a.q_len;
-          const uint32_t nkv = sbase + L::newkv_off(a.R, B) + qs * a.q_len * 512;
-          const int which = lane >> 4, p = lane & 15;
-          for (int i = 0; i < a.q_len; ++i) {
-            const int pos = first_new + i;
-            const int tk = pos - c * kChunk;
-            if (pos < 0 || tk < 0 || tk >= nk) continue;
-            uint32_t codes, params;
-            int4_quantise(ld_shared_v4(nkv + i * 512 + which * 256 + p * 16), codes, params);
-            const uint32_t row = stK + which * 2 * kTile + tk * kInt4Row;
-            st_shared_u32(row + 4 * p, codes);
-            if ((p & 3) == 0) st_shared_u32(row + kInt4Params + p, params);
-            const int id =
-                __ldg(a.block_tables + static_cast<int64_t>(s.b) * a.max_blocks + pos / a.block_size);
-            if (id >= 0 && id < a.num_blocks) {
-              const int64_t prow = (static_cast<int64_t>(id) * a.Hkv + s.h) * a.block_size +
-                                   pos % a.block_size;
-              uint32_t* pool = reinterpret_cast<uint32_t*>(
-                  reinterpret_cast<uint8_t*>(which ? a.v_pool : a.k_pool) + prow * kInt4Row);
-              pool[p] = codes;
-              if ((p & 3) == 0) pool[(kInt4Params + p) / 4] = params;
-            }
-          }
-          __syncwarp();
+      int jp = ((w - j) % NCS + NCS) % NCS;
+      bool held = false;      // the state buffer holds what this segment's earlier stages gave
+      do {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          oz[i] = 0.f;
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr) ot[gr][0][i] = ot[gr][1][i] = 0.f;
         }
-
-        // ---- S^T = K Q^T, 16 keys (g, g + 8) at a time ----
-        float x[NT][2][4];   // [tile][chunk h][key g: rows 2 t4, + 1; key g + 8: the same]
-        uint32_t kz[4];      // (s, z) of group t4: keys g, g + 8 of both chunks
-        ldsm_x4(stK + lm_par, kz[0], kz[1], kz[2], kz[3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t kb = stK + h * kTile;
-          uint32_t kw[4][2];
-          ldsm_x4(kb + lm_codes, kw[0][0], kw[0][1], kw[1][0], kw[1][1]);
-          ldsm_x4(kb + lm_codes + 32, kw[2][0], kw[2][1], kw[3][0], kw[3][1]);
-          const uint4 p0 = ld_shared_v4(kb + g * kInt4Row + kInt4Params);
-          const uint4 p1 = ld_shared_v4(kb + (g + 8) * kInt4Row + kInt4Params);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            x[nt][h][0] = x[nt][h][1] = x[nt][h][2] = x[nt][h][3] = 0.f;
-            mma_f16(x[nt][h], kz[2 * h], kz[2 * h + 1], kz[2 * h], kz[2 * h + 1], qzh[nt], qzl[nt]);
+        for (int left = kFlush; left > 0 && jp < npair; --left, jp += NCS) {
+          cp_async_wait<ND - 1>();
+          __syncwarp();                        // every lane's copies of this stage are in
+          const uint32_t stK = ring + slot * kStage4;
+          const uint32_t stV = stK + 2 * kTile;
+          const int c = s.c0 + 2 * jp;
+          const bool two = c + 1 < s.c1;
+          const int nk = two ? 2 * kChunk : kChunk;
+          const bool full = two && (c + 2) * kChunk <= Lc - a.q_len + 1;
+          if (APPEND && (c * kChunk + nk > Lc - a.q_len)) {
+            // new rows of these chunks: lanes 0-15 quantise the K row, 16-31 the V row, into the
+            // stage's tiles and into the pool (warps that share a stage write the same bytes)
+            const int first_new = Lc - a.q_len;
+            const uint32_t nkv = sbase + L::newkv_off(a.R, B) + qs * a.q_len * 512;
+            const int which = lane >> 4, p = lane & 15;
+            for (int i = 0; i < a.q_len; ++i) {
+              const int pos = first_new + i;
+              const int tk = pos - c * kChunk;
+              if (pos < 0 || tk < 0 || tk >= nk) continue;
+              uint32_t codes, params;
+              int4_quantise(ld_shared_v4(nkv + i * 512 + which * 256 + p * 16), codes, params);
+              const uint32_t row = stK + which * 2 * kTile + tk * kInt4Row;
+              st_shared_u32(row + 4 * p, codes);
+              if ((p & 3) == 0) st_shared_u32(row + kInt4Params + p, params);
+              const int id = __ldg(a.block_tables + static_cast<int64_t>(s.b) * a.max_blocks +
+                                   pos / a.block_size);
+              if (id >= 0 && id < a.num_blocks) {
+                const int64_t prow = (static_cast<int64_t>(id) * a.Hkv + s.h) * a.block_size +
+                                     pos % a.block_size;
+                uint32_t* pool = reinterpret_cast<uint32_t*>(
+                    reinterpret_cast<uint8_t*>(which ? a.v_pool : a.k_pool) + prow * kInt4Row);
+                pool[p] = codes;
+                if ((p & 3) == 0) pool[(kInt4Params + p) / 4] = params;
+              }
+            }
+            __syncwarp();
           }
-          // two groups at a time: their products do not wait on each other
+
+          // ---- S^T = K Q^T, 16 keys (g, g + 8) at a time ----
+          float x[2][4];       // [chunk h][key g: rows 2 t4, + 1; key g + 8: the same]
+          uint32_t kz[4];      // (s, z) of group t4: keys g, g + 8 of both chunks
+          ldsm_x4(stK + lm_par, kz[0], kz[1], kz[2], kz[3]);
 #pragma unroll
-          for (int gp = 0; gp < 4; gp += 2) {
-            float t[NT][2][4];
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t kb = stK + h * kTile;
+            uint32_t kw[4][2];
+            ldsm_x4(kb + lm_codes, kw[0][0], kw[0][1], kw[1][0], kw[1][1]);
+            ldsm_x4(kb + lm_codes + 32, kw[2][0], kw[2][1], kw[3][0], kw[3][1]);
+            const uint4 p0 = ld_shared_v4(kb + g * kInt4Row + kInt4Params);
+            const uint4 p1 = ld_shared_v4(kb + (g + 8) * kInt4Row + kInt4Params);
+            x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.f;
+            mma_f16(x[h], kz[2 * h], kz[2 * h + 1], kz[2 * h], kz[2 * h + 1], qc.x, qc.y);
+            // two groups at a time: their products do not wait on each other
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              const uint32_t m = part ? 0x00f000f0u : 0x000f000fu;
+            for (int gp = 0; gp < 4; gp += 2) {
+              float t[2][4];
 #pragma unroll
-              for (int j2 = 0; j2 < 2; ++j2) {
-                const uint32_t w0 = kw[gp + j2][0], w1 = kw[gp + j2][1];
+              for (int part = 0; part < 2; ++part) {
+                const uint32_t m = part ? 0x00f000f0u : 0x000f000fu;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  uint2 b;
-                  if constexpr (QR != 0) {
-                    const uint4 q4 = qf[nt][gp + j2];
-                    b = part ? make_uint2(q4.z, q4.w) : make_uint2(q4.x, q4.y);
-                  } else {
-                    b = ld_shared_v2(qb + nt * L::kQTile + (gp + j2) * 512 + part * 8);
-                  }
-                  if (part == 0) t[nt][j2][0] = t[nt][j2][1] = t[nt][j2][2] = t[nt][j2][3] = 0.f;
-                  mma_f16(t[nt][j2], w0 & m, w1 & m, (w0 >> 8) & m, (w1 >> 8) & m, b.x, b.y);
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t w0 = kw[gp + i][0], w1 = kw[gp + i][1];
+                  const uint2 b = ld_shared_v2(qb + (gp + i) * 512 + part * 8);
+                  if (part == 0) t[i][0] = t[i][1] = t[i][2] = t[i][3] = 0.f;
+                  mma_f16(t[i], w0 & m, w1 & m, (w0 >> 8) & m, (w1 >> 8) & m, b.x, b.y);
                 }
               }
-            }
 #pragma unroll
-            for (int j2 = 0; j2 < 2; ++j2) {
-              const float s0 = __low2float(as_half2(u4_word(p0, gp + j2)));
-              const float s1 = __low2float(as_half2(u4_word(p1, gp + j2)));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                x[nt][h][0] = fmaf(s0, t[nt][j2][0], x[nt][h][0]);
-                x[nt][h][1] = fmaf(s0, t[nt][j2][1], x[nt][h][1]);
-                x[nt][h][2] = fmaf(s1, t[nt][j2][2], x[nt][h][2]);
-                x[nt][h][3] = fmaf(s1, t[nt][j2][3], x[nt][h][3]);
+              for (int i = 0; i < 2; ++i) {
+                const float s0 = __low2float(as_half2(u4_word(p0, gp + i)));
+                const float s1 = __low2float(as_half2(u4_word(p1, gp + i)));
+                x[h][0] = fmaf(s0, t[i][0], x[h][0]);
+                x[h][1] = fmaf(s0, t[i][1], x[h][1]);
+                x[h][2] = fmaf(s1, t[i][2], x[h][2]);
+                x[h][3] = fmaf(s1, t[i][3], x[h][3]);
               }
             }
           }
-        }
 
-        // ---- V's scales and minima: half g of each key's eight, for keys 2 t4, 2 t4 + 1 of the
-        // two octets of both chunks ----
-        uint32_t vp[2][2];
-        ldsm_x4_trans(stV + lm_par, vp[0][0], vp[0][1], vp[1][0], vp[1][1]);
-        if (!full) {   // keys that no query may see may hold anything
+          // ---- V's scales and minima: half g of each key's eight, for keys 2 t4, 2 t4 + 1 of the
+          // two octets of both chunks ----
+          uint32_t vp[2][2];
+          ldsm_x4_trans(stV + lm_par, vp[0][0], vp[0][1], vp[1][0], vp[1][1]);
+          if (!full) {   // keys that no query may see may hold anything
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const int t0 = (c + h) * kChunk + 8 * o;
-              const int lim = h == 0 || two ? Lc : 0;
-              vp[h][o] &= (t0 + 2 * t4 < lim ? 0x0000ffffu : 0u) |
-                          (t0 + 2 * t4 + 1 < lim ? 0xffff0000u : 0u);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+              for (int o = 0; o < 2; ++o) {
+                const int t0 = (c + h) * kChunk + 8 * o;
+                const int lim = h == 0 || two ? Lc : 0;
+                vp[h][o] &= (t0 + 2 * t4 < lim ? 0x0000ffffu : 0u) |
+                            (t0 + 2 * t4 + 1 < lim ? 0xffff0000u : 0u);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  if (t0 + g >= lim - a.q_len + 1 + ((qis[nt] >> (16 * e)) & 0xffff))
-                    x[nt][h][2 * o + e] = kNegInf;
-            }
-        }
-        // even g: scales; bit 14 says 2 or more
-        const bool wide = ((vp[0][0] | vp[0][1] | vp[1][0] | vp[1][1]) & wide_mask) != 0;
+                  if (t0 + g >= lim - a.q_len + 1 + ((qis >> (16 * e)) & 0xffff))
+                    x[h][2 * o + e] = kNegInf;
+              }
+          }
+          // even g: scales; bit 14 says 2 or more
+          const bool wide = ((vp[0][0] | vp[0][1] | vp[1][0] | vp[1][1]) & wide_mask) != 0;
 
-        // ---- softmax weights against the reference (exp2 domain) ----
-        bool move = wide && shift != 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          // ---- softmax weights against the reference (exp2 domain) ----
+          bool move = wide && shift != 0.f;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            move |= fmaxf(fmaxf(x[nt][0][e], x[nt][0][2 + e]),
-                          fmaxf(x[nt][1][e], x[nt][1][2 + e])) > thr[nt][e];
-        if (__any_sync(0xffffffffu, move)) {
-          const float to = __any_sync(0xffffffffu, wide) ? 0.f : shift;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+            move |= fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e])) > thr[e];
+          if (__any_sync(0xffffffffu, move)) {
+            const float to = __any_sync(0xffffffffu, wide) ? 0.f : shift;
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(fmaxf(x[nt][0][e], x[nt][0][2 + e]),
-                               fmaxf(x[nt][1][e], x[nt][1][2 + e]));
+              float mx = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float m_old = thr[nt][e] == kNegInf ? kNegInf : -nm[nt][e];
-              const float m_new = fmaxf(m_old + (shift - to), mx * rsc[nt][e] - to);
+              const float m_old = thr[e] == kNegInf ? kNegInf : -nm[e];
+              const float m_new = fmaxf(m_old + (shift - to), mx * rsc[e] - to);
               alpha[e] = m_old == kNegInf ? 0.f : fast_exp2(m_old - m_new);
               if (m_new != kNegInf) {
-                nm[nt][e] = -m_new;
-                thr[nt][e] = (m_new + (to + kGrow)) / rsc[nt][e];
+                nm[e] = -m_new;
+                thr[e] = (m_new + (to + kGrow)) / rsc[e];
               }
-              tl[nt][e] *= alpha[e];
+              tl[e] *= alpha[e];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              oz[nt][i] *= alpha[i & 1];
+              oz[i] *= alpha[i & 1];
 #pragma unroll
               for (int gr = 0; gr < 4; ++gr) {
-                ot[nt][gr][0][i] *= alpha[i & 1];
-                ot[nt][gr][1][i] *= alpha[i & 1];
+                ot[gr][0][i] *= alpha[i & 1];
+                ot[gr][1][i] *= alpha[i & 1];
               }
             }
+            shift = to;
           }
-          shift = to;
-        }
-        uint32_t pb[NT][2][2];   // P^T of chunk h as the B operand
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t pb[2][2];   // P^T of chunk h as the B operand
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              x[nt][h][e] = fast_exp2(fmaf(x[nt][h][e], rsc[nt][e], nm[nt][e]));
-              x[nt][h][2 + e] = fast_exp2(fmaf(x[nt][h][2 + e], rsc[nt][e], nm[nt][e]));
+              x[h][e] = fast_exp2(fmaf(x[h][e], rsc[e], nm[e]));
+              x[h][2 + e] = fast_exp2(fmaf(x[h][2 + e], rsc[e], nm[e]));
             }
-            tl[nt][e] += (x[nt][0][e] + x[nt][0][2 + e]) + (x[nt][1][e] + x[nt][1][2 + e]);
+            tl[e] += (x[0][e] + x[0][2 + e]) + (x[1][e] + x[1][2 + e]);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int o = 0; o < 2; ++o)
-              pb[nt][h][o] = movmatrix_trans(pack_half2(x[nt][h][2 * o], x[nt][h][2 * o + 1]));
-        }
+              pb[h][o] = movmatrix_trans(pack_half2(x[h][2 * o], x[h][2 * o + 1]));
 
-        // ---- O^T += V^T (P s)^T and the minima's sums ----
+          // ---- O^T += V^T (P s)^T and the minima's sums ----
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t vb = stV + h * kTile;
-          uint32_t vw[4][2];
-          ldsm_x4_trans(vb + lm_codes, vw[0][0], vw[0][1], vw[1][0], vw[1][1]);
-          ldsm_x4_trans(vb + lm_codes + 32, vw[2][0], vw[2][1], vw[3][0], vw[3][1]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t vb = stV + h * kTile;
+            uint32_t vw[4][2];
+            ldsm_x4_trans(vb + lm_codes, vw[0][0], vw[0][1], vw[1][0], vw[1][1]);
+            ldsm_x4_trans(vb + lm_codes + 32, vw[2][0], vw[2][1], vw[3][0], vw[3][1]);
+            mma_f16(oz, vp[h][0], 0u, vp[h][1], 0u, pb[h][0], pb[h][1]);
+            const __half2 p0 = as_half2(pb[h][0]), p1 = as_half2(pb[h][1]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(oz[nt], vp[h][0], 0u, vp[h][1], 0u, pb[nt][h][0], pb[nt][h][1]);
-#pragma unroll
-          for (int gr = 0; gr < 4; ++gr) {
-            const uint32_t s0 = __shfl_sync(0xffffffffu, vp[h][0], 8 * gr + t4);
-            const uint32_t s1 = __shfl_sync(0xffffffffu, vp[h][1], 8 * gr + t4);
-            const uint32_t u0 = vw[gr][0] >> 8, u1 = vw[gr][1] >> 8;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const __half2 p0 = as_half2(pb[nt][h][0]), p1 = as_half2(pb[nt][h][1]);
-              const __half2 b0 = __hmul2(p0, as_half2(s0)), b1 = __hmul2(p1, as_half2(s1));
+            for (int gr = 0; gr < 4; ++gr) {
+              const __half2 s0 = as_half2(__shfl_sync(0xffffffffu, vp[h][0], 8 * gr + t4));
+              const __half2 s1 = as_half2(__shfl_sync(0xffffffffu, vp[h][1], 8 * gr + t4));
+              const uint32_t u0 = vw[gr][0] >> 8, u1 = vw[gr][1] >> 8;
+              const __half2 b0 = __hmul2(p0, s0), b1 = __hmul2(p1, s1);
               // what the products' rounding left over (exact)
-              const uint32_t r0 = half2_bits(__hfma2(p0, as_half2(s0), __hneg2(b0)));
-              const uint32_t r1 = half2_bits(__hfma2(p1, as_half2(s1), __hneg2(b1)));
+              const __half2 d0 = __hfma2(p0, s0, __hneg2(b0)), d1 = __hfma2(p1, s1, __hneg2(b1));
 #pragma unroll
               for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                   const uint32_t m = i ? 0x00f000f0u : 0x000f000fu;
-                  mma_f16(ot[nt][gr][i], vw[gr][0] & m, u0 & m, vw[gr][1] & m, u1 & m,
-                          part ? r0 : half2_bits(b0), part ? r1 : half2_bits(b1));
+                  mma_f16(ot[gr][i], vw[gr][0] & m, u0 & m, vw[gr][1] & m, u1 & m,
+                          half2_bits(part ? d0 : b0), half2_bits(part ? d1 : b1));
                 }
             }
           }
+          __syncwarp();                        // every lane has read the stage
+          walk.load(a, cur, w, lane, stK, kv_policy);
+          slot = slot + 1 == ND ? 0 : slot + 1;
         }
-        __syncwarp();                        // every lane has read the stage
-        walk.load(a, cur, w, lane, stK, kv_policy);
-        slot = slot + 1 == ND ? 0 : slot + 1;
-      }
-      j += npair;
-
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_qempty + qs * 8);
-
-      // ---- hand this warp's state to the epilogue: row g of tile (gr, i) is dim 32 gr + 4 g + i,
-      // row g + 8 dim 32 gr + 4 g + 2 + i ----
-      const int sb = k % SB;
-      if (k >= SB && !mbar_wait(bar_sfree + sb * 8, ((k / SB) - 1) & 1, abort)) flag_timeout(a, abort);
-      float* o_d = stO + sb * NCS * a.R * kSt;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        // ---- the sums go to the warp's state buffer: row g of tile (gr, i) is dim 32 gr + 4 g + i,
+        // row g + 8 dim 32 gr + 4 g + 2 + i ----
+        if (!held && k >= 1 && !mbar_wait(bar_sfree, (k - 1) & 1, abort)) flag_timeout(a, abort);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float lv = tl[nt][e];
-          lv += __shfl_xor_sync(0xffffffffu, lv, 4);
-          lv += __shfl_xor_sync(0xffffffffu, lv, 8);
-          lv += __shfl_xor_sync(0xffffffffu, lv, 16);
+          float lv = tl[e];
+          if (jp >= npair) {
+            lv += __shfl_xor_sync(0xffffffffu, lv, 4);
+            lv += __shfl_xor_sync(0xffffffffu, lv, 8);
+            lv += __shfl_xor_sync(0xffffffffu, lv, 16);
+          }
           float z[4];
 #pragma unroll
           for (int gr = 0; gr < 4; ++gr)
-            z[gr] = __shfl_sync(0xffffffffu, oz[nt][e], 8 * gr + 4 + t4);
-          const int r = 8 * (NT * rs + nt) + 2 * t4 + e;
+            z[gr] = __shfl_sync(0xffffffffu, oz[e], 8 * gr + 4 + t4);
+          const int r = r0 + e;
+          const int at = w * a.R + r;
+          const float m = thr[e] == kNegInf ? kNegInf : -nm[e];
+          float keep = 0.f;   // what the earlier sums are worth against the present reference
+          if (held && r < a.R && stM[at] != kNegInf) keep = fast_exp2(stM[at] - m);
+          __syncwarp();
           if (r < a.R) {
-            float* row = o_d + (w * a.R + r) * kSt + 4 * g;
+            float4* row = reinterpret_cast<float4*>(stO + at * kSt + 4 * g);
 #pragma unroll
-            for (int gr = 0; gr < 4; ++gr)
-              *reinterpret_cast<float4*>(row + 32 * gr) =
-                  make_float4(fmaf(ot[nt][gr][0][e], 0x1p24f, z[gr]),
-                              fmaf(ot[nt][gr][1][e], 0x1p20f, z[gr]),
-                              fmaf(ot[nt][gr][0][2 + e], 0x1p24f, z[gr]),
-                              fmaf(ot[nt][gr][1][2 + e], 0x1p20f, z[gr]));
+            for (int gr = 0; gr < 4; ++gr) {
+              float4 o = make_float4(fmaf(ot[gr][0][e], 0x1p24f, z[gr]),
+                                     fmaf(ot[gr][1][e], 0x1p20f, z[gr]),
+                                     fmaf(ot[gr][0][2 + e], 0x1p24f, z[gr]),
+                                     fmaf(ot[gr][1][2 + e], 0x1p20f, z[gr]));
+              if (held) {
+                const float4 b = row[8 * gr];
+                o.x = fmaf(b.x, keep, o.x);
+                o.y = fmaf(b.y, keep, o.y);
+                o.z = fmaf(b.z, keep, o.z);
+                o.w = fmaf(b.w, keep, o.w);
+              }
+              row[8 * gr] = o;
+            }
             if (g == 0) {
-              stM[(sb * NCS + w) * a.R + r] = thr[nt][e] == kNegInf ? kNegInf : -nm[nt][e];
-              stL[(sb * NCS + w) * a.R + r] = lv;
+              stM[at] = m;
+              stL[at] = lv;
             }
           }
         }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_sdone + sb * 8);
+        __syncwarp();
+        held = true;
+      } while (jp < npair);
+      j += npair;
+      if (lane == 0) mbar_arrive(bar_qempty + qs * 8);
+      if (lane == 0) mbar_arrive(bar_sdone);
       set_last(s, k);
       ++k;
       has = cur.next(s);
@@ -744,19 +703,19 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
 
   // ---- end of the slice ----
   if (last.k >= 0)
-    finish_slice<NCS, kSeg4, NCW, SB>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s,
+    finish_slice<NCS, kSeg4, NCW, 1>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s,
                                       fast_s, warp < NCW ? tid : tid - 32);
 }
 
 // ---------------------------------------------------------------------------------------------
 // Host side.
 
-template <int NCS, int RS, int ND, int NT, int SB, int QR, int MINB>
+template <int NCS, int RS, int ND, int MINB>
 Variant variant4(bool append) {
-  const void* fn =
-      append ? reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, QR, MINB, true>)
-             : reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, NT, SB, QR, MINB, false>);
-  return Variant{fn, NT, false, (NCS * RS + 2) * 32, &Smem4<NCS, RS, ND, NT, SB>::bytes};
+  const void* fn = append
+                       ? reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, MINB, true>)
+                       : reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, MINB, false>);
+  return Variant{fn, RS, false, (NCS * RS + 2) * 32, &Smem4<NCS, RS, ND>::bytes};
 }
 
 int launch_decode_int4(void* out, const void* q, const void* k_new, const void* v_new,
@@ -791,16 +750,20 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
 #ifndef V1
-#define V1 4, 1, 3, 1, 1, 0, 2
+#define V1 4, 1, 3, 2
 #endif
 #ifndef V2
-#define V2 6, 1, 3, 2, 1, 1, 1
+#define V2 2, 2, 3, 2
+#endif
+#ifndef V3
+#define V3 3, 3, 3, 1
 #endif
 #ifndef V4
-#define V4 3, 2, 3, 2, 1, 1, 1
+#define V4 2, 4, 3, 1
 #endif
   const Variant v = R <= 8    ? variant4<V1>(append)
                     : R <= 16 ? variant4<V2>(append)
+                    : R <= 24 ? variant4<V3>(append)
                               : variant4<V4>(append);
   const int newkv_bytes = append ? 2 * q_len * 512 : 0;
   const size_t smem = v.smem(R, num_seqs, newkv_bytes);
