@@ -478,11 +478,11 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps, positions, cos_sin, q_out=None, 
     if T <= 1:   # the stride of a single token means nothing
         qs, ks = hq * 128, hkv * 128
     if q_out is None:
-        q_out = torch.empty((T, hq, 128), dtype=_F16, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _require(fn, _is(q_out, _F16, dev) and q_out.shape == q.shape)
     if k_out is None:
-        k_out = torch.empty((T, hkv, 128), dtype=_F16, device=q.device)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     else:
         _require(fn, _is(k_out, _F16, dev) and k_out.shape == k.shape)
     _check(fn, (_lib or load()).pkv_qk_norm_rope(
@@ -507,11 +507,10 @@ def extend_tables(block_tables, context_lens, new_lens, block_size, free_blocks,
     _require(fn, context_lens.numel() == B and new_lens.numel() == B and free_count.numel() == 1)
     if out is None:
         on = block_tables.device
-        out = (torch.empty(max_tokens, dtype=_I64, device=on),
-               torch.empty(max_tokens, dtype=_I32, device=on),
-               torch.empty(max_tokens, dtype=_I64, device=on),
-               torch.empty(B + 1, dtype=_I32, device=on))
-        slots, seqs, pos, cu = out
+        slots = torch.empty(max_tokens, dtype=_I64, device=on)
+        seqs = torch.empty(max_tokens, dtype=_I32, device=on)
+        cu = torch.empty(B + 1, dtype=_I32, device=on)
+        out = slots, seqs, pos, cu = slots, seqs, torch.empty_like(slots), cu
     else:
         slots, seqs, pos, cu = out
         _require(fn, _is(slots, _I64, dev) and _is(seqs, _I32, dev) and _is(pos, _I64, dev) and
