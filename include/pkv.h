@@ -330,8 +330,8 @@ int pkv_paged_attn_decode_append_fp8(void* out, const void* q, const void* k_new
  * pkv_kv_append_int4: pkv_kv_append's scatter, each row quantised: z = the group's minimum, s =
  * (max - min) / 15 in binary32, rounded up to fp16 (down where 15 s + z would pass the largest fp16), code =
  * (x - z) / s rounded to nearest, ties to even, in 0 .. 15 (0 where s is 0). A group with a NaN or
- * an infinity gets s = z = NaN. Same slot rules and errors as pkv_kv_append; k, v fp16
- * [num_tokens][num_kv_heads][head_dim]; all four 16-byte aligned. */
+ * an infinity gets s = z = NaN. Same slot rules and errors as pkv_kv_append, and no slot twice; k,
+ * v fp16 [num_tokens][num_kv_heads][head_dim]; all four 16-byte aligned. */
 int pkv_kv_append_int4(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
                        void* k_cache, void* v_cache, int num_blocks, int num_kv_heads,
                        int head_dim, int block_size, pkv_stream_t stream);
@@ -347,8 +347,9 @@ int pkv_widen_blocks_int4(const void* k_cache, const void* v_cache, const int32_
                           int num_blocks_out, int num_kv_heads, int head_dim, int block_size,
                           pkv_stream_t stream);
 
-/* pkv_paged_attn_decode over a 4-bit cache. Scores use the keys s * code + z as they are (the
- * codes' products summed in fp32, then scaled); the values are widened to fp16(s * code + z).
+/* pkv_paged_attn_decode over a 4-bit cache. Keys and values are s * code + z as they are, not
+ * rounded to fp16: the codes' products are summed in fp32 and scaled then (keys), or taken with the
+ * scaled softmax weights in two fp16 parts (values). The weights themselves are fp16, as there.
  * (num_q_heads / num_kv_heads) * q_len <= 32, as there; other arguments, workspace and errors as
  * there too. */
 int pkv_paged_attn_decode_int4(void* out, const void* q, const void* k_cache,

@@ -83,17 +83,24 @@ def append(k, v, slots, k_pool, v_pool):
 def attention(q, k_pool, v_pool, tables, lens, scale):
     """Textbook attention over the values, fp64: (out, tol) float64 [B, q_len, Hq, 128].
 
-    tol is how far a result may be off that rounds each value and each softmax weight once to
-    fp16 (half a step, 2^-11 relative each; a weight below 2^-14 of a warp's largest by 2^-25
-    of it), sums in fp32, and rounds the output once (2^-11 relative, 2^-25 for subnormals).
+    tol is how far a result may be off that takes the codes' products on tensor cores, rounds each
+    softmax weight once to fp16 (half a step, 2^-11 relative; a weight below 2^-14 of a warp's
+    largest by 2^-25 of it), sums in fp32, and rounds the output once (2^-11 relative, 2^-25 for
+    subnormals). The room for one more rounding of 2^-11 per value is left.
+    A tensor core aligns the products of a dot by the sums of their operands' exponents, a
+    subnormal's counted as -14, and cuts below 2^-25 of the largest. Codes come as subnormals
+    c 2^-22 and c 2^-18, so a code's product with a weight w (scores: query element, scaled by
+    16 for the first kind) is cut below 2^(-25 - 14 + 22) = 2^-17 of the largest w, or lost whole.
+    Values: w = p s in two fp16 parts, the second under 2^-11 of the first: at most 2^-16 max(p s)
+    a key, or 16 p s. Scores: 16 products of a group's 32 with 2^-17 s max|q|, 16 with 2^-21 and
+    the sum itself: (2^-13 + 2^-16) s max|q|, the maximum over the group; its query sum times z is
+    split in two fp16 numbers, the second down to 2^-24 with the row's largest |q| at 2^-8 or
+    more: 2^-17 |z| max|q|, over the row.
     The fp32 sums of p s code and of p z may be kept apart: they nearly cancel where a value is
-    near zero, so their errors are relative to S = sum p (15 s + |z|). A tensor-core sum
-    truncates by less than 2^-23 of it, at most 64 times in a row here (64 steps of 16 keys a
-    warp): 2^-17 S.
-    Scores: products of q with codes and with minima are summed separately, so their error is
-    relative to sum |q| (15 s + |z|); at most 32 roundings of 2^-23 each (truncating tensor-core
-    sums) on the way, 2^-18. A relative error e of the weights moves the output by at most
-    2 e sum p |v|."""
+    near zero, so their errors are relative to S = sum p (15 s + |z|). A sum truncates by less
+    than 2^-23 of itself, at most 64 times in a row here: 2^-17 S. Likewise the scores' sums, at
+    most 32 times: 2^-18 sum |q| (15 s + |z|).
+    A relative error e of the weights moves the output by at most 2 e sum p |v|."""
     q = np.asarray(q, np.float64)
     B, q_len, hq, _ = q.shape
     hkv, bs = k_pool.shape[1], k_pool.shape[2]
@@ -119,12 +126,19 @@ def attention(q, k_pool, v_pool, tables, lens, scale):
                 x = qq @ K[:m].T * scale
                 p = np.exp(x - x.max(-1, keepdims=True))
                 L = p.sum(-1, keepdims=True)
-                e = 2.0 ** -18 * abs(scale) * (np.abs(qq) @ reach[:m].T).max(-1, keepdims=True)
+                qmax = np.abs(qq).reshape(group, 4, GROUP).max(-1)             # [group, 4]
+                s4, z4 = ks[:m, ::GROUP], np.abs(kz[:m, ::GROUP])              # [m, 4]
+                e = (2.0 ** -18 * (np.abs(qq) @ reach[:m].T) +
+                     (2.0 ** -13 + 2.0 ** -16) * (qmax @ s4.T) +
+                     2.0 ** -17 * qmax.max(-1, keepdims=True) * z4.sum(-1))
+                e = abs(scale) * e.max(-1, keepdims=True)
+                ps = (p / L)[:, :, None] * vs[:m, ::GROUP]                     # [group, m, 4]
+                cut = np.minimum(2.0 ** -16 * ps.max(1, keepdims=True), 16 * ps).sum(1)
                 avg = (p / L) @ np.abs(V[:m])
                 o = (p / L) @ V[:m]
                 out[b, i, h * group:(h + 1) * group] = o
                 tol[b, i, h * group:(h + 1) * group] += (
                     (2 * 2.0 ** -11 + 2 * e) * avg + 2.0 ** -11 * np.abs(o) +
-                    2.0 ** -17 * ((p / L) @ reach_v[:m]) +
-                    m * 2.0 ** -25 / L * np.abs(V[:m]).max())
+                    2.0 ** -17 * ((p / L) @ reach_v[:m]) + np.repeat(cut, GROUP, -1) +
+                    m * 2.0 ** -25 / L * np.nanmax(np.abs(V[:m])))
     return out, tol

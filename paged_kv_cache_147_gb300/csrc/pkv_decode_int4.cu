@@ -18,12 +18,15 @@
 //    whatever its size, which bounded the kernel at 3 TB/s.
 //  * Transposed tile: S^T = K Q^T and O^T = V^T P^T, keys (and output dims) on the mma's 16-row
 //    side, 8 query rows on its 8 columns.
-//  * Four bits at bits 0-3 (4-7) of a 16-bit half are the fp16 subnormal c 2^-24 (c 2^-20),
-//    exactly, and the products' sums are fp32: one AND of a word or of the word shifted by 8
-//    makes an mma operand of two codes.
+//  * Four bits at bits 2-5 (6-9) of a 16-bit half are the fp16 subnormal c 2^-22 (c 2^-18),
+//    exactly, and the products' sums are fp32: one AND of the word shifted left by 2 or right by 6
+//    makes an mma operand of two codes. (The tensor cores count a subnormal's exponent as -14 when
+//    they align products, and cut below 2^-25 of the largest: at bits 0-3, without the left shift,
+//    a product loses up to 2^-15 of a code step times the largest weight, always downwards, here
+//    2^-17. The shifts cost 0 to 3 % of the time.)
 //  * Keys: sum_d q_d (s c_d + z) = s sum_d q_d c_d + z sum_d q_d per group of 32 dims. The
 //    queries are scaled by a power of two that puts the row's largest between 2^10 and 2^11, those
-//    that meet codes at bits 0-3 by 16 more (both exact: what falls below fp16's smallest is
+//    that meet codes at bits 2-5 by 16 more (both exact: what falls below fp16's smallest is
 //    under 2^-34 of the row's largest). The group's sum is scaled by s in fp32; z times the
 //    group's query sum is one more product per 16 keys, the (s, z) words as they stand against
 //    (0, sum), the sum split in two fp16 numbers.
@@ -58,14 +61,25 @@ constexpr int kStage4 = 4 * kTile;           // K of two chunks, V of two chunks
 // Per-segment cost in chunks (see kSegCost): queries, hand-off and merge of a segment take a CTA
 // ~1.5 us, the time of a dozen chunks (70B mixed lengths: 62 us with 4, 55 with 8, 51 with 12).
 constexpr int kSeg4 = 12;
+// A unit of n chunks cut into slices of T costs about T chunks' time and a merge of n / T partials,
+// each kPartCost chunks' worth: least at T = sqrt(kPartCost n), so no slice is cut finer. One
+// sequence of 4096 tokens and 2 kv heads (all 304 CTAs otherwise) 44 -> 14 us, of 1536 36 -> 11;
+// with a cost of 1.5, 2.5, 4, 6 the lengths from 256 to 131072 stay within 8 % of each other.
+constexpr float kPartCost = 3.f;
+// Few short units: a whole unit for each CTA, when its warps then take at most kAlone rounds of
+// stages more than an equal share has; that costs less than writing and merging partials (one
+// sequence of 256 tokens 9.4 -> 7.2 us, 32 of 1024 with 8 kv heads 18.6 -> 16.3).
+constexpr int kAlone = 3;
+constexpr size_t kMaxSmem = 227 * 1024;
 // How far the softmax's reference stays below the running maximum (see above), and how far a
 // weight may grow past the maximum it was taken at before the reference moves.
 constexpr float kShift = 11.f, kGrow = 2.f;
 // Stages after which a warp's sums move to its state buffer. The tensor cores' fp32 sums truncate,
 // and the two large sums that make a value's (of p s c and of p z) do not lose alike: over 100
-// stages a warp (16384 tokens) their difference was off by 6.7e-4 relative, over 20 by 2.9e-4,
-// near what the rounded weights and output alone cost (2.6e-4); moving them costs 3 % of the time.
-constexpr int kFlush = 20;
+// stages a warp (16384 tokens) their difference was off by 6.7e-4 relative, over 16 by 2.8e-4, near
+// what the rounded weights and output alone cost (2.1e-4 to 2.6e-4). With 16 a sum takes 64
+// products (two chunks, weights and what they lost); moving the sums costs 3 to 4 % of the time.
+constexpr int kFlush = 16;
 
 // Shared-memory layout (offsets from a 128-byte aligned base). NCS: warps that share the stages
 // among them, RS: warps that take one stage, 8 query rows each, ND: stages in flight per warp.
@@ -183,6 +197,11 @@ struct StageWalk {
     cp_async_commit();
   }
 };
+
+// 0xffff in the halves of w that are NaN, 0 in the others.
+__device__ __forceinline__ uint32_t nan_halves(uint32_t w) {
+  return __hneu2_mask(as_half2(w), as_half2(w));
+}
 
 // The products without `volatile`: the compiler may order them (pkv_device.cuh's keep theirs).
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -305,11 +324,9 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
 
   // ---- this CTA's slice of the stream --------------------------------------------------------
   const int total = pre[B] * a.Hkv;
-  const int per = (total + gridDim.x - 1) / gridDim.x;
+  const int per = max(static_cast<int>((total + gridDim.x - 1) / gridDim.x),
+                      static_cast<int>(sqrtf(kPartCost * *longest_s)));
   int begin = blockIdx.x * per, end = min(total, begin + per);
-  // Few short units: a whole unit for each CTA. Its warps then take kAlone rounds of stages more
-  // than an equal share has, which costs less than writing partials and merging them (~4 us).
-  constexpr int kAlone = 3;
   if (B * a.Hkv <= gridDim.x && *longest_s <= 2 * NCS * ((per + 2 * NCS - 1) / (2 * NCS) + kAlone)) {
     const int b = blockIdx.x / a.Hkv;
     const int len = b < B ? pre[b + 1] - pre[b] : 0;
@@ -364,10 +381,10 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
         // score scale turns the queries' signs instead, so that a larger product is a larger score
         const int ex = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) : 127;
         float f = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
-        // codes come in as c 2^-20; a NaN or an infinity among the queries makes the scores NaN
+        // codes come in as c 2^-18; a NaN or an infinity among the queries makes the scores NaN
         float unit = top <= 65504.f
                          ? fabsf(a.scale_log2) *
-                               (1048576.f * __uint_as_float(static_cast<uint32_t>(ex - 10) << 23))
+                               (262144.f * __uint_as_float(static_cast<uint32_t>(ex - 10) << 23))
                          : __uint_as_float(0x7fffffffu);
         if (a.scale_log2 < 0.f) f = -f;
         if (unit == 0.f) unit = 0x1p-100f;   // so that masked scores stay -infinity
@@ -390,7 +407,7 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
                                   pack_half2(u[1].y, u[3].y)));                // dims 3, 7
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (gr == t4) own = sum * 0x1p-20f;   // in the products' units; at most 2^-4
+          if (gr == t4) own = sum * 0x1p-18f;   // in the products' units; at most 2^-2
         }
         const __half hi = __float2half_rn(own);
         const __half lo = __float2half_rn(own - __half2float(hi));
@@ -568,13 +585,13 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
               float t[2][4];
 #pragma unroll
               for (int part = 0; part < 2; ++part) {
-                const uint32_t m = part ? 0x00f000f0u : 0x000f000fu;
+                const uint32_t m = part ? 0x03c003c0u : 0x003c003cu;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                   const uint32_t w0 = kw[gp + i][0], w1 = kw[gp + i][1];
                   const uint2 b = ld_shared_v2(qb + (gp + i) * 512 + part * 8);
                   if (part == 0) t[i][0] = t[i][1] = t[i][2] = t[i][3] = 0.f;
-                  mma_f16(t[i], w0 & m, w1 & m, (w0 >> 8) & m, (w1 >> 8) & m, b.x, b.y);
+                  mma_f16(t[i], (w0 << 2) & m, (w1 << 2) & m, (w0 >> 6) & m, (w1 >> 6) & m, b.x, b.y);
                 }
               }
 #pragma unroll
@@ -607,6 +624,33 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
                   if (t0 + g >= lim - a.q_len + 1 + ((qis >> (16 * e)) & 0xffff))
                     x[h][2 * o + e] = kNegInf;
               }
+            // A NaN row of V is for the queries that see it only (a weight of 0 would not keep
+            // it from the others): its parameters become 0, and the minima's sums of the rows that
+            // see it NaN. Lane (g, t4) finds the first such key of half g, and holds the sums.
+            uint32_t nan = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int o = 0; o < 2; ++o) nan |= nan_halves(vp[h][o]);
+            if (__any_sync(0xffffffffu, nan != 0)) {
+              int at = 2 * kChunk;
+#pragma unroll
+              for (int h = 1; h >= 0; --h)
+#pragma unroll
+                for (int o = 1; o >= 0; --o) {
+                  const uint32_t b = nan_halves(vp[h][o]);
+                  if (b) at = h * kChunk + 8 * o + 2 * t4 + ((b & 0xffffu) ? 0 : 1);
+                  vp[h][o] &= ~b;
+                }
+              at = min(at, __shfl_xor_sync(0xffffffffu, at, 1));
+              at = min(at, __shfl_xor_sync(0xffffffffu, at, 2));
+              at = min(at, __shfl_xor_sync(0xffffffffu, at, 4));   // scale or minimum
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (at < 2 * kChunk &&
+                    c * kChunk + at < Lc - a.q_len + 1 + ((qis >> (16 * e)) & 0xffff))
+                  oz[e] = __uint_as_float(0x7fffffffu);
+            }
           }
           // even g: scales; bit 14 says 2 or more
           const bool wide = ((vp[0][0] | vp[0][1] | vp[1][0] | vp[1][1]) & wide_mask) != 0;
@@ -674,7 +718,8 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
             for (int gr = 0; gr < 4; ++gr) {
               const __half2 s0 = as_half2(__shfl_sync(0xffffffffu, vp[h][0], 8 * gr + t4));
               const __half2 s1 = as_half2(__shfl_sync(0xffffffffu, vp[h][1], 8 * gr + t4));
-              const uint32_t u0 = vw[gr][0] >> 8, u1 = vw[gr][1] >> 8;
+              const uint32_t l0 = vw[gr][0] << 2, l1 = vw[gr][1] << 2;
+              const uint32_t u0 = vw[gr][0] >> 6, u1 = vw[gr][1] >> 6;
               const __half2 b0 = __hmul2(p0, s0), b1 = __hmul2(p1, s1);
               // what the products' rounding left over (exact)
               const __half2 d0 = __hfma2(p0, s0, __hneg2(b0)), d1 = __hfma2(p1, s1, __hneg2(b1));
@@ -682,8 +727,8 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
               for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const uint32_t m = i ? 0x00f000f0u : 0x000f000fu;
-                  mma_f16(ot[gr][i], vw[gr][0] & m, u0 & m, vw[gr][1] & m, u1 & m,
+                  const uint32_t m = i ? 0x03c003c0u : 0x003c003cu;
+                  mma_f16(ot[gr][i], l0 & m, u0 & m, l1 & m, u1 & m,
                           half2_bits(part ? d0 : b0), half2_bits(part ? d1 : b1));
                 }
             }
@@ -717,10 +762,10 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
             float4* row = reinterpret_cast<float4*>(stO + at * kSt + 4 * g);
 #pragma unroll
             for (int gr = 0; gr < 4; ++gr) {
-              float4 o = make_float4(fmaf(ot[gr][0][e], 0x1p24f, z[gr]),
-                                     fmaf(ot[gr][1][e], 0x1p20f, z[gr]),
-                                     fmaf(ot[gr][0][2 + e], 0x1p24f, z[gr]),
-                                     fmaf(ot[gr][1][2 + e], 0x1p20f, z[gr]));
+              float4 o = make_float4(fmaf(ot[gr][0][e], 0x1p22f, z[gr]),
+                                     fmaf(ot[gr][1][e], 0x1p18f, z[gr]),
+                                     fmaf(ot[gr][0][2 + e], 0x1p22f, z[gr]),
+                                     fmaf(ot[gr][1][2 + e], 0x1p18f, z[gr]));
               if (held) {
                 const float4 b = row[8 * gr];
                 o.x = fmaf(b.x, keep, o.x);
@@ -758,12 +803,25 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
 // ---------------------------------------------------------------------------------------------
 // Host side.
 
-template <int NCS, int RS, int ND, int MINB>
-Variant variant4(bool append) {
-  const void* fn = append
-                       ? reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, MINB, true>)
-                       : reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, MINB, false>);
-  return Variant{fn, RS, false, (NCS * RS + 2) * 32, &Smem4<NCS, RS, ND>::bytes};
+template <int NCS, int RS, int ND, int MINB, bool APPEND>
+Variant variant4() {
+  return Variant{reinterpret_cast<const void*>(&decode_int4_kernel<NCS, RS, ND, MINB, APPEND>), RS,
+                 false, (NCS * RS + 2) * 32, &Smem4<NCS, RS, ND>::bytes};
+}
+
+// The variant for R query rows. Four consumer warps a CTA and two CTAs while the registers of 8
+// or 16 rows allow (a multiple of four of them per SM: one of its four schedulers takes every
+// fourth warp); beyond, one CTA of 9 or 8. Measured against others that fit, us (four drafts of 6
+// heads, mixed lengths to 2048, cut to the rows; 16 sequences of 4096 tokens, 8 kv heads):
+//   9..16 rows   <2, 2, 3, 2> 20.4 / 43.1, <4, 2, 3, 1> 22.3 / 45.2, <6, 2, 2, 1> 24.5 / 42.0
+//   17..24 rows  <3, 3, 3, 1> 27.2 / 65.3, <4, 3, 2, 1> 28.8 / 57.9
+//   25..32 rows  <2, 4, 3, 1> 31.1 / 77.7, <3, 4, 2, 1> 33.7 / 70.5
+template <bool APPEND>
+Variant choose4(int R) {
+  return R <= 8    ? variant4<4, 1, 3, 2, APPEND>()
+         : R <= 16 ? variant4<2, 2, 3, 2, APPEND>()
+         : R <= 24 ? variant4<3, 3, 3, 1, APPEND>()
+                   : variant4<2, 4, 3, 1, APPEND>();
 }
 
 int launch_decode_int4(void* out, const void* q, const void* k_new, const void* v_new,
@@ -797,25 +855,14 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   const WsLayout ws = ws_layout(num_seqs, Hkv, R);
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
-#ifndef V1
-#define V1 4, 1, 3, 2
-#endif
-#ifndef V2
-#define V2 2, 2, 3, 2
-#endif
-#ifndef V3
-#define V3 3, 3, 3, 1
-#endif
-#ifndef V4
-#define V4 2, 4, 3, 1
-#endif
-  const Variant v = R <= 8    ? variant4<V1>(append)
-                    : R <= 16 ? variant4<V2>(append)
-                    : R <= 24 ? variant4<V3>(append)
-                              : variant4<V4>(append);
   const int newkv_bytes = append ? 2 * q_len * 512 : 0;
-  const size_t smem = v.smem(R, num_seqs, newkv_bytes);
-  if (smem > 227 * 1024) return PKV_EINVAL;
+  Variant v = append ? choose4<true>(R) : choose4<false>(R);
+  size_t smem = v.smem(R, num_seqs, newkv_bytes);
+  if (append && smem > kMaxSmem) {   // thousands of sequences with 8 and more new tokens each
+    v = variant4<2, 4, 2, 1, true>();
+    smem = v.smem(R, num_seqs, newkv_bytes);
+  }
+  if (smem > kMaxSmem) return PKV_EINVAL;
   int status = PKV_OK;
   const int grid = grid_size(v, smem, &status);
   if (!grid) return status != PKV_OK ? status : PKV_EINVAL;

@@ -342,6 +342,181 @@ def test_fused_steps_in_a_row_with_and_without_early_start():
             pkv.set_early_start(before)
 
 
+@pytest.mark.parametrize("lens,bs,hq,hkv,q_len", [
+    ([1, 18, 33, 0, 250], 16, 9, 1, 1),               # 9 rows
+    ([40, 3, 200], 16, 12, 4, 5),                     # 15
+    ([40, 16, 200], 32, 17, 1, 1),                    # 17
+    ([64, 9, 30], 16, 5, 1, 5),                       # 25
+    ([64, 31, 700], 16, 32, 1, 1),                    # 32 heads
+    ([64, 31, 33, 100], 16, 2, 2, 32),                # 32 new tokens
+])
+def test_fused_append_of_9_to_32_rows(lens, bs, hq, hkv, q_len):
+    test_fused_append_decode_matches_oracle(lens, bs, hq, hkv, q_len)
+
+
+@pytest.mark.parametrize("hq,hkv,q_len", [(24, 1, 1), (1, 1, 24), (4, 1, 8), (1, 1, 32)])
+def test_fused_append_of_as_many_sequences_as_a_call_takes(hq, hkv, q_len):
+    # 4096 sequences: two of three empty (padding), the others short
+    lens = np.zeros(4096, np.int32)
+    lens[::3] = np.random.default_rng(2).integers(1, 50, len(lens[::3]))
+    test_fused_append_decode_matches_oracle(lens, 16, hq, hkv, q_len)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, -3.0])
+def test_decode_with_a_scale_that_is_not_positive(scale):
+    k, v, tables, lens, q = _case([900, 33, 2, 70], 16, 12, 2, 2, seed=17)
+    out = _decode(k, v, tables, lens, q, scale)
+    want, tol = int4.attention(q, k, v, tables, lens, scale)
+    _close(out, want, tol)
+
+
+@pytest.mark.parametrize("hq,q_len", [(32, 1), (48, 4)])
+def test_decode_of_long_slices(hq, q_len):
+    # 20 sequences of up to 6000 tokens, 8 kv heads: more stages a warp than it sums in one go. Keys
+    # grow along the context (the reference moves from one sum to the next), and values past
+    # two thirds of it pass the scale that moves the reference by kShift.
+    hkv, bs, B = 8, 16, 20
+    rng = np.random.default_rng(3)
+    lens = rng.integers(5000, 6000, B).astype(np.int32)
+    nblk = (lens + bs - 1) // bs
+    nb = int(nblk.sum())
+    tables = np.full((B, int(nblk.max())), -1, np.int32)
+    perm = rng.permutation(nb).astype(np.int32)
+    pos = np.full((nb, bs), 0.0)
+    at = 0
+    for b, n in enumerate(nblk):
+        tables[b, :n] = perm[at:at + n]
+        pos[tables[b, :n]] = (np.arange(n * bs) / lens[b]).reshape(n, bs)
+        at += n
+    q = rng.standard_normal((B, q_len, hq, 128)).astype(np.float16)
+    kd, vd = (torch.zeros(nb, hkv, bs, 80, dtype=torch.uint8, device=DEV) for _ in range(2))
+    gen = torch.Generator(DEV).manual_seed(5)
+    share = _dev(pos.reshape(-1), torch.float32)[:, None, None]
+    slots = torch.arange(nb * bs, device=DEV)
+    kx = torch.randn(nb * bs, hkv, 128, device=DEV, generator=gen) * (0.2 + share)
+    vx = torch.randn(nb * bs, hkv, 128, device=DEV, generator=gen) * torch.where(share > 0.66, 20., 1.)
+    pkv.kv_append_int4(kx.half(), vx.half(), slots, kd, vd)
+    qd = _dev(q)
+    out = torch.full_like(qd, float("nan"))
+    pkv.paged_attn_decode_int4(out, qd, kd, vd, _dev(tables), _dev(lens), 0.2,
+                               pkv.make_workspace(B, q_len, hq, hkv))
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == 0
+    k, v = kd.cpu().numpy(), vd.cpu().numpy()
+    assert (int4.parts(v)[1] >= 2).any() and (int4.parts(v)[1] < 2).any()
+    pick = [0, 7, 19]
+    want, tol = int4.attention(q[pick], k, v, tables[pick], lens[pick], 0.2)
+    _close(out[pick], want, tol)
+    assert torch.isfinite(out).all()
+
+
+def _same_nan_and_close(out, want, tol):
+    got = out.float().cpu().numpy().astype(np.float64)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    ok = ~np.isnan(want)
+    assert (np.abs(got - want)[ok] <= tol[ok]).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_decode_keeps_a_bad_query_to_its_row(what):
+    k, v, tables, lens, q = _case([130, 40], 16, 12, 2, 2, seed=23)
+    q[0, 1, 7, 100] = what
+    out = _decode(k, v, tables, lens, q, 0.1)
+    with np.errstate(invalid="ignore"):
+        want, tol = int4.attention(q, k, v, tables, lens, 0.1)
+    assert np.isnan(want[0, 1, 7]).all() and np.isnan(want).sum() == 128
+    _same_nan_and_close(out, want, tol)
+
+
+@pytest.mark.parametrize("q_len,hq,hkv", [(1, 12, 2), (4, 12, 2), (3, 6, 2)])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("back", [0, 1, 2])
+def test_decode_keeps_a_bad_row_to_the_queries_that_see_it(q_len, hq, hkv, which, back):
+    # one group of a row, `back` tokens from the end, is NaN (what the append makes of a NaN)
+    lens = [70, 33, 17, 48]
+    k, v, tables, lens, q = _case(lens, 16, hq, hkv, q_len, seed=29)
+    pool = k if which == "k" else v
+    for b in (0, 1, 3):
+        t = int(lens[b]) - 1 - back
+        row = pool[tables[b, t // 16], 1, t % 16]
+        row[32:48] = 0
+        row[72:76] = (0xFF, 0x7F, 0xFF, 0x7F)
+    out = _decode(k, v, tables, lens, q, 0.1)
+    with np.errstate(invalid="ignore"):
+        want, tol = int4.attention(q, k, v, tables, lens, 0.1)
+    sees = min(q_len, back + 1)
+    assert np.isnan(want).sum() == 3 * sees * (hq // hkv) * (128 if which == "k" else 32)
+    _same_nan_and_close(out, want, tol)
+
+
+def test_fused_append_of_a_nan_row():
+    # the last of three new tokens is NaN in one group: earlier drafts and other heads do not see it
+    k, v, tables, lens, q = _case([70, 35, 18], 16, 8, 2, 3, seed=33)
+    rng = np.random.default_rng(4)
+    kn, vn = (_rows(rng, (9, 2)) for _ in range(2))
+    vn[2, 0, 40] = np.nan
+    vn[5, 1, 127] = np.inf
+    kd, vd, qd = _dev(k), _dev(v), _dev(q)
+    out = torch.empty_like(qd)
+    pkv.paged_attn_decode_append_int4(out, qd, _dev(kn), _dev(vn), kd, vd, _dev(tables), _dev(lens),
+                                      0.1, pkv.make_workspace(3, 3, 8, 2))
+    assert pkv.device_error(clear=True) == 0
+    int4.append(kn, vn, _new_slots(tables, lens, 3, 16), k, v)
+    assert np.array_equal(kd.cpu().numpy(), k) and np.array_equal(vd.cpu().numpy(), v)
+    with np.errstate(invalid="ignore"):
+        want, tol = int4.attention(q, k, v, tables, lens, 0.1)
+    assert np.isnan(want).sum() == 2 * 4 * 32
+    _same_nan_and_close(out, want, tol)
+
+
+def test_two_captured_decodes_at_once_with_a_workspace_each():
+    cases = [_case(n, 16, 12, 2, 1, seed=i) for i, n in enumerate(([3000, 900], [2500, 17, 1200]))]
+    want = [int4.attention(c[4], *c[:4], 0.1) for c in cases]
+    runs = []
+    for k, v, tables, lens, q in cases:
+        a = [_dev(x) for x in (q, k, v, tables, lens)]
+        out, ws = torch.empty_like(a[0]), pkv.make_workspace(len(lens), 1, 12, 2)
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            for _ in range(4):
+                pkv.paged_attn_decode_int4(out, *a, 0.1, ws)
+        runs.append((graph, stream, out, a, ws))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream, out, *_ in runs:
+            with torch.cuda.stream(stream):
+                out.fill_(float("nan"))
+                graph.replay()
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == 0
+    for (_, _, out, *_), w in zip(runs, want):
+        _close(out, *w)
+
+
+def test_a_call_runs_on_the_current_stream():
+    # the query arrives on a side stream behind a long copy; a launch elsewhere would miss it
+    k, v, tables, lens, q = _case([300, 47], seed=41)
+    rng = np.random.default_rng(1)
+    x = _rows(rng, (2, 2))
+    a = [_dev(t) for t in (k, v, tables, lens, x, _new_slots(tables, lens, 1, 16))]
+    src, qd = _dev(q), torch.zeros(q.shape, dtype=torch.float16, device=DEV)
+    big = torch.zeros(1 << 28, dtype=torch.float32, device=DEV)
+    out, ws = torch.empty_like(qd), pkv.make_workspace(2, 1, 12, 2)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for _ in range(8):
+            big.add_(1)
+        qd.copy_(src)
+        rows = a[4] + 0
+        pkv.kv_append_int4(rows, rows, a[5], a[0], a[1])
+        pkv.paged_attn_decode_int4(out, qd, *a[:4], 0.1, ws)
+    torch.cuda.synchronize()
+    int4.append(x, x, _new_slots(tables, lens, 1, 16), k, v)
+    want, tol = int4.attention(q, k, v, tables, lens, 0.1)
+    _close(out, want, tol)
+
+
 # ----------------------------------------------------------------------------- refusals
 def test_binding_refuses_what_the_library_cannot_see():
     k = torch.zeros(4, 2, 16, 80, dtype=torch.uint8, device=DEV)
