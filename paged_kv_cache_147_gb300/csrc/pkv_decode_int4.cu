@@ -45,7 +45,12 @@
 //    to zero.
 //  * More than 8 rows: two to four warps take a stage, 8 rows each (and a copy of their own; all
 //    but the first come from L2). Two row tiles in one warp save the second masking of the codes
-//    but not the registers: with two, four drafts of 6 heads took 36 us, with one 27.
+//    but not the registers: with two, four drafts of 6 heads took 36 us, with one 25.
+// Where it stands: 64 sequences of 16384 tokens, 8 kv heads, 8 queries each take 134 us (5.0 TB/s,
+// 73 % of the copy rate). The loads alone take 104, the arithmetic alone 106; together they share
+// the SM's issue slots (50 % used, ALU 47 %, tensor 34 %, shared memory 34 %), and neither 12
+// warps instead of 8 (130) nor fewer instructions (the queries' operands loaded half as often: 140)
+// change much.
 #include <cuda_fp16.h>
 
 #include "pkv_decode_common.cuh"
@@ -579,30 +584,27 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
             const uint4 p1 = ld_shared_v4(kb + (g + 8) * kInt4Row + kInt4Params);
             x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.f;
             mma_f16(x[h], kz[2 * h], kz[2 * h + 1], kz[2 * h], kz[2 * h + 1], qc.x, qc.y);
-            // two groups at a time: their products do not wait on each other
+            // all groups at a time: their products do not wait on each other
+            float t[4][4];
 #pragma unroll
-            for (int gp = 0; gp < 4; gp += 2) {
-              float t[2][4];
+            for (int part = 0; part < 2; ++part) {
+              const uint32_t m = part ? 0x03c003c0u : 0x003c003cu;
 #pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                const uint32_t m = part ? 0x03c003c0u : 0x003c003cu;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint32_t w0 = kw[gp + i][0], w1 = kw[gp + i][1];
-                  const uint2 b = ld_shared_v2(qb + (gp + i) * 512 + part * 8);
-                  if (part == 0) t[i][0] = t[i][1] = t[i][2] = t[i][3] = 0.f;
-                  mma_f16(t[i], (w0 << 2) & m, (w1 << 2) & m, (w0 >> 6) & m, (w1 >> 6) & m, b.x, b.y);
-                }
+              for (int gr = 0; gr < 4; ++gr) {
+                const uint32_t w0 = kw[gr][0], w1 = kw[gr][1];
+                const uint2 b = ld_shared_v2(qb + gr * 512 + part * 8);
+                if (part == 0) t[gr][0] = t[gr][1] = t[gr][2] = t[gr][3] = 0.f;
+                mma_f16(t[gr], (w0 << 2) & m, (w1 << 2) & m, (w0 >> 6) & m, (w1 >> 6) & m, b.x, b.y);
               }
+            }
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float s0 = __low2float(as_half2(u4_word(p0, gp + i)));
-                const float s1 = __low2float(as_half2(u4_word(p1, gp + i)));
-                x[h][0] = fmaf(s0, t[i][0], x[h][0]);
-                x[h][1] = fmaf(s0, t[i][1], x[h][1]);
-                x[h][2] = fmaf(s1, t[i][2], x[h][2]);
-                x[h][3] = fmaf(s1, t[i][3], x[h][3]);
-              }
+            for (int gr = 0; gr < 4; ++gr) {
+              const float s0 = __low2float(as_half2(u4_word(p0, gr)));
+              const float s1 = __low2float(as_half2(u4_word(p1, gr)));
+              x[h][0] = fmaf(s0, t[gr][0], x[h][0]);
+              x[h][1] = fmaf(s0, t[gr][1], x[h][1]);
+              x[h][2] = fmaf(s1, t[gr][2], x[h][2]);
+              x[h][3] = fmaf(s1, t[gr][3], x[h][3]);
             }
           }
 
@@ -809,19 +811,25 @@ Variant variant4() {
                  false, (NCS * RS + 2) * 32, &Smem4<NCS, RS, ND>::bytes};
 }
 
-// The variant for R query rows. Four consumer warps a CTA and two CTAs while the registers of 8
-// or 16 rows allow (a multiple of four of them per SM: one of its four schedulers takes every
-// fourth warp); beyond, one CTA of 9 or 8. Measured against others that fit, us (four drafts of 6
-// heads, mixed lengths to 2048, cut to the rows; 16 sequences of 4096 tokens, 8 kv heads):
-//   9..16 rows   <2, 2, 3, 2> 20.4 / 43.1, <4, 2, 3, 1> 22.3 / 45.2, <6, 2, 2, 1> 24.5 / 42.0
-//   17..24 rows  <3, 3, 3, 1> 27.2 / 65.3, <4, 3, 2, 1> 28.8 / 57.9
-//   25..32 rows  <2, 4, 3, 1> 31.1 / 77.7, <3, 4, 2, 1> 33.7 / 70.5
+// The variant for R query rows. Four consumer warps a CTA and two CTAs for up to 16 rows, one CTA
+// of 12 beyond (a multiple of four of them per SM: one of its four schedulers takes every fourth
+// warp). Measured against others that fit, us (64 sequences of 16 to 2048 tokens, 2 kv heads; 16 of
+// 4096 tokens, 8 kv heads):
+//   16 rows   <2, 2, 3, 2> 20.4 / 43.4, <4, 2, 3, 1> 20.7 / 46.8, <6, 2, 2, 1> 22.3 / 43.3
+//   24 rows   <4, 3, 2, 1> 25.2 / 59.6, <3, 3, 3, 1> 27.5 / 69.6
+//   32 rows   <3, 4, 2, 1> 29.6 / 73.7, <2, 4, 3, 1> 30.8 / 78.6
+// Up to 8 rows, 12 warps in one CTA keep more in flight than two CTAs of 4, but hand a segment over
+// only once per SM and merge 12 states for it. That pays where a CTA has a segment or two, of many
+// stages: no more units than SMs, tables for 4096 tokens or more. <12, 1, 2, 1> against <4, 1, 3, 2>:
+// 16 sequences of 4096 tokens with 8 kv heads 25.7 against 27.0, one of 65536 30.8 against 35.8,
+// two of 131072 with one kv head 34.1 against 41.1; but two of about 70 tokens 7.3 against 6.5, and
+// 512 units of mixed lengths 65 against 51.
 template <bool APPEND>
-Variant choose4(int R) {
-  return R <= 8    ? variant4<4, 1, 3, 2, APPEND>()
+Variant choose4(int R, bool few_long) {
+  return R <= 8    ? (few_long ? variant4<12, 1, 2, 1, APPEND>() : variant4<4, 1, 3, 2, APPEND>())
          : R <= 16 ? variant4<2, 2, 3, 2, APPEND>()
-         : R <= 24 ? variant4<3, 3, 3, 1, APPEND>()
-                   : variant4<2, 4, 3, 1, APPEND>();
+         : R <= 24 ? variant4<4, 3, 2, 1, APPEND>()
+                   : variant4<3, 4, 2, 1, APPEND>();
 }
 
 int launch_decode_int4(void* out, const void* q, const void* k_new, const void* v_new,
@@ -856,7 +864,8 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
   const int newkv_bytes = append ? 2 * q_len * 512 : 0;
-  Variant v = append ? choose4<true>(R) : choose4<false>(R);
+  const bool few_long = num_seqs * Hkv <= sm_count() && max_ctx >= 4096;
+  Variant v = append ? choose4<true>(R, few_long) : choose4<false>(R, few_long);
   size_t smem = v.smem(R, num_seqs, newkv_bytes);
   if (append && smem > kMaxSmem) {   // thousands of sequences with 8 and more new tokens each
     v = variant4<2, 4, 2, 1, true>();

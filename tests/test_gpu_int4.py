@@ -354,6 +354,24 @@ def test_fused_append_of_9_to_32_rows(lens, bs, hq, hkv, q_len):
     test_fused_append_decode_matches_oracle(lens, bs, hq, hkv, q_len)
 
 
+@pytest.mark.parametrize("lens,bs,hq,hkv,q_len", [
+    ([5000, 30], 16, 12, 2, 1),                       # few units, long tables: 12 warps share each
+    ([4300, 0, 77, 4096], 64, 8, 4, 4),
+    ([9000], 256, 8, 1, 1),
+    ([33, 1], 4096 // 16, 3, 3, 2),                   # two blocks of 256: short contexts in there
+])
+def test_fused_append_of_few_sequences_with_long_tables(lens, bs, hq, hkv, q_len):
+    if max(lens) < 4096:   # widen the tables without lengthening the contexts
+        k, v, tables, lens, q = _case(lens, bs, hq, hkv, q_len, seed=77)
+        wide = np.full((len(lens), 20), -1, np.int32)
+        wide[:, :tables.shape[1]] = tables
+        out = _decode(k, v, wide, lens, q, 0.09)
+        want, tol = int4.attention(q, k, v, wide, lens, 0.09)
+        _close(out, want, tol)
+    else:
+        test_fused_append_decode_matches_oracle(lens, bs, hq, hkv, q_len)
+
+
 @pytest.mark.parametrize("hq,hkv,q_len", [(24, 1, 1), (1, 1, 24), (4, 1, 8), (1, 1, 32)])
 def test_fused_append_of_as_many_sequences_as_a_call_takes(hq, hkv, q_len):
     # 4096 sequences: two of three empty (padding), the others short
