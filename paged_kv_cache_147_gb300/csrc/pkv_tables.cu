@@ -13,7 +13,8 @@
 // blocks; the cluster barrier keeps the lengths and the stack's count, updated in place at the
 // end, from changing under a CTA that has not read them yet. Past kClusterTokens tokens (or
 // kClusterBlocks table entries to cut) one cluster's 8 SMs no longer write fast enough: a grid
-// over the whole GPU does the tokens and blocks first and a second, one-CTA launch the rest.
+// over the whole GPU does the tokens and blocks first and a second, one-CTA launch the rest; it
+// starts beside the first (dependent launch), scans, and writes when the first is done.
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
   const int64_t cap = static_cast<int64_t>(a.max_blocks) << sh;
   unsigned int bad = 0;
 
+  if (TOKENS && !STATE) griddep_launch_dependents();   // the second launch scans meanwhile
   int count = *a.free_count;
   if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = 0; }
   if (tid == 0) used_s = 0;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
   }
   if (bad) atomicOr(a.err, bad);
   if (STATE) {
-    if (TOKENS) cluster_wait();
+    if (TOKENS) cluster_wait(); else griddep_wait();
     for (int b = rank * kThreads + tid; b < n; b += ctas * kThreads)
       if (len[b] >= 0) a.lens[b] = len[b] + a.arg[b];
     if (rank == 0 && tid == 0) *a.free_count = count - used;
@@ -248,6 +250,7 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
   const int64_t cap = static_cast<int64_t>(a.max_blocks) << sh;
   unsigned int bad = 0;
 
+  if (BLOCKS && !STATE) griddep_launch_dependents();
   int count = *a.free_count;
   if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = a.num_blocks; }
   const int per = (n + kThreads - 1) / kThreads;
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
   }
   if (bad) atomicOr(a.err, bad);
   if (STATE) {
-    if (BLOCKS) cluster_wait();
+    if (BLOCKS) cluster_wait(); else griddep_wait();
     for (int b = rank * kThreads + tid; b < n; b += ctas * kThreads)
       if (keep[b] >= 0) a.lens[b] = keep[b];
     if (rank == 0 && tid == 0 && freed > 0) *a.free_count = count + freed;
@@ -297,9 +300,10 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
 
 int launch_status() { return cuda_status(cudaGetLastError()); }
 
-// `cluster` > 0: one cluster of that many CTAs; 0: `ctas` CTAs on their own.
+// `cluster` > 0: one cluster of that many CTAs; 0: `ctas` CTAs on their own; `second`: may start
+// while the launch before it, its own first half, still runs.
 int launch(const void* fn, const TableArgs& a, size_t smem, int cluster, int ctas,
-           cudaStream_t stream) {
+           cudaStream_t stream, bool second = false) {
   cudaError_t e = cudaSuccess;
   if (smem > 47 * 1024)   // past the default limit, beside the kernels' own 300 bytes
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -311,12 +315,17 @@ int launch(const void* fn, const TableArgs& a, size_t smem, int cluster, int cta
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  if (second) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = cluster ? 1 : 0;
+  cfg.numAttrs = second || cluster ? 1 : 0;
   void* params[1] = {const_cast<TableArgs*>(&a)};
   return cuda_status(cudaLaunchKernelExC(&cfg, fn, params));
 }
@@ -373,7 +382,7 @@ int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_
   const int st =
       launch(reinterpret_cast<const void*>(&extend_kernel<true, false>), a, smem, 0, ctas, s);
   if (st != PKV_OK) return st;
-  return launch(reinterpret_cast<const void*>(&extend_kernel<false, true>), a, smem, 0, 1, s);
+  return launch(reinterpret_cast<const void*>(&extend_kernel<false, true>), a, smem, 0, 1, s, true);
 }
 
 int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* keep_lens,
@@ -401,7 +410,7 @@ int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int3
   const int st =
       launch(reinterpret_cast<const void*>(&truncate_kernel<true, false>), a, smem, 0, ctas, s);
   if (st != PKV_OK) return st;
-  return launch(reinterpret_cast<const void*>(&truncate_kernel<false, true>), a, smem, 0, 1, s);
+  return launch(reinterpret_cast<const void*>(&truncate_kernel<false, true>), a, smem, 0, 1, s, true);
 }
 
 }  // extern "C"

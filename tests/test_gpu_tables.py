@@ -150,6 +150,42 @@ def test_captured_in_a_graph_and_replayed():
     assert pkv.device_error(clear=True) == 0
 
 
+def test_wide_calls_captured_in_a_graph_and_replayed():
+    # past one cluster's sizes: two launches a call, the second one's scan beside the first; three
+    # calls in a row, lengths and keep_lens written by a kernel right before each
+    rng = np.random.default_rng(19)
+    bs, B, cap = 16, 300, 90000
+    lens = rng.integers(0, 40, B)
+    tables, lens, free, count = _state(rng, lens, bs, 60, 26000)
+    new = rng.integers(0, 500, B).astype(np.int32)
+    assert new.sum() > 32768 and min(B * 60, len(free)) > 16384
+    d = [_dev(x) for x in (tables, lens, free, np.array([count], np.int32))]
+    news, keep, zero = _dev(new), torch.empty(B, dtype=torch.int32, device=DEV), _dev(0 * new)
+    out = pkv.extend_tables(d[0].clone(), d[1].clone(), zero, bs, d[2].clone(), d[3].clone(), cap)
+
+    def steps():
+        pkv.extend_tables(d[0], d[1], news + zero, bs, d[2], d[3], cap, out=out)
+        torch.div(d[1], 2, rounding_mode="floor", out=keep)
+        pkv.truncate_tables(d[0], d[1], keep, bs, d[2], d[3])
+        torch.sub(d[1], d[1], out=keep)
+        pkv.truncate_tables(d[0], d[1], keep, bs, d[2], d[3])
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        steps()
+    for run in (graph.replay, steps, graph.replay):
+        run()
+        t, l, c, slots, seqs, pos, cu, refused = step.extend(tables, lens, new, bs, free, count, cap)
+        assert not refused
+        for keep_h in (l // 2, 0 * l):
+            t, l, free, c = step.truncate(t, l, keep_h.astype(np.int32), bs, free, c)
+        tables, lens, count = t, l, c
+        for got, w in zip(d + list(out), (t, l, free, np.array([c]), slots, seqs, pos, cu)):
+            assert np.array_equal(got.cpu().numpy(), w)
+    assert pkv.device_error(clear=True) == 0
+
+
 def test_binding_refuses_wrong_types_and_shapes():
     z = torch.zeros(2, 4, dtype=torch.int32, device=DEV)
     n, one = z[0, :2].clone(), z[0, :1].clone()
