@@ -46,7 +46,7 @@
 //  * More than 8 rows: two to four warps take a stage, 8 rows each (and a copy of their own; all
 //    but the first come from L2). Two row tiles in one warp save the second masking of the codes
 //    but not the registers: with two, four drafts of 6 heads took 36 us, with one 25.
-// Where it stands: 64 sequences of 16384 tokens, 8 kv heads, 8 queries each take 134 us (5.0 TB/s,
+// Where it stands: 32 sequences of 16384 tokens, 8 kv heads, 8 queries each take 134 us (5.0 TB/s,
 // 73 % of the copy rate). The loads alone take 104, the arithmetic alone 106; together they share
 // the SM's issue slots (50 % used, ALU 47 %, tensor 34 %, shared memory 34 %), and neither 12
 // warps instead of 8 (130) nor fewer instructions (the queries' operands loaded half as often: 140)

@@ -44,57 +44,123 @@ __device__ __forceinline__ uint32_t int4_exact_code(float x, float lo, float s, 
   return min(c + (rem > 0.f || (rem == 0.f && (c & 1u)) ? 1u : 0u), 15u);
 }
 
-__device__ __forceinline__ void int4_quantise(const uint4& h, uint32_t& codes, uint32_t& params) {
-  const __half2* p = reinterpret_cast<const __half2*>(&h);
-  const __half2 lo2 = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
-  const __half2 hi2 = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
-  // (min, -max) in one register: one shuffle and one packed minimum per step
-  __half2 mm = __halves2half2(__hmin_nan(__low2half(lo2), __high2half(lo2)),
-                              __hneg(__hmax_nan(__low2half(hi2), __high2half(hi2))));
-  mm = __hmin2_nan(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
-  mm = __hmin2_nan(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
-  const float lo = __low2float(mm), hi = -__high2float(mm);
+// Two fp32 numbers in a register pair: one instruction for both.
+__device__ __forceinline__ uint64_t f32x2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 f32x2_parts(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// (s, z) of a group from (min, -max) of its elements; false for a NaN or an infinity in there.
+__device__ __forceinline__ bool int4_scale(__half2 mm, uint32_t& params, float& lo, float& sf) {
+  lo = __low2float(mm);
+  const float hi = -__high2float(mm);
   const float range = hi - lo;
-  if (!(range <= 131008.f)) {   // a NaN or an infinity
-    codes = 0u;
+  if (!(range <= 131008.f)) {
     params = 0x7fff7fffu;
-    return;
+    return false;
   }
   constexpr float kInv15 = 1.f / 15.f;
   const float q15 = range * kInv15;
   __half s = __float2half_ru(fmaf(fmaf(-15.f, q15, range), kInv15, q15));
-  float sf = __half2float(s);
+  sf = __half2float(s);
   if (fmaf(15.f, sf, lo) > 65504.f) {
     s = __hmin(s, __float2half_rz(__fdiv_rn(65504.f - lo, 15.f)));
     sf = __half2float(s);
   }
   const __half2 sz = __halves2half2(s, __low2half(mm));
   params = *reinterpret_cast<const uint32_t*>(&sz);
-  const float r = sf > 0.f ? __fdividef(1.f, sf) : 0.f;   // s is a multiple of 2^-24
-  float x[8], off = 0.f;
+  return true;
+}
+
+// The codes of 8 elements, r the approximate 1 / s (0 where s is 0).
+__device__ __forceinline__ uint32_t int4_codes(const uint4& h, float lo, float sf, float r) {
+  const __half2* p = reinterpret_cast<const __half2*>(&h);
+  const uint64_t nlo2 = f32x2(-lo, -lo), r2 = f32x2(r, r), magic2 = f32x2(kInt4Magic, kInt4Magic),
+                 minus2 = f32x2(-1.f, -1.f);
+  float off = 0.f;
   uint32_t c = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(p[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = x[i] - lo;
-    const float m = fmaf(d, r, kInt4Magic);
-    off = fmaxf(off, fabsf(fmaf(d, r, kInt4Magic - m)));
-    c += __float_as_uint(m) << (4 * i);
+    const uint64_t d = f32x2_add(f32x2(f.x, f.y), nlo2);
+    const uint64_t m = f32x2_fma(d, r2, magic2);
+    const float2 e = f32x2_parts(f32x2_fma(d, r2, f32x2_fma(m, minus2, magic2)));
+    const float2 mf = f32x2_parts(m);
+    off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
+    c += (__float_as_uint(mf.x) << (8 * i)) + (__float_as_uint(mf.y) << (8 * i + 4));
   }
   // the magic number's own bits, shifted and summed
   constexpr uint32_t kBias = 0x4b400000u + (0x4b400000u << 4) + (0x4b400000u << 8);
-  codes = c - kBias;
+  c -= kBias;
   if (off > 0.5f - 1e-5f) {
-    codes = 0u;
+    c = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      codes |= int4_exact_code(x[i], lo, sf, (x[i] - lo) * r) << (4 * i);
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(p[i]);
+      c |= int4_exact_code(f.x, lo, sf, (f.x - lo) * r) << (8 * i);
+      c |= int4_exact_code(f.y, lo, sf, (f.y - lo) * r) << (8 * i + 4);
+    }
   }
+  return c;
+}
+
+// s is a multiple of 2^-24: its reciprocal does not overflow.
+__device__ __forceinline__ float int4_reciprocal(float sf) {
+  return sf > 0.f ? __fdividef(1.f, sf) : 0.f;
+}
+
+// (min, -max) of 8 elements: one shuffle and one packed minimum take a step for both.
+__device__ __forceinline__ __half2 int4_extremes(const uint4& h) {
+  const __half2* p = reinterpret_cast<const __half2*>(&h);
+  const __half2 lo2 = __hmin2_nan(__hmin2_nan(p[0], p[1]), __hmin2_nan(p[2], p[3]));
+  const __half2 hi2 = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+  return __halves2half2(__hmin_nan(__low2half(lo2), __high2half(lo2)),
+                        __hneg(__hmax_nan(__low2half(hi2), __high2half(hi2))));
+}
+
+__device__ __forceinline__ void int4_quantise(const uint4& h, uint32_t& codes, uint32_t& params) {
+  __half2 mm = int4_extremes(h);
+  mm = __hmin2_nan(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
+  mm = __hmin2_nan(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
+  float lo, sf;
+  codes = 0u;
+  if (int4_scale(mm, params, lo, sf)) codes = int4_codes(h, lo, sf, int4_reciprocal(sf));
+}
+
+// A whole group (32 elements) in one thread: the same bytes.
+__device__ __forceinline__ void int4_quantise_group(const uint4 (&h)[4], uint4& codes,
+                                                    uint32_t& params) {
+  const __half2* p = reinterpret_cast<const __half2*>(h);
+  __half2 lo2 = p[0], hi2 = p[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) {
+    lo2 = __hmin2_nan(lo2, p[i]);
+    hi2 = __hmax2_nan(hi2, p[i]);
+  }
+  const __half2 mm = __halves2half2(__hmin_nan(__low2half(lo2), __high2half(lo2)),
+                                    __hneg(__hmax_nan(__low2half(hi2), __high2half(hi2))));
+  float lo, sf;
+  codes = make_uint4(0u, 0u, 0u, 0u);
+  if (!int4_scale(mm, params, lo, sf)) return;
+  const float r = int4_reciprocal(sf);
+  codes = make_uint4(int4_codes(h[0], lo, sf, r), int4_codes(h[1], lo, sf, r),
+                     int4_codes(h[2], lo, sf, r), int4_codes(h[3], lo, sf, r));
 }
 
 // Codes in the low halves of a word's two 16-bit halves, as fp16 (exact): c_lo takes bits 0-3,

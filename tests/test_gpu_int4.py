@@ -111,6 +111,29 @@ def test_append_bytes_over_all_magnitudes():
     assert np.array_equal(kd.cpu().numpy(), kc) and np.array_equal(vd.cpu().numpy(), vc)
 
 
+@pytest.mark.parametrize("hkv,T,bs", [(1, 16389, 16), (8, 2050, 64), (3, 5465, 32)])
+def test_large_appends_write_the_same_bytes(hkv, T, bs):
+    # 16384 rows and more go a group per thread: any bits (NaN and infinities among them), odd
+    # numbers of tokens, skipped and refused slots
+    rng = np.random.default_rng(T)
+    x = rng.integers(0, 1 << 16, (2, T, hkv, 128)).astype(np.uint16).view(np.float16)
+    x[:, ::2] = rng.standard_normal(x[:, ::2].shape).astype(np.float16)
+    x[:, 5] = 0.5                                            # s = 0
+    x[:, 7, :, :32] = np.arange(32).astype(np.float16)      # ties between codes
+    nb = T // bs + 2
+    slots = rng.permutation(nb * bs)[:T].astype(np.int64)
+    slots[[3, 4, T - 1]] = -1
+    slots[6] = nb * bs + 5
+    pools = [rng.integers(0, 256, (nb, hkv, bs, 80), dtype=np.uint8) for _ in range(2)]
+    d = [_dev(p) for p in pools]
+    pkv.kv_append_int4(_dev(x[0]), _dev(x[1]), _dev(slots), *d)
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == pkv.DEVERR_SLOT
+    int4.append(x[0], x[1], slots, *pools)
+    for got, want in zip(d, pools):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_append_skips_a_slot_past_the_pool_and_says_so():
     rng = np.random.default_rng(2)
     k = _rows(rng, (3, 2))
