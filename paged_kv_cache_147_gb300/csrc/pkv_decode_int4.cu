@@ -63,6 +63,7 @@ namespace {
 
 constexpr int kTile = kChunk * kInt4Row;     // one chunk's K (or V): 1280 bytes
 constexpr int kStage4 = 4 * kTile;           // K of two chunks, V of two chunks
+constexpr int kNewRow = 2 * kInt4Row;        // a new token's K and V
 // Per-segment cost in chunks (see kSegCost): queries, hand-off and merge of a segment take a CTA
 // ~1.5 us, the time of a dozen chunks (70B mixed lengths: 62 us with 4, 55 with 8, 51 with 12).
 constexpr int kSeg4 = 12;
@@ -93,8 +94,8 @@ struct Smem4 {
   static constexpr int kQTile = 5 * 512;              // 8 rows: fragments of 4 groups, constants
   static constexpr int kQBuf = RS * kQTile;
   static constexpr int kQ = NCS * RS * ND * kStage4;
-  static constexpr int kBars = kQ + 2 * kQBuf;        // qfull[2], qempty[2], sdone, sfree
-  static constexpr int kFlags = kBars + 6 * 8;
+  static constexpr int kBars = kQ + 2 * kQBuf;        // qfull[2], qempty[2], sdone, sfree, nfull[2]
+  static constexpr int kFlags = kBars + 8 * 8;
   static constexpr int kState = (kFlags + 64 + 15) & ~15;   // [NCS] segment states
   __host__ __device__ static int state_floats(int R) { return NCS * R * (kSt + 2); }
   __host__ __device__ static int seq_off(int R) { return kState + state_floats(R) * 4; }
@@ -280,6 +281,7 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
   const uint32_t bar_qempty = bar_qfull + 2 * 8;
   const uint32_t bar_sdone = bar_qempty + 2 * 8;
   const uint32_t bar_sfree = bar_sdone + 8;
+  const uint32_t bar_nfull = bar_sfree + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kFlags);
   int* npend_s = reinterpret_cast<int*>(smem + L::kFlags) + 1;   // then 2 x (b, h, nb)
   volatile int* fast_s = reinterpret_cast<volatile int*>(smem + L::kFlags) + 8;
@@ -300,6 +302,7 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_qfull + s * 8, 1);
       mbar_init(bar_qempty + s * 8, NCW);
+      mbar_init(bar_nfull + s * 8, 1);
     }
     mbar_init(bar_sdone, NCW);
     mbar_init(bar_sfree, 1);
@@ -423,17 +426,37 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
                                 static_cast<uint32_t>(__half_as_ushort(lo)) << 16,
                                 __float_as_uint(r0), __float_as_uint(r1)));
       }
-      if (APPEND) {   // new rows: K in lanes 0-15, V in 16-31
-        const uint32_t nkv = sbase + L::newkv_off(a.R, B) + (kk & 1) * a.q_len * 512;
-        const __half* src = lane < 16 ? a.k_new : a.v_new;
-        for (int i = 0; i < a.q_len; ++i) {
-          const int64_t row = (static_cast<int64_t>(sg.b) * a.q_len + i) * a.Hkv + sg.h;
-          st_shared_v4(nkv + i * 512 + lane * 16,
-                       __ldg(reinterpret_cast<const uint4*>(src + row * kD) + (lane & 15)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_qfull + (kk & 1) * 8);
+      if (!APPEND) return;
+      // the segment's new rows, K in lanes 0-15, V in 16-31: quantised once, into the pool and for
+      // the consumers, who need them when they come to the rows' chunks
+      const uint32_t nkv = sbase + L::newkv_off(a.R, B) + (kk & 1) * a.q_len * kNewRow;
+      const int which = lane >> 4, p = lane & 15;
+      const __half* src = which ? a.v_new : a.k_new;
+      for (int i = 0; i < a.q_len; ++i) {
+        const int pos = slen[sg.b] - a.q_len + i;
+        const int c = pos >> 4;
+        if (pos < 0 || c < sg.c0 || c >= sg.c1) continue;
+        const int id = __ldg(a.block_tables + static_cast<int64_t>(sg.b) * a.max_blocks +
+                             (c >> a.bs_shift));
+        const int64_t row = (static_cast<int64_t>(sg.b) * a.q_len + i) * a.Hkv + sg.h;
+        uint32_t codes, params;
+        int4_quantise(__ldg(reinterpret_cast<const uint4*>(src + row * kD) + p), codes, params);
+        const uint32_t to = nkv + i * kNewRow + which * kInt4Row;
+        st_shared_u32(to + 4 * p, codes);
+        if ((p & 3) == 0) st_shared_u32(to + kInt4Params + p, params);
+        if (id >= 0 && id < a.num_blocks) {
+          const int64_t prow = (static_cast<int64_t>(id) * a.Hkv + sg.h) * a.block_size +
+                               (pos & (a.block_size - 1));
+          uint32_t* pool = reinterpret_cast<uint32_t*>(
+              reinterpret_cast<uint8_t*>(which ? a.v_pool : a.k_pool) + prow * kInt4Row);
+          pool[p] = codes;
+          if ((p & 3) == 0) pool[(kInt4Params + p) / 4] = params;
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_qfull + (kk & 1) * 8);
+      if (lane == 0) mbar_arrive(bar_nfull + (kk & 1) * 8);
     };
     Seg s;
     bool has = cur.first(begin, s);
@@ -542,30 +565,16 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
           const int nk = two ? 2 * kChunk : kChunk;
           const bool full = two && (c + 2) * kChunk <= Lc - a.q_len + 1;
           if (APPEND && (c * kChunk + nk > Lc - a.q_len)) {
-            // new rows of these chunks: lanes 0-15 quantise the K row, 16-31 the V row, into the
-            // stage's tiles and into the pool (warps that share a stage write the same bytes)
+            // new rows of these chunks go into the stage's tiles
             const int first_new = Lc - a.q_len;
-            const uint32_t nkv = sbase + L::newkv_off(a.R, B) + qs * a.q_len * 512;
-            const int which = lane >> 4, p = lane & 15;
+            const uint32_t nkv = sbase + L::newkv_off(a.R, B) + qs * a.q_len * kNewRow;
+            if (!mbar_wait(bar_nfull + qs * 8, (k >> 1) & 1, abort)) flag_timeout(a, abort);
             for (int i = 0; i < a.q_len; ++i) {
-              const int pos = first_new + i;
-              const int tk = pos - c * kChunk;
-              if (pos < 0 || tk < 0 || tk >= nk) continue;
-              uint32_t codes, params;
-              int4_quantise(ld_shared_v4(nkv + i * 512 + which * 256 + p * 16), codes, params);
-              const uint32_t row = stK + which * 2 * kTile + tk * kInt4Row;
-              st_shared_u32(row + 4 * p, codes);
-              if ((p & 3) == 0) st_shared_u32(row + kInt4Params + p, params);
-              const int id = __ldg(a.block_tables + static_cast<int64_t>(s.b) * a.max_blocks +
-                                   pos / a.block_size);
-              if (id >= 0 && id < a.num_blocks) {
-                const int64_t prow = (static_cast<int64_t>(id) * a.Hkv + s.h) * a.block_size +
-                                     pos % a.block_size;
-                uint32_t* pool = reinterpret_cast<uint32_t*>(
-                    reinterpret_cast<uint8_t*>(which ? a.v_pool : a.k_pool) + prow * kInt4Row);
-                pool[p] = codes;
-                if ((p & 3) == 0) pool[(kInt4Params + p) / 4] = params;
-              }
+              const int tk = first_new + i - c * kChunk;
+              if (first_new + i < 0 || tk < 0 || tk >= nk || lane >= kInt4Row / 4) continue;
+              const uint32_t from = nkv + i * kNewRow + 4 * lane, to = stK + tk * kInt4Row + 4 * lane;
+              st_shared_u32(to, ld_shared_u32(from));
+              st_shared_u32(to + 2 * kTile, ld_shared_u32(from + kInt4Row));
             }
             __syncwarp();
           }
@@ -863,7 +872,7 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   const WsLayout ws = ws_layout(num_seqs, Hkv, R);
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
-  const int newkv_bytes = append ? 2 * q_len * 512 : 0;
+  const int newkv_bytes = append ? 2 * q_len * kNewRow : 0;
   const bool few_long = num_seqs * Hkv <= sm_count() && max_ctx >= 4096;
   Variant v = append ? choose4<true>(R, few_long) : choose4<false>(R, few_long);
   size_t smem = v.smem(R, num_seqs, newkv_bytes);
