@@ -126,8 +126,10 @@ int pkv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const int3
  * (sequence, kv head) arrival counters. Size it with pkv_decode_workspace_bytes() (for the
  * current device; the size depends on its SM count) and zero it once with
  * pkv_workspace_init() before first use; every decode call leaves the counters zeroed again.
- * One workspace must not be used by two calls that run concurrently. After a call that set
- * PKV_DEVERR_TIMEOUT, re-initialise it. */
+ * A workspace sized for the largest num_seqs and the largest q_len together serves smaller calls
+ * too, one after the other, if all of them are given the same workspace_bytes. One workspace must
+ * not be used by two calls that run concurrently. After a call that set PKV_DEVERR_TIMEOUT,
+ * re-initialise it. */
 size_t pkv_decode_workspace_bytes(int num_seqs, int q_len, int num_q_heads, int num_kv_heads,
                                   int head_dim);
 

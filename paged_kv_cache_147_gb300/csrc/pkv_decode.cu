@@ -1325,7 +1325,7 @@ int launch_decode(bool ring, void* out, const void* q, const void* k_new, const 
   if (rows >= (1ll << 31) || static_cast<int64_t>(num_seqs) * Hkv * ((max_ctx + kChunk - 1) / kChunk + kSegCost) >= (1ll << 30))
     return PKV_EINVAL;
   if (num_blocks == 0) return PKV_EINVAL;
-  const WsLayout ws = ws_layout(num_seqs, Hkv, R);
+  const WsLayout ws = ws_layout(num_seqs, Hkv, R, workspace_bytes);
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
   const int mt = R <= 16 ? 1 : 2;
@@ -1486,7 +1486,7 @@ size_t pkv_decode_workspace_bytes(int num_seqs, int q_len, int num_q_heads, int 
       num_q_heads % num_kv_heads || head_dim != kD || sm_count() == 0)
     return 0;
   const int R = num_q_heads / num_kv_heads * q_len;
-  return ws_layout(std::max(num_seqs, 1), num_kv_heads, R).total;
+  return ws_layout(std::max(num_seqs, 1), num_kv_heads, R, 0).total;
 }
 
 int pkv_set_early_start(int enable) {
@@ -1597,13 +1597,13 @@ int pkv_paged_attn_decode_noalloc(void* out, const void* q, const void* k_cache,
   if (num_seqs == 0) return PKV_OK;
   if (sm_count() == 0) return PKV_EINVAL;   // no usable current device
   const int R = num_q_heads / num_kv_heads * q_len;
-  const WsLayout ws = ws_layout(num_seqs, num_kv_heads, R);
+  const WsLayout ws = ws_layout(num_seqs, num_kv_heads, R, kFixedScratchBytes);
   if (ws.total > kFixedScratchBytes) return PKV_ENOSPC;
   int status = PKV_OK;
   void* scratch = fixed_scratch(&status);
   if (!scratch) return status;
   // the array keeps the previous call's contents; the arrival counters must start at zero
-  const cudaError_t e = cudaMemsetAsync(scratch, 0, ws.part_ml, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = cudaMemsetAsync(scratch, 0, ws.counter_bytes, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_status(e);
   return pkv_paged_attn_decode(out, q, k_cache, v_cache, num_blocks, block_tables,
                                max_blocks_per_seq, context_lens, num_seqs, q_len, num_q_heads,

@@ -598,17 +598,22 @@ inline int grid_size(const Variant& v, size_t smem, int* status) {
 }
 
 struct WsLayout {
-  size_t counters, part_ml, part_o, total;
+  size_t counters, counter_bytes, part_ml, part_o, total;
 };
 
-inline WsLayout ws_layout(int num_seqs, int Hkv, int R) {
+// Counters from the workspace's start, partials up to its end: a workspace of `bytes` that serves
+// calls of several sizes keeps the counters, which every call leaves zero, apart from the
+// partials, which it does not.
+inline WsLayout ws_layout(int num_seqs, int Hkv, int R, size_t bytes) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const size_t partials = static_cast<size_t>(2) * sm_count() * kMaxCtasPerSm;
+  const size_t ml = up(partials * R * 4 * sizeof(float)), o = up(partials * R * kD * sizeof(float));
   WsLayout w;
   w.counters = 0;
-  w.part_ml = up(static_cast<size_t>(num_seqs) * Hkv * sizeof(int));
-  w.part_o = w.part_ml + up(partials * R * 4 * sizeof(float));
-  w.total = w.part_o + up(partials * R * kD * sizeof(float));
+  w.counter_bytes = up(static_cast<size_t>(num_seqs) * Hkv * sizeof(int));
+  w.total = w.counter_bytes + ml + o;
+  w.part_o = std::max(w.total, bytes & ~static_cast<size_t>(255)) - o;
+  w.part_ml = w.part_o - ml;
   return w;
 }
 

@@ -869,7 +869,7 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
           (1ll << 30))
     return PKV_EINVAL;
   if (num_blocks == 0) return PKV_EINVAL;
-  const WsLayout ws = ws_layout(num_seqs, Hkv, R);
+  const WsLayout ws = ws_layout(num_seqs, Hkv, R, workspace_bytes);
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
   const int newkv_bytes = append ? 2 * q_len * kNewRow : 0;

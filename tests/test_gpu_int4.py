@@ -535,6 +535,29 @@ def test_two_captured_decodes_at_once_with_a_workspace_each():
         _close(out, *w)
 
 
+def test_one_workspace_for_calls_of_different_sizes():
+    # counters of a large batch lie where a smaller call's partials must not: many split units,
+    # then one sequence with 24 rows, and again
+    big = _case([1300] * 40, 16, 8, 8, 1, seed=51)
+    one = _case([6000], 16, 12, 2, 4, seed=52)
+    few = _case([4100, 700, 5000], 16, 8, 8, 1, seed=53)
+    ws = pkv.make_workspace(40, 4, 48, 8)
+    runs = []
+    for k, v, tables, lens, q in (few, big, one, big, few, one, big):
+        a = [_dev(x) for x in (q, k, v, tables, lens)]
+        out = torch.full_like(a[0], float("nan"))
+        pkv.paged_attn_decode_int4(out, *a, 0.1, ws)
+        runs.append((out, q, k, v, tables, lens))
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == 0
+    assert torch.equal(runs[0][0], runs[4][0]) and torch.equal(runs[2][0], runs[5][0])
+    assert torch.equal(runs[1][0], runs[3][0]) and torch.equal(runs[1][0], runs[6][0])
+    for out, q, k, v, tables, lens in runs[:3]:
+        pick = slice(0, 4)
+        want, tol = int4.attention(q[pick], k, v, tables[pick], lens[pick], 0.1)
+        _close(out[pick], want, tol)
+
+
 def test_a_call_runs_on_the_current_stream():
     # the query arrives on a side stream behind a long copy; a launch elsewhere would miss it
     k, v, tables, lens, q = _case([300, 47], seed=41)
