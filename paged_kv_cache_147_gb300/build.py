@@ -1,7 +1,9 @@
 """Builds libpkv.so (the CUDA kernels behind the C ABI in include/pkv.h) in-tree for sm_103a.
 
 The translation units compile in parallel with nvcc, then link into one shared object with
-the CUDA runtime linked statically, so the library needs only the driver at run time.
+the CUDA runtime linked statically, so the library needs only the driver at run time. Beside it
+goes _pkv_torch.so, the part of the Python binding that is compiled (csrc/pkv_torch.cpp), against
+the installed torch.
 """
 from __future__ import annotations
 
@@ -9,11 +11,17 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
+TORCH_LIB = os.path.join(HERE, "_pkv_torch.so")
+TORCH_SOURCE = "pkv_torch.cpp"
+TORCH_STAMP = os.path.join(BUILD, "pkv_torch.version")   # the torch it was compiled against
 SOURCES = ["pkv_decode.cu", "pkv_cache.cu", "pkv_host.cu", "pkv_blocks.cpp", "pkv_spec.cu",
            "pkv_prefill.cu", "pkv_cache_int4.cu", "pkv_decode_int4.cu", "pkv_norm_rope.cu",
            "pkv_tables.cu"]
@@ -33,17 +41,60 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != TORCH_SOURCE]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "pkv.h"))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _torch_stale() -> bool:
+    try:
+        with open(TORCH_STAMP) as f:
+            if f.read() != torch.__version__:
+                return True
+        t = os.path.getmtime(TORCH_LIB)
+    except OSError:
+        return True
+    deps = [os.path.join(CSRC, TORCH_SOURCE),
+            os.path.join(os.path.dirname(HERE), "include", "pkv.h")]
+    return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _start_torch_build(tmp: str) -> subprocess.Popen:
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+           os.path.join(CSRC, TORCH_SOURCE), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _finish_torch_build(p: subprocess.Popen, tmp: str) -> None:
+    text, _ = p.communicate()
+    if p.returncode != 0:
+        sys.stdout.write(text)
+        raise RuntimeError(f"g++ failed on {TORCH_SOURCE}")
+    os.replace(tmp, TORCH_LIB)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(torch.__version__)
 
 
 def build(force: bool = False, verbose: bool = False, defines=(), out: str | None = None) -> str:
     """Compiles libpkv.so. `defines` (e.g. ["PKV_DECODE_STAGES=10"]) and `out` build a
     variant elsewhere; the default library is rebuilt only when a source is newer."""
     lib = out or LIB
-    if not force and not defines and out is None and not _stale():
-        return LIB
+    torch_tmp, torch_build = TORCH_LIB + f".tmp{os.getpid()}", None
+    if not defines and out is None:
+        if force or _torch_stale():
+            os.makedirs(BUILD, exist_ok=True)
+            torch_build = _start_torch_build(torch_tmp)
+        if not force and not _stale():
+            if torch_build:
+                _finish_torch_build(torch_build, torch_tmp)
+            return LIB
     nvcc = _nvcc()
     bdir = BUILD if out is None else out + ".build"
     os.makedirs(bdir, exist_ok=True)
@@ -69,6 +120,8 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: str | Non
         sys.stdout.write(r.stdout)
         raise RuntimeError("linking libpkv.so failed")
     os.replace(tmp, lib)
+    if torch_build:
+        _finish_torch_build(torch_build, torch_tmp)
     return lib
 
 

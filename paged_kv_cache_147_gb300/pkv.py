@@ -151,24 +151,28 @@ def _p(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-# The newer entry points check what the library cannot see through a bare pointer: element type,
-# device, layout, shape. The checks are written out for speed: a decode step's calls are short.
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_F16, _F32, _U8, _I32, _I64 = torch.float16, torch.float32, torch.uint8, torch.int32, torch.int64
+# The 4-bit, norm and table calls go through a compiled binding: it checks what the library cannot
+# see through a bare pointer (element type, device, layout, shape), allocates the outputs and
+# makes the call. Their kernels are shorter than the same steps in Python.
+_TORCH_ENTRIES = ("kv_append_int4", "widen_blocks_int4", "paged_attn_decode_int4",
+                  "paged_attn_decode_append_int4", "qk_norm_rope", "extend_tables",
+                  "truncate_tables")
+_ops = None
 
 
-def _is(t: torch.Tensor, dtype, dev: int) -> bool:
-    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-
-
-def _on(stream, dev: int) -> int:
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-def _require(fn: str, ok: bool) -> None:
-    if not ok:
-        raise PkvError(fn, EINVAL)
+def _torch_ops():
+    """The compiled binding (built with the library), bound to the loaded library."""
+    global _ops
+    lib = load()
+    try:
+        from . import _pkv_torch
+    except ImportError as e:
+        raise RuntimeError("_pkv_torch.so is missing or does not fit the installed torch: build it "
+                           "with `python -m paged_kv_cache_147_gb300.build`") from e
+    _pkv_torch.bind(PkvError, *(ctypes.cast(getattr(lib, "pkv_" + n), ctypes.c_void_p).value
+                                for n in _TORCH_ENTRIES))
+    _ops = _pkv_torch
+    return _ops
 
 
 def version() -> int:
@@ -381,54 +385,21 @@ INT4_ROW = 80   # bytes of one row (token, kv head) of a 4-bit pool
 def kv_append_int4(k, v, slots, k_cache, v_cache, stream=None):
     """k, v fp16 [T, Hkv, 128]; slots int64 [T]; k_cache, v_cache one layer of uint8 4-bit rows
     [NB, Hkv, bs, 80]."""
-    fn, dev = "pkv_kv_append_int4", _device()
-    _require(fn, _is(k, _F16, dev) and _is(v, _F16, dev) and _is(slots, _I64, dev) and
-             _is(k_cache, _U8, dev) and _is(v_cache, _U8, dev) and k_cache.dim() == 4)
-    nb, hkv, bs, row = shape = k_cache.shape
-    n = slots.numel()
-    _require(fn, row == INT4_ROW and v_cache.shape == shape and k.shape == (n, hkv, 128) and
-             v.shape == k.shape)
-    _check(fn, (_lib or load()).pkv_kv_append_int4(
-        k.data_ptr(), v.data_ptr(), slots.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(),
-        nb, hkv, 128, bs, _on(stream, dev)))
+    (_ops or _torch_ops()).kv_append_int4(k, v, slots, k_cache, v_cache, stream)
 
 
 def widen_blocks_int4(k_cache, v_cache, src, dst, k_out, v_out, stream=None):
     """Blocks src[i] of the 4-bit pools [NB, Hkv, bs, 80] -> blocks dst[i] of the fp16 pools k_out,
     v_out [NB', Hkv, bs, 128]; src, dst int32."""
-    fn, dev = "pkv_widen_blocks_int4", _device()
-    _require(fn, _is(k_cache, _U8, dev) and _is(v_cache, _U8, dev) and _is(k_out, _F16, dev) and
-             _is(v_out, _F16, dev) and _is(src, _I32, dev) and _is(dst, _I32, dev) and
-             k_cache.dim() == 4 and k_out.dim() == 4)
-    nb, hkv, bs, row = shape = k_cache.shape
-    n, nb_out = src.numel(), k_out.shape[0]
-    _require(fn, row == INT4_ROW and v_cache.shape == shape and dst.numel() == n and
-             k_out.shape == (nb_out, hkv, bs, 128) and v_out.shape == k_out.shape)
-    _check(fn, (_lib or load()).pkv_widen_blocks_int4(
-        k_cache.data_ptr(), v_cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, nb,
-        k_out.data_ptr(), v_out.data_ptr(), nb_out, hkv, 128, bs, _on(stream, dev)))
+    (_ops or _torch_ops()).widen_blocks_int4(k_cache, v_cache, src, dst, k_out, v_out, stream)
 
 
 def paged_attn_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, scale, workspace,
                            stream=None):
     """paged_attn_decode over a 4-bit cache: uint8 pools [NB, Hkv, bs, 80] (kv_append_int4's
     rows); everything else as there."""
-    fn, dev = "pkv_paged_attn_decode_int4", _device()
-    _require(fn, _is(q, _F16, dev) and _is(out, _F16, dev) and _is(k_cache, _U8, dev) and
-             _is(v_cache, _U8, dev) and _is(block_tables, _I32, dev) and
-             _is(context_lens, _I32, dev) and workspace.get_device() == dev and
-             workspace.is_contiguous() and q.dim() == 4 and k_cache.dim() == 4 and
-             block_tables.dim() == 2)
-    B, q_len, hq, d = q.shape
-    nb, hkv, bs, row = shape = k_cache.shape
-    rows, width = block_tables.shape
-    _require(fn, row == INT4_ROW and v_cache.shape == shape and out.shape == q.shape and
-             rows == B and context_lens.numel() == B)
-    _check(fn, (_lib or load()).pkv_paged_attn_decode_int4(
-        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb,
-        block_tables.data_ptr(), width, context_lens.data_ptr(), B, q_len, hq, hkv, d, bs,
-        scale, workspace.data_ptr(), workspace.nbytes, _on(stream, dev)))
-    return out
+    return (_ops or _torch_ops()).paged_attn_decode_int4(
+        out, q, k_cache, v_cache, block_tables, context_lens, scale, workspace, stream)
 
 
 def paged_attn_decode_append_int4(out, q, k_new, v_new, k_cache, v_cache, block_tables,
@@ -436,23 +407,8 @@ def paged_attn_decode_append_int4(out, q, k_new, v_new, k_cache, v_cache, block_
     """paged_attn_decode_append over a 4-bit cache: the new fp16 rows k_new, v_new
     [B*q_len, Hkv, 128] are stored as kv_append_int4 stores them and attended over with the rest.
     Early-start caveat as there."""
-    fn, dev = "pkv_paged_attn_decode_append_int4", _device()
-    _require(fn, _is(q, _F16, dev) and _is(out, _F16, dev) and _is(k_new, _F16, dev) and
-             _is(v_new, _F16, dev) and _is(k_cache, _U8, dev) and _is(v_cache, _U8, dev) and
-             _is(block_tables, _I32, dev) and _is(context_lens, _I32, dev) and
-             workspace.get_device() == dev and workspace.is_contiguous() and q.dim() == 4 and
-             k_cache.dim() == 4 and block_tables.dim() == 2)
-    B, q_len, hq, d = q.shape
-    nb, hkv, bs, row = shape = k_cache.shape
-    rows, width = block_tables.shape
-    _require(fn, row == INT4_ROW and v_cache.shape == shape and out.shape == q.shape and
-             rows == B and context_lens.numel() == B and k_new.shape == (B * q_len, hkv, 128) and
-             v_new.shape == k_new.shape)
-    _check(fn, (_lib or load()).pkv_paged_attn_decode_append_int4(
-        out.data_ptr(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), nb, block_tables.data_ptr(), width, context_lens.data_ptr(), B, q_len,
-        hq, hkv, d, bs, scale, workspace.data_ptr(), workspace.nbytes, _on(stream, dev)))
-    return out
+    return (_ops or _torch_ops()).paged_attn_decode_append_int4(
+        out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, workspace, stream)
 
 
 # ------------------------------------------------------------------------------ norm + rotation
@@ -462,34 +418,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps, positions, cos_sin, q_out=None, 
     heads contiguous, tokens any stride apart: slices of a packed projection do), weights fp16
     [128], positions int64 [T] (negative: padding, left as it is), cos_sin a rope_table on the
     device -> (q_out, k_out), contiguous."""
-    fn, dev = "pkv_qk_norm_rope", _device()
-    _require(fn, q.dtype is _F16 and k.dtype is _F16 and q.get_device() == dev and
-             k.get_device() == dev and q.dim() == 3 and k.dim() == 3 and
-             _is(q_weight, _F16, dev) and _is(k_weight, _F16, dev) and
-             _is(positions, _I64, dev) and _is(cos_sin, _F32, dev) and cos_sin.dim() == 3)
-    T, hq, d = q.shape
-    _, hkv, _ = k.shape
-    (qs, qh, qd), (ks, kh, kd) = q.stride(), k.stride()
-    n_index = cos_sin.shape[0]
-    _require(fn, d == 128 and k.shape == (T, hkv, 128) and positions.numel() == T and qd == 1 and
-             kd == 1 and (qh == 128 or hq == 1) and (kh == 128 or hkv == 1) and
-             q_weight.numel() == 128 and k_weight.numel() == 128 and
-             cos_sin.shape == (n_index, 64, 2))
-    if T <= 1:   # the stride of a single token means nothing
-        qs, ks = hq * 128, hkv * 128
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        _require(fn, _is(q_out, _F16, dev) and q_out.shape == q.shape)
-    if k_out is None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-    else:
-        _require(fn, _is(k_out, _F16, dev) and k_out.shape == k.shape)
-    _check(fn, (_lib or load()).pkv_qk_norm_rope(
-        q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(), qs, ks,
-        q_weight.data_ptr(), k_weight.data_ptr(), eps, positions.data_ptr(), cos_sin.data_ptr(),
-        n_index, T, hq, hkv, 128, _on(stream, dev)))
-    return q_out, k_out
+    return (_ops or _torch_ops()).qk_norm_rope(
+        q, k, q_weight, k_weight, eps, positions, cos_sin, q_out, k_out, stream)
 
 
 # ------------------------------------------------------------------------------ tables on the GPU
@@ -499,45 +429,17 @@ def extend_tables(block_tables, context_lens, new_lens, block_size, free_blocks,
     per sequence, blocks off the stack free_blocks (int32 [num_blocks], free_count of them free;
     all updated in place) -> (slots int64, seq_ids int32, positions int64 [max_tokens],
     cu_new_lens int32 [B + 1]); `out` gives the four to write into."""
-    fn, dev = "pkv_extend_tables", _device()
-    _require(fn, _is(block_tables, _I32, dev) and _is(context_lens, _I32, dev) and
-             _is(new_lens, _I32, dev) and _is(free_blocks, _I32, dev) and
-             _is(free_count, _I32, dev) and block_tables.dim() == 2)
-    B, width = block_tables.shape
-    _require(fn, context_lens.numel() == B and new_lens.numel() == B and free_count.numel() == 1)
-    if out is None:
-        on = block_tables.device
-        slots = torch.empty(max_tokens, dtype=_I64, device=on)
-        seqs = torch.empty(max_tokens, dtype=_I32, device=on)
-        cu = torch.empty(B + 1, dtype=_I32, device=on)
-        out = slots, seqs, pos, cu = slots, seqs, torch.empty_like(slots), cu
-    else:
-        slots, seqs, pos, cu = out
-        _require(fn, _is(slots, _I64, dev) and _is(seqs, _I32, dev) and _is(pos, _I64, dev) and
-                 _is(cu, _I32, dev) and slots.numel() == max_tokens and
-                 seqs.numel() == max_tokens and pos.numel() == max_tokens and cu.numel() == B + 1)
-    _check(fn, (_lib or load()).pkv_extend_tables(
-        block_tables.data_ptr(), context_lens.data_ptr(), new_lens.data_ptr(), B, width,
-        block_size, free_blocks.data_ptr(), free_count.data_ptr(), free_blocks.numel(),
-        slots.data_ptr(), seqs.data_ptr(), pos.data_ptr(), cu.data_ptr(), max_tokens,
-        _on(stream, dev)))
-    return out
+    return (_ops or _torch_ops()).extend_tables(
+        block_tables, context_lens, new_lens, block_size, free_blocks, free_count, max_tokens,
+        out if out is None else tuple(out), stream)
 
 
 def truncate_tables(block_tables, context_lens, keep_lens, block_size, free_blocks, free_count,
                     stream=None):
     """Cuts sequences back to keep_lens tokens (int32 [B]; negative or past the length: as it is);
     their blocks go back on the stack. All updated in place."""
-    fn, dev = "pkv_truncate_tables", _device()
-    _require(fn, _is(block_tables, _I32, dev) and _is(context_lens, _I32, dev) and
-             _is(keep_lens, _I32, dev) and _is(free_blocks, _I32, dev) and
-             _is(free_count, _I32, dev) and block_tables.dim() == 2)
-    B, width = block_tables.shape
-    _require(fn, context_lens.numel() == B and keep_lens.numel() == B and free_count.numel() == 1)
-    _check(fn, (_lib or load()).pkv_truncate_tables(
-        block_tables.data_ptr(), context_lens.data_ptr(), keep_lens.data_ptr(), B, width,
-        block_size, free_blocks.data_ptr(), free_count.data_ptr(), free_blocks.numel(),
-        _on(stream, dev)))
+    (_ops or _torch_ops()).truncate_tables(
+        block_tables, context_lens, keep_lens, block_size, free_blocks, free_count, stream)
 
 
 # ------------------------------------------------------------------------------ host checks

@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import int4, step
 from paged_kv_cache_147_gb300 import build, pkv
@@ -163,3 +164,19 @@ def test_tables_refuse_bad_arguments(lib):
     assert cut(P, P, None, 3, 8, 16, P, P, 64, None) == pkv.EINVAL
     assert cut(P, P, P, 4097, 8, 16, P, P, 64, None) == pkv.EINVAL
     assert cut(P, P, P, 3, 8, 15, P, P, 64, None) == pkv.EINVAL
+
+
+# ----------------------------------------------------------------------------- the binding
+def test_compiled_binding_loads_and_refuses_what_is_not_on_a_gpu():
+    ops = pkv._torch_ops()
+    with pytest.raises(TypeError):
+        ops.kv_append_int4(1, 2)
+    rows, slots = torch.zeros(2, 2, 128, dtype=torch.float16), torch.zeros(2, dtype=torch.int64)
+    pool = torch.zeros(2, 2, 16, 80, dtype=torch.uint8)
+    with pytest.raises(RuntimeError):      # PkvError, or no CUDA device
+        pkv.kv_append_int4(rows, rows, slots, pool, pool)
+    with pytest.raises(RuntimeError):
+        pkv.truncate_tables(None, None, None, 16, None, None)
+    table = torch.zeros(2, 4, dtype=torch.int32)
+    with pytest.raises(RuntimeError):
+        pkv.extend_tables(table, table[0], table[0], 16, table[0], table[0, :1], 4)
