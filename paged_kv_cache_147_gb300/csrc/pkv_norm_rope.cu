@@ -174,7 +174,8 @@ int pkv_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, int
   a.num_tokens = num_tokens;
   a.hq = num_q_heads;
   a.heads = num_q_heads + num_kv_heads;
-  // what one wave of half-warps with a head each holds
+  // one head or four a half-warp, us: 896 heads 2.0 / 2.9, 9216 2.5 / 2.9, 16416 3.4 / 3.5, 18432
+  // 3.6 / 3.5, 36864 5.4 / 4.6, 147456 16.7 / 14.1
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (static_cast<int64_t>(num_tokens) * a.heads <= 16384) return launch<1, false>(a, st);
   return launch<4, true>(a, st);

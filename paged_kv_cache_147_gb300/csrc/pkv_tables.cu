@@ -26,7 +26,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kMaxTableSeqs = 4096;
 constexpr int kMaxCluster = 8;
-constexpr int kClusterTokens = 32768;
+// An extend and a cut in a row, one cluster against the grid and the second launch, us: 4096 tokens
+// 8.0 / 8.4, 8192 8.7 / 8.8, 16384 9.6 / 9.2, 32768 11.2 / 9.1, 262144 37 / 10.7. The cut's bound is
+// the tables' capacity, of which most calls cut little (320 entries 8.1 / 8.4, 4160 9.6 / 9.2).
+constexpr int kClusterTokens = 8192;
 constexpr int kClusterBlocks = 16384;
 
 struct TableArgs {

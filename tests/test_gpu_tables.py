@@ -121,9 +121,12 @@ def test_many_tokens_take_the_wide_path_and_agree_with_the_narrow_one():
     m = rng.integers(0, 900, B)
     tables, lens, free, count = _state(rng, lens, bs, 64, int((-(-(lens + m) // bs)).sum()))
     assert m.sum() > 65536 > (m // 2).sum()
-    _extend(tables, lens, m, bs, free, count, 65536, want_error=pkv.DEVERR_SPACE)   # one launch
+    _extend(tables, lens, m, bs, free, count, 65536, want_error=pkv.DEVERR_SPACE)
     _extend(tables, lens, m // 2, bs, free, count, 65536)
-    _extend(tables, lens, m // 2, bs, free, count, 65537)                           # two
+    _extend(tables, lens, m // 2, bs, free, count, 65537)
+    assert (m // 24).sum() < 8192
+    _extend(tables, lens, m // 24, bs, free, count, 8192)                           # one launch
+    _extend(tables, lens, m // 24, bs, free, count, 8193)                           # two
     _extend(tables, lens, m, bs, free, count, 400001)
     _extend(tables, lens, m, bs, free, count - 900, 400001, want_error=pkv.DEVERR_SPACE)
 
