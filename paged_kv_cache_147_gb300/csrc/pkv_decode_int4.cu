@@ -46,6 +46,9 @@
 //  * More than 8 rows: two to four warps take a stage, 8 rows each (and a copy of their own; all
 //    but the first come from L2). Two row tiles in one warp save the second masking of the codes
 //    but not the registers: with two, four drafts of 6 heads took 36 us, with one 25.
+//  * Fused append: the warp that prepares the queries also quantises the segment's new rows, into
+//    the pool and for the consumers, which copy them over their stage's stale ones (done by the
+//    consumers, 128 ragged sequences took 57 us instead of 54).
 // Where it stands: 32 sequences of 16384 tokens, 8 kv heads, 8 queries each take 134 us (5.0 TB/s,
 // 73 % of the copy rate). The loads alone take 104, the arithmetic alone 106; together they share
 // the SM's issue slots (50 % used, ALU 47 %, tensor 34 %, shared memory 34 %), and neither 12
@@ -82,9 +85,10 @@ constexpr size_t kMaxSmem = 227 * 1024;
 constexpr float kShift = 11.f, kGrow = 2.f;
 // Stages after which a warp's sums move to its state buffer. The tensor cores' fp32 sums truncate,
 // and the two large sums that make a value's (of p s c and of p z) do not lose alike: over 100
-// stages a warp (16384 tokens) their difference was off by 6.7e-4 relative, over 16 by 2.8e-4, near
-// what the rounded weights and output alone cost (2.1e-4 to 2.6e-4). With 16 a sum takes 64
-// products (two chunks, weights and what they lost); moving the sums costs 3 to 4 % of the time.
+// stages a warp (16384 tokens) their difference was off by 6.9e-4 relative, over 64 by 5.2e-4, over
+// 32 by 3.6e-4, over 16 by 2.9e-4, near what the rounded weights and output alone cost (2.7e-4).
+// With 16 a sum takes 64 products (two chunks, weights and what they lost); moving the sums costs
+// at most 3 % of the time (134.0 us against 130.5 without).
 constexpr int kFlush = 16;
 
 // Shared-memory layout (offsets from a 128-byte aligned base). NCS: warps that share the stages
