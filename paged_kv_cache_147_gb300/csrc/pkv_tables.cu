@@ -14,7 +14,9 @@
 // end, from changing under a CTA that has not read them yet. Past kClusterTokens tokens (or
 // kClusterBlocks table entries to cut) one cluster's 8 SMs no longer write fast enough: a grid
 // over the whole GPU does the tokens and blocks first and a second, one-CTA launch the rest; it
-// starts beside the first (dependent launch), scans, and writes when the first is done.
+// starts beside the first (dependent launch), scans, and writes when the first is done (256 prompts
+// of up to 4096 tokens, with the cut: 15.2 us one after the other, 11.9 so; a draft step of 64
+// sequences, cut and extend: 8.8).
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -23,12 +25,16 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 512;
+// Threads of a CTA: 256 while four sequences a thread suffice, or 1024 (an extend by 4 tokens and a
+// cut in a row, us, against the other: 1024 sequences 9.8 / 13.7, 4096 sequences 18.3 / 27).
+constexpr int kMaxThreads = 1024;
+int threads_for(int num_seqs) { return num_seqs <= 1024 ? 256 : kMaxThreads; }
 constexpr int kMaxTableSeqs = 4096;
 constexpr int kMaxCluster = 8;
 // An extend and a cut in a row, one cluster against the grid and the second launch, us: 4096 tokens
-// 8.0 / 8.4, 8192 8.7 / 8.8, 16384 9.6 / 9.2, 32768 11.2 / 9.1, 262144 37 / 10.7. The cut's bound is
-// the tables' capacity, of which most calls cut little (320 entries 8.1 / 8.4, 4160 9.6 / 9.2).
+// 7.3 / 7.8, 8192 8.3 / 8.1, 16384 10.1 / 8.6, 32768 12.6 / 8.4, 262144 61 / 10.5. The cut's bound
+// is the tables' capacity, of which most calls cut little (64 sequences whose tables hold 8320
+// entries, a draft step: 8.8 / 9.1).
 constexpr int kClusterTokens = 8192;
 constexpr int kClusterBlocks = 16384;
 
@@ -67,7 +73,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // Exclusive sums of two 64-bit values over the CTA's threads, and their totals.
 __device__ __forceinline__ void cta_scan(int64_t& x, int64_t& y, int64_t& total_x,
                                          int64_t& total_y, int64_t (*part)[2]) {
-  constexpr int kWarps = kThreads / 32;
+  const int warps = blockDim.x / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t ix = x, iy = y;
 #pragma unroll
@@ -79,15 +85,15 @@ __device__ __forceinline__ void cta_scan(int64_t& x, int64_t& y, int64_t& total_
   if (lane == 31) { part[warp][0] = ix; part[warp][1] = iy; }
   __syncthreads();
   // every warp scans the warps' sums by itself
-  int64_t px = lane < kWarps ? part[lane][0] : 0, py = lane < kWarps ? part[lane][1] : 0;
+  int64_t px = lane < warps ? part[lane][0] : 0, py = lane < warps ? part[lane][1] : 0;
 #pragma unroll
-  for (int o = 1; o < kWarps; o <<= 1) {
+  for (int o = 1; o < 32; o <<= 1) {
     const int64_t ux = __shfl_up_sync(0xffffffffu, px, o);
     const int64_t uy = __shfl_up_sync(0xffffffffu, py, o);
     if (lane >= o) { px += ux; py += uy; }
   }
-  total_x = __shfl_sync(0xffffffffu, px, kWarps - 1);
-  total_y = __shfl_sync(0xffffffffu, py, kWarps - 1);
+  total_x = __shfl_sync(0xffffffffu, px, warps - 1);
+  total_y = __shfl_sync(0xffffffffu, py, warps - 1);
   const int64_t bx = __shfl_sync(0xffffffffu, px, max(warp - 1, 0));
   const int64_t by = __shfl_sync(0xffffffffu, py, max(warp - 1, 0));
   x = ix - x + (warp ? bx : 0);
@@ -111,15 +117,15 @@ __device__ __forceinline__ int blocks_of(int64_t tokens, int shift) {
 // TOKENS: the token arrays and the new table entries; STATE: lengths, count and error bits.
 // Shared memory: tok[n + 1], blk[n + 1], len[n].
 template <bool TOKENS, bool STATE>
-__global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) extend_kernel(const TableArgs a) {
   extern __shared__ int smem[];
-  __shared__ int64_t part[kThreads / 32][2];
+  __shared__ int64_t part[kMaxThreads / 32][2];
   __shared__ int used_s;
   int* tok = smem;                       // first packed token of each sequence
   int* blk = tok + a.num_seqs + 1;       // first block (from the top of the stack)
   int* len = blk + a.num_seqs + 1;       // old length; -1: refused
   const int n = a.num_seqs, sh = a.bs_shift;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int rank = TOKENS && STATE ? cluster_rank() : blockIdx.x;
   const int ctas = TOKENS && STATE ? cluster_size() : gridDim.x;
   const int64_t cap = static_cast<int64_t>(a.max_blocks) << sh;
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
   if (tid == 0) used_s = 0;
 
   // ---- the scan: each thread takes `per` neighbouring sequences ----
-  const int per = (n + kThreads - 1) / kThreads;
+  const int per = (n + threads - 1) / threads;
   const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
   int64_t x = 0, y = 0;
   for (int b = b0; b < b1; ++b) {
@@ -179,8 +185,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
 
   if (TOKENS) {
     // ---- the new tokens, and the padding behind them, four neighbours a thread ----
-    for (int64_t i0 = 4 * (static_cast<int64_t>(rank) * kThreads + tid); i0 < a.max_tokens;
-         i0 += 4 * static_cast<int64_t>(ctas) * kThreads) {
+    for (int64_t i0 = 4 * (static_cast<int64_t>(rank) * threads + tid); i0 < a.max_tokens;
+         i0 += 4 * static_cast<int64_t>(ctas) * threads) {
       int64_t slot[4], pos[4];
       int seq[4];
       int b = i0 < live ? find(tok, n, static_cast<int>(i0)) : n;
@@ -220,19 +226,19 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
       }
     }
     // ---- the new table entries ----
-    for (int k = rank * kThreads + tid; k < used; k += ctas * kThreads) {
+    for (int k = rank * threads + tid; k < used; k += ctas * threads) {
       const int b = find(blk, n, k);
       if (len[b] < 0) continue;
       const int id = a.free_blocks[count - 1 - k];
       if (id < 0 || id >= a.num_blocks) bad |= PKV_DEVERR_BLOCK_ID;
       a.tables[static_cast<int64_t>(b) * a.max_blocks + blocks_of(len[b], sh) + (k - blk[b])] = id;
     }
-    for (int b = rank * kThreads + tid; b <= n; b += ctas * kThreads) a.cu[b] = tok[b];
+    for (int b = rank * threads + tid; b <= n; b += ctas * threads) a.cu[b] = tok[b];
   }
   if (bad) atomicOr(a.err, bad);
   if (STATE) {
     if (TOKENS) cluster_wait(); else griddep_wait();
-    for (int b = rank * kThreads + tid; b < n; b += ctas * kThreads)
+    for (int b = rank * threads + tid; b < n; b += ctas * threads)
       if (len[b] >= 0) a.lens[b] = len[b] + a.arg[b];
     if (rank == 0 && tid == 0) *a.free_count = count - used;
   }
@@ -241,13 +247,13 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TableArgs a) {
 // BLOCKS: the table entries and the stack; STATE: lengths and count. Shared memory: blk[n + 1],
 // keep[n].
 template <bool BLOCKS, bool STATE>
-__global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) truncate_kernel(const TableArgs a) {
   extern __shared__ int smem[];
-  __shared__ int64_t part[kThreads / 32][2];
+  __shared__ int64_t part[kMaxThreads / 32][2];
   int* blk = smem;                       // first freed block of each sequence
   int* keep = blk + a.num_seqs + 1;      // length kept; -1: as it is
   const int n = a.num_seqs, sh = a.bs_shift;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   const int rank = BLOCKS && STATE ? cluster_rank() : blockIdx.x;
   const int ctas = BLOCKS && STATE ? cluster_size() : gridDim.x;
   const int64_t cap = static_cast<int64_t>(a.max_blocks) << sh;
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
   if (BLOCKS && !STATE) griddep_launch_dependents();
   int count = *a.free_count;
   if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = a.num_blocks; }
-  const int per = (n + kThreads - 1) / kThreads;
+  const int per = (n + threads - 1) / threads;
   const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
   int64_t x = 0, unused = 0;
   for (int b = b0; b < b1; ++b) {
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
   if (BLOCKS && STATE) cluster_arrive();   // this CTA has read the lengths and the count
 
   if (BLOCKS) {
-    for (int k = rank * kThreads + tid; k < freed; k += ctas * kThreads) {
+    for (int k = rank * threads + tid; k < freed; k += ctas * threads) {
       const int b = find(blk, n, k);
       int32_t* entry = a.tables + static_cast<int64_t>(b) * a.max_blocks +
                        blocks_of(keep[b], sh) + (k - blk[b]);
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const TableArgs a) {
   if (bad) atomicOr(a.err, bad);
   if (STATE) {
     if (BLOCKS) cluster_wait(); else griddep_wait();
-    for (int b = rank * kThreads + tid; b < n; b += ctas * kThreads)
+    for (int b = rank * threads + tid; b < n; b += ctas * threads)
       if (keep[b] >= 0) a.lens[b] = keep[b];
     if (rank == 0 && tid == 0 && freed > 0) *a.free_count = count + freed;
   }
@@ -308,13 +314,13 @@ int launch_status() { return cuda_status(cudaGetLastError()); }
 int launch(const void* fn, const TableArgs& a, size_t smem, int cluster, int ctas,
            cudaStream_t stream, bool second = false) {
   cudaError_t e = cudaSuccess;
-  if (smem > 47 * 1024)   // past the default limit, beside the kernels' own 300 bytes
+  if (smem > 47 * 1024)   // past the default limit, beside the kernels' own 528 bytes
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>((3 * kMaxTableSeqs + 2) * sizeof(int)));
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster ? cluster : ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_for(a.num_seqs));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -376,11 +382,12 @@ int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_
                  ((at(slot_out) | at(seq_out) | at(position_out)) & 15u) == 0, device_error_ptr()};
   if (!a.err) return launch_status();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int threads = threads_for(num_seqs);
   const size_t smem = (3 * static_cast<size_t>(num_seqs) + 2) * sizeof(int);
   if (max_tokens <= kClusterTokens)
     return launch(reinterpret_cast<const void*>(&extend_kernel<true, true>), a, smem,
-                  cluster_for(max_tokens, 4 * kThreads), 0, s);
-  const int ctas = std::min(2 * sm_count(), (max_tokens / 4 + kThreads) / kThreads);
+                  cluster_for(max_tokens, 4 * threads), 0, s);
+  const int ctas = std::min(1024 / threads * sm_count(), (max_tokens / 4 + threads) / threads);
   if (ctas < 1) return launch_status();
   const int st =
       launch(reinterpret_cast<const void*>(&extend_kernel<true, false>), a, smem, 0, ctas, s);
@@ -401,14 +408,16 @@ int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int3
                  num_blocks, 0, false, device_error_ptr()};
   if (!a.err) return launch_status();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int threads = threads_for(num_seqs);
   const size_t smem = (2 * static_cast<size_t>(num_seqs) + 1) * sizeof(int);
   // at most this many entries leave the tables
   const int64_t most = std::min<int64_t>(static_cast<int64_t>(num_seqs) * max_blocks_per_seq,
                                          num_blocks);
   if (most <= kClusterBlocks)
     return launch(reinterpret_cast<const void*>(&truncate_kernel<true, true>), a, smem,
-                  cluster_for(most, 4 * kThreads), 0, s);
-  const int ctas = std::min<int64_t>(sm_count(), (most + kThreads - 1) / kThreads);
+                  cluster_for(most, 4 * threads), 0, s);
+  const int ctas =
+      std::min<int64_t>(2 * sm_count(), (most + threads - 1) / threads);
   if (ctas < 1) return launch_status();
   const int st =
       launch(reinterpret_cast<const void*>(&truncate_kernel<true, false>), a, smem, 0, ctas, s);
