@@ -418,8 +418,9 @@ int pkv_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, int
  * keep_lens[b] tokens (rejected drafts; 0 to give a sequence up); a negative or larger value
  * leaves it as it is. Blocks past ceil(keep / block_size) leave the table (entries become -1) for
  * the top of the stack, in such an order that cutting off what an extend just added restores the
- * stack. If more blocks came back than the stack holds (num_blocks), nothing is changed and
- * PKV_DEVERR_SPACE set. keep_lens (device): int32 [num_seqs]. */
+ * stack. A context outside [0, max_blocks * block_size] stays as it is and sets
+ * PKV_DEVERR_CONTEXT. If more blocks came back than the stack holds (num_blocks), nothing is
+ * changed and PKV_DEVERR_SPACE set. keep_lens (device): int32 [num_seqs]. */
 int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* new_lens,
                       int num_seqs, int max_blocks_per_seq, int block_size, int32_t* free_blocks,
                       int32_t* free_count, int num_blocks, int64_t* slot_out, int32_t* seq_out,

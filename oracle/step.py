@@ -41,7 +41,8 @@ def extend(tables, lens, new, bs, free, count, max_tokens):
 
 
 def truncate(tables, lens, keep, bs, free, count):
-    """-> (tables, lens, free, count); unchanged if the stack would overflow."""
+    """-> (tables, lens, free, count); unchanged if the stack would overflow; a sequence whose
+    length its table cannot hold stays as it is."""
     tables, lens, free = tables.copy(), lens.copy(), np.asarray(free).copy()
     gone = [(b, j) for b, (n, m) in enumerate(zip(lens.tolist(), keep.tolist()))
             if 0 <= n <= tables.shape[1] * bs and 0 <= m < n
@@ -52,7 +53,7 @@ def truncate(tables, lens, keep, bs, free, count):
         free[count + len(gone) - 1 - r] = tables[b, j]
         tables[b, j] = -1
     for b, m in enumerate(keep.tolist()):
-        if 0 <= m < lens[b]:
+        if 0 <= m < lens[b] <= tables.shape[1] * bs:
             lens[b] = m
     return tables, lens, free, count + len(gone)
 

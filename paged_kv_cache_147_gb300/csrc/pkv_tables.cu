@@ -372,8 +372,9 @@ int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_
   if (!valid_tables(num_seqs, max_blocks_per_seq, block_size, num_blocks) || max_tokens < 0)
     return PKV_EINVAL;
   if (num_seqs == 0 && max_tokens == 0) return PKV_OK;
-  if ((num_seqs > 0 && (!context_lens || !new_lens || !block_tables)) || !free_blocks ||
-      !free_count || !cu_new_lens || (max_tokens > 0 && (!slot_out || !seq_out || !position_out)))
+  if ((num_seqs > 0 && (!context_lens || !new_lens)) ||
+      (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) ||
+      (num_blocks > 0 && !free_blocks) || !free_count || !cu_new_lens || (max_tokens > 0 && (!slot_out || !seq_out || !position_out)))
     return PKV_EINVAL;
   const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
   TableArgs a = {block_tables, context_lens, new_lens, free_blocks, free_count, slot_out, seq_out,
@@ -401,7 +402,8 @@ int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int3
                         pkv_stream_t stream) {
   if (!valid_tables(num_seqs, max_blocks_per_seq, block_size, num_blocks)) return PKV_EINVAL;
   if (num_seqs == 0) return PKV_OK;
-  if (!block_tables || !context_lens || !keep_lens || !free_blocks || !free_count)
+  if ((max_blocks_per_seq > 0 && !block_tables) || !context_lens || !keep_lens ||
+      (num_blocks > 0 && !free_blocks) || !free_count)
     return PKV_EINVAL;
   TableArgs a = {block_tables, context_lens, keep_lens, free_blocks, free_count, nullptr, nullptr,
                  nullptr, nullptr, num_seqs, max_blocks_per_seq, block_size, log2_of(block_size),

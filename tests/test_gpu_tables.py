@@ -114,6 +114,31 @@ def test_truncate_refuses_more_blocks_than_the_stack_holds():
     assert d[4].item() == 3
 
 
+def test_truncate_leaves_a_length_the_table_cannot_hold():
+    rng = np.random.default_rng(7)
+    tables, lens, free, count = _state(rng, [50, 90, 33], 16, 6, 4)
+    lens = np.array([50, 97, -5], np.int32)            # 96 is the most a table holds
+    keep = np.array([20, 40, 0], np.int32)
+    d = [_dev(x) for x in (tables, lens, keep, free, np.array([count], np.int32))]
+    pkv.truncate_tables(d[0], d[1], d[2], 16, d[3], d[4])
+    assert pkv.device_error(clear=True) == pkv.DEVERR_CONTEXT
+    want = step.truncate(tables, lens, keep, 16, free, count)
+    assert want[1].tolist() == [20, 97, -5]
+    for got, w in zip((d[0], d[1], d[3], d[4]), want[:3] + (np.array([want[3]]),)):
+        assert np.array_equal(got.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("width", [0, 3])
+def test_no_blocks_at_all(width):
+    # an empty pool (and empty tables): nothing can be served, nothing is touched
+    tables, lens = np.full((2, width), -1, np.int32), np.zeros(2, np.int32)
+    free, new = np.zeros(0, np.int32), np.array([0, 5], np.int32)
+    d, *_ = _extend(tables, lens, new, 16, free, 0, 8,
+                    want_error=pkv.DEVERR_SPACE if width else pkv.DEVERR_POSITION)
+    pkv.truncate_tables(d[0], d[1], d[2], 16, d[3], d[4])
+    assert pkv.device_error(clear=True) == 0 and d[1].tolist() == [0, 0] and d[4].item() == 0
+
+
 def test_many_tokens_take_the_wide_path_and_agree_with_the_narrow_one():
     rng = np.random.default_rng(13)
     B, bs = 200, 16
