@@ -2,7 +2,7 @@
 // types, devices and shapes, outputs allocated by torch, the current stream, one C call. A decode
 // step makes several of these calls of a few microseconds each, and the same written with ctypes
 // and Tensor attributes took longer than the kernels: norm of 64 tokens 15.8 us a call (2.3 of
-// them on the GPU), now 6.0; two table calls with four outputs 26.4 (8.9), now 14.3; append and
+// them on the GPU), now 5.9; two table calls with four outputs 26.4 (8.8), now 11.6; append and
 // widening of 64 tokens 14.3 (4.7), now 8.2.
 //
 // The library itself is reached through the addresses of its entry points, handed over by bind(),
