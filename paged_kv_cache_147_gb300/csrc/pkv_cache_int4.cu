@@ -23,6 +23,7 @@ kv_append_int4_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                       const int64_t* __restrict__ slots, int num_tokens,
                       uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
                       int64_t num_slots, int num_kv_heads, int bs_shift, unsigned int* err) {
+  griddep_wait();
   const int lane = threadIdx.x & 31, c = lane & (kRowLanes - 1);
   const unsigned warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const unsigned pair = warp / num_kv_heads;
@@ -63,6 +64,7 @@ kv_append_int4_groups_kernel(const uint4* __restrict__ k, const uint4* __restric
                              uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
                              int64_t num_slots, int num_kv_heads, int bs_shift,
                              unsigned int* err) {
+  griddep_wait();
   const int lane = threadIdx.x & 31, g = lane & 3;
   const unsigned warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const unsigned job = warp >> 1, which = warp & 1;
@@ -96,6 +98,7 @@ widen_blocks_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __r
                          int num_blocks, int num_blocks_out, int parts, int block_rows,
                          uint4* __restrict__ k_out, uint4* __restrict__ v_out,
                          unsigned int* err) {
+  griddep_wait();
   const int job = blockIdx.x / parts, part = blockIdx.x - job * parts;
   const int which = job & 1;
   const int32_t s = __ldg(src + (job >> 1)), d = __ldg(dst + (job >> 1));
@@ -170,11 +173,11 @@ int pkv_kv_append_int4(const void* k, const void* v, const int64_t* slot_mapping
   unsigned int* err = device_error_ptr();
   if (!err) return launch_status();
   const auto kernel = groups ? &kv_append_int4_groups_kernel : &kv_append_int4_kernel;
-  kernel<<<static_cast<unsigned>(blocks), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping, num_tokens,
-      static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
-      static_cast<int64_t>(num_blocks) * block_size, num_kv_heads, log2_of(block_size), err);
-  return launch_status();
+  return launch_waiting(kernel, static_cast<unsigned>(blocks), kThreads, stream,
+                        static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping,
+                        num_tokens, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
+                        static_cast<int64_t>(num_blocks) * block_size, num_kv_heads,
+                        log2_of(block_size), err);
 }
 
 int pkv_widen_blocks_int4(const void* k_cache, const void* v_cache, const int32_t* src,
@@ -194,12 +197,11 @@ int pkv_widen_blocks_int4(const void* k_cache, const void* v_cache, const int32_
   if (rows * kRowLanes > 0x3fffffff || 2LL * n * parts > 0x7fffffff) return PKV_EINVAL;
   unsigned int* err = device_error_ptr();
   if (!err) return launch_status();
-  widen_blocks_int4_kernel<<<static_cast<unsigned>(2LL * n * parts), kThreads, 0,
-                             static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), src, dst,
-      num_blocks, num_blocks_out, static_cast<int>(parts), static_cast<int>(rows),
-      static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), err);
-  return launch_status();
+  return launch_waiting(&widen_blocks_int4_kernel, static_cast<unsigned>(2LL * n * parts), kThreads,
+                        stream, static_cast<const uint8_t*>(k_cache),
+                        static_cast<const uint8_t*>(v_cache), src, dst, num_blocks, num_blocks_out,
+                        static_cast<int>(parts), static_cast<int>(rows), static_cast<uint4*>(k_out),
+                        static_cast<uint4*>(v_out), err);
 }
 
 }  // extern "C"

@@ -23,6 +23,25 @@ int sm_count();
 // cuTensorMapEncodeTiled from the driver, resolved once through the runtime.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// Launches a kernel whose threads all begin with griddep_wait(): its CTAs may take their places
+// while the kernel before it ends (programmatic dependent launch), and see all that it wrote. It
+// lets nothing start early itself. In a row with other short kernels that saves 0.2 to 1 us each
+// (append and widening of 64 tokens 4.8 -> 3.8 us, two table calls 8.8 -> 8.2).
+template <class... P, class... A>
+int launch_waiting(void (*kernel)(P...), unsigned grid, unsigned block, pkv_stream_t stream,
+                   A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...));
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline bool valid_block_size(int bs) {

@@ -59,6 +59,7 @@ __device__ __forceinline__ void store(__half* p, uint2 v) {
 
 template <int HPT, bool STREAM>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a) {
+  griddep_wait();
   const int l = threadIdx.x & 15;
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 4;
   const int64_t t = unit / a.groups;
@@ -129,8 +130,8 @@ int launch(NormRopeArgs& a, cudaStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(a.num_tokens) * a.groups * 16 + kThreads - 1) /
                          kThreads;
   if (blocks > 0x7fffffff) return PKV_EINVAL;
-  norm_rope_kernel<HPT, STREAM><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-  return launch_status();
+  return launch_waiting(&norm_rope_kernel<HPT, STREAM>, static_cast<unsigned>(blocks), kThreads,
+                        stream, a);
 }
 
 }  // namespace

@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kMaxThreads) extend_kernel(const TableArgs a) 
   const int64_t cap = static_cast<int64_t>(a.max_blocks) << sh;
   unsigned int bad = 0;
 
+  if (TOKENS) griddep_wait();                          // the launch before this call's
   if (TOKENS && !STATE) griddep_launch_dependents();   // the second launch scans meanwhile
   int count = *a.free_count;
   if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = 0; }
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kMaxThreads) truncate_kernel(const TableArgs a
   const int64_t cap = static_cast<int64_t>(a.max_blocks) << sh;
   unsigned int bad = 0;
 
+  if (BLOCKS) griddep_wait();
   if (BLOCKS && !STATE) griddep_launch_dependents();
   int count = *a.free_count;
   if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = a.num_blocks; }
@@ -309,10 +311,11 @@ __global__ void __launch_bounds__(kMaxThreads) truncate_kernel(const TableArgs a
 
 int launch_status() { return cuda_status(cudaGetLastError()); }
 
-// `cluster` > 0: one cluster of that many CTAs; 0: `ctas` CTAs on their own; `second`: may start
-// while the launch before it, its own first half, still runs.
+// `cluster` > 0: one cluster of that many CTAs; 0: `ctas` CTAs on their own. May start while the
+// launch before it ends: the first (or only) launch of a call waits for that before it reads
+// anything, a second one before it writes.
 int launch(const void* fn, const TableArgs& a, size_t smem, int cluster, int ctas,
-           cudaStream_t stream, bool second = false) {
+           cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (smem > 47 * 1024)   // past the default limit, beside the kernels' own 528 bytes
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -323,18 +326,15 @@ int launch(const void* fn, const TableArgs& a, size_t smem, int cluster, int cta
   cfg.blockDim = dim3(threads_for(a.num_seqs));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  if (second) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-  } else {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = second || cluster ? 1 : 0;
+  cfg.numAttrs = cluster ? 2 : 1;
   void* params[1] = {const_cast<TableArgs*>(&a)};
   return cuda_status(cudaLaunchKernelExC(&cfg, fn, params));
 }
@@ -393,7 +393,7 @@ int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_
   const int st =
       launch(reinterpret_cast<const void*>(&extend_kernel<true, false>), a, smem, 0, ctas, s);
   if (st != PKV_OK) return st;
-  return launch(reinterpret_cast<const void*>(&extend_kernel<false, true>), a, smem, 0, 1, s, true);
+  return launch(reinterpret_cast<const void*>(&extend_kernel<false, true>), a, smem, 0, 1, s);
 }
 
 int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* keep_lens,
@@ -424,7 +424,7 @@ int pkv_truncate_tables(int32_t* block_tables, int32_t* context_lens, const int3
   const int st =
       launch(reinterpret_cast<const void*>(&truncate_kernel<true, false>), a, smem, 0, ctas, s);
   if (st != PKV_OK) return st;
-  return launch(reinterpret_cast<const void*>(&truncate_kernel<false, true>), a, smem, 0, 1, s, true);
+  return launch(reinterpret_cast<const void*>(&truncate_kernel<false, true>), a, smem, 0, 1, s);
 }
 
 }  // extern "C"
