@@ -96,3 +96,80 @@ def test_prompts_then_drafts_with_rollback():
     tables, lens, free, count = step.truncate(tables, lens, keep, bs, free, count)
     assert d[3].item() == count and d[1][2].item() == 0
     assert pkv.device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("B,fused", [(3, False), (40, False), (40, True)])
+def test_steps_in_a_row_without_a_pause(B, fused):
+    # every call reads what the one before it wrote, with no synchronisation and no other kernel in
+    # between (their launches overlap); issued one by one and as a captured graph
+    rng = np.random.default_rng(B)
+    hq, hkv, bs, width, q_len, steps = 12, 2, 16, 30, 3, 5
+    scale, eps = 128 ** -0.5, 1e-6
+    lens = rng.integers(0, 300, B).astype(np.int32)
+    need = -(-lens // bs)
+    nb = int(need.sum()) + 3 * B
+    perm = rng.permutation(nb).astype(np.int32)
+    tables = np.full((B, width), -1, np.int32)
+    tables[np.arange(width)[None] < need[:, None]] = perm[:need.sum()]
+    free = np.concatenate([perm[need.sum():], perm[:need.sum()]])
+    count = nb - int(need.sum())
+    k0, v0 = (int4.quantise(rng.standard_normal((nb, hkv, bs, 128)).astype(np.float16)) for _ in range(2))
+    table = pkv.rope_table(1024).to(DEV)
+    w = [_dev((1 + 0.2 * rng.standard_normal(128)).astype(np.float16)) for _ in range(2)]
+    qs, ks, vs = (_dev(rng.standard_normal((steps, B * q_len, h, 128)).astype(np.float16))
+                  for h in (hq, hkv, hkv))
+    new = np.full(B, q_len, np.int32)
+    newd, keeps = _dev(new), []
+    t, l, f, c, sim = tables, lens, free, count, []
+    for i in range(steps):          # what the tables must be, and how much each step takes back
+        t, l, c, s, _, _, _, refused = step.extend(t, l, new, bs, f, c, B * q_len)
+        assert not refused
+        sim.append((t, l, s))
+        keeps.append((l - rng.integers(0, q_len, B)).astype(np.int32))
+        t, l, f, c = step.truncate(t, l, keeps[-1], bs, f, c)
+    keepd = [_dev(x) for x in keeps]
+    start = [_dev(x) for x in (tables, lens, free, np.array([count], np.int32), k0, v0)]
+    d = [x.clone() for x in start]
+    ws = pkv.make_workspace(B, q_len, hq, hkv)
+    outs = [torch.empty(B, q_len, hq, 128, dtype=torch.float16, device=DEV) for _ in range(steps)]
+    q_out, k_out = torch.empty_like(qs), torch.empty_like(ks)
+    maps = pkv.extend_tables(d[0].clone(), d[1].clone(), 0 * newd, bs, d[2].clone(), d[3].clone(),
+                             B * q_len)
+
+    def run():
+        for i in range(steps):
+            pkv.extend_tables(d[0], d[1], newd, bs, d[2], d[3], B * q_len, out=maps)
+            pkv.qk_norm_rope(qs[i], ks[i], *w, eps, maps[2], table, q_out[i], k_out[i])
+            args = (d[4], d[5], d[0], d[1], scale, ws)
+            q = q_out[i].view(B, q_len, hq, 128)
+            if fused:
+                pkv.paged_attn_decode_append_int4(outs[i], q, k_out[i], vs[i], *args)
+            else:
+                pkv.kv_append_int4(k_out[i], vs[i], maps[0], d[4], d[5])
+                pkv.paged_attn_decode_int4(outs[i], q, *args)
+            pkv.truncate_tables(d[0], d[1], keepd[i], bs, d[2], d[3])
+
+    run()
+    torch.cuda.synchronize()
+    kp, vp = k0.copy(), v0.copy()
+    for i, (t_i, l_i, s_i) in enumerate(sim):
+        int4.append(f16_host(k_out[i]), f16_host(vs[i]), s_i, kp, vp)
+        want, tol = int4.attention(f16_host(q_out[i].view(B, q_len, hq, 128)), kp, vp, t_i, l_i, scale)
+        assert (np.abs(outs[i].float().cpu().numpy() - want) <= tol).all(), i
+    first = [o.clone() for o in outs] + [x.clone() for x in d]
+    for got, want in zip(d, (t, l, f, np.array([c]), kp, vp)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        run()
+    for again in (run, graph.replay, run, graph.replay):
+        for x, y in zip(d, start):
+            x.copy_(y)
+        for o in outs:
+            o.fill_(float("nan"))
+        again()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs + d, first))
+    assert pkv.device_error(clear=True) == 0
