@@ -28,11 +28,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // lets nothing start early itself. In a row with other short kernels that saves 0.2 to 1 us each
 // (append and widening of 64 tokens 4.8 -> 3.8 us, two table calls 8.8 -> 8.2).
 template <class... P, class... A>
-int launch_waiting(void (*kernel)(P...), unsigned grid, unsigned block, pkv_stream_t stream,
-                   A... args) {
+int launch_waiting(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                   pkv_stream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

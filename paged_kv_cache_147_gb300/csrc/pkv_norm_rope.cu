@@ -131,7 +131,7 @@ int launch(NormRopeArgs& a, cudaStream_t stream) {
                          kThreads;
   if (blocks > 0x7fffffff) return PKV_EINVAL;
   return launch_waiting(&norm_rope_kernel<HPT, STREAM>, static_cast<unsigned>(blocks), kThreads,
-                        stream, a);
+                        0, stream, a);
 }
 
 }  // namespace
