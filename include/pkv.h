@@ -406,7 +406,8 @@ int pkv_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, int
  *   cu_new_lens[b] = where sequence b's tokens start (int32 [num_seqs + 1], the last the total)
  *   seq_out[i] = b, position_out[i] = its position, slot_out[i] = the slot of pkv_slot_mapping
  * (int32, int64, int64 [max_tokens]); entries behind the last token get -1, so that the arrays
- * serve as they are as the padded inputs of pkv_kv_append and pkv_qk_norm_rope. A sequence that
+ * serve as they are as the padded inputs of pkv_kv_append and pkv_qk_norm_rope. A call with no
+ * sequences and no tokens writes cu_new_lens[0] = 0 and needs no other array. A sequence that
  * cannot be served keeps its table and length, its tokens get -1 in all three arrays but keep
  * their places, and an error bit is set: new_lens < 0 or a context outside [0, max_blocks *
  * block_size] PKV_DEVERR_CONTEXT (a negative count has no places), past the table

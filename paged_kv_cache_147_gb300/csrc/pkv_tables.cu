@@ -311,6 +311,19 @@ __global__ void __launch_bounds__(kMaxThreads) truncate_kernel(const TableArgs a
 
 int launch_status() { return cuda_status(cudaGetLastError()); }
 
+// The one number an extend of no sequences by no tokens writes: cu_new_lens[0] = 0. Such a call may
+// come without outputs, so an address that CUDA does not know (or no device at all) is left alone.
+int write_empty_total(int32_t* cu, cudaStream_t stream) {
+  cudaPointerAttributes at = {};
+  if (!cu) return PKV_OK;
+  if (cudaPointerGetAttributes(&at, cu) != cudaSuccess) {
+    cudaGetLastError();   // not this call's to report
+    return PKV_OK;
+  }
+  if (at.type == cudaMemoryTypeUnregistered) return PKV_OK;
+  return cuda_status(cudaMemsetAsync(cu, 0, sizeof(int32_t), stream));
+}
+
 // `cluster` > 0: one cluster of that many CTAs; 0: `ctas` CTAs on their own. May start while the
 // launch before it ends: the first (or only) launch of a call waits for that before it reads
 // anything, a second one before it writes.
@@ -371,7 +384,8 @@ int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_
                       pkv_stream_t stream) {
   if (!valid_tables(num_seqs, max_blocks_per_seq, block_size, num_blocks) || max_tokens < 0)
     return PKV_EINVAL;
-  if (num_seqs == 0 && max_tokens == 0) return PKV_OK;
+  if (num_seqs == 0 && max_tokens == 0)
+    return write_empty_total(cu_new_lens, static_cast<cudaStream_t>(stream));
   if ((num_seqs > 0 && (!context_lens || !new_lens)) ||
       (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) ||
       (num_blocks > 0 && !free_blocks) || !free_count || !cu_new_lens || (max_tokens > 0 && (!slot_out || !seq_out || !position_out)))

@@ -230,3 +230,27 @@ def test_binding_refuses_wrong_types_and_shapes():
         with pytest.raises(pkv.PkvError) as e:
             call()
         assert e.value.status == pkv.EINVAL
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_neither_sequences_nor_tokens_still_give_a_total(given):
+    # an idle step: the total of no tokens is written, whatever the memory held before
+    z = torch.zeros(0, 4, dtype=torch.int32, device=DEV)
+    e, free = z[:, 0].clone(), torch.arange(5, dtype=torch.int32, device=DEV)
+    count = torch.full((1,), 5, dtype=torch.int32, device=DEV)
+    wide = torch.zeros(0, dtype=torch.int64, device=DEV)
+    cu = torch.full((1,), 77, dtype=torch.int32, device=DEV)
+    if given:
+        pkv.extend_tables(z, e, e, 16, free, count, 0, out=(wide, e, wide, cu))
+    else:
+        del cu          # the next allocation of this size takes its place
+        cu = pkv.extend_tables(z, e, e, 16, free, count, 0)[3]
+    assert cu.tolist() == [0] and count.item() == 5 and free.tolist() == [0, 1, 2, 3, 4]
+    # captured as well
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        pkv.extend_tables(z, e, e, 16, free, count, 0, out=(wide, e, wide, cu))
+    cu.fill_(77)
+    graph.replay()
+    assert cu.tolist() == [0] and pkv.device_error(clear=True) == 0
