@@ -413,7 +413,8 @@ int pkv_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, int
  * block_size] PKV_DEVERR_CONTEXT (a negative count has no places), past the table
  * PKV_DEVERR_POSITION, past max_tokens or the free blocks PKV_DEVERR_SPACE (every later sequence
  * that needs blocks, or tokens, is then refused too). A free id outside [0, num_blocks) goes into
- * the table as it is, its tokens get slot -1, and PKV_DEVERR_BLOCK_ID is set.
+ * the table as it is, its tokens get slot -1, and PKV_DEVERR_BLOCK_ID is set. A *free_count outside
+ * [0, num_blocks] sets PKV_DEVERR_SPACE and stays as it is; the stack counts as empty.
  *
  * pkv_truncate_tables: cuts every sequence with 0 <= keep_lens[b] < context_lens[b] back to
  * keep_lens[b] tokens (rejected drafts; 0 to give a sequence up); a negative or larger value
@@ -421,7 +422,8 @@ int pkv_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, int
  * the top of the stack, in such an order that cutting off what an extend just added restores the
  * stack. A context outside [0, max_blocks * block_size] stays as it is and sets
  * PKV_DEVERR_CONTEXT. If more blocks came back than the stack holds (num_blocks), nothing is
- * changed and PKV_DEVERR_SPACE set. keep_lens (device): int32 [num_seqs]. */
+ * changed and PKV_DEVERR_SPACE set; a *free_count outside [0, num_blocks] stays as it is, sets that
+ * bit too and counts as a full stack. keep_lens (device): int32 [num_seqs]. */
 int pkv_extend_tables(int32_t* block_tables, int32_t* context_lens, const int32_t* new_lens,
                       int num_seqs, int max_blocks_per_seq, int block_size, int32_t* free_blocks,
                       int32_t* free_count, int num_blocks, int64_t* slot_out, int32_t* seq_out,

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kMaxThreads) extend_kernel(const TableArgs a) 
     if (TOKENS) cluster_wait(); else griddep_wait();
     for (int b = rank * threads + tid; b < n; b += ctas * threads)
       if (len[b] >= 0) a.lens[b] = len[b] + a.arg[b];
-    if (rank == 0 && tid == 0) *a.free_count = count - used;
+    if (rank == 0 && tid == 0 && used > 0) *a.free_count = count - used;
   }
 }
 

@@ -254,3 +254,22 @@ def test_neither_sequences_nor_tokens_still_give_a_total(given):
     cu.fill_(77)
     graph.replay()
     assert cu.tolist() == [0] and pkv.device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("count", [999, -1])
+@pytest.mark.parametrize("max_tokens", [300, 8193])     # one launch, two
+def test_a_free_count_no_stack_has_stays_as_it_is(count, max_tokens):
+    rng = np.random.default_rng(21)
+    tables, lens, free, _ = _state(rng, [20, 16, 40, 5, 0, 31], 16, 6, 9)
+    new = np.array([40, 0, 8, 40, 3, 1], np.int32)     # the third and the last need no block
+    keep = np.array([19, 16, 0, 0, 0, 31], np.int32)   # the first keeps its blocks
+    d = [_dev(x) for x in (tables, lens, new, free, np.array([count], np.int32))]
+    pkv.extend_tables(d[0], d[1], d[2], 16, d[3], d[4], max_tokens)
+    assert pkv.device_error(clear=True) == pkv.DEVERR_SPACE and d[4].item() == count
+    assert np.array_equal(d[0].cpu().numpy(), tables) and np.array_equal(d[3].cpu().numpy(), free)
+    assert d[1].tolist() == [20, 16, 48, 5, 0, 32]
+    d[1].copy_(_dev(lens))
+    pkv.truncate_tables(d[0], d[1], _dev(keep), 16, d[3], d[4])
+    assert pkv.device_error(clear=True) == pkv.DEVERR_SPACE and d[4].item() == count
+    assert np.array_equal(d[0].cpu().numpy(), tables) and np.array_equal(d[3].cpu().numpy(), free)
+    assert np.array_equal(d[1].cpu().numpy(), lens)
