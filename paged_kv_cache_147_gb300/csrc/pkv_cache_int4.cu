@@ -19,10 +19,9 @@ constexpr int kRowLanes = 16;
 // Half-warp = one (token, kv head): its K row and its V row. The two half-warps of a warp take
 // neighbouring tokens of one head, which usually are neighbouring rows of a block.
 __global__ void __launch_bounds__(kThreads)
-kv_append_int4_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
-                      const int64_t* __restrict__ slots, int num_tokens,
-                      uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
-                      int64_t num_slots, int num_kv_heads, int bs_shift, unsigned int* err) {
+kv_append_int4_kernel(const uint4* k, const uint4* v, const int64_t* slots, int num_tokens,
+                      uint8_t* k_cache, uint8_t* v_cache, int64_t num_slots, int num_kv_heads,
+                      int bs_shift, unsigned int* err) {
   griddep_wait();
   const int lane = threadIdx.x & 31, c = lane & (kRowLanes - 1);
   const unsigned warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -30,12 +29,12 @@ kv_append_int4_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
   const int h = static_cast<int>(warp - pair * num_kv_heads);
   const int64_t t = 2 * static_cast<int64_t>(pair) + (lane >> 4);
   const bool in = t < num_tokens;
-  const int64_t slot = in ? __ldg(slots + t) : -1;
+  const int64_t slot = in ? slots[t] : -1;
   if (in && slot >= num_slots && c == 0 && h == 0) atomicOr(err, PKV_DEVERR_SLOT);
   const bool live = slot >= 0 && slot < num_slots;
   const int64_t src = (t * num_kv_heads + h) * kRowLanes + c;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint4 x = live ? __ldg(k + src) : zero, y = live ? __ldg(v + src) : zero;
+  const uint4 x = live ? k[src] : zero, y = live ? v[src] : zero;
   uint32_t kc, kp, vc, vp;
   int4_quantise(x, kc, kp);
   int4_quantise(y, vc, vp);
@@ -59,11 +58,9 @@ kv_append_int4_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
 // 64 tokens of 2 heads 2.1 against 2.3).
 constexpr int kGroupRows = 16384;
 __global__ void __launch_bounds__(kThreads)
-kv_append_int4_groups_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
-                             const int64_t* __restrict__ slots, int num_tokens,
-                             uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
-                             int64_t num_slots, int num_kv_heads, int bs_shift,
-                             unsigned int* err) {
+kv_append_int4_groups_kernel(const uint4* k, const uint4* v, const int64_t* slots, int num_tokens,
+                             uint8_t* k_cache, uint8_t* v_cache, int64_t num_slots,
+                             int num_kv_heads, int bs_shift, unsigned int* err) {
   griddep_wait();
   const int lane = threadIdx.x & 31, g = lane & 3;
   const unsigned warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -72,7 +69,7 @@ kv_append_int4_groups_kernel(const uint4* __restrict__ k, const uint4* __restric
   const int h = static_cast<int>(job - oct * num_kv_heads);
   const int64_t t = 8 * static_cast<int64_t>(oct) + (lane >> 2);
   if (t >= num_tokens) return;
-  const int64_t slot = __ldg(slots + t);
+  const int64_t slot = slots[t];
   if (slot >= num_slots && g == 0 && h == 0 && which == 0) atomicOr(err, PKV_DEVERR_SLOT);
   if (slot < 0 || slot >= num_slots) return;
   const uint4* src = (which ? v : k) + (t * num_kv_heads + h) * kRowLanes + 4 * g;
@@ -93,15 +90,13 @@ kv_append_int4_groups_kernel(const uint4* __restrict__ k, const uint4* __restric
 // blocks are written past the caches' usual order (streaming): the pools stay in L2 (9.8 -> 7.5 us).
 constexpr int kWiden = 4;
 __global__ void __launch_bounds__(kThreads)
-widen_blocks_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
-                         const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
-                         int num_blocks, int num_blocks_out, int parts, int block_rows,
-                         uint4* __restrict__ k_out, uint4* __restrict__ v_out,
-                         unsigned int* err) {
+widen_blocks_int4_kernel(const uint8_t* k_cache, const uint8_t* v_cache, const int32_t* src,
+                         const int32_t* dst, int num_blocks, int num_blocks_out, int parts,
+                         int block_rows, uint4* k_out, uint4* v_out, unsigned int* err) {
   griddep_wait();
   const int job = blockIdx.x / parts, part = blockIdx.x - job * parts;
   const int which = job & 1;
-  const int32_t s = __ldg(src + (job >> 1)), d = __ldg(dst + (job >> 1));
+  const int32_t s = src[job >> 1], d = dst[job >> 1];
   if (s < 0 || s >= num_blocks || d < 0 || d >= num_blocks_out) {
     if (part == 0 && threadIdx.x == 0) atomicOr(err, PKV_DEVERR_BLOCK_ID);
     return;
@@ -118,8 +113,8 @@ widen_blocks_int4_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __r
       const int row = r + i * kRows;
       w[i] = sz[i] = 0u;
       if (row < block_rows) {
-        w[i] = __ldg(from + row * (kInt4Row / 4) + c);
-        sz[i] = __ldg(from + row * (kInt4Row / 4) + kInt4Params / 4 + (c >> 2));
+        w[i] = from[row * (kInt4Row / 4) + c];
+        sz[i] = from[row * (kInt4Row / 4) + kInt4Params / 4 + (c >> 2)];
       }
     }
 #pragma unroll

@@ -143,7 +143,7 @@ struct StageWalk {
     nn = min(16, (np - jp + NCS - 1) / NCS);
     const int c = s.c0 + 2 * (jp + (lane >> 1) * NCS) + (lane & 1);
     if ((lane >> 1) < nn && c < s.c1) {
-      ids = __ldg(a.block_tables + static_cast<int64_t>(s.b) * a.max_blocks + (c >> a.bs_shift));
+      ids = a.block_tables[static_cast<int64_t>(s.b) * a.max_blocks + (c >> a.bs_shift)];
       at = (s.h << 8) | ((c & ((1 << a.bs_shift) - 1)) << 4);
     }
     jp += nn * NCS;
@@ -274,7 +274,7 @@ __device__ __forceinline__ void merge_rows(const DecodeArgs& a, const float* stO
 // (merges each segment's per-warp states, writes outputs and split units' partials).
 template <int NCS, int RS, int ND, int MINB, bool APPEND>
 __global__ void __launch_bounds__((NCS * RS + 2) * 32, MINB)
-decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
+decode_int4_kernel(const DecodeArgs a, const __half* q_in) {
   using L = Smem4<NCS, RS, ND>;
   constexpr int NCW = NCS * RS;
   if (!APPEND) griddep_wait();   // (the fused form reads ahead; see the early-start contract)
@@ -380,7 +380,7 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
             q_in + ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr)
-          v[gr] = row < a.R ? __ldg(src + 4 * gr + t4) : make_uint4(0, 0, 0, 0);
+          v[gr] = row < a.R ? src[4 * gr + t4] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
@@ -443,11 +443,10 @@ decode_int4_kernel(const DecodeArgs a, const __half* __restrict__ q_in) {
         const int pos = slen[sg.b] - a.q_len + i;
         const int c = pos >> 4;
         if (pos < 0 || c < sg.c0 || c >= sg.c1) continue;
-        const int id = __ldg(a.block_tables + static_cast<int64_t>(sg.b) * a.max_blocks +
-                             (c >> a.bs_shift));
+        const int id = a.block_tables[static_cast<int64_t>(sg.b) * a.max_blocks + (c >> a.bs_shift)];
         const int64_t row = (static_cast<int64_t>(sg.b) * a.q_len + i) * a.Hkv + sg.h;
         uint32_t codes, params;
-        int4_quantise(__ldg(reinterpret_cast<const uint4*>(src + row * kD) + p), codes, params);
+        int4_quantise(reinterpret_cast<const uint4*>(src + row * kD)[p], codes, params);
         const uint32_t to = nkv + i * kNewRow + which * kInt4Row;
         st_shared_u32(to + 4 * p, codes);
         if ((p & 3) == 0) st_shared_u32(to + kInt4Params + p, params);

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
   const int64_t t = unit / a.groups;
   const int h0 = static_cast<int>(unit - t * a.groups) * HPT;
   const bool in = t < a.num_tokens;
-  const int64_t pos = in ? __ldg(a.positions + t) : -1;
+  const int64_t pos = in ? a.positions[t] : -1;
   if (pos >= a.n_index && l == 0 && h0 == 0) atomicOr(a.err, PKV_DEVERR_POSITION);
   const bool live = pos >= 0 && pos < a.n_index;
   uint2 lo[HPT], hi[HPT];
@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
   }
   float4 cs[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   if (live) {
-    cs[0] = __ldg(a.cos_sin + pos * 32 + 2 * l);
-    cs[1] = __ldg(a.cos_sin + pos * 32 + 2 * l + 1);
+    cs[0] = a.cos_sin[pos * 32 + 2 * l];
+    cs[1] = a.cos_sin[pos * 32 + 2 * l + 1];
   }
   const float c[4] = {cs[0].x, cs[0].z, cs[1].x, cs[1].z};
   const float s[4] = {cs[0].y, cs[0].w, cs[1].y, cs[1].w};
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
     const float r = rsqrtf(fmaf(sum, 1.f / kHead, a.eps));
     const __half* w = h < a.hq ? a.q_weight : a.k_weight;
     float wx[4], wy[4];
-    unpack4(__ldg(reinterpret_cast<const uint2*>(w + 4 * l)), wx);
-    unpack4(__ldg(reinterpret_cast<const uint2*>(w + 64 + 4 * l)), wy);
+    unpack4(*reinterpret_cast<const uint2*>(w + 4 * l), wx);
+    unpack4(*reinterpret_cast<const uint2*>(w + 64 + 4 * l), wy);
     float ox[4], oy[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

@@ -70,6 +70,13 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
+// The scan of a call's second launch runs before its wait. What the kernels before the call wrote is
+// in L2 by then (the first launch waited for them before it let the second one in), so it reads there.
+template <bool BEFORE_WAIT>
+__device__ __forceinline__ int scan_load(const int32_t* p) {
+  return BEFORE_WAIT ? __ldcg(p) : *p;
+}
+
 // Exclusive sums of two 64-bit values over the CTA's threads, and their totals.
 __device__ __forceinline__ void cta_scan(int64_t& x, int64_t& y, int64_t& total_x,
                                          int64_t& total_y, int64_t (*part)[2]) {
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(kMaxThreads) extend_kernel(const TableArgs a) 
 
   if (TOKENS) griddep_wait();                          // the launch before this call's
   if (TOKENS && !STATE) griddep_launch_dependents();   // the second launch scans meanwhile
-  int count = *a.free_count;
+  int count = scan_load<!TOKENS>(a.free_count);
   if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = 0; }
   if (tid == 0) used_s = 0;
 
@@ -142,7 +149,7 @@ __global__ void __launch_bounds__(kMaxThreads) extend_kernel(const TableArgs a) 
   const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
   int64_t x = 0, y = 0;
   for (int b = b0; b < b1; ++b) {
-    const int ctx = a.lens[b], m = a.arg[b];
+    const int ctx = scan_load<!TOKENS>(a.lens + b), m = scan_load<!TOKENS>(a.arg + b);
     const bool ok = ctx >= 0 && ctx <= cap && m >= 0 && ctx + static_cast<int64_t>(m) <= cap;
     x += max(m, 0);
     if (ok) y += blocks_of(ctx + static_cast<int64_t>(m), sh) - blocks_of(ctx, sh);
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(kMaxThreads) extend_kernel(const TableArgs a) 
   cta_scan(x, y, total_x, total_y, part);
   int used = 0;
   for (int b = b0; b < b1; ++b) {
-    const int ctx = a.lens[b], m = a.arg[b];
+    const int ctx = scan_load<!TOKENS>(a.lens + b), m = scan_load<!TOKENS>(a.arg + b);
     bool ok = true;
     int need = 0;
     if (ctx < 0 || ctx > cap || m < 0) {
@@ -262,13 +269,13 @@ __global__ void __launch_bounds__(kMaxThreads) truncate_kernel(const TableArgs a
 
   if (BLOCKS) griddep_wait();
   if (BLOCKS && !STATE) griddep_launch_dependents();
-  int count = *a.free_count;
+  int count = scan_load<!BLOCKS>(a.free_count);
   if (count < 0 || count > a.num_blocks) { bad |= PKV_DEVERR_SPACE; count = a.num_blocks; }
   const int per = (n + threads - 1) / threads;
   const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
   int64_t x = 0, unused = 0;
   for (int b = b0; b < b1; ++b) {
-    const int ctx = a.lens[b], m = a.arg[b];
+    const int ctx = scan_load<!BLOCKS>(a.lens + b), m = scan_load<!BLOCKS>(a.arg + b);
     if (ctx >= 0 && ctx <= cap && m >= 0 && m < ctx) x += blocks_of(ctx, sh) - blocks_of(m, sh);
   }
   int64_t total, total_unused;
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kMaxThreads) truncate_kernel(const TableArgs a
   const bool fits = count + total <= a.num_blocks;
   if (!fits) bad |= PKV_DEVERR_SPACE;
   for (int b = b0; b < b1; ++b) {
-    const int ctx = a.lens[b], m = a.arg[b];
+    const int ctx = scan_load<!BLOCKS>(a.lens + b), m = scan_load<!BLOCKS>(a.arg + b);
     const bool known = ctx >= 0 && ctx <= cap;
     if (!known) bad |= PKV_DEVERR_CONTEXT;
     const bool cut = known && m >= 0 && m < ctx;

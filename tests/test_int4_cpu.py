@@ -1,6 +1,8 @@
 """CPU pins of the 4-bit oracle and the step oracle, and the host refusals of the entry points
 around the 4-bit cache (their argument checks run before any CUDA call)."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -164,6 +166,18 @@ def test_tables_refuse_bad_arguments(lib):
     assert cut(P, P, None, 3, 8, 16, P, P, 64, None) == pkv.EINVAL
     assert cut(P, P, P, 4097, 8, 16, P, P, 64, None) == pkv.EINVAL
     assert cut(P, P, P, 3, 8, 15, P, P, 64, None) == pkv.EINVAL
+
+
+# ------------------------------------------------------------------------- launches that wait
+@pytest.mark.parametrize("source", ["pkv_cache_int4.cu", "pkv_decode_int4.cu", "pkv_norm_rope.cu",
+                                    "pkv_tables.cu"])
+def test_kernels_that_start_early_read_through_plain_loads(source):
+    # their CTAs are resident while the kernel before them still writes what they will read:
+    # no load there may be declared read-only (__ldg, const __restrict__)
+    with open(os.path.join(build.CSRC, source)) as f:
+        code = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+    assert "griddep_wait()" in code
+    assert not re.findall(r"__ldg\b|__restrict__|__restrict\b|ld\.global\.nc", code)
 
 
 # ----------------------------------------------------------------------------- the binding
