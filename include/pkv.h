@@ -176,7 +176,8 @@ int pkv_paged_attn_decode(void* out, const void* q, const void* k_cache, const v
  * pools, not by pkv_copy_blocks, and not by the caller's own kernel (say, one that advances
  * context_lens on the device). A copy (cudaMemcpyAsync) or any other kernel in between is
  * enough; otherwise turn the overlap off with pkv_set_early_start(0). The library's other
- * kernels never let the next kernel start early. */
+ * kernels let the next one start early, if at all, only once the kernel before them has completed
+ * (pkv_paged_attn_decode_int4 does), so one of them in between is enough too. */
 int pkv_paged_attn_decode_append(void* out, const void* q, const void* k_new, const void* v_new,
                                  void* k_cache, void* v_cache, int num_blocks,
                                  const int32_t* block_tables, int max_blocks_per_seq,
@@ -363,7 +364,12 @@ int pkv_paged_attn_decode_int4(void* out, const void* q, const void* k_cache,
 
 /* pkv_paged_attn_decode_append over a 4-bit cache: the step's new rows k_new, v_new (fp16, as
  * there) are stored as pkv_kv_append_int4 stores them (the same bytes) and attended over in that
- * form. One launch per layer, with the early-start contract of pkv_paged_attn_decode_append. */
+ * form. One launch per layer, with the early-start contract of pkv_paged_attn_decode_append.
+ * As there, the last q_len positions of every context are taken for new rows: nothing else tells
+ * the call which sequences have any. One without (refused by pkv_extend_tables, or idle) would have
+ * its last cached rows overwritten, so give it a length of 0 in this call's context_lens: it then
+ * gets zeros and nothing of it is written. Or use pkv_kv_append_int4, which skips slots of -1, and
+ * pkv_paged_attn_decode_int4. */
 int pkv_paged_attn_decode_append_int4(void* out, const void* q, const void* k_new,
                                       const void* v_new, void* k_cache, void* v_cache,
                                       int num_blocks, const int32_t* block_tables,
@@ -415,6 +421,11 @@ int pkv_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, int
  * that needs blocks, or tokens, is then refused too). A free id outside [0, num_blocks) goes into
  * the table as it is, its tokens get slot -1, and PKV_DEVERR_BLOCK_ID is set. A *free_count outside
  * [0, num_blocks] sets PKV_DEVERR_SPACE and stays as it is; the stack counts as empty.
+ *
+ * A fused append + decode (any cache type) behind it: the call reads tables and lengths early, so
+ * it needs a launch in between (pkv_qk_norm_rope, a copy) or pkv_set_early_start(0); and it takes
+ * q_len new rows of every sequence, so new_lens[b] has to be q_len for all, and where one can be
+ * refused (seq_out[cu_new_lens[b]] is -1 then) or is idle, its length in that call has to be 0.
  *
  * pkv_truncate_tables: cuts every sequence with 0 <= keep_lens[b] < context_lens[b] back to
  * keep_lens[b] tokens (rejected drafts; 0 to give a sequence up); a negative or larger value

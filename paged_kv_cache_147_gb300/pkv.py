@@ -406,7 +406,11 @@ def paged_attn_decode_append_int4(out, q, k_new, v_new, k_cache, v_cache, block_
                                   context_lens, scale, workspace, stream=None):
     """paged_attn_decode_append over a 4-bit cache: the new fp16 rows k_new, v_new
     [B*q_len, Hkv, 128] are stored as kv_append_int4 stores them and attended over with the rest.
-    Early-start caveat as there."""
+    Early-start caveat as there.
+
+    WARNING: the last q_len positions of every context are written. A sequence without q_len new
+    tokens (refused by extend_tables, or idle) needs a length of 0 in context_lens here: zeros come
+    out and its rows stay. kv_append_int4 + paged_attn_decode_int4 go by the slots instead."""
     return (_ops or _torch_ops()).paged_attn_decode_append_int4(
         out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, workspace, stream)
 
@@ -428,7 +432,9 @@ def extend_tables(block_tables, context_lens, new_lens, block_size, free_blocks,
     """Grows the tables (int32 [B, max_blocks]) and lengths (int32 [B]) for new_lens more tokens
     per sequence, blocks off the stack free_blocks (int32 [num_blocks], free_count of them free;
     all updated in place) -> (slots int64, seq_ids int32, positions int64 [max_tokens],
-    cu_new_lens int32 [B + 1]); `out` gives the four to write into."""
+    cu_new_lens int32 [B + 1]); `out` gives the four to write into. A sequence that cannot be served
+    keeps its table and length, and its tokens get -1: a fused append + decode behind this call
+    needs a length of 0 for it (and a launch in between, see paged_attn_decode_append)."""
     return (_ops or _torch_ops()).extend_tables(
         block_tables, context_lens, new_lens, block_size, free_blocks, free_count, max_tokens,
         out if out is None else tuple(out), stream)

@@ -173,3 +173,52 @@ def test_steps_in_a_row_without_a_pause(B, fused):
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(outs + d, first))
     assert pkv.device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_refused_and_idle_sequences_keep_their_cached_rows(fused):
+    # five sequences, no free block: the second needs one and is refused, the fourth is idle. Their
+    # cached rows stay whichever way the step takes, though the norm left their keys as they were
+    rng = np.random.default_rng(8)
+    B, q_len, hq, hkv, bs, width = 5, 2, 12, 2, 16, 6
+    scale, eps = 128 ** -0.5, 1e-6
+    lens = np.array([20, 31, 46, 9, 33], np.int32)
+    new = np.array([2, 2, 2, 0, 2], np.int32)
+    need = -(-lens // bs)
+    nb = int(need.sum())
+    tables = np.full((B, width), -1, np.int32)
+    tables[np.arange(width)[None] < need[:, None]] = rng.permutation(nb)
+    free = np.zeros(nb, np.int32)
+    k0, v0 = (int4.quantise(rng.standard_normal((nb, hkv, bs, 128)).astype(np.float16)) for _ in range(2))
+    td, ld, kd, vd, news = (_dev(x) for x in (tables, lens, k0, v0, new))
+    T = B * q_len
+    slots, seqs, pos, cu = pkv.extend_tables(td, ld, news, bs, _dev(free), _dev(np.zeros(1, np.int32)), T)
+    assert pkv.device_error(clear=True) == pkv.DEVERR_SPACE
+    wt, wl, _, ws, _, _, _, refused = step.extend(tables, lens, new, bs, free, 0, T)
+    assert refused == [1] and np.array_equal(slots.cpu().numpy(), ws)
+    x = [_dev(rng.standard_normal((T, h, 128)).astype(np.float16)) for h in (hq, hkv, hkv)]
+    w = [_dev((1 + 0.2 * rng.standard_normal(128)).astype(np.float16)) for _ in range(2)]
+    q, k = (torch.full_like(t, float("nan")) for t in x[:2])
+    pkv.qk_norm_rope(*x[:2], *w, eps, pos, pkv.rope_table(64).to(DEV), q, k)
+    # the packed tokens of each sequence (those of one without new tokens are somebody else's)
+    rows = (cu[:-1, None] + torch.arange(q_len, device=DEV)).clamp(max=T - 1)
+    qb = q[rows]
+    out = torch.full_like(qb, float("nan"))
+    space = pkv.make_workspace(B, q_len, hq, hkv)
+    if fused:
+        served = (seqs[rows[:, 0]] >= 0) & (news == q_len)
+        step_lens = torch.where(served, ld, 0)
+        kb, vb = (t[rows].view(T, hkv, 128) for t in (k, x[2]))
+        pkv.paged_attn_decode_append_int4(out, qb, kb, vb, kd, vd, td, step_lens, scale, space)
+    else:
+        pkv.kv_append_int4(k, x[2], slots, kd, vd)
+        pkv.paged_attn_decode_int4(out, qb, kd, vd, td, ld, scale, space)
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == 0
+    int4.append(f16_host(k), f16_host(x[2]), ws, k0, v0)
+    assert np.array_equal(kd.cpu().numpy(), k0) and np.array_equal(vd.cpu().numpy(), v0)
+    some = [0, 2, 4]
+    want, tol = int4.attention(f16_host(qb)[some], k0, v0, wt[some], wl[some], scale)
+    assert (np.abs(out[some].float().cpu().numpy() - want) <= tol).all()
+    if fused:
+        assert (out[[1, 3]] == 0).all()
