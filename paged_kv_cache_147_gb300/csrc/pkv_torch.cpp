@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -95,6 +96,17 @@ struct Args {
     Py_DECREF(handle);
     if (PyErr_Occurred()) throw Raised();
     return s;
+  }
+};
+
+// Outputs of a call with the stream argument i, allocated on the stream that it runs on: memory freed
+// on another one may still be in use there.
+struct Outputs {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  Outputs(const Args& A, int i, pkv_stream_t s) {
+    if (A.a[i] != Py_None)
+      guard.reset_stream(
+          c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), A.dev));
   }
 };
 
@@ -198,6 +210,7 @@ PyObject* qk_norm_rope(Args& A) {
   }
   const float eps = A.number(4);
   const pkv_stream_t s = A.stream(9);
+  const Outputs on(A, 9, s);
   if (!qo.defined()) qo = at::empty({T, hq, 128}, q.options());
   if (!ko.defined()) ko = at::empty({T, hkv, 128}, q.options());
   const int st = lib.qk_norm_rope(ptr(qo), ptr(ko), ptr(q), ptr(k), qs, ks, ptr(qw), ptr(kw), eps,
@@ -224,6 +237,7 @@ PyObject* extend_tables(Args& A) {
   at::Tensor slots, seqs, pos, cu;
   PyObject* r;
   if (A.a[7] == Py_None) {
+    const Outputs on(A, 8, s);
     const auto wide = bt.options().dtype(kI64), narrow = bt.options();
     slots = at::empty({n}, wide);
     seqs = at::empty({n}, narrow);

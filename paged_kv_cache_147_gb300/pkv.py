@@ -147,6 +147,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(n: int, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """A call's output, allocated on the stream that the call runs on: memory freed on another one
+    may still be in use there."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
 def _p(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -189,7 +198,7 @@ def device_error(clear: bool = True, stream=None) -> int:
 # ------------------------------------------------------------------------------ slot mapping
 def slot_mapping(seq_ids, positions, block_tables, block_size, out=None, stream=None):
     n = positions.numel()
-    out = torch.empty(n, dtype=torch.int64, device=positions.device) if out is None else out
+    out = _empty(n, torch.int64, positions.device, stream) if out is None else out
     _check("pkv_slot_mapping", load().pkv_slot_mapping(
         _p(seq_ids), _p(positions), n, _p(block_tables), block_tables.shape[0],
         block_tables.shape[1], block_size, _p(out), _stream(stream)))
@@ -199,7 +208,7 @@ def slot_mapping(seq_ids, positions, block_tables, block_size, out=None, stream=
 def ring_slot_mapping(seq_ids, positions, block_tables, sink, window, block_size, out=None,
                       stream=None):
     n = positions.numel()
-    out = torch.empty(n, dtype=torch.int64, device=positions.device) if out is None else out
+    out = _empty(n, torch.int64, positions.device, stream) if out is None else out
     _check("pkv_ring_slot_mapping", load().pkv_ring_slot_mapping(
         _p(seq_ids), _p(positions), n, _p(block_tables), block_tables.shape[0],
         block_tables.shape[1], sink, window, block_size, _p(out), _stream(stream)))
@@ -254,8 +263,8 @@ def workspace_init(workspace, stream=None):
 
 def make_workspace(num_seqs, q_len, num_q_heads, num_kv_heads, device="cuda", stream=None):
     """Allocates (through torch) and zeroes a decode workspace."""
-    ws = torch.empty(decode_workspace_bytes(num_seqs, q_len, num_q_heads, num_kv_heads),
-                     dtype=torch.uint8, device=device)
+    ws = _empty(decode_workspace_bytes(num_seqs, q_len, num_q_heads, num_kv_heads), torch.uint8,
+                device, stream)
     workspace_init(ws, stream)
     return ws
 
@@ -479,9 +488,9 @@ def spec_verify(target_logits, draft_logits, drafts, u_accept, u_sample, n_accep
     u_sample [B] float32 -> (n_accept, next_token) int32 [B] (device tensors)."""
     B, K1, V = target_logits.shape
     if n_accept is None:
-        n_accept = torch.empty(B, dtype=torch.int32, device=target_logits.device)
+        n_accept = _empty(B, torch.int32, target_logits.device, stream)
     if next_token is None:
-        next_token = torch.empty(B, dtype=torch.int32, device=target_logits.device)
+        next_token = _empty(B, torch.int32, target_logits.device, stream)
     _check("pkv_spec_verify", load().pkv_spec_verify(
         _p(target_logits), _p(draft_logits), _p(drafts), _p(u_accept), _p(u_sample), B, K1 - 1,
         V, _p(n_accept), _p(next_token), _stream(stream)))
