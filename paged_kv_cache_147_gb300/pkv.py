@@ -234,12 +234,17 @@ def kv_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
 
 
 def copy_blocks(k_cache, v_cache, src, dst, stream=None):
-    """k_cache, v_cache [layers, NB, Hkv, bs, D] (or one layer [NB, Hkv, bs, D])."""
+    """k_cache, v_cache [layers, NB, Hkv, bs, D] (or one layer [NB, Hkv, bs, D]) of any cache type:
+    fp16 rows, uint8 E4M3 codes or uint8 4-bit rows (D = 80)."""
     kc = k_cache if k_cache.dim() == 5 else k_cache.unsqueeze(0)
     layers, nb, hkv, bs, d = kc.shape
+    row, layer = d * kc.element_size(), kc.stride(0) * kc.element_size()   # bytes
+    if row % 2 or layer % 2 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise PkvError("pkv_copy_blocks", EINVAL)
+    # the library counts in fp16 elements
     _check("pkv_copy_blocks", load().pkv_copy_blocks(
-        _p(k_cache), _p(v_cache), _p(src), _p(dst), src.numel(), kc.stride(0), layers, nb, hkv,
-        d, bs, _stream(stream)))
+        _p(k_cache), _p(v_cache), _p(src), _p(dst), src.numel(), layer // 2, layers, nb, hkv,
+        row // 2, bs, _stream(stream)))
 
 
 # ------------------------------------------------------------------------------ attention

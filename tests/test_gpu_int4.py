@@ -172,6 +172,21 @@ def test_copy_blocks_moves_4_bit_blocks():
     assert np.array_equal(kd.cpu().numpy(), k) and np.array_equal(vd.cpu().numpy(), v)
 
 
+@pytest.mark.parametrize("row", [80, 128])     # 4-bit rows, E4M3 codes
+def test_copy_blocks_of_byte_pools_moves_those_blocks_and_no_others(row):
+    rng = np.random.default_rng(row)
+    pools = [rng.integers(0, 256, (3, 7, 2, 16, row), dtype=np.uint8) for _ in range(2)]
+    src, dst = np.array([3, 5], np.int32), np.array([0, 6], np.int32)
+    d = [_dev(p) for p in pools]
+    pkv.copy_blocks(*d, _dev(src), _dev(dst))                               # every layer
+    pkv.copy_blocks(d[0][1], d[1][1], _dev(src[:1]), _dev(dst[:1] + 1))     # one of them
+    for p, got in zip(pools, d):
+        p[:, dst] = p[:, src]
+        p[1, 1] = p[1, 3]
+        assert np.array_equal(got.cpu().numpy(), p)
+    assert pkv.device_error(clear=True) == 0
+
+
 # ----------------------------------------------------------------------------- decode
 CASES = [
     ([38, 101], 16, 12, 2, 1),                        # the tiny batch

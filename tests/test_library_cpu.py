@@ -110,3 +110,34 @@ def test_new_entry_points_reject_bad_arguments_before_any_launch(lib):
                                                 None, 0, None) == pkv.EINVAL
     assert lib.pkv_pool_create(0, 16, 64, None) == pkv.EINVAL
     assert lib.pkv_pool_stats(None, None, None, None, None, None) == pkv.EINVAL
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.float16, 128), (torch.uint8, 128), (torch.uint8, 80)])
+@pytest.mark.parametrize("layers", [1, 3])
+def test_copy_blocks_counts_the_bytes_of_the_pools_it_is_given(monkeypatch, dtype, d, layers):
+    # fp16, E4M3 and 4-bit pools; the library counts rows and layers in fp16 elements
+    class Fake:
+        @staticmethod
+        def pkv_copy_blocks(*args):
+            calls.append(args)
+            return pkv.OK
+
+    class Stream:
+        cuda_stream = 0
+
+    calls = []
+    monkeypatch.setattr(pkv, "load", lambda: Fake)
+    pool = torch.zeros(layers, 6, 2, 16, d, dtype=dtype)
+    ids = torch.zeros(2, dtype=torch.int32)
+    for p in (pool, pool[0]):
+        pkv.copy_blocks(p, p, ids, ids, stream=Stream)
+        _, _, _, _, n, layer, num_layers, nb, hkv, row, bs, _ = calls[-1]
+        assert (n, num_layers, nb, hkv, bs) == (2, layers if p is pool else 1, 6, 2, 16)
+        assert 2 * row == d * pool.element_size()                       # bytes of a row
+        if p is pool:
+            assert 2 * layer == pool[0].numel() * pool.element_size()   # of a layer
+    done = len(calls)
+    for k, v in ((pool, pool[:, :2]), (pool, pool.float()), (pool[..., :d - 1].byte(),) * 2):
+        with pytest.raises(pkv.PkvError):
+            pkv.copy_blocks(k, v, ids, ids, stream=Stream)
+    assert len(calls) == done
