@@ -376,11 +376,14 @@ decode_int4_kernel(const DecodeArgs a, const __half* q_in) {
         uint4 v[4];
         __half2 big = as_half2(0u);
         const int qi = row / a.G;
+        // a query before its sequence's first token sees nothing, whatever it holds: taken as zeros, it
+        // keeps a NaN from its scores, which are all masked
+        const bool sees = row < a.R && slen[sg.b] - a.q_len + qi >= 0;
         const uint4* src = reinterpret_cast<const uint4*>(
             q_in + ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr)
-          v[gr] = row < a.R ? src[4 * gr + t4] : make_uint4(0, 0, 0, 0);
+          v[gr] = sees ? src[4 * gr + t4] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr)
 #pragma unroll

@@ -484,6 +484,31 @@ def test_decode_keeps_a_bad_query_to_its_row(what):
     _same_nan_and_close(out, want, tol)
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("hq,hkv,q_len", [(2, 1, 4), (4, 1, 4), (12, 2, 4), (1, 1, 32)])
+@pytest.mark.parametrize("fused", [False, True])
+def test_a_bad_query_that_sees_no_token_gets_zeros(what, hq, hkv, q_len, fused):
+    # contexts shorter than their drafts: the first queries see nothing and are padding
+    k, v, tables, lens, q = _case([2, 40, 1], 16, hq, hkv, q_len, seed=24)
+    blind = [(b, i) for b in (0, 1, 2) for i in range(q_len) if lens[b] - q_len + i < 0]
+    for b, i in blind:
+        q[b, i] = what
+    if fused:
+        rng = np.random.default_rng(7)
+        kn, vn = (_rows(rng, (3 * q_len, hkv)) for _ in range(2))
+        qd = _dev(q)
+        out = torch.full_like(qd, float("nan"))
+        pkv.paged_attn_decode_append_int4(out, qd, _dev(kn), _dev(vn), _dev(k), _dev(v), _dev(tables),
+                                          _dev(lens), 0.1, pkv.make_workspace(3, q_len, hq, hkv))
+        assert pkv.device_error(clear=True) == 0
+        int4.append(kn, vn, _new_slots(tables, lens, q_len, 16), k, v)
+    else:
+        out = _decode(k, v, tables, lens, q, 0.1)
+    want, tol = int4.attention(q, k, v, tables, lens, 0.1)
+    _close(out, want, tol)
+    assert len(blind) >= 5 and all((out[b, i] == 0).all() for b, i in blind)
+
+
 @pytest.mark.parametrize("q_len,hq,hkv", [(1, 12, 2), (4, 12, 2), (3, 6, 2)])
 @pytest.mark.parametrize("which", ["k", "v"])
 @pytest.mark.parametrize("back", [0, 1, 2])
