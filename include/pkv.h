@@ -369,7 +369,7 @@ int pkv_paged_attn_decode_int4(void* out, const void* q, const void* k_cache,
  * the call which sequences have any. One without (refused by pkv_extend_tables, or idle) would have
  * its last cached rows overwritten, so give it a length of 0 in this call's context_lens: it then
  * gets zeros and nothing of it is written. Or use pkv_kv_append_int4, which skips slots of -1, and
- * pkv_paged_attn_decode_int4. */
+ * pkv_paged_attn_decode_int4. A context length that sets PKV_DEVERR_CONTEXT counts as 0 here. */
 int pkv_paged_attn_decode_append_int4(void* out, const void* q, const void* k_new,
                                       const void* v_new, void* k_cache, void* v_cache,
                                       int num_blocks, const int32_t* block_tables,

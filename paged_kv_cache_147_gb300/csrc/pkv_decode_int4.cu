@@ -322,7 +322,8 @@ decode_int4_kernel(const DecodeArgs a, const __half* q_in) {
     const int lim = a.max_blocks * a.block_size;
     if (ctx < 0 || ctx > lim) {
       atomicOr(a.err, PKV_DEVERR_CONTEXT);
-      ctx = ctx < 0 ? 0 : lim;
+      // no position of such a context is where the caller thinks: a fused call writes nothing of it
+      ctx = APPEND || ctx < 0 ? 0 : lim;
     }
     const int nchunks = (ctx + kChunk - 1) / kChunk;
     longest = max(longest, nchunks);

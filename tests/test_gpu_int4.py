@@ -380,6 +380,43 @@ def test_fused_steps_in_a_row_with_and_without_early_start():
             pkv.set_early_start(before)
 
 
+@pytest.mark.parametrize("width,q_len", [(7, 1), (7, 3), (260, 1), (260, 3)])
+@pytest.mark.parametrize("what", ["block", "last block", "negative", "past the table"])
+def test_fused_append_with_a_bad_block_or_length_writes_nothing_else(width, q_len, what):
+    # the second of four sequences is bad; the others, and every byte that is not theirs, as ever
+    hq, hkv, bs = 8, 2, 16
+    k, v, tables, lens, q = _case([100, 97, 18, 60], bs, hq, hkv, q_len, seed=37, extra=300)
+    rng = np.random.default_rng(6)
+    full = np.full((4, width), -1, np.int32)
+    full[:, :7] = tables[:, :7]
+    spare = np.setdiff1d(np.arange(k.shape[0]), tables)[:width]
+    own = full[1] < 0
+    full[1, own] = spare[:own.sum()]              # a table that is full: every entry could be written
+    kn, vn = (_rows(rng, (4 * q_len, hkv)) for _ in range(2))
+    said, bits = lens.copy(), pkv.DEVERR_CONTEXT
+    if what == "block":
+        full[1, 2], bits = k.shape[0] + 5, pkv.DEVERR_BLOCK_ID
+    elif what == "last block":                    # where new rows would go
+        full[1, (lens[1] - 1) // bs], bits = -7, pkv.DEVERR_BLOCK_ID
+    else:
+        said[1] = -4 if what == "negative" else width * bs + 1
+    kd, vd, qd = _dev(k), _dev(v), _dev(q)
+    out = torch.full_like(qd, float("nan"))
+    pkv.paged_attn_decode_append_int4(out, qd, _dev(kn), _dev(vn), kd, vd, _dev(full), _dev(said),
+                                      0.1, pkv.make_workspace(4, q_len, hq, hkv))
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == bits
+    slots = _new_slots(np.where(full < k.shape[0], full, -1), lens, q_len, bs).reshape(4, q_len)
+    if bits == pkv.DEVERR_CONTEXT:
+        slots[1] = -1
+        assert (out[1] == 0).all()
+    int4.append(kn, vn, slots.reshape(-1), k, v)
+    assert np.array_equal(kd.cpu().numpy(), k) and np.array_equal(vd.cpu().numpy(), v)
+    some = [0, 2, 3]
+    want, tol = int4.attention(q[some], k, v, full[some], lens[some], 0.1)
+    _close(out[some], want, tol)
+
+
 @pytest.mark.parametrize("lens,bs,hq,hkv,q_len", [
     ([1, 18, 33, 0, 250], 16, 9, 1, 1),               # 9 rows
     ([40, 3, 200], 16, 12, 4, 5),                     # 15
