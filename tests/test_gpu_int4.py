@@ -380,6 +380,30 @@ def test_fused_steps_in_a_row_with_and_without_early_start():
             pkv.set_early_start(before)
 
 
+@pytest.mark.parametrize("lens,width,hq,hkv,q_len", [
+    ([33, 1], 300, 3, 3, 2),                          # 12 warps, most of them without a stage
+    ([17, 40, 2], 256, 12, 2, 1),
+    ([33, 47, 96, 9], 257, 8, 4, 4),
+    ([64, 5], 512, 24, 2, 2),                         # 24 rows
+])
+def test_fused_append_of_short_contexts_in_long_tables(lens, width, hq, hkv, q_len):
+    k, v, tables, lens, q = _case(lens, 16, hq, hkv, q_len, seed=width)
+    wide = np.full((len(lens), width), -1, np.int32)
+    wide[:, :tables.shape[1]] = tables
+    rng = np.random.default_rng(98)
+    kn, vn = (_rows(rng, (len(lens) * q_len, hkv)) for _ in range(2))
+    kd, vd, qd = _dev(k), _dev(v), _dev(q)
+    out = torch.full_like(qd, float("nan"))
+    pkv.paged_attn_decode_append_int4(out, qd, _dev(kn), _dev(vn), kd, vd, _dev(wide), _dev(lens),
+                                      0.09, pkv.make_workspace(len(lens), q_len, hq, hkv))
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == 0
+    int4.append(kn, vn, _new_slots(wide, lens, q_len, 16), k, v)
+    assert np.array_equal(kd.cpu().numpy(), k) and np.array_equal(vd.cpu().numpy(), v)
+    want, tol = int4.attention(q, k, v, wide, lens, 0.09)
+    _close(out, want, tol)
+
+
 @pytest.mark.parametrize("width,q_len", [(7, 1), (7, 3), (260, 1), (260, 3)])
 @pytest.mark.parametrize("what", ["block", "last block", "negative", "past the table"])
 def test_fused_append_with_a_bad_block_or_length_writes_nothing_else(width, q_len, what):
