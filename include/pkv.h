@@ -353,8 +353,8 @@ int pkv_widen_blocks_int4(const void* k_cache, const void* v_cache, const int32_
 /* pkv_paged_attn_decode over a 4-bit cache. Keys and values are s * code + z as they are, not
  * rounded to fp16: the codes' products are summed in fp32 and scaled then (keys), or taken with the
  * scaled softmax weights in two fp16 parts (values). The weights themselves are fp16, as there.
- * (num_q_heads / num_kv_heads) * q_len <= 32, as there; other arguments, workspace and errors as
- * there too. */
+ * (num_q_heads / num_kv_heads) * q_len <= 32, as there, and num_kv_heads <= 2^20; other arguments,
+ * workspace and errors as there too. */
 int pkv_paged_attn_decode_int4(void* out, const void* q, const void* k_cache,
                                const void* v_cache, int num_blocks, const int32_t* block_tables,
                                int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,

@@ -856,7 +856,8 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
                        float scale, void* workspace, size_t workspace_bytes, bool append,
                        pkv_stream_t stream) {
   if (num_seqs < 0 || q_len < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || head_dim != kD ||
-      !valid_block_size(block_size) || num_blocks < 0 || max_blocks < 0)
+      !valid_block_size(block_size) || num_blocks < 0 || max_blocks < 0 ||
+      Hkv > (1 << 20))   // a stage's place is packed as head << 8 | row
     return PKV_EINVAL;
   const int G = Hq / Hkv;
   if (static_cast<int64_t>(G) * q_len > 32) return PKV_EINVAL;

@@ -141,6 +141,14 @@ def test_decode_refuses_bad_arguments(lib):
                None) == pkv.EINVAL
 
 
+def test_decode_refuses_more_heads_than_it_can_count(lib):
+    # a call within every other limit: one block, one sequence
+    for hkv in ((1 << 20) + 1, 1 << 23, 1 << 26):
+        for fn, new in ((lib.pkv_paged_attn_decode_int4, ()), (lib.pkv_paged_attn_decode_append_int4, (P, P))):
+            assert fn(P, P, *new, P, P, 1, P, 1, P, 1, 1, hkv, hkv, 128, 16, 0.1, P, 1 << 40,
+                      None) == pkv.EINVAL
+
+
 def test_norm_rope_refuses_bad_arguments(lib):
     def norm(qo=P, ko=P, q=P, k=P, qs=1536, ks=256, eps=1e-6, n=16, T=3, hq=12, hkv=2, d=128, pos=P):
         return lib.pkv_qk_norm_rope(qo, ko, q, k, qs, ks, P, P, eps, pos, P, n, T, hq, hkv, d, None)
