@@ -99,6 +99,17 @@ struct Args {
   }
 };
 
+// The library is called without Python's lock: a launch waits where the GPU's queue is full, and
+// other threads go on meanwhile.
+template <class F>
+int unlocked(F&& call) {
+  struct Lock {
+    PyThreadState* const state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return call();
+}
+
 // Outputs of a call with the stream argument i, allocated on the stream that it runs on: memory freed
 // on another one may still be in use there.
 struct Outputs {
@@ -133,8 +144,11 @@ PyObject* kv_append_int4(Args& A) {   // k, v, slots, k_cache, v_cache, stream
   if (kc.size(3) != kRow || !same(vc, kc) || !shaped(k, {n, hkv, 128}) || !same(v, k) ||
       !fits(nb) || !fits(hkv) || !fits(bs) || !fits(n))
     return fail(A.fn, PKV_EINVAL);
-  const int st = lib.kv_append_int4(ptr(k), ptr(v), ptr<int64_t>(slots), n, ptr(kc), ptr(vc), nb,
-                                    hkv, 128, bs, A.stream(5));
+  const pkv_stream_t s = A.stream(5);
+  const int st = unlocked([&] {
+    return lib.kv_append_int4(ptr(k), ptr(v), ptr<int64_t>(slots), n, ptr(kc), ptr(vc), nb, hkv, 128,
+                              bs, s);
+  });
   return st ? fail(A.fn, st) : none();
 }
 
@@ -147,9 +161,11 @@ PyObject* widen_blocks_int4(Args& A) {   // k_cache, v_cache, src, dst, k_out, v
   if (kc.size(3) != kRow || !same(vc, kc) || dst.numel() != n || !shaped(ko, {nbo, hkv, bs, 128}) ||
       !same(vo, ko) || !fits(nb) || !fits(nbo) || !fits(hkv) || !fits(bs) || !fits(n))
     return fail(A.fn, PKV_EINVAL);
-  const int st =
-      lib.widen_blocks_int4(ptr(kc), ptr(vc), ptr<int32_t>(src), ptr<int32_t>(dst), n, nb, ptr(ko),
-                            ptr(vo), nbo, hkv, 128, bs, A.stream(6));
+  const pkv_stream_t s = A.stream(6);
+  const int st = unlocked([&] {
+    return lib.widen_blocks_int4(ptr(kc), ptr(vc), ptr<int32_t>(src), ptr<int32_t>(dst), n, nb,
+                                 ptr(ko), ptr(vo), nbo, hkv, 128, bs, s);
+  });
   return st ? fail(A.fn, st) : none();
 }
 
@@ -175,12 +191,13 @@ PyObject* decode(Args& A) {
   const float scale = A.number(at0 + 4);
   const pkv_stream_t s = A.stream(at0 + 6);
   const int32_t *btp = ptr<int32_t>(bt), *clp = ptr<int32_t>(cl);
-  const int st =
-      APPEND ? lib.decode_append_int4(ptr(out), ptr(q), ptr(kn), ptr(vn), ptr(kc), ptr(vc), nb, btp,
-                                      width, clp, B, q_len, hq, hkv, d, bs, scale, ptr(ws),
-                                      ws.nbytes(), s)
-             : lib.decode_int4(ptr(out), ptr(q), ptr(kc), ptr(vc), nb, btp, width, clp, B, q_len,
-                               hq, hkv, d, bs, scale, ptr(ws), ws.nbytes(), s);
+  const int st = unlocked([&] {
+    return APPEND ? lib.decode_append_int4(ptr(out), ptr(q), ptr(kn), ptr(vn), ptr(kc), ptr(vc), nb,
+                                           btp, width, clp, B, q_len, hq, hkv, d, bs, scale,
+                                           ptr(ws), ws.nbytes(), s)
+                  : lib.decode_int4(ptr(out), ptr(q), ptr(kc), ptr(vc), nb, btp, width, clp, B,
+                                    q_len, hq, hkv, d, bs, scale, ptr(ws), ws.nbytes(), s);
+  });
   if (st) return fail(A.fn, st);
   Py_INCREF(A.a[0]);
   return A.a[0];
@@ -210,11 +227,13 @@ PyObject* qk_norm_rope(Args& A) {
   }
   const float eps = A.number(4);
   const pkv_stream_t s = A.stream(9);
-  const Outputs on(A, 9, s);
-  if (!qo.defined()) qo = at::empty({T, hq, 128}, q.options());
-  if (!ko.defined()) ko = at::empty({T, hkv, 128}, q.options());
-  const int st = lib.qk_norm_rope(ptr(qo), ptr(ko), ptr(q), ptr(k), qs, ks, ptr(qw), ptr(kw), eps,
-                                  ptr<int64_t>(pos), ptr<float>(cs), n_index, T, hq, hkv, 128, s);
+  const int st = unlocked([&] {
+    const Outputs on(A, 9, s);
+    if (!qo.defined()) qo = at::empty({T, hq, 128}, q.options());
+    if (!ko.defined()) ko = at::empty({T, hkv, 128}, q.options());
+    return lib.qk_norm_rope(ptr(qo), ptr(ko), ptr(q), ptr(k), qs, ks, ptr(qw), ptr(kw), eps,
+                            ptr<int64_t>(pos), ptr<float>(cs), n_index, T, hq, hkv, 128, s);
+  });
   if (st) return fail(A.fn, st);
   PyObject* r = PyTuple_New(2);
   if (!r) return nullptr;
@@ -235,21 +254,8 @@ PyObject* extend_tables(Args& A) {
     return fail(A.fn, PKV_EINVAL);
   const pkv_stream_t s = A.stream(8);
   at::Tensor slots, seqs, pos, cu;
-  PyObject* r;
-  if (A.a[7] == Py_None) {
-    const Outputs on(A, 8, s);
-    const auto wide = bt.options().dtype(kI64), narrow = bt.options();
-    slots = at::empty({n}, wide);
-    seqs = at::empty({n}, narrow);
-    pos = at::empty({n}, wide);
-    cu = at::empty({B + 1}, narrow);
-    r = PyTuple_New(4);
-    if (!r) return nullptr;
-    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(slots));
-    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(seqs));
-    PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(pos));
-    PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(cu));
-  } else {
+  const bool given = A.a[7] != Py_None;
+  if (given) {
     if (!PyTuple_Check(A.a[7]) || PyTuple_GET_SIZE(A.a[7]) != 4) return fail(A.fn, PKV_EINVAL);
     Args O{A.fn, &PyTuple_GET_ITEM(A.a[7], 0), A.dev};
     slots = O.tensor(0, kI64);
@@ -259,16 +265,31 @@ PyObject* extend_tables(Args& A) {
     if (!O.ok || slots.numel() != n || seqs.numel() != n || pos.numel() != n ||
         cu.numel() != B + 1)
       return fail(A.fn, PKV_EINVAL);
-    r = A.a[7];
-    Py_INCREF(r);
   }
-  const int st = lib.extend_tables(ptr<int32_t>(bt), ptr<int32_t>(cl), ptr<int32_t>(nl), B, width,
-                                   bs, ptr<int32_t>(fb), ptr<int32_t>(fc), nb, ptr<int64_t>(slots),
-                                   ptr<int32_t>(seqs), ptr<int64_t>(pos), ptr<int32_t>(cu), n, s);
-  if (st) {
-    Py_DECREF(r);
-    return fail(A.fn, st);
+  const int st = unlocked([&] {
+    if (!given) {
+      const Outputs on(A, 8, s);
+      const auto wide = bt.options().dtype(kI64), narrow = bt.options();
+      slots = at::empty({n}, wide);
+      seqs = at::empty({n}, narrow);
+      pos = at::empty({n}, wide);
+      cu = at::empty({B + 1}, narrow);
+    }
+    return lib.extend_tables(ptr<int32_t>(bt), ptr<int32_t>(cl), ptr<int32_t>(nl), B, width, bs,
+                             ptr<int32_t>(fb), ptr<int32_t>(fc), nb, ptr<int64_t>(slots),
+                             ptr<int32_t>(seqs), ptr<int64_t>(pos), ptr<int32_t>(cu), n, s);
+  });
+  if (st) return fail(A.fn, st);
+  if (given) {
+    Py_INCREF(A.a[7]);
+    return A.a[7];
   }
+  PyObject* r = PyTuple_New(4);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(slots)));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(seqs)));
+  PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(pos)));
+  PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(std::move(cu)));
   return r;
 }
 
@@ -282,8 +303,11 @@ PyObject* truncate_tables(Args& A) {
   if (cl.numel() != B || kl.numel() != B || fc.numel() != 1 || !fits(B) || !fits(width) ||
       !fits(nb))
     return fail(A.fn, PKV_EINVAL);
-  const int st = lib.truncate_tables(ptr<int32_t>(bt), ptr<int32_t>(cl), ptr<int32_t>(kl), B, width,
-                                     bs, ptr<int32_t>(fb), ptr<int32_t>(fc), nb, A.stream(6));
+  const pkv_stream_t s = A.stream(6);
+  const int st = unlocked([&] {
+    return lib.truncate_tables(ptr<int32_t>(bt), ptr<int32_t>(cl), ptr<int32_t>(kl), B, width, bs,
+                               ptr<int32_t>(fb), ptr<int32_t>(fc), nb, s);
+  });
   return st ? fail(A.fn, st) : none();
 }
 

@@ -1,5 +1,8 @@
 """Calls on a given stream: what they allocate belongs to that stream, so that it never lies on memory
-that kernels of the current stream still use."""
+that kernels of the current stream still use. Calls that wait for the GPU's queue: other threads run."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -58,3 +61,34 @@ def test_a_call_inside_a_stream_context_gives_outputs_of_that_stream():
         for what, outs in _calls(None):
             assert [_pool_stream(t) for t in outs] == [side.cuda_stream] * len(outs), what
     assert pkv.device_error(clear=True) == 0
+
+
+def test_a_call_that_waits_for_the_queue_lets_other_threads_run():
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table, lens, keep = torch.full((2, 4), -1, **i32), torch.zeros(2, **i32), torch.zeros(2, **i32)
+    free, count = torch.arange(8, **i32), torch.full((1,), 8, **i32)
+    gaps, done = [0.0], threading.Event()
+
+    def watch():
+        last = time.monotonic()
+        while not done.is_set():
+            time.sleep(0.002)
+            now = time.monotonic()
+            gaps.append(now - last)
+            last = now
+
+    pkv.truncate_tables(table, lens, keep, 16, free, count)
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=watch)
+    thread.start()
+    waited = 0.0
+    torch.cuda._sleep(2_000_000_000)      # about a second: the calls behind it fill the queue
+    for _ in range(4000):
+        before = time.monotonic()
+        pkv.truncate_tables(table, lens, keep, 16, free, count)
+        waited = max(waited, time.monotonic() - before)
+    done.set()
+    thread.join()
+    torch.cuda.synchronize()
+    assert waited > 0.3, "no call had to wait"
+    assert max(gaps) < waited / 2, (max(gaps), waited)
