@@ -115,9 +115,11 @@ int unlocked(F&& call) {
 struct Outputs {
   c10::cuda::OptionalCUDAStreamGuard guard;
   Outputs(const Args& A, int i, pkv_stream_t s) {
-    if (A.a[i] != Py_None)
-      guard.reset_stream(
-          c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), A.dev));
+    if (A.a[i] == Py_None) return;
+    // (the legacy default stream has two handles)
+    const auto handle = static_cast<cudaStream_t>(s);
+    guard.reset_stream(handle == cudaStreamLegacy ? c10::cuda::getDefaultCUDAStream(A.dev)
+                                                  : c10::cuda::getStreamFromExternal(handle, A.dev));
   }
 };
 

@@ -152,6 +152,10 @@ def _empty(n: int, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
     may still be in use there."""
     if stream is None:
         return torch.empty(n, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # another library's, or a bare handle's holder
+        handle = stream.cuda_stream
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle > 1 else
+                  torch.cuda.default_stream(device))
     with torch.cuda.stream(stream):
         return torch.empty(n, dtype=dtype, device=device)
 

@@ -55,6 +55,19 @@ def test_outputs_of_a_call_on_a_given_stream_belong_to_it():
     assert pkv.device_error(clear=True) == 0
 
 
+def test_a_stream_may_be_any_object_with_a_handle():
+    class Handle:
+        def __init__(self, value):
+            self.cuda_stream = value
+
+    side = torch.cuda.Stream()
+    # a stream of another library's making; the default stream by both of its handles
+    for handle, want in ((side.cuda_stream, side.cuda_stream), (0, 0), (1, 0)):
+        for what, outs in _calls(Handle(handle)):
+            assert [_pool_stream(t) for t in outs] == [want] * len(outs), (what, handle)
+    assert pkv.device_error(clear=True) == 0
+
+
 def test_a_call_inside_a_stream_context_gives_outputs_of_that_stream():
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
