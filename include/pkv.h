@@ -134,11 +134,11 @@ size_t pkv_decode_workspace_bytes(int num_seqs, int q_len, int num_q_heads, int 
                                   int head_dim);
 
 /* Turns the launch overlap of the fused-append calls (pkv_paged_attn_decode_append, its FP8 and
- * 4-bit forms and pkv_ring_attn_decode_append) on (enable != 0, the default) or off, for every call made afterwards in this process,
- * including calls captured into a CUDA graph afterwards. With it off a fused call starts only
- * after the kernel before it has completed, so it may follow a kernel that writes its pools,
- * block tables or context lengths. Returns the previous setting (0 or 1). Not part of the
- * pages' design: a scheduling control of this implementation. */
+ * 4-bit forms and pkv_ring_attn_decode_append) on (enable != 0, the default) or off, for every
+ * call made afterwards in this process, including calls captured into a CUDA graph afterwards.
+ * With it off a fused call starts only after the kernel before it has completed, so it may follow
+ * a kernel that writes its pools, block tables or context lengths. Returns the previous setting (0
+ * or 1). Not part of the pages' design: a scheduling control of this implementation. */
 int pkv_set_early_start(int enable);
 int pkv_workspace_init(void* workspace, size_t workspace_bytes, pkv_stream_t stream);
 
@@ -331,10 +331,10 @@ int pkv_paged_attn_decode_append_fp8(void* out, const void* q, const void* k_new
  * when it is called with head_dim 40 (a row of 80 bytes is 40 fp16 elements).
  *
  * pkv_kv_append_int4: pkv_kv_append's scatter, each row quantised: z = the group's minimum, s =
- * (max - min) / 15 in binary32, rounded up to fp16 (down where 15 s + z would pass the largest fp16), code =
- * (x - z) / s rounded to nearest, ties to even, in 0 .. 15 (0 where s is 0). A group with a NaN or
- * an infinity gets s = z = NaN. Same slot rules and errors as pkv_kv_append, and no slot twice; k,
- * v fp16 [num_tokens][num_kv_heads][head_dim]; all four 16-byte aligned. */
+ * (max - min) / 15 in binary32, rounded up to fp16 (down where 15 s + z would pass the largest
+ * fp16), code = (x - z) / s rounded to nearest, ties to even, in 0 .. 15 (0 where s is 0). A group
+ * with a NaN or an infinity gets s = z = NaN. Same slot rules and errors as pkv_kv_append, and no
+ * slot twice; k, v fp16 [num_tokens][num_kv_heads][head_dim]; all four 16-byte aligned. */
 int pkv_kv_append_int4(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
                        void* k_cache, void* v_cache, int num_blocks, int num_kv_heads,
                        int head_dim, int block_size, pkv_stream_t stream);

@@ -3,8 +3,8 @@
 //
 // Both move bytes: the append reads 256 and writes 80 per row, the widening the other way round.
 // 16 lanes take a row, 8 elements (16 fp16 bytes, 4 bytes of codes) each, or, in large appends, 4
-// lanes a group of 32 each. 8192 tokens of 8 heads (44 MB each way): append 10.6 us, widening 7.5
-// (4.2 and 5.9 TB/s).
+// lanes a group of 32 each. 8192 tokens of 8 heads (44 MB each way): append 10.1 us, widening 6.9
+// (4.4 and 6.4 TB/s).
 #include <algorithm>
 
 #include "pkv_int4.cuh"
@@ -53,9 +53,10 @@ kv_append_int4_kernel(const uint4* k, const uint4* v, const int64_t* slots, int 
 
 // Many rows: a thread takes a whole group (64 bytes in, 16 + 4 out), a warp the K or the V rows of
 // eight neighbouring tokens of one head. The group's minimum, maximum and scale are then computed
-// once instead of in four lanes, which is what a full GPU spends its time on otherwise: 65536 tokens of 8 heads 91 us against 66, 8192 tokens 14.2 against 10.6 (2048 tokens 4.8
-// against 4.2); below kGroupRows the longer chain per thread shows (512 tokens 2.75 against 3.0,
-// 64 tokens of 2 heads 2.1 against 2.3).
+// once instead of in four lanes, which is what a full GPU spends its time on otherwise: 65536 tokens
+// of 8 heads 91 us against 66, 8192 tokens 14.2 against 10.6 (2048 tokens 4.8 against 4.2); below
+// kGroupRows the longer chain per thread shows (512 tokens 2.75 against 3.0, 64 tokens of 2 heads
+// 2.1 against 2.3).
 constexpr int kGroupRows = 16384;
 __global__ void __launch_bounds__(kThreads)
 kv_append_int4_groups_kernel(const uint4* k, const uint4* v, const int64_t* slots, int num_tokens,
@@ -194,7 +195,8 @@ int pkv_widen_blocks_int4(const void* k_cache, const void* v_cache, const int32_
   if (!err) return launch_status();
   // Shared memory that it does not use keeps a small grid at four CTAs an SM: behind a fused decode,
   // which lets its successor in early, the first SMs to finish would take all of it (a fused step
-  // of 64 ragged sequences and the widening 18.6 us -> 17.0, of 32 of 50 to 8000 tokens 51.3 -> 49.9).
+  // of 64 ragged sequences and the widening 18.4 us -> 16.7, of 32 of 50 to 8000 tokens 51.2 -> 49.6;
+  // on its own or behind an append a widening takes as long either way).
   const int64_t grid = 2LL * n * parts;
   const size_t smem = grid <= 4LL * sm_count() ? 46 * 1024 : 0;
   return launch_waiting(&widen_blocks_int4_kernel, static_cast<unsigned>(grid), kThreads, smem,

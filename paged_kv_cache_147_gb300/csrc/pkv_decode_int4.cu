@@ -40,7 +40,10 @@
 //    maximum lazily). p and p s are fp16: the reference stays kShift = 11 powers of two below
 //    the maximum while every scale is below 2 (p < 2^13, p s < 2^14, and values of 1e-6 still
 //    count); the first scale of 2 or more (values over a range of 30) moves it up to the maximum
-//    (p <= 4, p s <= 4 x 8736) for the rest of the segment.
+//    (p <= 4, p s <= 4 x 8736) for the rest of the segment. That one rounding of a weight (2^-11 of
+//    it at most on the way to a matrix operand; the sum of the weights takes them unrounded) is
+//    what the output's error is above the plain form's, which keeps them in fp32: 2.4e-4 to 3.0e-4
+//    of the output's norm against 2.1e-4, of which the fp16 output itself is nearly all.
 //  * Tokens past the context hold anything: their scores are masked and their (s, z) of V set
 //    to zero.
 //  * More than 8 rows: two to four warps take a stage, 8 rows each (and a copy of their own; all
@@ -381,7 +384,8 @@ decode_int4_kernel(const DecodeArgs a, const __half* q_in) {
         // keeps a NaN from its scores, which are all masked
         const bool sees = row < a.R && slen[sg.b] - a.q_len + qi >= 0;
         const uint4* src = reinterpret_cast<const uint4*>(
-            q_in + ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
+            q_in +
+            ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr)
           v[gr] = sees ? src[4 * gr + t4] : make_uint4(0, 0, 0, 0);
@@ -837,10 +841,11 @@ Variant variant4() {
 //   32 rows   <3, 4, 2, 1> 29.6 / 73.7, <2, 4, 3, 1> 30.8 / 78.6
 // Up to 8 rows, 12 warps in one CTA keep more in flight than two CTAs of 4, but hand a segment over
 // only once per SM and merge 12 states for it. That pays where a CTA has a segment or two, of many
-// stages: no more units than SMs, tables for 4096 tokens or more. <12, 1, 2, 1> against <4, 1, 3, 2>:
-// 16 sequences of 4096 tokens with 8 kv heads 25.7 against 27.0, one of 65536 30.8 against 35.8,
-// two of 131072 with one kv head 34.1 against 41.1; but two of about 70 tokens 7.3 against 6.5, and
-// 512 units of mixed lengths 65 against 51.
+// stages: no more units than SMs, tables for 4096 tokens or more (the lengths are on the GPU; a few
+// short contexts in tables as wide as a server's capacity pay for that). <12, 1, 2, 1> against
+// <4, 1, 3, 2>: 16 sequences of 4096 tokens with 8 kv heads 25.7 against 27.0, one of 65536 30.8
+// against 35.8, two of 131072 with one kv head 34.1 against 41.1; but two of about 70 tokens 7.3
+// against 6.5, and 512 units of mixed lengths 65 against 51.
 template <bool APPEND>
 Variant choose4(int R, bool few_long) {
   return R <= 8    ? (few_long ? variant4<12, 1, 2, 1, APPEND>() : variant4<4, 1, 3, 2, APPEND>())
@@ -935,7 +940,7 @@ int launch_decode_int4(void* out, const void* q, const void* k_new, const void* 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   // The plain form waits for the kernel before it as its first step: its CTAs only take their places
-  // early (one sequence of 101 tokens 6.5 -> 5.8 us in a row, 16 of 4096 25.5 -> 25.0).
+  // early (one sequence of 101 tokens 6.5 -> 5.8 us in a row, 16 of 4096 25.4 -> 24.9).
   cfg.numAttrs = (!append || early_start_enabled()) ? 1 : 0;
   return cuda_status(cudaLaunchKernelExC(&cfg, v.fn, params));
 }

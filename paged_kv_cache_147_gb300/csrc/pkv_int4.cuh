@@ -29,8 +29,10 @@ constexpr int kInt4Params = 64;     // offset of the (s, z) pairs
 // correctly rounded quotient (Markstein's theorem on division by a correctly rounded
 // reciprocal). The codes come from a product with an approximate 1 / s, rounded to an integer by
 // adding 1.5 2^23 in the same operation (conversions run at a sixteenth of its rate and made the
-// append compute-bound); products nearer than 1e-5 to a border between two codes, 20 times what
-// they can be off, send the lane through int4_exact_code.
+// append compute-bound); products nearer than 1e-5 to a border between two codes send the lane
+// through int4_exact_code. That is twice what they can be off: the reciprocal by 2 units in the last
+// place (2^-22 of it), x - z by half of one, so a quotient at the last border, 14.5, by
+// 14.5 (2^-22 + 2^-24) + 2^-25 = 4.4e-6.
 constexpr float kInt4Magic = 12582912.f;   // 1.5 * 2^23, bits 0x4b400000
 
 // The code of x in a group with minimum lo and scale s > 0, q its approximate (x - lo) / s: the

@@ -1,9 +1,9 @@
 // pkv_torch.cpp -- the Python side of the 4-bit, norm and table calls: checks of the tensors'
 // types, devices and shapes, outputs allocated by torch, the current stream, one C call. A decode
 // step makes several of these calls of a few microseconds each, and the same written with ctypes
-// and Tensor attributes took longer than the kernels: norm of 64 tokens 15.8 us a call (2.3 of
-// them on the GPU), now 5.9; two table calls with four outputs 26.4 (8.8), now 11.6; append and
-// widening of 64 tokens 14.3 (4.7), now 8.2.
+// and Tensor attributes took longer than the kernels: norm of 64 tokens 15.8 us a call (2.0 of
+// them on the GPU), now 5.7; two table calls with four outputs 26.4 (8.8), now 11.3; append and
+// widening of 64 tokens 14.3 (3.4), now 4.9.
 //
 // The library itself is reached through the addresses of its entry points, handed over by bind(),
 // so that this file needs no second copy of it and a variant can be bound instead.
