@@ -422,10 +422,11 @@ int pkv_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k, int
  * the table as it is, its tokens get slot -1, and PKV_DEVERR_BLOCK_ID is set. A *free_count outside
  * [0, num_blocks] sets PKV_DEVERR_SPACE and stays as it is; the stack counts as empty.
  *
- * A fused append + decode (any cache type) behind it: the call reads tables and lengths early, so
- * it needs a launch in between (pkv_qk_norm_rope, a copy) or pkv_set_early_start(0); and it takes
- * q_len new rows of every sequence, so new_lens[b] has to be q_len for all, and where one can be
- * refused (seq_out[cu_new_lens[b]] is -1 then) or is idle, its length in that call has to be 0.
+ * A fused append + decode (any cache type) behind either call reads tables and lengths early, so it
+ * needs a launch in between (pkv_qk_norm_rope, a copy) or pkv_set_early_start(0). And it takes q_len
+ * new rows of every sequence: the length of one that was refused, or that has fewer (an idle one),
+ * has to be 0 in its context_lens. One with new tokens was served if cu_new_lens[b] < max_tokens
+ * and seq_out[cu_new_lens[b]] is b.
  *
  * pkv_truncate_tables: cuts every sequence with 0 <= keep_lens[b] < context_lens[b] back to
  * keep_lens[b] tokens (rejected drafts; 0 to give a sequence up); a negative or larger value

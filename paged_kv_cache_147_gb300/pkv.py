@@ -438,8 +438,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps, positions, cos_sin, q_out=None, 
                  stream=None):
     """Per-head RMS norm and rotation: q fp16 [T, Hq, 128], k fp16 [T, Hkv, 128] (each token's
     heads contiguous, tokens a stride of at least that apart, a multiple of 4: slices of a packed
-    projection do), weights fp16 [128], positions int64 [T] (negative: padding, left as it is), cos_sin a rope_table on the
-    device -> (q_out, k_out), contiguous."""
+    projection do), weights fp16 [128], positions int64 [T] (negative: padding, left as it is),
+    cos_sin a rope_table on the device -> (q_out, k_out), contiguous."""
     return (_ops or _torch_ops()).qk_norm_rope(
         q, k, q_weight, k_weight, eps, positions, cos_sin, q_out, k_out, stream)
 

@@ -206,7 +206,7 @@ def test_refused_and_idle_sequences_keep_their_cached_rows(fused):
     out = torch.full_like(qb, float("nan"))
     space = pkv.make_workspace(B, q_len, hq, hkv)
     if fused:
-        served = (seqs[rows[:, 0]] >= 0) & (news == q_len)
+        served = (seqs[rows[:, 0]] == torch.arange(B, device=DEV)) & (news == q_len)
         step_lens = torch.where(served, ld, 0)
         kb, vb = (t[rows].view(T, hkv, 128) for t in (k, x[2]))
         pkv.paged_attn_decode_append_int4(out, qb, kb, vb, kd, vd, td, step_lens, scale, space)
