@@ -41,9 +41,8 @@
 //    the maximum while every scale is below 2 (p < 2^13, p s < 2^14, and values of 1e-6 still
 //    count); the first scale of 2 or more (values over a range of 30) moves it up to the maximum
 //    (p <= 4, p s <= 4 x 8736) for the rest of the segment. That one rounding of a weight (2^-11 of
-//    it at most on the way to a matrix operand; the sum of the weights takes them unrounded) is
-//    what the output's error is above the plain form's, which keeps them in fp32: 2.4e-4 to 3.0e-4
-//    of the output's norm against 2.1e-4, of which the fp16 output itself is nearly all.
+//    it at most; the weights' sum takes them unrounded) is what the error has over attention in
+//    fp32 with the same fp16 output: 2.4e-4 to 3.0e-4 of the output's norm against 2.1e-4.
 //  * Tokens past the context hold anything: their scores are masked and their (s, z) of V set
 //    to zero.
 //  * More than 8 rows: two to four warps take a stage, 8 rows each (and a copy of their own; all
