@@ -9,8 +9,8 @@
  *   - paged decode attention: each sequence's few newest query tokens attend over all of its
  *     cached K/V, read indirectly through its block table, with GQA head groups;
  *   - sink + ring decode attention with RoPE applied at read time;
- * and around it: an FP8 (E4M3) and a 4-bit form of the cache with their appends and decodes, the
- * per-head norm and rotation of queries and keys before them, verification of speculative drafts
+ * and around it: an FP8 (E4M3), a 4-bit and an 8-bit block-scaled form of the cache with their
+ * appends and decodes, attention over the blocks of a long context that a score selects, the per-head norm and rotation of queries and keys before them, verification of speculative drafts
  * (accept/reject, next token), block tables and slot maps kept on the device, and a host block
  * pool that hands out the block tables (prefix sharing, reference counts, copy-on-write pairs).
  *
@@ -377,6 +377,103 @@ int pkv_paged_attn_decode_append_int4(void* out, const void* q, const void* k_ne
                                       int num_seqs, int q_len, int num_q_heads, int num_kv_heads,
                                       int head_dim, int block_size, float scale, void* workspace,
                                       size_t workspace_bytes, pkv_stream_t stream);
+
+/* ---- 8-bit cache with a scale per block and head ----------------------------------------------
+ * [VLLM] §工程权衡 (量化与 KV Cache 精度的权衡): FP8's half of the memory, with scales that come from the
+ * data instead of a calibration, and a finer step (1/127 to 1/64 of a block's largest element against
+ * E4M3's 1/16 of each). The page fixes no layout; here, per layer,
+ *   k_cache, v_cache  uint8 [num_blocks][num_kv_heads][block_size][128], codes,
+ *   kv_scales         float [num_blocks][num_kv_heads][2], the scale of the block's K and of its V,
+ *                     powers of two from 2^-30 to 2^9,
+ *   k_bounds          uint8 [num_blocks][num_kv_heads][2][128], the least and the greatest K code of
+ *                     each channel among the rows written into the block (only for
+ *                     pkv_select_blocks: NULL where it is not used),
+ * and element value = scale * (code - 128). Start with zeroed scales. Codes 16-byte, bounds 16-byte,
+ * scales 8-byte aligned, here and below.
+ *
+ * pkv_kv_append_int8: pkv_kv_append's scatter, quantised. For each block that rows of the call go
+ * to and each kv head, and for K and V apart: the scale becomes the least one s with |x| <= 127 s for
+ * all new rows, or the one the block has if that is larger; a new row's codes are x / s rounded to
+ * nearest, ties to even (+-127 at most: only past 65024), plus 128. What the block held moves to the
+ * new scale, its codes (without the offset) rounded in the same way. But a call that writes a block's
+ * first row (slot % block_size == 0) starts the block afresh: scale and bounds are those of the call's
+ * rows, and every row that the call does not write becomes zero (code 128). So append tokens in
+ * order, and the scales follow; rows cut off behind a context stay in the scale and the bounds
+ * until their block is started again. A NaN or an infinity makes the scale NaN, and with it all of
+ * the block (codes 128), until it is started again.
+ * Same slot rules and errors as pkv_kv_append, no slot twice, and the tokens of one block have to lie
+ * within block_size consecutive tokens of the call, in any order (a sequence's new tokens next to each
+ * other do); other orders race on the block's scale. k, v fp16 [num_tokens][num_kv_heads][head_dim],
+ * 16-byte aligned. */
+int pkv_kv_append_int8(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
+                       void* k_cache, void* v_cache, float* kv_scales, void* k_bounds,
+                       int num_blocks, int num_kv_heads, int head_dim, int block_size,
+                       pkv_stream_t stream);
+
+/* Widens blocks: pkv_widen_blocks_int4's operation, every element fp16(scale * (code - 128)). */
+int pkv_widen_blocks_int8(const void* k_cache, const void* v_cache, const float* kv_scales,
+                          const int32_t* src, const int32_t* dst, int n, int num_blocks,
+                          void* k_out, void* v_out, int num_blocks_out, int num_kv_heads,
+                          int head_dim, int block_size, pkv_stream_t stream);
+
+/* pkv_copy_blocks for this cache: codes, scales and (unless NULL) bounds of blocks src[i] -> dst[i],
+ * in each of num_layers layers that lie one behind the other in all four arrays. */
+int pkv_copy_blocks_int8(void* k_cache, void* v_cache, float* kv_scales, void* k_bounds,
+                         const int32_t* src, const int32_t* dst, int n, int num_layers,
+                         int num_blocks, int num_kv_heads, int head_dim, int block_size,
+                         pkv_stream_t stream);
+
+/* pkv_paged_attn_decode over this cache: keys and values scale * (code - 128) as they are, not
+ * rounded to fp16; the softmax weights are fp16, as there. Scales are powers of two (or 0, or NaN,
+ * which reaches the queries that see a row of the block). (num_q_heads / num_kv_heads) * q_len <= 32
+ * and num_kv_heads <= 2^20; other arguments, workspace and errors as there too. */
+int pkv_paged_attn_decode_int8(void* out, const void* q, const void* k_cache,
+                               const void* v_cache, const float* kv_scales, int num_blocks,
+                               const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* context_lens, int num_seqs, int q_len,
+                               int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                               float scale, void* workspace, size_t workspace_bytes,
+                               pkv_stream_t stream);
+
+/* The same with a block table for each kv head: head_tables (device) int32 [num_seqs][num_kv_heads]
+ * [max_blocks_per_head]. Attention runs over the listed blocks as if they were the whole context, of
+ * context_lens[b] tokens; pkv_select_blocks writes both. */
+int pkv_selected_attn_decode_int8(void* out, const void* q, const void* k_cache,
+                                  const void* v_cache, const float* kv_scales, int num_blocks,
+                                  const int32_t* head_tables, int max_blocks_per_head,
+                                  const int32_t* context_lens, int num_seqs, int q_len,
+                                  int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  float scale, void* workspace, size_t workspace_bytes,
+                                  pkv_stream_t stream);
+
+/* Chooses up to `budget` blocks of every sequence for each kv head, for a decode over a long context
+ * that reads only those. For sequence b with N = ceil(context_lens[b] / block_size) blocks:
+ *   - N <= budget: all of them;
+ *   - else the first keep_first, the last keep_last (at least those that hold the last q_len tokens,
+ *     the queries' own), and of the others those with the greatest scores, the lower block first
+ *     among equal ones, `budget` blocks in all.
+ * A block's score is the greatest, over the rows of q (new tokens and heads of the kv head's group),
+ * of  2^e s_K sum_d max(p_d lo_d, p_d hi_d):  p = q / 2^e rounded to nearest, ties to even, with 2^e
+ * what the append would take for the row as a scale, (lo, hi) the block's bounds without the offset and
+ * s_K its K scale. That is an upper bound of the rounded row's products with the block's keys (for a
+ * positive score scale), exact in fp32. A row before its sequence's first token, or with a NaN or an
+ * infinity, does not count; a block with a NaN scale comes before all others; one with an id outside
+ * [0, num_blocks) comes last and sets PKV_DEVERR_BLOCK_ID (contexts within the budget are not scored,
+ * and their ids not looked at).
+ *   tables_out [num_seqs][num_kv_heads][budget]: the chosen blocks' ids in the order of the context,
+ *     entries behind them -1;
+ *   lens_out [num_seqs]: the tokens in them (the last block's part counts as in context_lens),
+ * int32 (device), for pkv_selected_attn_decode_int8. q fp16 [num_seqs][q_len][num_q_heads][head_dim]
+ * as for the decode. Requires (num_q_heads / num_kv_heads) * q_len <= 32, keep_first + max(keep_last,
+ * 1 + ceil((q_len - 1) / block_size)) <= budget and max_blocks_per_seq <= 262144. A context length
+ * outside [0, max_blocks_per_seq * block_size] sets PKV_DEVERR_CONTEXT and counts as the nearest
+ * one within. The outputs must not overlap the inputs. */
+int pkv_select_blocks(int32_t* tables_out, int32_t* lens_out, const void* q,
+                      const float* kv_scales, const void* k_bounds, int num_blocks,
+                      const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* context_lens, int num_seqs, int q_len, int num_q_heads,
+                      int num_kv_heads, int head_dim, int block_size, int budget, int keep_first,
+                      int keep_last, pkv_stream_t stream);
 
 /* ---- per-head norm with the position rotation ------------------------------------------------
  * What comes between a layer's projections and its cache, for every token t with positions[t] >= 0

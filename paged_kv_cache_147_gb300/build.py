@@ -23,7 +23,7 @@ TORCH_SOURCE = "pkv_torch.cpp"
 TORCH_STAMP = os.path.join(BUILD, "pkv_torch.version")   # the torch and Python it was compiled for
 SOURCES = ["pkv_decode.cu", "pkv_cache.cu", "pkv_host.cu", "pkv_blocks.cpp", "pkv_spec.cu",
            "pkv_prefill.cu", "pkv_cache_int4.cu", "pkv_decode_int4.cu", "pkv_norm_rope.cu",
-           "pkv_tables.cu"]
+           "pkv_tables.cu", "pkv_cache_int8.cu", "pkv_decode_int8.cu", "pkv_select.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "-diag-suppress", "177"]

@@ -215,63 +215,6 @@ __device__ __forceinline__ uint32_t nan_halves(uint32_t w) {
   return __hneu2_mask(as_half2(w), as_half2(w));
 }
 
-// The products without `volatile`: the compiler may order them (pkv_device.cuh's keep theirs).
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// One warp's merge of a segment's NCS states (stO, stM, stL) into the unit's output (complete) or its
-// normalised partial at po, pml: merge_segment's arithmetic, four rows at a time, their loads
-// ahead of their sums (merge_segment takes a row at a time, with a division for its address:
-// 2.1 us for 8 rows, which bounded batches of short contexts).
-template <int NCS>
-__device__ __forceinline__ void merge_rows(const DecodeArgs& a, const float* stO, const float* stM,
-                                           const float* stL, const Seg& s, bool complete,
-                                           float* po, float* pml, int lane) {
-  float w[NCS], row_m, row_l;
-#pragma unroll
-  for (int ww = 0; ww < NCS; ++ww) w[ww] = 0.f;
-  if (lane < a.R) {
-    row_weights<NCS>(stM, stL, a.R, lane, w, row_m, row_l);
-    if (!complete)
-      *reinterpret_cast<float4*>(pml + lane * 4) = make_float4(row_m, row_l, 0.f, 0.f);
-  }
-  __half* out = out_row(a, s.b, s.h, 0);
-  int gg = 0;   // the row's head in the group
-#pragma unroll 1
-  for (int r0 = 0; r0 < a.R; r0 += 4) {
-    float4 acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = min(r0 + i, a.R - 1);
-      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int ww = 0; ww < NCS; ++ww) {
-        const float wt = __shfl_sync(0xffffffffu, w[ww], r);
-        const float4 v = reinterpret_cast<const float4*>(stO + (ww * a.R + r) * kSt)[lane];
-        acc[i].x += wt * v.x; acc[i].y += wt * v.y; acc[i].z += wt * v.z; acc[i].w += wt * v.w;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (r0 + i >= a.R) break;
-      if (complete)
-        store_half4(out + lane * 4, acc[i]);
-      else
-        reinterpret_cast<float4*>(po + (r0 + i) * kD)[lane] = acc[i];
-      out += kD;
-      if (++gg == a.G) {   // the next query token's heads
-        gg = 0;
-        out += (a.Hq - a.G) * kD;
-      }
-    }
-  }
-}
-
 // Warps 0 .. NCS RS - 1 consume; the next one prepares the queries, the last one is the epilogue
 // (merges each segment's per-warp states, writes outputs and split units' partials).
 template <int NCS, int RS, int ND, int MINB, bool APPEND>

@@ -1,0 +1,730 @@
+// pkv_decode_int8.cu -- paged decode attention over an 8-bit cache (pkv_int8.cuh's blocks) for
+// sm_103a, over whole contexts or over the blocks that pkv_select_blocks chose for each head.
+//
+// What it computes: pkv_paged_attn_decode's operation with K_t[d] = s_K (code_K - 128) and V_t[d] =
+// s_V (code_V - 128), (s_K, s_V) of the block and kv head that hold the row. With a table per kv head
+// it runs over that table's blocks as if they were the whole context.
+//
+// What bounds it: 256 bytes per (token, kv head). Stream, slices, split units and merges are those of
+// pkv_decode.cu (pkv_decode_common.cuh); the warps' own rings of cp.async stages, the transposed
+// tile, the query and the epilogue warp those of pkv_decode_int4.cu. What is its own:
+//  * A stage is two 16-token chunks, K and V, 2048 contiguous bytes each, and the two chunks' scales
+//    (blocks are 16 tokens or more, so a chunk has one of each). 16-byte pieces are exchanged by row
+//    (piece p of row r lies at p ^ (r & 7)): ldmatrix then reads 8 rows without a bank conflict.
+//  * Keys go to the tensor cores as they stand: a byte u in the low half of a 16-bit word is the fp16
+//    subnormal u 2^-24, exactly, so one AND or one byte permutation makes an operand of two codes.
+//    The offset's share, 128 sum_d q_d, is taken off in the accumulators' first value. (A tensor core
+//    counts a subnormal's exponent as -14 when it aligns products and cuts below 2^-25 of the
+//    largest: 2^-15 of a code step of the row's largest |q|.)
+//  * Values lose the offset before the product (1024 + u by a byte permutation, minus 1152, packed):
+//    sums of weights times u would be off by the truncation of 128 times the weights' sum.
+//  * The block's value scale is a power of two and goes into the exponent: a weight is w = 2^(x + e_V
+//    - M), x the score in powers of two, M the reference that follows the largest x + e_V (lazily, kept
+//    kShift below it, so that w fills fp16's range upwards and small weights keep their bits). The sum
+//    of the softmax weights takes w 2^-e_V. O = sum w code and that sum share the reference M, so the
+//    merges of warps and slices are those of the other caches.
+//  * Codes are never NaN or infinite, whatever a masked row holds: only a scale can be. A NaN scale
+//    reaches the queries that see a row of its block.
+#include <cuda_fp16.h>
+
+#include "pkv_decode_common.cuh"
+#include "pkv_device.cuh"
+#include "pkv_int8.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kTile8 = kChunk * kD;          // one chunk's K (or V): 2048 bytes
+constexpr int kStage8 = 4 * kTile8;          // K of two chunks, V of two chunks
+// Per-segment cost in chunks (see kSegCost): as for the 4-bit cache, whose segments do the same work.
+constexpr int kSeg8 = 8;
+// No slice finer than sqrt(kPartCost * the longest unit's chunks), and whole units to a CTA where
+// that costs at most kAlone rounds of stages (see pkv_decode_int4.cu).
+constexpr float kPartCost = 3.f;
+constexpr int kAlone = 3;
+constexpr size_t kMaxSmem = 227 * 1024;
+// How far the softmax's reference is put below the running maximum, and how far a weight may pass
+// the maximum before the reference moves: weights stay below 2^13.
+constexpr float kShift = 11.f, kGrow = 2.f;
+
+// What the kernel needs beside DecodeArgs.
+struct Int8Args {
+  const __half* q;
+  const float* scales;   // [num_blocks][Hkv][2]
+  int head_tables;       // a table per (sequence, kv head) instead of one per sequence
+};
+
+// Shared-memory layout (offsets from a 128-byte aligned base). NCS: warps that share the stages
+// among them, RS: warps that take one stage, 8 query rows each, ND: stages in flight per warp.
+template <int NCS, int RS, int ND>
+struct Smem8 {
+  static constexpr int kQTile = 5 * 512;              // 8 rows: fragments of 8 pieces, constants
+  static constexpr int kQBuf = RS * kQTile;
+  static constexpr int kQ = NCS * RS * ND * kStage8;
+  static constexpr int kScales = kQ + 2 * kQBuf;      // per stage: (s_K, s_V) of both chunks
+  static constexpr int kBars = kScales + NCS * RS * ND * 16;   // qfull[2], qempty[2], sdone, sfree
+  static constexpr int kFlags = kBars + 6 * 8;
+  static constexpr int kState = (kFlags + 64 + 15) & ~15;      // [NCS] segment states
+  __host__ __device__ static int state_floats(int R) { return NCS * R * (kSt + 2); }
+  __host__ __device__ static int seq_off(int R) { return kState + state_floats(R) * 4; }
+  __host__ static size_t bytes(int R, int B, int) {
+    return 128 + static_cast<size_t>(seq_off(R)) + (2 * static_cast<size_t>(B) + 1) * 4;
+  }
+  // the merge of split units stages at least two partials in the stage memory
+  static_assert(kQ >= 8 * RS * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
+};
+
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A warp's walk over the stages it loads: stage jp of a segment goes to warp (jp + stages before
+// the segment) mod NCS. Pool rows are fetched for up to 16 of the warp's stages at once (lane l:
+// chunk l & 1 of the (l / 2)-th), one group ahead of their use.
+template <int NCS>
+struct StageWalk8 {
+  Seg s;
+  int j, jp;        // stages of the slice before the segment; the warp's next stage in it
+  bool has;
+  int rows, n, i;   // current group: pool rows per lane, stages, position
+  int ids, at, nn;  // group ahead: block ids, (h << 8 | first row in the block) per lane, stages
+
+  __device__ __forceinline__ static int npair(const Seg& s) { return (s.c1 - s.c0 + 1) >> 1; }
+  __device__ __forceinline__ void enter(int w) { jp = ((w - j) % NCS + NCS) % NCS; }
+
+  // requests the block ids of the next group
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Int8Args& x,
+                                        const CursorT<kSeg8>& cur, int w, int lane) {
+    nn = 0;
+    ids = -1;
+    at = -1;
+    while (has && jp >= npair(s)) {
+      j += npair(s);
+      has = cur.next(s);
+      enter(w);
+    }
+    if (!has) return;
+    const int np = npair(s);
+    nn = min(16, (np - jp + NCS - 1) / NCS);
+    const int c = s.c0 + 2 * (jp + (lane >> 1) * NCS) + (lane & 1);
+    if ((lane >> 1) < nn && c < s.c1) {
+      const int64_t table = x.head_tables ? static_cast<int64_t>(s.b) * a.Hkv + s.h : s.b;
+      ids = a.block_tables[table * a.max_blocks + (c >> a.bs_shift)];
+      at = (s.h << 8) | ((c & ((1 << a.bs_shift) - 1)) << 4);
+    }
+    jp += nn * NCS;
+  }
+  // makes it the current one: rows (-1: no chunk, -2: bad block id)
+  __device__ __forceinline__ void take(const DecodeArgs& a) {
+    rows = -1;
+    if (at >= 0) {
+      if (ids >= 0 && ids < a.num_blocks) {
+        rows = (ids * a.Hkv + (at >> 8)) * a.block_size + (at & 255);
+      } else {
+        atomicOr(a.err, PKV_DEVERR_BLOCK_ID);
+        rows = -2;
+      }
+    }
+    n = nn;
+    i = 0;
+  }
+  __device__ __forceinline__ void start(const DecodeArgs& a, const Int8Args& x,
+                                        const CursorT<kSeg8>& cur, int begin, int w, int lane) {
+    j = 0;
+    has = cur.first(begin, s);
+    enter(w);
+    fetch(a, x, cur, w, lane);
+    take(a);
+    fetch(a, x, cur, w, lane);
+  }
+  // requests the warp's next stage into buffer `dst` (its scales to `sdst`), if there is one; one
+  // group of copies
+  __device__ __forceinline__ void load(const DecodeArgs& a, const Int8Args& x,
+                                       const CursorT<kSeg8>& cur, int w, int lane, uint32_t dst,
+                                       uint32_t sdst, uint64_t policy) {
+    if (i == n) {
+      take(a);
+      fetch(a, x, cur, w, lane);
+    }
+    if (i < n) {
+      // piece lane & 7 of rows 4 j + (lane >> 3), j < 4
+      const uint32_t even = (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
+      const uint32_t odd = even ^ 64u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = __shfl_sync(0xffffffffu, rows, 2 * i + h);
+        const uint32_t kd = dst + h * kTile8, vd = kd + 2 * kTile8;
+        if (r >= 0) {
+          const int64_t off = static_cast<int64_t>(r) * kD + lane * 16;
+          const uint8_t* ks = reinterpret_cast<const uint8_t*>(a.k_pool) + off;
+          const uint8_t* vs = reinterpret_cast<const uint8_t*>(a.v_pool) + off;
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            cp_async_16_hint(kd + p * 512 + ((p & 1) ? odd : even), ks + p * 512, policy);
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            cp_async_16_hint(vd + p * 512 + ((p & 1) ? odd : even), vs + p * 512, policy);
+          if (lane == h)
+            cp_async_8(sdst + h * 8, x.scales + 2 * static_cast<int64_t>(r >> (a.bs_shift + 4)));
+        } else if (r == -2) {   // a chunk behind a bad block id reads as zeros
+          const uint4 z = make_uint4(kInt8Zeros, kInt8Zeros, kInt8Zeros, kInt8Zeros);
+          for (int p = lane; p < kTile8 / 16; p += 32) {
+            st_shared_v4(kd + p * 16, z);
+            st_shared_v4(vd + p * 16, z);
+          }
+          if (lane < 2) st_shared_u32(sdst + h * 8 + lane * 4, 0x3f800000u);
+        }
+      }
+      ++i;
+    }
+    cp_async_commit();
+  }
+};
+
+// The exponent of a power of two as a number (NaN of a NaN); 2^-60 stands in for 0.
+__device__ __forceinline__ float exponent_of(float s) {
+  const float e = static_cast<float>(static_cast<int>(__float_as_uint(s) >> 23) - 127);
+  return s == s ? fmaxf(e, -60.f) : s;
+}
+
+// Warps 0 .. NCS RS - 1 consume; the next one prepares the queries, the last one is the epilogue
+// (merges each segment's per-warp states, writes outputs and split units' partials).
+template <int NCS, int RS, int ND, int MINB>
+__global__ void __launch_bounds__((NCS * RS + 2) * 32, MINB)
+decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
+  using L = Smem8<NCS, RS, ND>;
+  constexpr int NCW = NCS * RS;
+  griddep_wait();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar_qfull = sbase + L::kBars;
+  const uint32_t bar_qempty = bar_qfull + 2 * 8;
+  const uint32_t bar_sdone = bar_qempty + 2 * 8;
+  const uint32_t bar_sfree = bar_sdone + 8;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kFlags);
+  int* npend_s = reinterpret_cast<int*>(smem + L::kFlags) + 1;   // then 2 x (b, h, nb)
+  volatile int* fast_s = reinterpret_cast<volatile int*>(smem + L::kFlags) + 8;
+  int* longest_s = reinterpret_cast<int*>(smem + L::kFlags) + 9;
+  float* stO = reinterpret_cast<float*>(smem + L::kState);       // [NCS][R][kSt]
+  float* stM = stO + NCS * a.R * kSt;                             // [NCS][R]
+  float* stL = stM + NCS * a.R;                                   // [NCS][R]
+  int* pre = reinterpret_cast<int*>(smem + L::seq_off(a.R));
+  int* slen = pre + a.num_seqs + 1;
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int B = a.num_seqs;
+
+  // ---- per-sequence lengths and chunk counts -------------------------------------------------
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar_qfull + s * 8, 1);
+      mbar_init(bar_qempty + s * 8, NCW);
+    }
+    mbar_init(bar_sdone, NCW);
+    mbar_init(bar_sfree, 1);
+    *abort = 0;
+    *npend_s = 0;
+    *longest_s = 0;
+    pre[0] = 0;
+  }
+  int longest = 0;
+  for (int b = tid; b < B; b += blockDim.x) {
+    int ctx = a.context_lens[b];
+    const int lim = a.max_blocks * a.block_size;
+    if (ctx < 0 || ctx > lim) {
+      atomicOr(a.err, PKV_DEVERR_CONTEXT);
+      ctx = ctx < 0 ? 0 : lim;
+    }
+    const int nchunks = (ctx + kChunk - 1) / kChunk;
+    longest = max(longest, nchunks);
+    slen[b] = ctx;
+    pre[b + 1] = nchunks > 0 ? nchunks + kSeg8 : 0;
+  }
+  fence_barrier_init();
+  __syncthreads();
+  if (longest > 0) atomicMax(longest_s, longest);
+  if (warp == 0) scan_chunks(pre, B, lane);
+  __syncthreads();
+
+  // ---- this CTA's slice of the stream --------------------------------------------------------
+  const int total = pre[B] * a.Hkv;
+  const int per = max(static_cast<int>((total + gridDim.x - 1) / gridDim.x),
+                      static_cast<int>(sqrtf(kPartCost * *longest_s)));
+  int begin = blockIdx.x * per, end = min(total, begin + per);
+  if (B * a.Hkv <= gridDim.x && *longest_s <= 2 * NCS * ((per + 2 * NCS - 1) / (2 * NCS) + kAlone)) {
+    const int b = blockIdx.x / a.Hkv;
+    const int len = b < B ? pre[b + 1] - pre[b] : 0;
+    begin = len > 0 ? pre[b] * a.Hkv + (blockIdx.x - b * a.Hkv) * len : 0;
+    end = begin + len;
+  }
+  const CursorT<kSeg8> cur{pre, B, a.Hkv, end};
+
+  // let the next kernel on the stream launch as SM resources free up (it waits for this one
+  // before it reads anything this kernel writes)
+  if (tid == 0) griddep_launch_dependents();
+
+  LastSeg last{-1, 0, 0, 0, 0, true, false};
+  auto set_last = [&](const Seg& s, int k) {
+    last = LastSeg{k, s.b, s.h, s.nb, 2 * static_cast<int>(blockIdx.x) + (k == 0 ? 0 : 1),
+                   s.c0 == 0 && s.c1 == s.nb, s.c0 == 0};
+  };
+
+  if (warp == NCW) {
+    // =================================== queries =============================================
+    // Queries of segment kk into buffer kk & 1 as the products' B operands: for lane (g, t4), row g
+    // of each tile, the dims 16 p + 4 t4 .. + 3 of piece p, paired as the codes are ((0, 2) and
+    // (1, 3)). And per lane, for rows 2 t4 and 2 t4 + 1: what the codes' offset adds to a product
+    // (negative), and what makes scores of the products.
+    auto prepare = [&](const Seg& sg, int kk) {
+      const uint32_t qb = sbase + L::kQ + (kk & 1) * L::kQBuf;
+#pragma unroll 1
+      for (int tile = 0; 8 * tile < a.R; ++tile) {
+        const int row = 8 * tile + g;
+        const int qi = row / a.G;
+        // a query before its sequence's first token sees nothing, whatever it holds: taken as zeros,
+        // it keeps a NaN from its scores, which are all masked
+        const bool sees = row < a.R && slen[sg.b] - a.q_len + qi >= 0;
+        const uint2* src = reinterpret_cast<const uint2*>(
+            x8.q +
+            ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
+        uint2 v[8];
+        __half2 big = __half2half2(__ushort_as_half(0));
+#pragma unroll
+        for (int p = 0; p < 8; ++p) v[p] = sees ? src[4 * p + t4] : make_uint2(0, 0);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[p].x)));
+          big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[p].y)));
+        }
+        big = __hmax2_nan(big, __lowhigh2highlow(big));
+        big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const float top = __low2float(big);
+        // 2^(10 - exponent of the row's largest), which comes to lie in [2^10, 2^11); a negative
+        // score scale turns the queries' signs instead, so that a larger product is a larger score
+        const int ex = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) : 127;
+        float f = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
+        // codes come in as u 2^-24; a NaN or an infinity among the queries makes the scores NaN
+        const float unit = top <= 65504.f
+                               ? fabsf(a.scale_log2) *
+                                     (0x1p24f * __uint_as_float(static_cast<uint32_t>(ex - 10) << 23))
+                               : __uint_as_float(kNanBits);
+        if (a.scale_log2 < 0.f) f = -f;
+        float sum = 0.f;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          float2 u = __half22float2(*reinterpret_cast<const __half2*>(&v[p].x));
+          float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[p].y));
+          u.x *= f; u.y *= f; y.x *= f; y.y *= f;
+          sum += (u.x + u.y) + (y.x + y.y);
+          v[p] = make_uint2(pack_half2(u.x, y.x), pack_half2(u.y, y.y));
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          st_shared_v4(qb + tile * L::kQTile + p * 512 + lane * 16,
+                       make_uint4(v[2 * p].x, v[2 * p].y, v[2 * p + 1].x, v[2 * p + 1].y));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const float o = sum * -0x1p-17f;   // 128 2^-24
+        const float o0 = __shfl_sync(0xffffffffu, o, 8 * t4), o1 = __shfl_sync(0xffffffffu, o, 8 * t4 + 4);
+        const float r0 = __shfl_sync(0xffffffffu, unit, 8 * t4);
+        const float r1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
+        st_shared_v4(qb + tile * L::kQTile + 2048 + lane * 16,
+                     make_uint4(__float_as_uint(o0), __float_as_uint(o1), __float_as_uint(r0),
+                                __float_as_uint(r1)));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_qfull + (kk & 1) * 8);
+    };
+    Seg s;
+    bool has = cur.first(begin, s);
+    for (int k = 0; has; ++k) {
+      if (k >= 2 && !mbar_wait(bar_qempty + (k & 1) * 8, ((k >> 1) - 1) & 1, abort))
+        flag_timeout(a, abort);
+      prepare(s, k);
+      has = cur.next(s);
+    }
+    // sequences without any chunk get zeros (their units are in no CTA's slice)
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+      if (pre[b + 1] != pre[b]) continue;
+      const int n = a.q_len * a.Hq * kD;
+      for (int i = lane; i < n; i += 32)
+        a.out[static_cast<int64_t>(b) * n + i] = __float2half_rn(0.f);
+    }
+    return;
+  }
+  if (warp == NCW + 1) {
+    // =================================== epilogue ============================================
+    Seg s;
+    if (cur.first(begin, s)) {
+      int npend = 0, k = 0;
+      Seg nx = s;
+      while (cur.next(nx)) {
+        if (!mbar_wait(bar_sdone, k & 1, abort)) flag_timeout(a, abort);
+        const bool complete = (s.c0 == 0 && s.c1 == s.nb);
+        const int slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
+        merge_rows<NCS>(a, stO, stM, stL, s, complete,
+                        a.part_o + static_cast<int64_t>(slot) * a.R * kD,
+                        a.part_ml + static_cast<int64_t>(slot) * a.R * 4, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sfree);
+        if (!complete && lane == 0) {
+          // announce the partial (release) and see who else has arrived (acquire)
+          const int ua = unit_first<kSeg8>(pre, a.Hkv, s.b, s.h, s.nb);
+          const int parts = (ua + s.nb - 1) / per - ua / per + 1;
+          if (atomic_add_acq_rel(a.counters + s.b * a.Hkv + s.h, 1) == parts - 1) {
+            npend_s[1 + 3 * npend] = s.b;
+            npend_s[2 + 3 * npend] = s.h;
+            npend_s[3 + 3 * npend] = s.nb;
+            ++npend;
+          }
+        }
+        s = nx;
+        ++k;
+      }
+      if (lane == 0) *npend_s = npend;
+      set_last(s, k);
+    }
+  } else {
+    // =================================== consumers ===========================================
+    const int w = warp % NCS, rs = warp / NCS;   // share of the stages, query rows 8 rs .. + 7
+    // ldmatrix: lane l addresses row l & 15 of a chunk, matrices 0, 1 the two key octets of piece 2 i,
+    // 2, 3 of piece 2 i + 1
+    const uint32_t lm_row = (lane & 15) * 128;
+    const uint32_t lm_x = lane & 7, lm_p = lane >> 4;
+    const uint64_t kv_policy = l2_policy_evict_first();
+    const uint32_t ring = sbase + warp * (ND * kStage8);
+    const uint32_t sring = sbase + L::kScales + warp * (ND * 16);
+    StageWalk8<NCS> walk;
+    walk.start(a, x8, cur, begin, w, lane);
+    for (int i = 0; i < ND; ++i)
+      walk.load(a, x8, cur, w, lane, ring + i * kStage8, sring + i * 16, kv_policy);
+    int slot = 0;   // ring position of the warp's next stage
+    int j = 0, k = 0;
+    Seg s;
+    bool has = cur.first(begin, s);
+    while (has) {
+      const int qs = k & 1;
+      const uint32_t qb = sbase + L::kQ + qs * L::kQBuf + rs * L::kQTile + lane * 16;
+      if (!mbar_wait(bar_qfull + qs * 8, (k >> 1) & 1, abort)) flag_timeout(a, abort);
+      const int Lc = slen[s.b];
+      const uint4 qc = ld_shared_v4(qb + 2048);
+      const float off[2] = {__uint_as_float(qc.x), __uint_as_float(qc.y)};
+      const float rsc[2] = {__uint_as_float(qc.z), __uint_as_float(qc.w)};
+
+      // per row: the reference's negative (0 before the first score), the value above which it
+      // moves, the sum of the softmax weights
+      float nm[2] = {0.f, 0.f}, thr[2] = {kNegInf, kNegInf}, tl[2] = {0.f, 0.f};
+      float ot[8][4];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) ot[p][0] = ot[p][1] = ot[p][2] = ot[p][3] = 0.f;
+      const int r0 = 8 * rs + 2 * t4;
+      // query tokens of rows 2 t4, 2 t4 + 1: they see keys before Lc - q_len + 1 + these
+      const int qi0 = min(r0 / a.G, a.q_len - 1), qi1 = min((r0 + 1) / a.G, a.q_len - 1);
+
+      const int nchunk = s.c1 - s.c0;
+      const int npair = (nchunk + 1) >> 1;
+      int jp = ((w - j) % NCS + NCS) % NCS;
+      for (; jp < npair; jp += NCS) {
+        cp_async_wait<ND - 1>();
+        __syncwarp();                        // every lane's copies of this stage are in
+        const uint32_t stK = ring + slot * kStage8;
+        const uint32_t stV = stK + 2 * kTile8;
+        const int c = s.c0 + 2 * jp;
+        const bool two = c + 1 < s.c1;
+        const bool full = two && (c + 2) * kChunk <= Lc - a.q_len + 1;
+        const uint4 sc = ld_shared_v4(sring + slot * 16);
+
+        // ---- S^T = K Q^T, 16 keys (g, g + 8) at a time ----
+        float x[2][4];       // [chunk h][key g: rows 2 t4, + 1; key g + 8: the same]
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[h][0] = x[h][2] = off[0];
+          x[h][1] = x[h][3] = off[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 b = ld_shared_v4(qb + i * 512);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w0, w1, w2, w3;
+            ldsm_x4(stK + h * kTile8 + lm_row + (((2 * i + lm_p) ^ lm_x) << 4), w0, w1, w2, w3);
+            mma_f16(x[h], w0 & 0x00ff00ffu, w1 & 0x00ff00ffu, __byte_perm(w0, 0u, 0x4341),
+                    __byte_perm(w1, 0u, 0x4341), b.x, b.y);
+            mma_f16(x[h], w2 & 0x00ff00ffu, w3 & 0x00ff00ffu, __byte_perm(w2, 0u, 0x4341),
+                    __byte_perm(w3, 0u, 0x4341), b.z, b.w);
+          }
+        }
+
+        // ---- scores in powers of two, plus the value scale's exponent, against the reference ----
+        const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.z)};
+        const float ve[2] = {exponent_of(__uint_as_float(sc.y)), exponent_of(__uint_as_float(sc.w))};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float m = rsc[e] * ks[h], z = ve[h] + nm[e];
+            x[h][e] = fmaf(x[h][e], m, z);
+            x[h][2 + e] = fmaf(x[h][2 + e], m, z);
+          }
+        if (!full) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int lim = h == 0 || two ? Lc - a.q_len + 1 - (c + h) * kChunk : -(1 << 30);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              if (g + 8 * o >= lim + qi0) x[h][2 * o] = kNegInf;
+              if (g + 8 * o >= lim + qi1) x[h][2 * o + 1] = kNegInf;
+            }
+          }
+        }
+        bool move = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          move |= fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e])) > thr[e];
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            // how far the reference moves up (from nothing: to where it belongs)
+            float by = mx - kShift;
+            float alpha = 1.f;
+            if (thr[e] == kNegInf) {
+              alpha = 0.f;
+              if (mx != kNegInf) thr[e] = kShift + kGrow;
+              else by = 0.f;
+            } else {
+              by = fmaxf(by, 0.f);
+              alpha = fast_exp2(-by);
+            }
+            nm[e] -= by;
+            tl[e] *= alpha;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[h][e] -= by;
+              x[h][2 + e] -= by;
+            }
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+              ot[p][e] *= alpha;
+              ot[p][2 + e] *= alpha;
+            }
+          }
+        }
+        uint32_t pb[2][2];   // P^T of chunk h as the B operand
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // (a NaN scale, or what lies behind the last chunk: only weights may carry it)
+          const float iv = ve[h] == ve[h] ? fast_exp2(-ve[h]) : 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[h][e] = fast_exp2(x[h][e]);
+          tl[0] = fmaf(x[h][0] + x[h][2], iv, tl[0]);
+          tl[1] = fmaf(x[h][1] + x[h][3], iv, tl[1]);
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+            pb[h][o] = movmatrix_trans(pack_half2(x[h][2 * o], x[h][2 * o + 1]));
+        }
+
+        // ---- O^T += V^T P^T: row g of tile p is dim 16 p + 2 g, row g + 8 dim 16 p + 2 g + 1 ----
+        const __half2 kOff = __half2half2(__ushort_as_half(0x6480));   // 1152
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+            ldsm_x4_trans(stV + h * kTile8 + lm_row + (((2 * i + lm_p) ^ lm_x) << 4), v[0], v[1], v[2],
+                          v[3]);
+            uint32_t f[4][2];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t lo = __byte_perm(v[q], 0x64646464u, 0x4240);
+              const uint32_t hi = __byte_perm(v[q], 0x64646464u, 0x4341);
+              const __half2 l2 = __hsub2(*reinterpret_cast<const __half2*>(&lo), kOff);
+              const __half2 h2 = __hsub2(*reinterpret_cast<const __half2*>(&hi), kOff);
+              f[q][0] = *reinterpret_cast<const uint32_t*>(&l2);
+              f[q][1] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            mma_f16(ot[2 * i], f[0][0], f[0][1], f[1][0], f[1][1], pb[h][0], pb[h][1]);
+            mma_f16(ot[2 * i + 1], f[2][0], f[2][1], f[3][0], f[3][1], pb[h][0], pb[h][1]);
+          }
+        }
+        __syncwarp();                        // every lane has read the stage
+        walk.load(a, x8, cur, w, lane, stK, sring + slot * 16, kv_policy);
+        slot = slot + 1 == ND ? 0 : slot + 1;
+      }
+      // ---- the sums go to the warp's state buffer ----
+      if (k >= 1 && !mbar_wait(bar_sfree, (k - 1) & 1, abort)) flag_timeout(a, abort);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float lv = tl[e];
+        lv += __shfl_xor_sync(0xffffffffu, lv, 4);
+        lv += __shfl_xor_sync(0xffffffffu, lv, 8);
+        lv += __shfl_xor_sync(0xffffffffu, lv, 16);
+        const int r = r0 + e;
+        const int at = w * a.R + r;
+        if (r < a.R) {
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            *reinterpret_cast<float2*>(stO + at * kSt + 16 * p + 2 * g) =
+                make_float2(ot[p][e], ot[p][2 + e]);
+          if (g == 0) {
+            // scores that are all NaN have moved no reference
+            stM[at] = thr[e] == kNegInf && lv == lv ? kNegInf : -nm[e];
+            stL[at] = lv;
+          }
+        }
+      }
+      __syncwarp();
+      j += npair;
+      if (lane == 0) mbar_arrive(bar_qempty + qs * 8);
+      if (lane == 0) mbar_arrive(bar_sdone);
+      set_last(s, k);
+      ++k;
+      has = cur.next(s);
+    }
+    cp_async_wait<0>();
+  }
+
+  // ---- end of the slice ----
+  if (last.k >= 0)
+    finish_slice<NCS, kSeg8, NCW, 1>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s,
+                                      fast_s, warp < NCW ? tid : tid - 32);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host side.
+
+template <int NCS, int RS, int ND, int MINB>
+Variant variant8() {
+  return Variant{reinterpret_cast<const void*>(&decode_int8_kernel<NCS, RS, ND, MINB>), RS, false,
+                 (NCS * RS + 2) * 32, &Smem8<NCS, RS, ND>::bytes};
+}
+
+Variant choose8(int R) {
+  return R <= 8    ? variant8<4, 1, 2, 2>()
+         : R <= 16 ? variant8<2, 2, 2, 2>()
+         : R <= 24 ? variant8<3, 3, 2, 1>()
+                   : variant8<2, 4, 2, 1>();
+}
+
+int launch_decode_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                       const float* kv_scales, int num_blocks, const int32_t* block_tables,
+                       int max_blocks, const int32_t* context_lens, int num_seqs, int q_len, int Hq,
+                       int Hkv, int head_dim, int block_size, float scale, void* workspace,
+                       size_t workspace_bytes, bool head_tables, pkv_stream_t stream) {
+  if (num_seqs < 0 || q_len < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || head_dim != kD ||
+      !valid_block_size(block_size) || num_blocks < 0 || max_blocks < 0 ||
+      Hkv > (1 << 20))   // a stage's place is packed as head << 8 | row
+    return PKV_EINVAL;
+  const int G = Hq / Hkv;
+  if (static_cast<int64_t>(G) * q_len > 32) return PKV_EINVAL;
+  if (num_seqs == 0) return PKV_OK;
+  if (num_seqs > kMaxSeqs) return PKV_EINVAL;
+  const int R = G * q_len;
+  if (!out || !q || !k_cache || !v_cache || !kv_scales || !block_tables || !context_lens ||
+      !workspace)
+    return PKV_EINVAL;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(kv_scales) & 7u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PKV_EINVAL;
+  // all chunk indices and pool rows fit in int32
+  const int64_t rows = static_cast<int64_t>(num_blocks) * Hkv * block_size;
+  const int64_t max_ctx = static_cast<int64_t>(max_blocks) * block_size;
+  if (rows >= (1ll << 31) || max_ctx >= (1ll << 31) ||
+      static_cast<int64_t>(num_seqs) * Hkv * ((max_ctx + kChunk - 1) / kChunk + kSeg8) >=
+          (1ll << 30))
+    return PKV_EINVAL;
+  if (num_blocks == 0) return PKV_EINVAL;
+  const WsLayout ws = ws_layout(num_seqs, Hkv, R, workspace_bytes);
+  if (workspace_bytes < ws.total) return PKV_ENOSPC;
+
+  const Variant v = choose8(R);
+  const size_t smem = v.smem(R, num_seqs, 0);
+  if (smem > kMaxSmem) return PKV_EINVAL;
+  int status = PKV_OK;
+  const int grid = grid_size(v, smem, &status);
+  if (!grid) return status != PKV_OK ? status : PKV_EINVAL;
+
+  unsigned int* err = device_error_ptr();
+  if (!err) return cuda_status(cudaGetLastError());
+  DecodeArgs args = {};
+  args.out = static_cast<__half*>(out);
+  args.block_tables = block_tables;
+  args.context_lens = context_lens;
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  args.counters = reinterpret_cast<int*>(wsb + ws.counters);
+  args.part_ml = reinterpret_cast<float*>(wsb + ws.part_ml);
+  args.part_o = reinterpret_cast<float*>(wsb + ws.part_o);
+  args.err = err;
+  args.num_blocks = num_blocks;
+  args.max_blocks = max_blocks;
+  args.num_seqs = num_seqs;
+  args.q_len = q_len;
+  args.Hq = Hq;
+  args.Hkv = Hkv;
+  args.G = G;
+  args.R = R;
+  args.block_size = block_size;
+  int shift = 0;
+  while ((kChunk << shift) < block_size) ++shift;
+  args.bs_shift = shift;
+  args.scale_log2 = scale * 1.4426950408889634f;
+  args.k_pool = static_cast<__half*>(const_cast<void*>(k_cache));
+  args.v_pool = static_cast<__half*>(const_cast<void*>(v_cache));
+
+  Int8Args args8{static_cast<const __half*>(q), kv_scales, head_tables ? 1 : 0};
+  void* params[2] = {&args, &args8};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(v.threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelExC(&cfg, v.fn, params));
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_paged_attn_decode_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const float* kv_scales, int num_blocks, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                               int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                               int block_size, float scale, void* workspace,
+                               size_t workspace_bytes, pkv_stream_t stream) {
+  return launch_decode_int8(out, q, k_cache, v_cache, kv_scales, num_blocks, block_tables,
+                            max_blocks_per_seq, context_lens, num_seqs, q_len, num_q_heads,
+                            num_kv_heads, head_dim, block_size, scale, workspace, workspace_bytes,
+                            false, stream);
+}
+
+int pkv_selected_attn_decode_int8(void* out, const void* q, const void* k_cache,
+                                  const void* v_cache, const float* kv_scales, int num_blocks,
+                                  const int32_t* head_tables, int max_blocks_per_head,
+                                  const int32_t* context_lens, int num_seqs, int q_len,
+                                  int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  float scale, void* workspace, size_t workspace_bytes,
+                                  pkv_stream_t stream) {
+  return launch_decode_int8(out, q, k_cache, v_cache, kv_scales, num_blocks, head_tables,
+                            max_blocks_per_head, context_lens, num_seqs, q_len, num_q_heads,
+                            num_kv_heads, head_dim, block_size, scale, workspace, workspace_bytes,
+                            true, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,82 @@
+// pkv_int8.cuh -- the 8-bit cache's format and its quantisation.
+//
+// A block of tokens of one kv head shares one scale for its keys and one for its values; a row (one
+// token, one kv head, K or V) is 128 bytes of codes, an element's value is scale * (code - 128).
+// Scales are powers of two, 2^-30 to 2^9:
+//  * a block's scale has to grow when a larger row arrives. A code then moves to the new grid by
+//    rint(c 2^-k); the errors of repeated moves are halves of ever larger steps, together less than
+//    one step of the last scale, where arbitrary scales, growing a little with every token, would
+//    add half a step each time. A scale has at most one bit more than the rows need.
+//  * codes times scale are exact wherever they go (fp16, fp32), and so are sums of codes times whole
+//    numbers: the block selection gives the same answer in any order of summation.
+// Codes lie in 1 .. 255 (128 is zero): as unsigned bytes one byte permutation makes fp16 numbers of
+// them. A scale that is NaN says that a NaN or an infinity was written; all of the block is NaN then.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+constexpr int kInt8Low = -30, kInt8High = 9;   // exponents of a scale
+constexpr uint32_t kInt8Zeros = 0x80808080u;   // four codes of zero
+constexpr uint32_t kNanBits = 0x7fffffffu;
+// 1.5 * 2^23 + 128: added to a number of at most 127 (in size) it leaves the code, ties to even, in
+// the sum's lowest byte.
+constexpr float kInt8Magic = 12582912.f + 128.f;
+
+// The least scale s with top <= 127 s (2^9 at most); NaN for a top that is NaN or infinite.
+__device__ __forceinline__ float int8_scale(float top) {
+  if (!(top <= 65504.f)) return __uint_as_float(kNanBits);
+  // 127 is 1.984375 * 2^6: adding 2^17 - 1 to the bits carries into the exponent past that
+  const int e = static_cast<int>((__float_as_uint(top) + 0x1ffffu) >> 23) - 6;
+  return __uint_as_float(static_cast<uint32_t>(min(max(e, 127 + kInt8Low), 127 + kInt8High)) << 23);
+}
+
+// 1 / s of a power of two (0 for NaN).
+__device__ __forceinline__ float int8_inverse(float s) {
+  return s == s ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
+}
+
+// What `top` needs, and what the block has: the larger, NaN if either is.
+__device__ __forceinline__ float int8_grown(float need, float old) {
+  return old != old ? old : (need != need ? need : fmaxf(need, old));
+}
+
+__device__ __forceinline__ uint32_t int8_pack(float a, float b, float c, float d) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// Codes of 8 elements at scale s, r = int8_inverse(s). Only at the greatest scale can an element
+// pass 127.5 steps: 65024 = 127 * 2^9 bounds them all.
+__device__ __forceinline__ uint2 int8_codes(const uint4& h, float r) {
+  if (r == 0.f) return make_uint2(kInt8Zeros, kInt8Zeros);
+  const __half2 most = __half2half2(__ushort_as_half(0x7bf0)),
+                least = __half2half2(__ushort_as_half(0xfbf0));
+  const __half2* p = reinterpret_cast<const __half2*>(&h);
+  float m[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(__hmax2(__hmin2(p[i], most), least));
+    m[2 * i] = fmaf(f.x, r, kInt8Magic);
+    m[2 * i + 1] = fmaf(f.y, r, kInt8Magic);
+  }
+  return make_uint2(int8_pack(m[0], m[1], m[2], m[3]), int8_pack(m[4], m[5], m[6], m[7]));
+}
+
+// Code i of a word as a float, without the offset.
+template <int I>
+__device__ __forceinline__ float int8_value(uint32_t w) {
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | I)) - (8388608.f + 128.f);
+}
+
+// Four codes on a grid 1 / f times as coarse (f <= 1, a power of two or 0).
+__device__ __forceinline__ uint32_t int8_rescaled(uint32_t w, float f) {
+  return int8_pack(fmaf(int8_value<0>(w), f, kInt8Magic), fmaf(int8_value<1>(w), f, kInt8Magic),
+                   fmaf(int8_value<2>(w), f, kInt8Magic), fmaf(int8_value<3>(w), f, kInt8Magic));
+}
+
+}  // namespace pkv

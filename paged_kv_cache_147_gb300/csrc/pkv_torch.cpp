@@ -1,4 +1,4 @@
-// pkv_torch.cpp -- the Python side of the 4-bit, norm and table calls: checks of the tensors'
+// pkv_torch.cpp -- the Python side of the 4-bit, 8-bit, norm and table calls: checks of the tensors'
 // types, devices and shapes, outputs allocated by torch, the current stream, one C call. A decode
 // step makes several of these calls of a few microseconds each, and the same written with ctypes
 // and Tensor attributes took longer than the kernels: norm of 64 tokens 15.8 us a call (2.0 of
@@ -30,8 +30,14 @@ struct {
   decltype(&pkv_qk_norm_rope) qk_norm_rope;
   decltype(&pkv_extend_tables) extend_tables;
   decltype(&pkv_truncate_tables) truncate_tables;
+  decltype(&pkv_kv_append_int8) kv_append_int8;
+  decltype(&pkv_widen_blocks_int8) widen_blocks_int8;
+  decltype(&pkv_copy_blocks_int8) copy_blocks_int8;
+  decltype(&pkv_paged_attn_decode_int8) decode_int8;
+  decltype(&pkv_selected_attn_decode_int8) selected_decode_int8;
+  decltype(&pkv_select_blocks) select_blocks;
 } lib;
-constexpr int kEntryPoints = 7;
+constexpr int kEntryPoints = 13;
 PyObject* error_class = nullptr;   // pkv.PkvError(entry point, status)
 
 constexpr auto kF16 = at::kHalf;
@@ -313,6 +319,151 @@ PyObject* truncate_tables(Args& A) {
   return st ? fail(A.fn, st) : none();
 }
 
+// An 8-bit cache's pools, scales and (at i + 3, None allowed) bounds, at arguments i ..; `lead`
+// dimensions before the block's.
+struct Int8Cache {
+  const at::Tensor &k, &v, &scales;
+  at::Tensor bounds;
+  int64_t nb = 0, hkv = 0, bs = 0;
+  bool ok = false;
+  Int8Cache(Args& A, int i, bool with_bounds, int lead = 0)
+      : k(A.tensor(i, kU8)), v(A.tensor(i + 1, kU8)), scales(A.tensor(i + 2, kF32)) {
+    if (with_bounds && A.a[i + 3] != Py_None) bounds = A.tensor(i + 3, kU8);
+    if (!A.ok || k.dim() != lead + 4) return;
+    nb = k.size(lead);
+    hkv = k.size(lead + 1);
+    bs = k.size(lead + 2);
+    if (k.size(lead + 3) != 128 || !same(v, k) || !fits(nb) || !fits(hkv) || !fits(bs)) return;
+    if (lead) {
+      const int64_t layers = k.size(0);
+      ok = fits(layers) && shaped(scales, {layers, nb, hkv, 2}) &&
+           (!bounds.defined() || shaped(bounds, {layers, nb, hkv, 2, 128}));
+    } else {
+      ok = shaped(scales, {nb, hkv, 2}) &&
+           (!bounds.defined() || shaped(bounds, {nb, hkv, 2, 128}));
+    }
+  }
+  void* bounds_ptr() const { return bounds.defined() ? ptr(bounds) : nullptr; }
+};
+
+// k, v, slots, k_cache, v_cache, kv_scales, k_bounds, stream
+PyObject* kv_append_int8(Args& A) {
+  const at::Tensor &k = A.tensor(0, kF16), &v = A.tensor(1, kF16), &slots = A.tensor(2, kI64);
+  const Int8Cache c(A, 3, true);
+  const int64_t n = slots.numel();
+  if (!c.ok || !shaped(k, {n, c.hkv, 128}) || !same(v, k) || !fits(n)) return fail(A.fn, PKV_EINVAL);
+  const pkv_stream_t s = A.stream(7);
+  const int st = unlocked([&] {
+    return lib.kv_append_int8(ptr(k), ptr(v), ptr<int64_t>(slots), n, ptr(c.k), ptr(c.v),
+                              ptr<float>(c.scales), c.bounds_ptr(), c.nb, c.hkv, 128, c.bs, s);
+  });
+  return st ? fail(A.fn, st) : none();
+}
+
+// k_cache, v_cache, kv_scales, src, dst, k_out, v_out, stream
+PyObject* widen_blocks_int8(Args& A) {
+  const Int8Cache c(A, 0, false);
+  const at::Tensor &src = A.tensor(3, kI32), &dst = A.tensor(4, kI32), &ko = A.tensor(5, kF16),
+                   &vo = A.tensor(6, kF16);
+  if (!c.ok || !A.ok || ko.dim() != 4) return fail(A.fn, PKV_EINVAL);
+  const int64_t n = src.numel(), nbo = ko.size(0);
+  if (dst.numel() != n || !shaped(ko, {nbo, c.hkv, c.bs, 128}) || !same(vo, ko) || !fits(nbo) ||
+      !fits(n))
+    return fail(A.fn, PKV_EINVAL);
+  const pkv_stream_t s = A.stream(7);
+  const int st = unlocked([&] {
+    return lib.widen_blocks_int8(ptr(c.k), ptr(c.v), ptr<float>(c.scales), ptr<int32_t>(src),
+                                 ptr<int32_t>(dst), n, c.nb, ptr(ko), ptr(vo), nbo, c.hkv, 128, c.bs,
+                                 s);
+  });
+  return st ? fail(A.fn, st) : none();
+}
+
+// k_cache, v_cache, kv_scales, k_bounds, src, dst, stream
+PyObject* copy_blocks_int8(Args& A) {
+  const at::Tensor& k = A.any(0);
+  const int lead = A.ok && k.dim() == 5 ? 1 : 0;
+  const Int8Cache c(A, 0, true, lead);
+  const at::Tensor &src = A.tensor(4, kI32), &dst = A.tensor(5, kI32);
+  const int64_t n = A.ok ? src.numel() : 0;
+  if (!c.ok || !A.ok || dst.numel() != n || !fits(n)) return fail(A.fn, PKV_EINVAL);
+  const int64_t layers = lead ? c.k.size(0) : 1;
+  const pkv_stream_t s = A.stream(6);
+  const int st = unlocked([&] {
+    return lib.copy_blocks_int8(ptr(c.k), ptr(c.v), ptr<float>(c.scales), c.bounds_ptr(),
+                                ptr<int32_t>(src), ptr<int32_t>(dst), n, layers, c.nb, c.hkv, 128,
+                                c.bs, s);
+  });
+  return st ? fail(A.fn, st) : none();
+}
+
+// out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, scale, workspace, stream; tables
+// of two dimensions (one per sequence) or three (one per sequence and kv head)
+PyObject* paged_attn_decode_int8(Args& A) {
+  const at::Tensor &out = A.tensor(0, kF16), &q = A.tensor(1, kF16);
+  const Int8Cache c(A, 2, false);
+  const at::Tensor &bt = A.tensor(5, kI32), &cl = A.tensor(6, kI32), &ws = A.any(8);
+  if (!c.ok || !A.ok || !ws.is_cuda() || ws.get_device() != A.dev || !ws.is_contiguous() ||
+      q.dim() != 4 || (bt.dim() != 2 && bt.dim() != 3))
+    return fail(A.fn, PKV_EINVAL);
+  const int64_t B = q.size(0), q_len = q.size(1), hq = q.size(2), d = q.size(3);
+  const bool heads = bt.dim() == 3;
+  const int64_t width = bt.size(heads ? 2 : 1);
+  if (!same(out, q) || bt.size(0) != B || (heads && bt.size(1) != c.hkv) || cl.numel() != B ||
+      !fits(B) || !fits(q_len) || !fits(hq) || !fits(d) || !fits(width))
+    return fail(A.fn, PKV_EINVAL);
+  const float scale = A.number(7);
+  const pkv_stream_t s = A.stream(9);
+  const auto call = heads ? lib.selected_decode_int8 : lib.decode_int8;
+  const int st = unlocked([&] {
+    return call(ptr(out), ptr(q), ptr(c.k), ptr(c.v), ptr<float>(c.scales), c.nb, ptr<int32_t>(bt),
+                width, ptr<int32_t>(cl), B, q_len, hq, c.hkv, d, c.bs, scale, ptr(ws), ws.nbytes(),
+                s);
+  });
+  if (st) return fail(A.fn, st);
+  Py_INCREF(A.a[0]);
+  return A.a[0];
+}
+
+// q, kv_scales, k_bounds, block_tables, context_lens, block_size, budget, keep_first, keep_last,
+// tables_out, lens_out, stream
+PyObject* select_blocks(Args& A) {
+  const at::Tensor &q = A.tensor(0, kF16), &sc = A.tensor(1, kF32), &kb = A.tensor(2, kU8),
+                   &bt = A.tensor(3, kI32), &cl = A.tensor(4, kI32);
+  const int64_t bs = A.whole(5), budget = A.whole(6), first = A.whole(7), last = A.whole(8);
+  if (!A.ok || q.dim() != 4 || kb.dim() != 4 || bt.dim() != 2) return fail(A.fn, PKV_EINVAL);
+  const int64_t B = q.size(0), q_len = q.size(1), hq = q.size(2), d = q.size(3);
+  const int64_t nb = kb.size(0), hkv = kb.size(1), width = bt.size(1);
+  if (!shaped(kb, {nb, hkv, 2, 128}) || !shaped(sc, {nb, hkv, 2}) || bt.size(0) != B ||
+      cl.numel() != B || budget < 1 || !fits(B) || !fits(q_len) || !fits(hq) || !fits(d) ||
+      !fits(nb) || !fits(hkv) || !fits(width))
+    return fail(A.fn, PKV_EINVAL);
+  at::Tensor tables, lens;
+  if (A.a[9] != Py_None) {
+    tables = A.tensor(9, kI32);
+    if (!A.ok || !shaped(tables, {B, hkv, budget})) return fail(A.fn, PKV_EINVAL);
+  }
+  if (A.a[10] != Py_None) {
+    lens = A.tensor(10, kI32);
+    if (!A.ok || lens.numel() != B) return fail(A.fn, PKV_EINVAL);
+  }
+  const pkv_stream_t s = A.stream(11);
+  const int st = unlocked([&] {
+    const Outputs on(A, 11, s);
+    if (!tables.defined()) tables = at::empty({B, hkv, budget}, bt.options());
+    if (!lens.defined()) lens = at::empty({B}, bt.options());
+    return lib.select_blocks(ptr<int32_t>(tables), ptr<int32_t>(lens), ptr(q), ptr<float>(sc),
+                             ptr(kb), nb, ptr<int32_t>(bt), width, ptr<int32_t>(cl), B, q_len, hq,
+                             hkv, d, bs, budget, first, last, s);
+  });
+  if (st) return fail(A.fn, st);
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(tables)));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(lens)));
+  return r;
+}
+
 // C++ exceptions (no CUDA device, no memory for an output) become the Python ones torch raises.
 template <PyObject* (*F)(Args&), Py_ssize_t N>
 PyObject* entry(const char* fn, PyObject* const* args, Py_ssize_t n) {
@@ -345,6 +496,11 @@ PKV_ENTRY(paged_attn_decode_append_int4, decode<true>, 11)
 PKV_ENTRY(qk_norm_rope, qk_norm_rope, 10)
 PKV_ENTRY(extend_tables, extend_tables, 9)
 PKV_ENTRY(truncate_tables, truncate_tables, 7)
+PKV_ENTRY(kv_append_int8, kv_append_int8, 8)
+PKV_ENTRY(widen_blocks_int8, widen_blocks_int8, 8)
+PKV_ENTRY(copy_blocks_int8, copy_blocks_int8, 7)
+PKV_ENTRY(paged_attn_decode_int8, paged_attn_decode_int8, 10)
+PKV_ENTRY(select_blocks, select_blocks, 12)
 
 // bind(error class, addresses of the entry points in the order of `lib`)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -377,6 +533,11 @@ PyMethodDef methods[] = {
     PKV_METHOD(qk_norm_rope),
     PKV_METHOD(extend_tables),
     PKV_METHOD(truncate_tables),
+    PKV_METHOD(kv_append_int8),
+    PKV_METHOD(widen_blocks_int8),
+    PKV_METHOD(copy_blocks_int8),
+    PKV_METHOD(paged_attn_decode_int8),
+    PKV_METHOD(select_blocks),
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&bind)), METH_FASTCALL,
      nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -31,7 +31,9 @@ SYMBOLS = (
     "pkv_pool_refcount", "pkv_spec_verify", "pkv_set_early_start", "pkv_paged_prefill",
     "pkv_ring_attn_decode_append", "pkv_kv_append_int4", "pkv_widen_blocks_int4",
     "pkv_paged_attn_decode_int4", "pkv_paged_attn_decode_append_int4", "pkv_qk_norm_rope",
-    "pkv_extend_tables", "pkv_truncate_tables",
+    "pkv_extend_tables", "pkv_truncate_tables", "pkv_kv_append_int8", "pkv_widen_blocks_int8",
+    "pkv_copy_blocks_int8", "pkv_paged_attn_decode_int8", "pkv_selected_attn_decode_int8",
+    "pkv_select_blocks",
 )
 
 OK, EINVAL, ERANGE, ENOSPC, ECUDA_BASE = 0, -22, -34, -28, -1000
@@ -129,6 +131,15 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
                                    P]),
         "pkv_extend_tables": (i32, [P, P, P, i32, i32, i32, P, P, i32, P, P, P, P, i32, P]),
         "pkv_truncate_tables": (i32, [P, P, P, i32, i32, i32, P, P, i32, P]),
+        "pkv_kv_append_int8": (i32, [P, P, P, i32, P, P, P, P, i32, i32, i32, i32, P]),
+        "pkv_widen_blocks_int8": (i32, [P, P, P, P, P, i32, i32, P, P, i32, i32, i32, i32, P]),
+        "pkv_copy_blocks_int8": (i32, [P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P]),
+        "pkv_paged_attn_decode_int8": (i32, [P, P, P, P, P, i32, P, i32, P, i32, i32, i32, i32, i32,
+                                             i32, f32, P, sz, P]),
+        "pkv_selected_attn_decode_int8": (i32, [P, P, P, P, P, i32, P, i32, P, i32, i32, i32, i32,
+                                                i32, i32, f32, P, sz, P]),
+        "pkv_select_blocks": (i32, [P, P, P, P, P, i32, P, i32, P, i32, i32, i32, i32, i32, i32, i32,
+                                    i32, i32, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name, None)    # an older build may lack newer entry points
@@ -164,12 +175,13 @@ def _p(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-# The 4-bit, norm and table calls go through a compiled binding: it checks what the library cannot
+# The 4-bit, 8-bit, norm and table calls go through a compiled binding: it checks what the library cannot
 # see through a bare pointer (element type, device, layout, shape), allocates the outputs and
 # makes the call. Their kernels are shorter than the same steps in Python.
 _TORCH_ENTRIES = ("kv_append_int4", "widen_blocks_int4", "paged_attn_decode_int4",
                   "paged_attn_decode_append_int4", "qk_norm_rope", "extend_tables",
-                  "truncate_tables")
+                  "truncate_tables", "kv_append_int8", "widen_blocks_int8", "copy_blocks_int8",
+                  "paged_attn_decode_int8", "selected_attn_decode_int8", "select_blocks")
 _ops = None
 
 
@@ -239,7 +251,8 @@ def kv_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
 
 def copy_blocks(k_cache, v_cache, src, dst, stream=None):
     """k_cache, v_cache [layers, NB, Hkv, bs, D] (or one layer [NB, Hkv, bs, D]) of any cache type:
-    fp16 rows, uint8 E4M3 codes or uint8 4-bit rows (D = 80)."""
+    fp16 rows, uint8 E4M3 codes or uint8 4-bit rows (D = 80); copy_blocks_int8 copies those of an
+    8-bit cache, whose scales go with them."""
     kc = k_cache if k_cache.dim() == 5 else k_cache.unsqueeze(0)
     layers, nb, hkv, bs, d = kc.shape
     row, layer = d * kc.element_size(), kc.stride(0) * kc.element_size()   # bytes
@@ -431,6 +444,60 @@ def paged_attn_decode_append_int4(out, q, k_new, v_new, k_cache, v_cache, block_
     out and its rows stay. kv_append_int4 + paged_attn_decode_int4 go by the slots instead."""
     return (_ops or _torch_ops()).paged_attn_decode_append_int4(
         out, q, k_new, v_new, k_cache, v_cache, block_tables, context_lens, scale, workspace, stream)
+
+
+# ------------------------------------------------------------------------------ 8-bit cache
+def make_int8_cache(num_blocks, num_kv_heads, block_size, layers=None, bounds=True, device="cuda"):
+    """A zeroed 8-bit cache: (k_cache, v_cache uint8 [NB, Hkv, bs, 128], kv_scales float32
+    [NB, Hkv, 2], k_bounds uint8 [NB, Hkv, 2, 128] or None), with a leading dimension where `layers`
+    is given. k_bounds are for select_blocks."""
+    lead = () if layers is None else (layers,)
+
+    def zeros(*shape, dtype=torch.uint8):
+        return torch.zeros(*lead, num_blocks, num_kv_heads, *shape, dtype=dtype, device=device)
+
+    return (zeros(block_size, 128), zeros(block_size, 128), zeros(2, dtype=torch.float32),
+            zeros(2, 128) if bounds else None)
+
+
+def kv_append_int8(k, v, slots, k_cache, v_cache, kv_scales, k_bounds=None, stream=None):
+    """k, v fp16 [T, Hkv, 128]; slots int64 [T]; one layer of an 8-bit cache (make_int8_cache).
+    A block's scale grows with the rows written into it; writing its first row starts it afresh,
+    its other rows zero. The tokens of one block lie within block_size consecutive ones of the call."""
+    (_ops or _torch_ops()).kv_append_int8(k, v, slots, k_cache, v_cache, kv_scales, k_bounds, stream)
+
+
+def widen_blocks_int8(k_cache, v_cache, kv_scales, src, dst, k_out, v_out, stream=None):
+    """Blocks src[i] of the 8-bit cache -> blocks dst[i] of the fp16 pools k_out, v_out
+    [NB', Hkv, bs, 128]; src, dst int32."""
+    (_ops or _torch_ops()).widen_blocks_int8(k_cache, v_cache, kv_scales, src, dst, k_out, v_out,
+                                             stream)
+
+
+def copy_blocks_int8(k_cache, v_cache, kv_scales, k_bounds, src, dst, stream=None):
+    """copy_blocks for an 8-bit cache (one layer, or layers in a leading dimension): codes, scales
+    and, unless None, bounds."""
+    (_ops or _torch_ops()).copy_blocks_int8(k_cache, v_cache, kv_scales, k_bounds, src, dst, stream)
+
+
+def paged_attn_decode_int8(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, scale,
+                           workspace, stream=None):
+    """paged_attn_decode over an 8-bit cache (make_int8_cache's pools and scales). block_tables
+    [B, width], or [B, Hkv, width]: a table per kv head, with context_lens the tokens in it
+    (select_blocks' two results)."""
+    return (_ops or _torch_ops()).paged_attn_decode_int8(
+        out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, scale, workspace, stream)
+
+
+def select_blocks(q, kv_scales, k_bounds, block_tables, context_lens, block_size, budget,
+                  keep_first=1, keep_last=1, tables_out=None, lens_out=None, stream=None):
+    """Blocks of each sequence that the queries q [B, q_len, Hq, 128] attend to, up to `budget` per kv
+    head: the first keep_first, the last keep_last (and those of the last q_len tokens), and those
+    whose keys may have the largest products with a query -> (tables int32 [B, Hkv, budget], -1
+    behind the chosen blocks; lens int32 [B], the tokens in them), for paged_attn_decode_int8."""
+    return (_ops or _torch_ops()).select_blocks(
+        q, kv_scales, k_bounds, block_tables, context_lens, block_size, budget, keep_first,
+        keep_last, tables_out, lens_out, stream)
 
 
 # ------------------------------------------------------------------------------ norm + rotation
