@@ -14,218 +14,269 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarpRows = 16;    // rows of a block that a warp holds in registers
-constexpr int kSpan = 16;        // tokens whose blocks one team looks after in a large call
 
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ uint4 pick(bool second, const __half2 (&a)[4], const __half2 (&b)[4]) {
+  return second ? make_uint4(h2_bits(b[0]), h2_bits(b[1]), h2_bits(b[2]), h2_bits(b[3]))
+                : make_uint4(h2_bits(a[0]), h2_bits(a[1]), h2_bits(a[2]), h2_bits(a[3]));
+}
 
-// A team of W warps (W rows of 16 make a block) takes, for one kv head and K or V, every block whose
-// first row of the call is among its `span` tokens; the block's other rows are among the bs - 1
-// tokens behind that one. All rows stay in registers between the pass that finds the scale and the
-// one that writes codes.
-template <int W>
-__global__ void __launch_bounds__(W < 4 ? kThreads : W * 32)
-kv_append_int8_kernel(const uint4* k, const uint4* v, const int64_t* slots, int num_tokens,
-                      uint8_t* k_cache, uint8_t* v_cache, float* scales, uint8_t* bounds,
-                      int64_t num_slots, int num_kv_heads, int span, unsigned jobs,
-                      unsigned int* err) {
-  griddep_wait();
-  constexpr int kTeams = W < 4 ? 4 / W : 1;
-  constexpr int kBs = W * kWarpRows;
-  constexpr int kShift = W == 1 ? 4 : W == 2 ? 5 : W == 4 ? 6 : W == 8 ? 7 : 8;
-  __shared__ float top_s[kTeams][W];
-  __shared__ uint32_t rows_s[kTeams][W];          // which rows of the block the call writes
-  __shared__ uint4 ends_s[kTeams][W][32];         // per channel least and greatest new element
-  const int lane = threadIdx.x & 31;
-  const int team = threadIdx.x / (W * 32), w = (threadIdx.x >> 5) % W;
-  const unsigned job = blockIdx.x * kTeams + team;
-  if (job >= jobs) return;
-  const unsigned which = job & 1;
-  const unsigned part = (job >> 1) / num_kv_heads;
-  const int h = static_cast<int>((job >> 1) - part * num_kv_heads);
-  const int64_t first = static_cast<int64_t>(part) * span;
-  auto team_sync = [&]() {
-    if (W == 1) __syncwarp();
-    else named_barrier_sync(1 + team, W * 32);
-  };
-  // the block of a token, -1 for none
-  auto block_of = [&](int64_t t) -> int64_t {
-    if (t < 0 || t >= num_tokens) return -1;
-    const int64_t s = slots[t];
-    return s >= 0 && s < num_slots ? s >> kShift : -1;
-  };
-  if (which == 0 && h == 0 && w == 0 && lane < span && first + lane < num_tokens &&
-      slots[first + lane] >= num_slots)
-    atomicOr(err, PKV_DEVERR_SLOT);
+struct AppendArgs {
+  const uint4* k;
+  const uint4* v;
+  const int64_t* slots;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* scales;
+  uint8_t* bounds;
+  unsigned int* err;
+  int64_t num_slots;
+  int num_tokens, num_kv_heads, span;
+  unsigned jobs;
+};
 
-  const int64_t mine = lane < span ? block_of(first + lane) : -1;
-  const int64_t before = lane < span ? block_of(first + lane - 1) : -1;
-  unsigned heads = __ballot_sync(0xffffffffu, mine >= 0 && mine != before);
-  const uint4* src = which ? v : k;
-  uint8_t* cache = which ? v_cache : k_cache;
+// What the G warps that take a block's rows share.
+template <int G, int BS>
+struct Shared {
+  float top[G];
+  uint32_t rows[BS / kWarpRows];   // which rows of the block the call writes, 16 to a word
+  uint4 ends[G][32];               // per channel least and greatest new element
+};
+
+// The rows of one call that go to one block (slots sl[0 ..], the block's first one first, all within
+// BS tokens from t0 on; G = 1: within 16), for kv head h and K or V, by G warps: warp w has 16 tokens'
+// rows in its registers between the pass that finds the scale and the one that writes codes.
+template <int G, int BS, class Sync>
+__device__ __forceinline__ void append_block(const AppendArgs& a, const int64_t* sl, int64_t t0,
+                                             int h, int which, int w, int lane, Shared<G, BS>& sh,
+                                             Sync sync) {
+  constexpr int kShift = BS == 16 ? 4 : BS == 32 ? 5 : BS == 64 ? 6 : BS == 128 ? 7 : 8;
+  constexpr int kWords = BS / kWarpRows;
+  const uint4* src = which ? a.v : a.k;
   const int c = lane & 15, odd = lane >> 4;
-
-  for (; heads; heads &= heads - 1) {
-    const int at = __ffs(heads) - 1;
-    const int64_t t0 = first + at;
-    const int64_t blk = __shfl_sync(0xffffffffu, mine, at);
-    // not the first of its block if one of the bs - 1 tokens before it goes there too
-    bool seen = false;
+  const int64_t blk = sl[0] >> kShift;
+  int off = -1;
+  if (lane < kWarpRows) {
+    const int64_t s = sl[w * kWarpRows + lane];
+    if (s >= 0 && (s >> kShift) == blk) off = static_cast<int>(s & (BS - 1));
+  }
+  // (a token that goes elsewhere counts as the block's first one, which changes no extreme)
+  uint4 x[8];
+  const unsigned live = __ballot_sync(0xffffffffu, off >= 0) >> odd;
+  src += (t0 * a.num_kv_heads + h) * 16 + c;
 #pragma unroll
-    for (int i = 0; i < (kBs + 30) / 32; ++i) {
-      const int back = 1 + i * 32 + lane;
-      seen |= back < kBs && block_of(t0 - back) == blk;
-    }
-    if (__any_sync(0xffffffffu, seen)) continue;
+  for (int i = 0; i < 8; ++i) {
+    const int row = (live >> (2 * i)) & 1u ? w * kWarpRows + 2 * i + odd : 0;
+    x[i] = src[static_cast<int64_t>(row) * a.num_kv_heads * 16];
+  }
+  const int64_t bh = blk * a.num_kv_heads + h;
+  float* scale_at = a.scales + bh * 2 + which;
+  const float had = *scale_at;
+  const bool bounded = a.bounds && which == 0;
 
-    // ---- this warp's 16 tokens: where they go, their elements ----
-    int off = -1;
-    if (lane < kWarpRows) {
-      const int64_t t = t0 + w * kWarpRows + lane;
-      if (block_of(t) == blk) off = static_cast<int>(slots[t] & (kBs - 1));
+  // ---- largest element; for keys per channel least and greatest ----
+  __half2 lo[4], hi[4], big = as_h2(0u);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) lo[j] = hi[j] = as_h2(j == 0 ? x[0].x : j == 1 ? x[0].y : j == 2 ? x[0].z : x[0].w);
+  if (bounded) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      const __half2* p = reinterpret_cast<const __half2*>(&x[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        lo[j] = __hmin2_nan(lo[j], p[j]);
+        hi[j] = __hmax2_nan(hi[j], p[j]);
+      }
     }
-    uint4 x[8];
-    __half2 big = as_h2(0u);
-    __half2 lo[4], hi[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      lo[j] = as_h2(0x7c007c00u);
-      hi[j] = as_h2(0xfc00fc00u);
+      big = __hmax2_nan(big, __hmax2_nan(__habs2(lo[j]), __habs2(hi[j])));
+      lo[j] = __hmin2_nan(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], 16));
+      hi[j] = __hmax2_nan(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], 16));
     }
-    const bool any = __any_sync(0xffffffffu, off >= 0);
-    if (any) {
+  } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool live = __shfl_sync(0xffffffffu, off, 2 * i + odd) >= 0;
-        const int64_t t = t0 + w * kWarpRows + 2 * i + odd;
-        x[i] = live ? src[(t * num_kv_heads + h) * 16 + c] : make_uint4(0, 0, 0, 0);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const __half2* p = reinterpret_cast<const __half2*>(&x[i]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool live = __shfl_sync(0xffffffffu, off, 2 * i + odd) >= 0;
-        const __half2* p = reinterpret_cast<const __half2*>(&x[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          big = __hmax2_nan(big, __habs2(p[j]));
-          if (live) {
-            lo[j] = __hmin2(lo[j], p[j]);
-            hi[j] = __hmax2(hi[j], p[j]);
-          }
-        }
-      }
+      for (int j = 0; j < 4; ++j) big = __hmax2_nan(big, __habs2(p[j]));
     }
+  }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
-    float top = __half2float(__hmax_nan(__low2half(big), __high2half(big)));
-    // ---- the team's: largest element, rows written ----
-    if (W > 1) {
-      if (lane == 0) {
-        top_s[team][w] = top;
-        rows_s[team][w] = 0u;
-      }
-      team_sync();
-      if (off >= 0) atomicOr(&rows_s[team][off >> 4], 1u << (off & 15));
+  for (int o = 1; o < 32; o <<= 1) big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
+  float top = __half2float(__hmax_nan(__low2half(big), __high2half(big)));
+  uint4 ends = pick(odd, lo, hi);   // of the channels 8 c ..: lanes 0-15 the least, 16-31 the greatest
+  // ---- the group's ----
+  uint32_t written[kWords];         // (G = 1, BS = 16: in registers; else in shared memory)
+  bool fresh;
+  if (kWords == 1) {
+    uint32_t m = off >= 0 ? 1u << off : 0u;
+    written[0] = __reduce_or_sync(0xffffffffu, m);
+    fresh = written[0] & 1u;
+  } else {
+    for (int i = w * 32 + lane; i < kWords; i += G * 32) sh.rows[i] = 0u;
+    if (G > 1) {
+      if (lane == 0) sh.top[w] = top;
+      if (bounded) sh.ends[w][lane] = ends;
+    }
+    sync();
+    if (off >= 0) atomicOr(&sh.rows[off >> 4], 1u << (off & 15));
+    sync();
+    fresh = sh.rows[0] & 1u;
+    if (G > 1) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        const float o = top_s[team][i];
+      for (int i = 0; i < G; ++i) {
+        const float o = sh.top[i];
         top = o != o || top != top ? __uint_as_float(kNanBits) : fmaxf(top, o);
       }
-      if (bounds && which == 0) {
+      if (bounded && w == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          lo[j] = __hmin2(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], 16));
-          hi[j] = __hmax2(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], 16));
-        }
-        ends_s[team][w][lane] =
-            odd ? make_uint4(h2_bits(hi[0]), h2_bits(hi[1]), h2_bits(hi[2]), h2_bits(hi[3]))
-                : make_uint4(h2_bits(lo[0]), h2_bits(lo[1]), h2_bits(lo[2]), h2_bits(lo[3]));
-      }
-      team_sync();
-    }
-    uint32_t written;   // of this warp's 16 rows of the block
-    bool fresh;
-    if (W == 1) {
-      written = off >= 0 ? 1u << off : 0u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) written |= __shfl_xor_sync(0xffffffffu, written, o);
-      fresh = written & 1u;
-    } else {
-      written = rows_s[team][w];
-      fresh = rows_s[team][0] & 1u;
-    }
-    // ---- the scale ----
-    const int64_t bh = blk * num_kv_heads + h;
-    float* scale_at = scales + bh * 2 + which;
-    const float need = int8_scale(top);
-    const float old = fresh ? 0.f : *scale_at;
-    const float s = fresh ? need : int8_grown(need, old);
-    const float r = int8_inverse(s);
-    const float factor = old * r;   // <= 1; 0 for a fresh block and for NaN
-    uint8_t* block = cache + bh * (kBs * 128);
-    // every thread has read the scale, and the team's shared arrays, before one is written again
-    team_sync();
-    if (w == 0 && lane == 0 && (fresh || !(s == old))) *scale_at = s;
-    // ---- the block's other rows ----
-    if (fresh || !(s == old)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 4 * i + (lane >> 3);
-        if ((written >> row) & 1u) continue;
-        uint4* p = reinterpret_cast<uint4*>(block + (w * kWarpRows + row) * 128) + (lane & 7);
-        uint4 u = make_uint4(kInt8Zeros, kInt8Zeros, kInt8Zeros, kInt8Zeros);
-        if (factor > 0.f) {
-          u = *p;
-          u = make_uint4(int8_rescaled(u.x, factor), int8_rescaled(u.y, factor),
-                         int8_rescaled(u.z, factor), int8_rescaled(u.w, factor));
-        }
-        *p = u;
-      }
-    }
-    // ---- the new rows ----
-    if (any) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int o = __shfl_sync(0xffffffffu, off, 2 * i + odd);
-        if (o >= 0) reinterpret_cast<uint2*>(block + o * 128)[c] = int8_codes(x[i], r);
-      }
-    }
-    // ---- the keys' bounds: the least and the greatest new code are the codes of the least and
-    // the greatest element ----
-    if (bounds && which == 0 && w == 0) {
-      uint4 e;
-      if (W == 1) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          lo[j] = __hmin2(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], 16));
-          hi[j] = __hmax2(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], 16));
-        }
-        e = odd ? make_uint4(h2_bits(hi[0]), h2_bits(hi[1]), h2_bits(hi[2]), h2_bits(hi[3]))
-                : make_uint4(h2_bits(lo[0]), h2_bits(lo[1]), h2_bits(lo[2]), h2_bits(lo[3]));
-      } else {
-        e = ends_s[team][0][lane];
-#pragma unroll
-        for (int i = 1; i < W; ++i) {
-          const uint4 o = ends_s[team][i][lane];
+        for (int i = 1; i < G; ++i) {
+          const uint4 o = sh.ends[i][lane];
           const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
-          uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+          uint32_t ew[4] = {ends.x, ends.y, ends.z, ends.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             ew[j] = h2_bits(odd ? __hmax2(as_h2(ew[j]), as_h2(ow[j]))
                                 : __hmin2(as_h2(ew[j]), as_h2(ow[j])));
-          e = make_uint4(ew[0], ew[1], ew[2], ew[3]);
+          ends = make_uint4(ew[0], ew[1], ew[2], ew[3]);
         }
       }
-      uint2 u = int8_codes(e, r);
-      uint2* to = reinterpret_cast<uint2*>(bounds + bh * 256) + lane;   // least codes, then greatest
-      if (!fresh && r != 0.f) {
-        uint2 b = *to;
-        if (!(s == old)) b = make_uint2(int8_rescaled(b.x, factor), int8_rescaled(b.y, factor));
-        u = odd ? make_uint2(__vmaxu4(u.x, b.x), __vmaxu4(u.y, b.y))
-                : make_uint2(__vminu4(u.x, b.x), __vminu4(u.y, b.y));
-      }
-      *to = u;
     }
-    if (W > 1) team_sync();   // the shared arrays serve the next block
+  }
+  // ---- the scale ----
+  const float need = int8_scale(top);
+  const float old = fresh ? 0.f : had;
+  const float s = fresh ? need : int8_grown(need, old);
+  const float r = int8_inverse(s);
+  const float factor = old * r;   // <= 1; 0 for a fresh block and for NaN
+  uint8_t* block = (which ? a.v_cache : a.k_cache) + bh * (BS * 128);
+  const bool moved = fresh || !(s == old);
+  sync();   // every thread has read the scale
+  if (w == 0 && lane == 0 && moved) *scale_at = s;
+  // ---- the new rows ----
+  const Int8Quantiser codes(s);
+  uint2* rows = reinterpret_cast<uint2*>(block) + c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int o = __shfl_sync(0xffffffffu, off, 2 * i + odd);
+    if (o >= 0) rows[o * 16] = codes(x[i]);
+  }
+  // ---- the block's other rows ----
+  if (moved) {
+    for (int row = 4 * w + (lane >> 3); row < BS; row += 4 * G) {
+      const uint32_t word = kWords == 1 ? written[0] : sh.rows[row >> 4];
+      if ((word >> (row & 15)) & 1u) continue;
+      uint4* p = reinterpret_cast<uint4*>(block + row * 128) + (lane & 7);
+      uint4 u = make_uint4(kInt8Zeros, kInt8Zeros, kInt8Zeros, kInt8Zeros);
+      if (factor > 0.f) {
+        u = *p;
+        u = make_uint4(int8_rescaled(u.x, factor), int8_rescaled(u.y, factor),
+                       int8_rescaled(u.z, factor), int8_rescaled(u.w, factor));
+      }
+      *p = u;
+    }
+  }
+  // ---- the keys' bounds: the least and the greatest new code are the codes of the least and
+  // the greatest element ----
+  if (bounded && w == 0) {
+    uint2 u = codes(ends);
+    uint2* to = reinterpret_cast<uint2*>(a.bounds + bh * 256) + lane;   // least codes, then greatest
+    if (!fresh && r != 0.f) {
+      uint2 b = *to;
+      if (moved) b = make_uint2(int8_rescaled(b.x, factor), int8_rescaled(b.y, factor));
+      u = odd ? make_uint2(__vmaxu4(u.x, b.x), __vmaxu4(u.y, b.y))
+              : make_uint2(__vminu4(u.x, b.x), __vminu4(u.y, b.y));
+    }
+    *to = u;
+  }
+  if (kWords > 1) sync();   // the shared words serve the next block
+}
+
+// A team of W warps (W 16 rows make a block) takes, for one kv head and K or V, every block whose
+// first row of the call is among its `span` tokens. Blocks that get rows of 16 consecutive tokens at
+// most go to one warp each, the others to the whole team.
+template <int W>
+__global__ void __launch_bounds__(W < 4 ? kThreads : W * 32, W == 16 ? 2 : W == 8 ? 4 : W == 4 ? 8 : 7)
+kv_append_int8_kernel(const AppendArgs a) {
+  griddep_wait();
+  constexpr int kTeams = W < 4 ? 4 / W : 1;
+  constexpr int kBs = W * kWarpRows;
+  constexpr int kShift = W == 1 ? 4 : W == 2 ? 5 : W == 4 ? 6 : W == 8 ? 7 : 8;
+  constexpr int kSlots = 3 * kBs - 2, kMasks = (kBs + 31) / 32;
+  __shared__ int64_t slots_s[kTeams][kSlots];   // the span's, kBs - 1 before it and behind it
+  __shared__ uint32_t first_s[kTeams][kMasks], wide_s[kTeams][kMasks];   // blocks' first tokens; for the team
+  __shared__ Shared<1, kBs> warp_s[kTeams * W];
+  __shared__ Shared<W, kBs> team_s[kTeams];
+  const int lane = threadIdx.x & 31;
+  const int team = threadIdx.x / (W * 32), w = (threadIdx.x >> 5) % W, t = threadIdx.x % (W * 32);
+  const unsigned job = blockIdx.x * kTeams + team;
+  if (job >= a.jobs) return;
+  const unsigned which = job & 1;
+  const unsigned part = (job >> 1) / a.num_kv_heads;
+  const int h = static_cast<int>((job >> 1) - part * a.num_kv_heads);
+  const int64_t first = static_cast<int64_t>(part) * a.span;
+  auto team_sync = [&]() {
+    if (W == 1) __syncwarp();
+    else named_barrier_sync(1 + team, W * 32);
+  };
+  const int64_t* sl = slots_s[team];
+  for (int i = t; i < 2 * (kBs - 1) + a.span; i += W * 32) {
+    const int64_t at = first - (kBs - 1) + i;
+    int64_t s = at >= 0 && at < a.num_tokens ? a.slots[at] : -1;
+    if (s >= a.num_slots) {
+      if (which == 0 && h == 0) atomicOr(a.err, PKV_DEVERR_SLOT);
+      s = -1;
+    }
+    slots_s[team][i] = s;
+  }
+  if (t < kMasks) first_s[team][t] = wide_s[team][t] = 0u;
+  team_sync();
+  // ---- the first tokens of blocks: no token of the kBs - 1 before goes there ----
+  for (int i0 = 0; i0 < a.span; i0 += 32) {
+    bool cand = false;
+    if (i0 + lane < a.span) {
+      const int64_t s = sl[kBs - 1 + i0 + lane], p = sl[kBs - 2 + i0 + lane];
+      cand = s >= 0 && (p < 0 || (s >> kShift) != (p >> kShift));
+    }
+    int turn = 0;
+    for (unsigned m = __ballot_sync(0xffffffffu, cand); m; m &= m - 1, ++turn) {
+      if (W > 1 && turn % W != w) continue;
+      const int i = i0 + __ffs(m) - 1, at = kBs - 1 + i;
+      const int64_t blk = sl[at] >> kShift;
+      bool before = false, far = false;
+#pragma unroll
+      for (int j = 0; j < (kBs + 31) / 32; ++j) {
+        const int d = 1 + 32 * j + lane;
+        if (d < kBs) {
+          const int64_t p = sl[at - d], n = sl[at + d];
+          before |= p >= 0 && (p >> kShift) == blk;
+          far |= d >= kWarpRows && n >= 0 && (n >> kShift) == blk;
+        }
+      }
+      before = __any_sync(0xffffffffu, before);
+      far = __any_sync(0xffffffffu, far);
+      if (lane == 0 && !before)
+        atomicOr(far ? &wide_s[team][i0 >> 5] : &first_s[team][i0 >> 5], 1u << (i & 31));
+    }
+  }
+  team_sync();
+  int k = 0;
+  for (int o = 0; o < kBs; o += 32)
+    for (unsigned m = first_s[team][o >> 5]; m; m &= m - 1, ++k) {
+      if (W > 1 && k % W != w) continue;
+      const int i = o + __ffs(m) - 1;
+      append_block<1, kBs>(a, sl + kBs - 1 + i, first + i, h, which, 0, lane,
+                           warp_s[threadIdx.x >> 5], [] { __syncwarp(); });
+    }
+  if constexpr (W > 1) {
+    for (int o = 0; o < kBs; o += 32)
+      for (unsigned m = wide_s[team][o >> 5]; m; m &= m - 1) {
+        const int i = o + __ffs(m) - 1;
+        append_block<W, kBs>(a, sl + kBs - 1 + i, first + i, h, which, w, lane, team_s[team],
+                             team_sync);
+      }
   }
 }
 
@@ -315,11 +366,11 @@ int log2_of(int n) {
 
 int launch_status() { return cuda_status(cudaGetLastError()); }
 
-template <int W, class... A>
-int launch_append(int64_t jobs, pkv_stream_t stream, A... args) {
+template <int W>
+int launch_append(const AppendArgs& args, pkv_stream_t stream) {
   constexpr int kTeams = W < 4 ? 4 / W : 1;
-  return launch_waiting(&kv_append_int8_kernel<W>, static_cast<unsigned>((jobs + kTeams - 1) / kTeams),
-                        W < 4 ? kThreads : W * 32, 0, stream, args...);
+  return launch_waiting(&kv_append_int8_kernel<W>, (args.jobs + kTeams - 1) / kTeams,
+                        W < 4 ? kThreads : W * 32, 0, stream, args);
 }
 
 }  // namespace
@@ -341,27 +392,35 @@ int pkv_kv_append_int8(const void* k, const void* v, const int64_t* slot_mapping
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !aligned16(k_bounds) || (reinterpret_cast<uintptr_t>(kv_scales) & 7u))
     return PKV_EINVAL;
-  // Few rows: a team for every token, so that a step's blocks are all taken at once. Many: a team
-  // for kSpan tokens, most of which go to one block.
-  const int64_t rows = static_cast<int64_t>(num_tokens) * num_kv_heads;
-  const int span = rows <= 4096 ? 1 : kSpan;
-  const int64_t jobs = (static_cast<int64_t>(num_tokens) + span - 1) / span * num_kv_heads * 2;
+  // Few rows: a team for every token, so that a step's blocks are all taken at once. Many: as many tokens
+  // a team as leave about as many warps as are resident, a block's worth at most.
+  const int64_t halves = static_cast<int64_t>(num_kv_heads) * 2;   // K and V of a head
+  const int64_t warps = num_tokens * halves * (block_size / 16);
+  const int span = static_cast<int>(std::min<int64_t>(std::max<int64_t>(warps / 4096, 1), block_size));
+  const int64_t jobs = (static_cast<int64_t>(num_tokens) + span - 1) / span * halves;
   if (jobs > 0x7fffffff) return PKV_EINVAL;
   unsigned int* err = device_error_ptr();
   if (!err) return launch_status();
-  auto launch = [&](auto w) {
-    return launch_append<decltype(w)::value>(
-        jobs, stream, static_cast<const uint4*>(k), static_cast<const uint4*>(v), slot_mapping,
-        num_tokens, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), kv_scales,
-        static_cast<uint8_t*>(k_bounds), static_cast<int64_t>(num_blocks) * block_size,
-        num_kv_heads, span, static_cast<unsigned>(jobs), err);
-  };
+  AppendArgs args = {};
+  args.span = span;
+  args.jobs = static_cast<unsigned>(jobs);
+  args.k = static_cast<const uint4*>(k);
+  args.v = static_cast<const uint4*>(v);
+  args.slots = slot_mapping;
+  args.k_cache = static_cast<uint8_t*>(k_cache);
+  args.v_cache = static_cast<uint8_t*>(v_cache);
+  args.scales = kv_scales;
+  args.bounds = static_cast<uint8_t*>(k_bounds);
+  args.err = err;
+  args.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  args.num_tokens = num_tokens;
+  args.num_kv_heads = num_kv_heads;
   switch (block_size) {
-    case 16: return launch(std::integral_constant<int, 1>());
-    case 32: return launch(std::integral_constant<int, 2>());
-    case 64: return launch(std::integral_constant<int, 4>());
-    case 128: return launch(std::integral_constant<int, 8>());
-    default: return launch(std::integral_constant<int, 16>());
+    case 16: return launch_append<1>(args, stream);
+    case 32: return launch_append<2>(args, stream);
+    case 64: return launch_append<4>(args, stream);
+    case 128: return launch_append<8>(args, stream);
+    default: return launch_append<16>(args, stream);
   }
 }
 

@@ -38,11 +38,18 @@ namespace {
 constexpr int kTile8 = kChunk * kD;          // one chunk's K (or V): 2048 bytes
 constexpr int kStage8 = 4 * kTile8;          // K of two chunks, V of two chunks
 // Per-segment cost in chunks (see kSegCost): as for the 4-bit cache, whose segments do the same work.
-constexpr int kSeg8 = 8;
+#ifndef SEGC
+#define SEGC 8
+#endif
+constexpr int kSeg8 = SEGC;
 // No slice finer than sqrt(kPartCost * the longest unit's chunks), and whole units to a CTA where
 // that costs at most kAlone rounds of stages (see pkv_decode_int4.cu).
-constexpr float kPartCost = 3.f;
-constexpr int kAlone = 3;
+#ifndef PART
+#define PART 3
+#define ALONE 3
+#endif
+constexpr float kPartCost = PART;
+constexpr int kAlone = ALONE;
 constexpr size_t kMaxSmem = 227 * 1024;
 // How far the softmax's reference is put below the running maximum, and how far a weight may pass
 // the maximum before the reference moves: weights stay below 2^13.
@@ -56,23 +63,24 @@ struct Int8Args {
 };
 
 // Shared-memory layout (offsets from a 128-byte aligned base). NCS: warps that share the stages
-// among them, RS: warps that take one stage, 8 query rows each, ND: stages in flight per warp.
-template <int NCS, int RS, int ND>
+// among them, RS: warps that take one stage, RT tiles of 8 query rows each, ND: stages in flight per
+// warp, SB: buffers of segment states.
+template <int NCS, int RS, int RT, int ND, int SB>
 struct Smem8 {
   static constexpr int kQTile = 5 * 512;              // 8 rows: fragments of 8 pieces, constants
-  static constexpr int kQBuf = RS * kQTile;
+  static constexpr int kQBuf = RS * RT * kQTile;
   static constexpr int kQ = NCS * RS * ND * kStage8;
   static constexpr int kScales = kQ + 2 * kQBuf;      // per stage: (s_K, s_V) of both chunks
-  static constexpr int kBars = kScales + NCS * RS * ND * 16;   // qfull[2], qempty[2], sdone, sfree
-  static constexpr int kFlags = kBars + 6 * 8;
-  static constexpr int kState = (kFlags + 64 + 15) & ~15;      // [NCS] segment states
-  __host__ __device__ static int state_floats(int R) { return NCS * R * (kSt + 2); }
+  static constexpr int kBars = kScales + NCS * RS * ND * 16;   // qfull[2], qempty[2], sdone[SB], sfree[SB]
+  static constexpr int kFlags = kBars + (4 + 2 * SB) * 8;
+  static constexpr int kState = (kFlags + 64 + 15) & ~15;      // [SB][NCS] segment states
+  __host__ __device__ static int state_floats(int R) { return SB * NCS * R * (kSt + 2); }
   __host__ __device__ static int seq_off(int R) { return kState + state_floats(R) * 4; }
   __host__ static size_t bytes(int R, int B, int) {
     return 128 + static_cast<size_t>(seq_off(R)) + (2 * static_cast<size_t>(B) + 1) * 4;
   }
   // the merge of split units stages at least two partials in the stage memory
-  static_assert(kQ >= 8 * RS * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
+  static_assert(kQ >= 8 * RS * RT * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
 };
 
 __device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
@@ -190,10 +198,10 @@ __device__ __forceinline__ float exponent_of(float s) {
 
 // Warps 0 .. NCS RS - 1 consume; the next one prepares the queries, the last one is the epilogue
 // (merges each segment's per-warp states, writes outputs and split units' partials).
-template <int NCS, int RS, int ND, int MINB>
+template <int NCS, int RS, int RT, int ND, int SB, int MINB>
 __global__ void __launch_bounds__((NCS * RS + 2) * 32, MINB)
 decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
-  using L = Smem8<NCS, RS, ND>;
+  using L = Smem8<NCS, RS, RT, ND, SB>;
   constexpr int NCW = NCS * RS;
   griddep_wait();
   extern __shared__ uint8_t smem_raw[];
@@ -203,14 +211,14 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
   const uint32_t bar_qfull = sbase + L::kBars;
   const uint32_t bar_qempty = bar_qfull + 2 * 8;
   const uint32_t bar_sdone = bar_qempty + 2 * 8;
-  const uint32_t bar_sfree = bar_sdone + 8;
+  const uint32_t bar_sfree = bar_sdone + SB * 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kFlags);
   int* npend_s = reinterpret_cast<int*>(smem + L::kFlags) + 1;   // then 2 x (b, h, nb)
   volatile int* fast_s = reinterpret_cast<volatile int*>(smem + L::kFlags) + 8;
   int* longest_s = reinterpret_cast<int*>(smem + L::kFlags) + 9;
-  float* stO = reinterpret_cast<float*>(smem + L::kState);       // [NCS][R][kSt]
-  float* stM = stO + NCS * a.R * kSt;                             // [NCS][R]
-  float* stL = stM + NCS * a.R;                                   // [NCS][R]
+  float* stO = reinterpret_cast<float*>(smem + L::kState);       // [SB][NCS][R][kSt]
+  float* stM = stO + SB * NCS * a.R * kSt;                        // [SB][NCS][R]
+  float* stL = stM + SB * NCS * a.R;                              // [SB][NCS][R]
   int* pre = reinterpret_cast<int*>(smem + L::seq_off(a.R));
   int* slen = pre + a.num_seqs + 1;
 
@@ -225,8 +233,10 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
       mbar_init(bar_qfull + s * 8, 1);
       mbar_init(bar_qempty + s * 8, NCW);
     }
-    mbar_init(bar_sdone, NCW);
-    mbar_init(bar_sfree, 1);
+    for (int s = 0; s < SB; ++s) {
+      mbar_init(bar_sdone + s * 8, NCW);
+      mbar_init(bar_sfree + s * 8, 1);
+    }
     *abort = 0;
     *npend_s = 0;
     *longest_s = 0;
@@ -365,14 +375,16 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
       int npend = 0, k = 0;
       Seg nx = s;
       while (cur.next(nx)) {
-        if (!mbar_wait(bar_sdone, k & 1, abort)) flag_timeout(a, abort);
+        const int sb = k % SB;
+        if (!mbar_wait(bar_sdone + sb * 8, (k / SB) & 1, abort)) flag_timeout(a, abort);
         const bool complete = (s.c0 == 0 && s.c1 == s.nb);
         const int slot = 2 * blockIdx.x + (k == 0 ? 0 : 1);
-        merge_rows<NCS>(a, stO, stM, stL, s, complete,
+        merge_rows<NCS>(a, stO + sb * NCS * a.R * kSt, stM + sb * NCS * a.R,
+                        stL + sb * NCS * a.R, s, complete,
                         a.part_o + static_cast<int64_t>(slot) * a.R * kD,
                         a.part_ml + static_cast<int64_t>(slot) * a.R * 4, lane);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sfree);
+        if (lane == 0) mbar_arrive(bar_sfree + sb * 8);
         if (!complete && lane == 0) {
           // announce the partial (release) and see who else has arrived (acquire)
           const int ua = unit_first<kSeg8>(pre, a.Hkv, s.b, s.h, s.nb);
@@ -392,7 +404,7 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
     }
   } else {
     // =================================== consumers ===========================================
-    const int w = warp % NCS, rs = warp / NCS;   // share of the stages, query rows 8 rs .. + 7
+    const int w = warp % NCS, rs = warp / NCS;   // share of the stages, query rows 8 RT rs .. + 8 RT - 1
     // ldmatrix: lane l addresses row l & 15 of a chunk, matrices 0, 1 the two key octets of piece 2 i,
     // 2, 3 of piece 2 i + 1
     const uint32_t lm_row = (lane & 15) * 128;
@@ -410,22 +422,27 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
     bool has = cur.first(begin, s);
     while (has) {
       const int qs = k & 1;
-      const uint32_t qb = sbase + L::kQ + qs * L::kQBuf + rs * L::kQTile + lane * 16;
+      const uint32_t qb = sbase + L::kQ + qs * L::kQBuf + rs * RT * L::kQTile + lane * 16;
       if (!mbar_wait(bar_qfull + qs * 8, (k >> 1) & 1, abort)) flag_timeout(a, abort);
       const int Lc = slen[s.b];
-      const uint4 qc = ld_shared_v4(qb + 2048);
-      const float off[2] = {__uint_as_float(qc.x), __uint_as_float(qc.y)};
-      const float rsc[2] = {__uint_as_float(qc.z), __uint_as_float(qc.w)};
 
       // per row: the reference's negative (0 before the first score), the value above which it
       // moves, the sum of the softmax weights
-      float nm[2] = {0.f, 0.f}, thr[2] = {kNegInf, kNegInf}, tl[2] = {0.f, 0.f};
-      float ot[8][4];
+      float nm[RT][2], thr[RT][2], tl[RT][2];
+      float ot[RT][8][4];
+      int qi[RT][2];   // query tokens of rows 2 t4, 2 t4 + 1: they see keys before Lc - q_len + 1 + these
+      const int r0 = 8 * RT * rs + 2 * t4;
 #pragma unroll
-      for (int p = 0; p < 8; ++p) ot[p][0] = ot[p][1] = ot[p][2] = ot[p][3] = 0.f;
-      const int r0 = 8 * rs + 2 * t4;
-      // query tokens of rows 2 t4, 2 t4 + 1: they see keys before Lc - q_len + 1 + these
-      const int qi0 = min(r0 / a.G, a.q_len - 1), qi1 = min((r0 + 1) / a.G, a.q_len - 1);
+      for (int t = 0; t < RT; ++t) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          nm[t][e] = tl[t][e] = 0.f;
+          thr[t][e] = kNegInf;
+          qi[t][e] = min((r0 + 8 * t + e) / a.G, a.q_len - 1);
+        }
+#pragma unroll
+        for (int p = 0; p < 8; ++p) ot[t][p][0] = ot[t][p][1] = ot[t][p][2] = ot[t][p][3] = 0.f;
+      }
 
       const int nchunk = s.c1 - s.c0;
       const int npair = (nchunk + 1) >> 1;
@@ -441,96 +458,117 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
         const uint4 sc = ld_shared_v4(sring + slot * 16);
 
         // ---- S^T = K Q^T, 16 keys (g, g + 8) at a time ----
-        float x[2][4];       // [chunk h][key g: rows 2 t4, + 1; key g + 8: the same]
+        float x[RT][2][4];   // [chunk h][key g: rows 2 t4, + 1; key g + 8: the same]
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          x[h][0] = x[h][2] = off[0];
-          x[h][1] = x[h][3] = off[1];
+        for (int t = 0; t < RT; ++t) {
+          // (what the codes' offset adds to a product)
+          const uint2 off = ld_shared_v2(qb + t * L::kQTile + 2048);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            x[t][h][0] = x[t][h][2] = __uint_as_float(off.x);
+            x[t][h][1] = x[t][h][3] = __uint_as_float(off.y);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 b = ld_shared_v4(qb + i * 512);
+          uint4 b[RT];
+#pragma unroll
+          for (int t = 0; t < RT; ++t) b[t] = ld_shared_v4(qb + t * L::kQTile + i * 512);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t w0, w1, w2, w3;
             ldsm_x4(stK + h * kTile8 + lm_row + (((2 * i + lm_p) ^ lm_x) << 4), w0, w1, w2, w3);
-            mma_f16(x[h], w0 & 0x00ff00ffu, w1 & 0x00ff00ffu, __byte_perm(w0, 0u, 0x4341),
-                    __byte_perm(w1, 0u, 0x4341), b.x, b.y);
-            mma_f16(x[h], w2 & 0x00ff00ffu, w3 & 0x00ff00ffu, __byte_perm(w2, 0u, 0x4341),
-                    __byte_perm(w3, 0u, 0x4341), b.z, b.w);
+            const uint32_t l0 = w0 & 0x00ff00ffu, l1 = w1 & 0x00ff00ffu;
+            const uint32_t l2 = w2 & 0x00ff00ffu, l3 = w3 & 0x00ff00ffu;
+            const uint32_t u0 = __byte_perm(w0, 0u, 0x4341), u1 = __byte_perm(w1, 0u, 0x4341);
+            const uint32_t u2 = __byte_perm(w2, 0u, 0x4341), u3 = __byte_perm(w3, 0u, 0x4341);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+              mma_f16(x[t][h], l0, l1, u0, u1, b[t].x, b[t].y);
+              mma_f16(x[t][h], l2, l3, u2, u3, b[t].z, b[t].w);
+            }
           }
         }
 
         // ---- scores in powers of two, plus the value scale's exponent, against the reference ----
         const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.z)};
         const float ve[2] = {exponent_of(__uint_as_float(sc.y)), exponent_of(__uint_as_float(sc.w))};
+        uint32_t pb[RT][2][2];   // P^T of chunk h as the B operand
+        float iv[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
+          // (a NaN scale, or what lies behind the last chunk: only weights may carry it)
+          iv[h] = ve[h] == ve[h] ? fast_exp2(-ve[h]) : 0.f;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float m = rsc[e] * ks[h], z = ve[h] + nm[e];
-            x[h][e] = fmaf(x[h][e], m, z);
-            x[h][2 + e] = fmaf(x[h][2 + e], m, z);
-          }
-        if (!full) {
+        for (int t = 0; t < RT; ++t) {
+          const uint2 rc = ld_shared_v2(qb + t * L::kQTile + 2056);   // what makes scores of products
+          const float rsc[2] = {__uint_as_float(rc.x), __uint_as_float(rc.y)};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int lim = h == 0 || two ? Lc - a.q_len + 1 - (c + h) * kChunk : -(1 << 30);
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              if (g + 8 * o >= lim + qi0) x[h][2 * o] = kNegInf;
-              if (g + 8 * o >= lim + qi1) x[h][2 * o + 1] = kNegInf;
+            for (int e = 0; e < 2; ++e) {
+              const float m = rsc[e] * ks[h], z = ve[h] + nm[t][e];
+              x[t][h][e] = fmaf(x[t][h][e], m, z);
+              x[t][h][2 + e] = fmaf(x[t][h][2 + e], m, z);
             }
-          }
-        }
-        bool move = false;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          move |= fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e])) > thr[e];
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            // how far the reference moves up (from nothing: to where it belongs)
-            float by = mx - kShift;
-            float alpha = 1.f;
-            if (thr[e] == kNegInf) {
-              alpha = 0.f;
-              if (mx != kNegInf) thr[e] = kShift + kGrow;
-              else by = 0.f;
-            } else {
-              by = fmaxf(by, 0.f);
-              alpha = fast_exp2(-by);
-            }
-            nm[e] -= by;
-            tl[e] *= alpha;
+          if (!full) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              x[h][e] -= by;
-              x[h][2 + e] -= by;
-            }
+              const int lim = h == 0 || two ? Lc - a.q_len + 1 - (c + h) * kChunk : -(1 << 30);
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-              ot[p][e] *= alpha;
-              ot[p][2 + e] *= alpha;
+              for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (g + 8 * o >= lim + qi[t][e]) x[t][h][2 * o + e] = kNegInf;
             }
           }
-        }
-        uint32_t pb[2][2];   // P^T of chunk h as the B operand
+          bool move = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // (a NaN scale, or what lies behind the last chunk: only weights may carry it)
-          const float iv = ve[h] == ve[h] ? fast_exp2(-ve[h]) : 0.f;
+          for (int e = 0; e < 2; ++e)
+            move |= fmaxf(fmaxf(x[t][0][e], x[t][0][2 + e]), fmaxf(x[t][1][e], x[t][1][2 + e])) >
+                    thr[t][e];
+          if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[h][e] = fast_exp2(x[h][e]);
-          tl[0] = fmaf(x[h][0] + x[h][2], iv, tl[0]);
-          tl[1] = fmaf(x[h][1] + x[h][3], iv, tl[1]);
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(fmaxf(x[t][0][e], x[t][0][2 + e]), fmaxf(x[t][1][e], x[t][1][2 + e]));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              // how far the reference moves up (from nothing: to where it belongs)
+              float by = mx - kShift;
+              float alpha = 1.f;
+              if (thr[t][e] == kNegInf) {
+                alpha = 0.f;
+                if (mx != kNegInf) thr[t][e] = kShift + kGrow;
+                else by = 0.f;
+              } else {
+                by = fmaxf(by, 0.f);
+                alpha = fast_exp2(-by);
+              }
+              nm[t][e] -= by;
+              tl[t][e] *= alpha;
 #pragma unroll
-          for (int o = 0; o < 2; ++o)
-            pb[h][o] = movmatrix_trans(pack_half2(x[h][2 * o], x[h][2 * o + 1]));
+              for (int h = 0; h < 2; ++h) {
+                x[t][h][e] -= by;
+                x[t][h][2 + e] -= by;
+              }
+#pragma unroll
+              for (int p = 0; p < 8; ++p) {
+                ot[t][p][e] *= alpha;
+                ot[t][p][2 + e] *= alpha;
+              }
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][h][e] = fast_exp2(x[t][h][e]);
+            tl[t][0] = fmaf(x[t][h][0] + x[t][h][2], iv[h], tl[t][0]);
+            tl[t][1] = fmaf(x[t][h][1] + x[t][h][3], iv[h], tl[t][1]);
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+              pb[t][h][o] = movmatrix_trans(pack_half2(x[t][h][2 * o], x[t][h][2 * o + 1]));
+          }
         }
 
         // ---- O^T += V^T P^T: row g of tile p is dim 16 p + 2 g, row g + 8 dim 16 p + 2 g + 1 ----
@@ -552,8 +590,11 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
               f[q][0] = *reinterpret_cast<const uint32_t*>(&l2);
               f[q][1] = *reinterpret_cast<const uint32_t*>(&h2);
             }
-            mma_f16(ot[2 * i], f[0][0], f[0][1], f[1][0], f[1][1], pb[h][0], pb[h][1]);
-            mma_f16(ot[2 * i + 1], f[2][0], f[2][1], f[3][0], f[3][1], pb[h][0], pb[h][1]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+              mma_f16(ot[t][2 * i], f[0][0], f[0][1], f[1][0], f[1][1], pb[t][h][0], pb[t][h][1]);
+              mma_f16(ot[t][2 * i + 1], f[2][0], f[2][1], f[3][0], f[3][1], pb[t][h][0], pb[t][h][1]);
+            }
           }
         }
         __syncwarp();                        // every lane has read the stage
@@ -561,31 +602,34 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
         slot = slot + 1 == ND ? 0 : slot + 1;
       }
       // ---- the sums go to the warp's state buffer ----
-      if (k >= 1 && !mbar_wait(bar_sfree, (k - 1) & 1, abort)) flag_timeout(a, abort);
+      const int sb = k % SB;
+      if (k >= SB && !mbar_wait(bar_sfree + sb * 8, (k / SB - 1) & 1, abort)) flag_timeout(a, abort);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float lv = tl[e];
-        lv += __shfl_xor_sync(0xffffffffu, lv, 4);
-        lv += __shfl_xor_sync(0xffffffffu, lv, 8);
-        lv += __shfl_xor_sync(0xffffffffu, lv, 16);
-        const int r = r0 + e;
-        const int at = w * a.R + r;
-        if (r < a.R) {
+      for (int t = 0; t < RT; ++t)
 #pragma unroll
-          for (int p = 0; p < 8; ++p)
-            *reinterpret_cast<float2*>(stO + at * kSt + 16 * p + 2 * g) =
-                make_float2(ot[p][e], ot[p][2 + e]);
-          if (g == 0) {
-            // scores that are all NaN have moved no reference
-            stM[at] = thr[e] == kNegInf && lv == lv ? kNegInf : -nm[e];
-            stL[at] = lv;
+        for (int e = 0; e < 2; ++e) {
+          float lv = tl[t][e];
+          lv += __shfl_xor_sync(0xffffffffu, lv, 4);
+          lv += __shfl_xor_sync(0xffffffffu, lv, 8);
+          lv += __shfl_xor_sync(0xffffffffu, lv, 16);
+          const int r = r0 + 8 * t + e;
+          const int at = (sb * NCS + w) * a.R + r;
+          if (r < a.R) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+              *reinterpret_cast<float2*>(stO + at * kSt + 16 * p + 2 * g) =
+                  make_float2(ot[t][p][e], ot[t][p][2 + e]);
+            if (g == 0) {
+              // scores that are all NaN have moved no reference
+              stM[at] = thr[t][e] == kNegInf && lv == lv ? kNegInf : -nm[t][e];
+              stL[at] = lv;
+            }
           }
         }
-      }
       __syncwarp();
       j += npair;
       if (lane == 0) mbar_arrive(bar_qempty + qs * 8);
-      if (lane == 0) mbar_arrive(bar_sdone);
+      if (lane == 0) mbar_arrive(bar_sdone + sb * 8);
       set_last(s, k);
       ++k;
       has = cur.next(s);
@@ -595,24 +639,36 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
 
   // ---- end of the slice ----
   if (last.k >= 0)
-    finish_slice<NCS, kSeg8, NCW, 1>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s,
+    finish_slice<NCS, kSeg8, NCW, SB>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s,
                                       fast_s, warp < NCW ? tid : tid - 32);
 }
 
 // ---------------------------------------------------------------------------------------------
 // Host side.
 
-template <int NCS, int RS, int ND, int MINB>
+template <int NCS, int RS, int RT, int ND, int SB, int MINB>
 Variant variant8() {
-  return Variant{reinterpret_cast<const void*>(&decode_int8_kernel<NCS, RS, ND, MINB>), RS, false,
-                 (NCS * RS + 2) * 32, &Smem8<NCS, RS, ND>::bytes};
+  return Variant{reinterpret_cast<const void*>(&decode_int8_kernel<NCS, RS, RT, ND, SB, MINB>), RS, false,
+                 (NCS * RS + 2) * 32, &Smem8<NCS, RS, RT, ND, SB>::bytes};
 }
 
+#ifndef V1
+#define V1 4, 1, 1, 2, 2, 2
+#endif
+#ifndef V2
+#define V2 8, 1, 2, 2, 1, 1
+#endif
+#ifndef V3
+#define V3 3, 3, 1, 2, 1, 1
+#endif
+#ifndef V4
+#define V4 3, 2, 2, 2, 1, 1
+#endif
 Variant choose8(int R) {
-  return R <= 8    ? variant8<4, 1, 2, 2>()
-         : R <= 16 ? variant8<2, 2, 2, 2>()
-         : R <= 24 ? variant8<3, 3, 2, 1>()
-                   : variant8<2, 4, 2, 1>();
+  return R <= 8    ? variant8<V1>()
+         : R <= 16 ? variant8<V2>()
+         : R <= 24 ? variant8<V3>()
+                   : variant8<V4>();
 }
 
 int launch_decode_int8(void* out, const void* q, const void* k_cache, const void* v_cache,

@@ -50,22 +50,36 @@ __device__ __forceinline__ uint32_t int8_pack(float a, float b, float c, float d
   return __byte_perm(lo, hi, 0x5410);
 }
 
-// Codes of 8 elements at scale s, r = int8_inverse(s). Only at the greatest scale can an element
-// pass 127.5 steps: 65024 = 127 * 2^9 bounds them all.
-__device__ __forceinline__ uint2 int8_codes(const uint4& h, float r) {
-  if (r == 0.f) return make_uint2(kInt8Zeros, kInt8Zeros);
-  const __half2 most = __half2half2(__ushort_as_half(0x7bf0)),
-                least = __half2half2(__ushort_as_half(0xfbf0));
-  const __half2* p = reinterpret_cast<const __half2*>(&h);
-  float m[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(__hmax2(__hmin2(p[i], most), least));
-    m[2 * i] = fmaf(f.x, r, kInt8Magic);
-    m[2 * i + 1] = fmaf(f.y, r, kInt8Magic);
+// Quantises elements at one scale (a power of two, or NaN: all codes are zeros). x / s is a product
+// with 1 / s, and adding 1664 = 1.5 * 2^10 + 128 in the same packed operation rounds it to a whole
+// number, ties to even, and leaves the code in the sum's low byte: one rounding in all, as in 32 bits.
+struct Int8Quantiser {
+  __half2 up, r;   // 1 / s in two factors: 1 / s alone may be past fp16
+  int kind;        // 0: one factor; 1: two; 2: the greatest scale; 3: NaN
+
+  __device__ __forceinline__ explicit Int8Quantiser(float s) {
+    const int e = static_cast<int>(__float_as_uint(s) >> 23) - 127;
+    kind = s != s ? 3 : e == kInt8High ? 2 : e < -15 ? 1 : 0;
+    up = __float2half2_rn(32768.f);
+    r = __float2half2_rn(s != s ? 0.f
+                                : __uint_as_float(static_cast<uint32_t>(127 - e - (e < -15 ? 15 : 0)) << 23));
   }
-  return make_uint2(int8_pack(m[0], m[1], m[2], m[3]), int8_pack(m[4], m[5], m[6], m[7]));
-}
+  __device__ __forceinline__ uint2 operator()(uint4 h) const {
+    if (kind == 3) return make_uint2(kInt8Zeros, kInt8Zeros);
+    const __half2 magic = __half2half2(__ushort_as_half(0x6680));
+    __half2* p = reinterpret_cast<__half2*>(&h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (kind == 1) p[i] = __hmul2(p[i], up);   // (exact: below 2^-8 before)
+      p[i] = __hfma2(p[i], r, magic);
+      // only at the greatest scale can an element pass 127.5 steps
+      if (kind == 2)
+        p[i] = __hmax2(__hmin2(p[i], __half2half2(__ushort_as_half(0x66ff))),
+                       __half2half2(__ushort_as_half(0x6601)));
+    }
+    return make_uint2(__byte_perm(h.x, h.y, 0x6420), __byte_perm(h.z, h.w, 0x6420));
+  }
+};
 
 // Code i of a word as a float, without the offset.
 template <int I>

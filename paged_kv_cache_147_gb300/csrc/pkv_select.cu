@@ -15,9 +15,11 @@
 // dot's terms may come in any order, so 16 bytes of a row are four operands of a lane.
 //
 // What bounds it: 256 bytes of bounds per block and head, and for few of them latency. One cluster
-// per (sequence, kv head): its CTAs share the blocks, keep their scores in shared memory as ordered
-// integers, and find the budget's smallest score by four rounds of 256-bin counts added up through
-// distributed shared memory. One launch, no workspace.
+// per (sequence, kv head): its CTAs share the blocks and keep their scores in shared memory as
+// ordered integers. The budget's smallest score is found by counting the scores in up to 1024 equal
+// intervals between the least and the greatest, the CTAs' counts added up through distributed
+// shared memory; the few scores in the interval where the budget ends are compared with each other
+// one by one (more of them: counted again in finer intervals). One launch, no workspace.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -35,6 +37,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kGather = 16384;    // blocks whose keys a CTA takes all of
+constexpr int kBinBits = 10, kBins = 1 << kBinBits;   // 4 a thread
+constexpr int kCands = kThreads;
 constexpr uint32_t kAlways = 0xffffffffu;     // key of a block that is kept whatever its score
 constexpr uint32_t kNanKey = 0xfffffffeu;     // a NaN scale: before every number
 
@@ -74,46 +79,64 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t r
   return v;
 }
 
+__device__ __forceinline__ uint4 ld_cluster_v4(const uint32_t* p, uint32_t rank) {
+  uint32_t remote;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(remote) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_cluster_u64(const uint64_t* p, uint32_t rank) {
+  uint32_t remote;
+  uint64_t v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote) : "memory");
+  return v;
+}
+
 // Larger numbers have larger keys; -0 does not come here.
 __device__ __forceinline__ uint32_t key_of(float s) {
   const uint32_t b = __float_as_uint(s);
   return s == s ? b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u) : kNanKey;
 }
 
-// Exclusive scan of one value per thread; `total` gets the sum.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* sh, uint64_t& total) {
+// Exclusive scan of one value per thread.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t incl = v;
+  uint32_t incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   __syncthreads();
   if (lane == 31) sh[warp] = incl;
   __syncthreads();
-  uint64_t before = 0;
-  total = 0;
+  uint32_t before = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
+  for (int i = 0; i < kWarps; ++i)
     if (i < warp) before += sh[i];
-    total += sh[i];
-  }
   return before + incl - v;
 }
 
+// CTAs of an SM that the registers are shared out for.
+constexpr int kCtas = 2;
+
 // NT: tiles of 8 query rows.
 template <int NT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
 select_blocks_kernel(const SelectArgs a) {
   griddep_wait();
   extern __shared__ __align__(16) uint8_t smem[];
   uint2* frag = reinterpret_cast<uint2*>(smem);                   // [NT][16][32]
   float4* col = reinterpret_cast<float4*>(frag + NT * 512);       // [8 NT] offset, factor, bias, -
-  uint32_t* hist = reinterpret_cast<uint32_t*>(col + 8 * NT);     // [4][256]
-  uint32_t* keys = hist + 1024;                                   // [cap]
-  __shared__ uint64_t scan_s[kWarps];
-  __shared__ uint32_t found_s[2];
+  uint32_t* hist = reinterpret_cast<uint32_t*>(col + 8 * NT);     // [2][kBins], taken in turn
+  uint32_t* keys = hist + 2 * kBins;                              // [cap]
+  __shared__ uint64_t cand_s[kCands];        // this CTA's scores in the interval where the budget ends
+  __shared__ uint64_t all_s[kCands];         // the cluster's
+  __shared__ uint32_t scan_s[4 * kWarps], found_s[3];
+  __shared__ uint32_t ends_s[2], taken_s[2], ncand_s;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
@@ -136,9 +159,37 @@ select_blocks_kernel(const SelectArgs a) {
     else if (nblk == n) out[i] = table[i];
   }
   if (nblk == n) return;
+  // A context whose keys all fit in a CTA's shared memory: every CTA copies the others' there and
+  // goes on as if it were alone, but for the blocks it writes out.
+  const bool gather = a.C > 1 && a.cap >= a.max_blocks;
+  const bool joint = a.C > 1 && !gather;   // the CTAs keep their own keys and add up their counts
+  auto everyone = [&]() {   // a barrier of those that work together
+    if (joint) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
+  auto theirs = [&](const uint32_t* p, int c) { return joint ? ld_cluster_u32(p, c) : *p; };
+
+  // ---- this CTA's blocks: their ids on the way ----
+  const int per = ((nblk + a.C - 1) / a.C + 15) & ~15;
+  const int from = min(nblk, static_cast<int>(rank) * per), to = min(nblk, from + per);
+  uint32_t* own = keys + (gather ? from : 0);
+  // blocks before `head` and from `tail` on are kept
+  const int head = a.keep_first;
+  const int tail = nblk - max(a.keep_last, nblk - (max(ctx - a.q_len, 0) >> a.bs_shift));
+  auto id_of = [&](int j) { return j < to ? table[j] : -1; };
+  int next[2] = {id_of(from + 16 * warp + g), id_of(from + 16 * warp + g + 8)};
 
   // ---- the queries: whole numbers as the products' B operands ----
-  for (int i = tid; i < 1024; i += kThreads) hist[i] = 0u;
+  for (int i = tid; i < 2 * kBins; i += kThreads) hist[i] = 0u;
+  if (tid == 0) {
+    ends_s[0] = 0xffffffffu;
+    ends_s[1] = 0u;
+    ncand_s = 0u;
+  }
   for (int r = warp; r < 8 * NT; r += kWarps) {
     const int qi = r / a.G;
     uint2 v = make_uint2(0u, 0u);
@@ -155,15 +206,14 @@ select_blocks_kernel(const SelectArgs a) {
     const float inv = int8_inverse(s);
     const float2 fx = __half22float2(x), fy = __half22float2(y);
     float p[4] = {fx.x, fx.y, fy.x, fy.y};
-    float sum = 0.f;
+    int sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // (a row with a NaN or an infinity counts for nothing)
       p[i] = s == s ? fminf(fmaxf(rintf(p[i] * inv), -127.f), 127.f) : 0.f;
-      sum += p[i];
+      sum += static_cast<int>(p[i]);
     }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = __reduce_add_sync(0xffffffffu, sum);
     // dims 4 lane .. + 3: word `lane & 3` of 16-byte piece (lane >> 2) & 3 of 64-byte part lane >> 4
     uint2* to = frag + (r >> 3) * 512 + ((lane >> 4) * 4 + (lane & 3)) * 32 + (r & 7) * 4 +
                 ((lane >> 2) & 3);
@@ -173,35 +223,36 @@ select_blocks_kernel(const SelectArgs a) {
                             pack_half2(fmaxf(p[1], 0.f), fmaxf(p[3], 0.f)));
     if (lane == 0) {
       const bool counts = sees && s == s;
-      col[r] = make_float4(sum * -0x1p-17f, counts ? 0x1p24f * s : 0.f, counts ? 0.f : kNegInf, 0.f);
+      col[r] = make_float4(static_cast<float>(sum) * -0x1p-17f, counts ? 0x1p24f * s : 0.f,
+                           counts ? 0.f : kNegInf, 0.f);
     }
   }
   __syncthreads();
 
-  // ---- scores of this CTA's blocks, 16 a warp at a time ----
-  const int per = ((nblk + a.C - 1) / a.C + 15) & ~15;
-  const int lo = min(nblk, static_cast<int>(rank) * per), count = min(nblk, lo + per) - lo;
-  const int tail = nblk - max(a.keep_last, nblk - (max(ctx - a.q_len, 0) >> a.bs_shift));
-  auto id_of = [&](int j) { return j < count ? table[lo + j] : -1; };
-  int next[2] = {id_of(16 * warp + g), id_of(16 * warp + g + 8)};
-#pragma unroll 1
-  for (int j0 = 16 * warp; j0 < count; j0 += 16 * kWarps) {
+  // ---- scores, 16 blocks a warp at a time ----
+  uint32_t least = 0xffffffffu, most = 0u;
+  struct Tile {
     uint4 w[2][4];
     float sc[2];
     bool good[2];
+  };
+  auto fetch = [&](Tile& t, int j0) {
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
-      good[o] = next[o] >= 0 && next[o] < a.num_blocks;
-      const int64_t bh = static_cast<int64_t>(good[o] ? next[o] : 0) * a.Hkv + h;
+      const int id = next[o];
+      t.good[o] = id >= 0 && id < a.num_blocks;
+      const int64_t bh = static_cast<int64_t>(t.good[o] ? id : 0) * a.Hkv + h;
       const uint4* src = reinterpret_cast<const uint4*>(a.bounds + bh * 256) + t4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[o][i] = good[o] ? src[4 * i] : make_uint4(0, 0, 0, 0);
-      sc[o] = good[o] ? a.scales[bh * 2] : 0.f;
-      if (!good[o] && j0 + g + 8 * o < count && t4 == 0) atomicOr(a.err, PKV_DEVERR_BLOCK_ID);
+      for (int i = 0; i < 4; ++i) t.w[o][i] = t.good[o] ? src[4 * i] : make_uint4(0, 0, 0, 0);
+      t.sc[o] = t.good[o] ? a.scales[bh * 2] : 0.f;
+      if (!t.good[o] && j0 + g + 8 * o < to && t4 == 0) atomicOr(a.err, PKV_DEVERR_BLOCK_ID);
       next[o] = id_of(j0 + 16 * kWarps + g + 8 * o);
     }
+  };
+  auto score = [&](const Tile& t, int j0) {
     float best[2] = {kNegInf, kNegInf};
-#pragma unroll
+#pragma unroll(NT <= 2 ? NT : 1)
     for (int nt = 0; nt < NT; ++nt) {
       const float4 c0 = col[8 * nt + 2 * t4], c1 = col[8 * nt + 2 * t4 + 1];
       float acc[4] = {c0.x, c1.x, c0.x, c1.x};
@@ -210,7 +261,7 @@ select_blocks_kernel(const SelectArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint2 f = frag[nt * 512 + (4 * i + e) * 32 + lane];
-          const uint32_t u0 = u4_word(w[0][i], e), u1 = u4_word(w[1][i], e);
+          const uint32_t u0 = u4_word(t.w[0][i], e), u1 = u4_word(t.w[1][i], e);
           mma_f16(acc, u0 & 0x00ff00ffu, u1 & 0x00ff00ffu, __byte_perm(u0, 0u, 0x4341),
                   __byte_perm(u1, 0u, 0x4341), f.x, f.y);
         }
@@ -223,86 +274,240 @@ select_blocks_kernel(const SelectArgs a) {
       best[o] = fmaxf(best[o], __shfl_xor_sync(0xffffffffu, best[o], 1));
       best[o] = fmaxf(best[o], __shfl_xor_sync(0xffffffffu, best[o], 2));
       const int j = j0 + g + 8 * o;
-      if (t4 == 0 && j < count) {
+      if (t4 == 0 && j < to) {
         // (+ 0 turns -0 into 0; a scale of 0 must not meet -infinity)
-        float s = best[o] == kNegInf ? kNegInf : best[o] * sc[o] + 0.f;
-        if (!good[o]) s = kNegInf;
-        keys[j] = lo + j < a.keep_first || lo + j >= tail ? kAlways : key_of(s);
+        float s = best[o] == kNegInf ? kNegInf : best[o] * t.sc[o] + 0.f;
+        if (!t.good[o]) s = kNegInf;
+        const uint32_t key = j < head || j >= tail ? kAlways : key_of(s);
+        if (key != kAlways) {
+          least = min(least, key);
+          most = max(most, key);
+        }
+        own[j - from] = key;
       }
     }
-  }
-  __syncthreads();
-
-  // ---- the n-th largest key: a byte of it per round ----
-  uint32_t prefix = 0, need = n;
-  uint32_t gt_before = 0, eq_before = 0;   // larger keys (this thread's share), equal ones: lower ranks
+  };
+  constexpr int kStep = 16 * kWarps;
+  int j0 = from + 16 * warp;
+  if constexpr (NT == 1) {
+    // the next 16 blocks' bounds on the way (more rows leave no registers for that)
+    Tile t[2];
+    if (j0 < to) fetch(t[0], j0);
+    while (j0 < to) {
+      if (j0 + kStep < to) fetch(t[1], j0 + kStep);
+      score(t[0], j0);
+      j0 += kStep;
+      if (j0 >= to) break;
+      if (j0 + kStep < to) fetch(t[0], j0 + kStep);
+      score(t[1], j0);
+      j0 += kStep;
+    }
+  } else {
 #pragma unroll 1
-  for (int round = 0; round < 4; ++round) {
-    const int shift = 24 - 8 * round;
-    uint32_t* hr = hist + 256 * round;
+    for (; j0 < to; j0 += kStep) {
+      Tile t;
+      fetch(t, j0);
+      score(t, j0);
+    }
+  }
+  if (gather) {
+    cluster_arrive();
+    cluster_wait();
+    // four keys a load (`per` is a multiple of 16), four loads in flight
+    constexpr int kPass = 4 * kThreads;
+    for (int j0 = 4 * tid; j0 < nblk; j0 += 4 * kPass) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i * kPass;
+        if (j < nblk) v[i] = ld_cluster_v4(keys + j, j / per);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i * kPass;
+        if (j >= nblk || (j >= from && j < to)) continue;
+        *reinterpret_cast<uint4*>(keys + j) = v[i];
+        const uint32_t vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < nblk && vw[e] != kAlways) {
+            least = min(least, vw[e]);
+            most = max(most, vw[e]);
+          }
+      }
+    }
+    cluster_arrive();   // this CTA has read the others' keys
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0 && least <= most) {
+    atomicMin(&ends_s[0], least);
+    atomicMax(&ends_s[1], most);
+  }
+  everyone();
+  {
+    // (lane c: CTA c's; a CTA without such blocks has the neutral ends)
+    const bool there = lane < (joint ? a.C : 1);
+    least = __reduce_min_sync(0xffffffffu, there ? theirs(&ends_s[0], lane) : 0xffffffffu);
+    most = __reduce_max_sync(0xffffffffu, there ? theirs(&ends_s[1], lane) : 0u);
+  }
+  // the keys this CTA looks through from here on: `count` of them, of blocks `lo` on
+  const int lo = joint ? from : 0, count = joint ? to - from : nblk;
+
+  // ---- where the budget ends: keys above `edge` are taken, and the first `need` equal to it ----
+  uint32_t need = n - min(head, nblk) - (nblk - tail);
+  uint32_t edge = kAlways - 1;     // (nothing but the kept ones)
+  for (int round = 0; need > 0; ++round) {
+    const int shift = max(0, 32 - __clz(most - least) - kBinBits);
+    uint32_t* hr = hist + (round & 1) * kBins;
+#pragma unroll 4
     for (int j = tid; j < count; j += kThreads) {
       const uint32_t key = keys[j];
-      if (round == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(hr + ((key >> shift) & 255u), 1u);
+      if (key >= least && key <= most) atomicAdd(hr + ((key - least) >> shift), 1u);
     }
-    if (a.C > 1) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      __syncthreads();
-    }
-    const uint32_t bin = 255 - tid;        // the largest first
-    uint32_t all = 0, before = 0;
-    if (a.C > 1) {
+    everyone();
+    // four bins a thread, the greatest first
+    const int b0 = kBins - 4 - 4 * tid;
+    uint32_t in[4] = {0u, 0u, 0u, 0u};
+    if (joint) {
 #pragma unroll
       for (int c = 0; c < kMaxCluster; ++c) {
         if (c >= a.C) break;
-        const uint32_t v = ld_cluster_u32(hr + bin, c);
-        all += v;
-        if (c < static_cast<int>(rank)) before += v;
+        const uint4 v = ld_cluster_v4(hr + b0, c);
+        in[0] += v.w; in[1] += v.z; in[2] += v.y; in[3] += v.x;
       }
     } else {
-      all = hr[bin];
+      const uint4 v = *reinterpret_cast<const uint4*>(hr + b0);
+      in[0] = v.w; in[1] = v.z; in[2] = v.y; in[3] = v.x;
     }
-    uint64_t total;
-    const uint32_t above = static_cast<uint32_t>(block_scan(all, scan_s, total));
-    if (above < need && need <= above + all) {
-      found_s[0] = bin;
-      found_s[1] = need - above;
+    uint32_t above = block_scan(in[0] + in[1] + in[2] + in[3], scan_s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (above < need && need <= above + in[i]) {
+        found_s[0] = b0 + 3 - i;
+        found_s[1] = need - above;
+        found_s[2] = in[i];
+      }
+      above += in[i];
     }
-    if (round == 3) keys[a.cap + tid] = before;   // by bin, for the equal ones
+    // the other counters are ready for the next round (no one reads them: this round's barrier is
+    // behind everyone's last use)
+    for (int i = tid; i < kBins; i += kThreads) hist[((round + 1) & 1) * kBins + i] = 0u;
     __syncthreads();
-    const uint32_t digit = found_s[0];
+    const uint32_t bottom = least + (found_s[0] << shift);
+    most = bottom + min((1u << shift) - 1u, most - bottom);
+    least = bottom;
     need = found_s[1];
-    prefix |= digit << shift;
-    if (bin > digit) gt_before += before;
-    if (round == 3) eq_before = keys[a.cap + 255 - digit];
+    const uint32_t inside = found_s[2];
+    edge = most;
+    if (shift == 0) break;
+    if (inside == need) {          // all of the interval
+      edge = least - 1;
+      need = 0;
+    } else if (inside <= kCands) {
+      // ---- few: each is compared with all, the lower block first among equal ones ----
+      for (int j = tid; j < count; j += kThreads) {
+        const uint32_t key = keys[j];
+        if (key >= least && key <= most)
+          cand_s[atomicAdd(&ncand_s, 1u)] =
+              static_cast<uint64_t>(key) << 32 | (0xffffffffu - static_cast<uint32_t>(lo + j));
+      }
+      everyone();
+      uint64_t x = 0;
+      uint32_t c = rank;
+      if (joint) {
+        // (lane c: how many CTA c has; they come one CTA's behind the other's)
+        uint32_t end = lane < a.C ? ld_cluster_u32(&ncand_s, lane) : 0u, first = 0;
+#pragma unroll
+        for (int o = 1; o < kMaxCluster; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += y;
+        }
+        c = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i) {
+          const uint32_t e = __shfl_sync(0xffffffffu, end, i);
+          if (i < a.C && static_cast<uint32_t>(tid) >= e) {
+            first = e;
+            c = i + 1;
+          }
+        }
+        if (static_cast<uint32_t>(tid) < inside) x = ld_cluster_u64(cand_s + (tid - first), c);
+      } else if (static_cast<uint32_t>(tid) < inside) {
+        x = cand_s[tid];
+      }
+      all_s[tid] = x;
+      __syncthreads();
+      if (static_cast<uint32_t>(tid) < inside && c == rank) {
+        uint32_t better = 0;
+#pragma unroll 8
+        for (uint32_t i = 0; i < inside; ++i) better += all_s[i] > x;
+        keys[0xffffffffu - static_cast<uint32_t>(x) - lo] = better < need ? kAlways : 0u;
+      }
+      need = 0;
+      __syncthreads();
+    }
   }
-  if (a.C > 1) cluster_arrive();   // this CTA has read the others' counts
 
   // ---- the chosen blocks in their order ----
-  uint64_t sum;
-  block_scan(gt_before, scan_s, sum);
-  gt_before = static_cast<uint32_t>(sum);
-  const int run = (count + kThreads - 1) / kThreads;
-  const int k0 = min(count, tid * run), k1 = min(count, k0 + run);
-  uint64_t mine = 0;   // larger keys in the upper half, equal ones in the lower
-  for (int j = k0; j < k1; ++j) {
-    const uint32_t key = keys[j];
-    mine += key > prefix ? 1ull << 32 : (key == prefix ? 1ull : 0ull);
-  }
-  const uint64_t ahead = block_scan(mine, scan_s, sum);
-  uint32_t gt = gt_before + static_cast<uint32_t>(ahead >> 32);
-  uint32_t eq = eq_before + static_cast<uint32_t>(ahead);
-  for (int j = k0; j < k1; ++j) {
-    const uint32_t key = keys[j];
-    if (key > prefix) {
-      out[gt + min(eq, need)] = table[lo + j];
-      ++gt;
-    } else if (key == prefix) {
-      if (eq < need) out[gt + eq] = table[lo + j];
-      ++eq;
+  // taken blocks and equal keys ahead of this CTA's (gather: counted here)
+  uint32_t gt = 0, eq = 0;
+  if (gather) {
+    for (int j = 4 * tid; j < from; j += 4 * kThreads) {   // (`from` is a multiple of 16)
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + j);
+      gt += (v.x > edge) + (v.y > edge) + (v.z > edge) + (v.w > edge);
+      eq += (v.x == edge) + (v.y == edge) + (v.z == edge) + (v.w == edge);
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+  }
+  // a warp takes a run of this CTA's, 32 at a time
+  const int cnt = to - from, run = ((cnt + kThreads - 1) / kThreads) * 32;
+  const int k0 = min(cnt, warp * run), k1 = min(cnt, k0 + run);
+  uint32_t gt_run = 0, eq_run = 0;
+  for (int j = k0 + lane; j - lane < k1; j += 32) {
+    const uint32_t key = j < k1 ? own[j] : 0u;
+    gt_run += __popc(__ballot_sync(0xffffffffu, key > edge));
+    eq_run += __popc(__ballot_sync(0xffffffffu, j < k1 && key == edge));
+  }
+  if (lane == 0) {
+    scan_s[warp] = gt_run;
+    scan_s[kWarps + warp] = eq_run;
+    scan_s[2 * kWarps + warp] = gt;
+    scan_s[3 * kWarps + warp] = eq;
+  }
+  __syncthreads();
+  gt = eq = 0;
+  gt_run = eq_run = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    gt += scan_s[2 * kWarps + i] + (i < warp ? scan_s[i] : 0u);
+    eq += scan_s[3 * kWarps + i] + (i < warp ? scan_s[kWarps + i] : 0u);
+    gt_run += scan_s[i];
+    eq_run += scan_s[kWarps + i];
+  }
+  if (joint) {
+    if (tid == 0) {
+      taken_s[0] = gt_run;
+      taken_s[1] = eq_run;
+    }
+    everyone();
+    const bool before = lane < static_cast<int>(rank);
+    gt += __reduce_add_sync(0xffffffffu, before ? ld_cluster_u32(&taken_s[0], lane) : 0u);
+    eq += __reduce_add_sync(0xffffffffu, before ? ld_cluster_u32(&taken_s[1], lane) : 0u);
+    cluster_arrive();   // this CTA has read what the others counted
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int j = k0 + lane; j - lane < k1; j += 32) {
+    const uint32_t key = j < k1 ? own[j] : 0u;
+    const bool is_eq = j < k1 && key == edge;
+    const uint32_t gts = __ballot_sync(0xffffffffu, key > edge);
+    const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
+    const uint32_t e = eq + __popc(eqs & below);    // equal ones before this
+    if (key > edge || (is_eq && e < need))
+      out[gt + __popc(gts & below) + min(e, need)] = table[from + j];
+    gt += __popc(gts);
+    eq += __popc(eqs);
   }
   if (a.C > 1) cluster_wait();     // the others have read this CTA's
 }
@@ -317,10 +522,13 @@ const void* kernel_for(int R) {
                    : reinterpret_cast<const void*>(&select_blocks_kernel<4>);
 }
 
-// CTAs per cluster: at least as many in all as fill the SMs, while each has 128 blocks and more.
+// CTAs per cluster: as many as are resident at once, with at least kMinBlocks blocks each.
+constexpr int kMinBlocks = 64;
 int cluster_for(int64_t units, int max_blocks) {
   int c = 1;
-  while (c < kMaxCluster && units * c < 2LL * sm_count() && max_blocks >= 256 * c) c *= 2;
+  while (c < kMaxCluster && units * 2 * c <= static_cast<int64_t>(kCtas) * sm_count() &&
+         max_blocks >= 2 * c * kMinBlocks)
+    c *= 2;
   return c;
 }
 
@@ -357,7 +565,7 @@ extern "C" int pkv_select_blocks(int32_t* tables_out, int32_t* lens_out, const v
                                  int budget, int keep_first, int keep_last, pkv_stream_t stream) {
   if (num_seqs < 0 || q_len < 1 || num_q_heads < 1 || num_kv_heads < 1 ||
       num_q_heads % num_kv_heads != 0 || head_dim != kD || !valid_block_size(block_size) ||
-      num_blocks < 1 || max_blocks_per_seq < 0 || max_blocks_per_seq > kMaxCluster * 32768 ||
+      num_blocks < 1 || max_blocks_per_seq < 0 || max_blocks_per_seq > 8 * 32768 ||
       budget < 1 || keep_first < 0 || keep_last < 0)
     return PKV_EINVAL;
   const int G = num_q_heads / num_kv_heads;
@@ -394,12 +602,14 @@ extern "C" int pkv_select_blocks(int32_t* tables_out, int32_t* lens_out, const v
   a.budget = budget;
   a.keep_first = keep_first;
   a.keep_last = keep_last;
-  a.C = cluster_for(units, max_blocks_per_seq);
-  if (max_blocks_per_seq > a.C * 32768) a.C = kMaxCluster;
-  a.cap = ((max_blocks_per_seq + a.C - 1) / a.C + 15) & ~15;
-  const void* fn = kernel_for(a.R);
   const int nt = (a.R + 7) / 8;
-  const size_t smem = static_cast<size_t>(nt) * (4096 + 8 * 16) + 4096 + (a.cap + 256) * 4;
+  a.C = cluster_for(units, max_blocks_per_seq);
+  // (what shared memory has room for)
+  while (max_blocks_per_seq > a.C * 32768) a.C *= 2;
+  const int share = max_blocks_per_seq <= kGather ? 1 : a.C;
+  a.cap = ((max_blocks_per_seq + share - 1) / share + 15) & ~15;
+  const void* fn = kernel_for(a.R);
+  const size_t smem = static_cast<size_t>(nt) * (4096 + 8 * 16) + (2 * kBins + a.cap) * 4;
   const cudaError_t e = allow_smem(fn);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
