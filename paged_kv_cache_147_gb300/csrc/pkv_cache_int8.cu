@@ -44,22 +44,26 @@ struct Shared {
   uint4 ends[G][32];               // per channel least and greatest new element
 };
 
+// Where a token's row goes: its block (-1: nowhere) and its place there.
+struct Slot {
+  int blk, off;
+};
+
 // The rows of one call that go to one block (slots sl[0 ..], the block's first one first, all within
 // BS tokens from t0 on; G = 1: within 16), for kv head h and K or V, by G warps: warp w has 16 tokens'
 // rows in its registers between the pass that finds the scale and the one that writes codes.
 template <int G, int BS, class Sync>
-__device__ __forceinline__ void append_block(const AppendArgs& a, const int64_t* sl, int64_t t0,
-                                             int h, int which, int w, int lane, Shared<G, BS>& sh,
+__device__ __forceinline__ void append_block(const AppendArgs& a, const Slot* sl, int64_t t0, int h,
+                                             int which, int w, int lane, Shared<G, BS>& sh,
                                              Sync sync) {
-  constexpr int kShift = BS == 16 ? 4 : BS == 32 ? 5 : BS == 64 ? 6 : BS == 128 ? 7 : 8;
   constexpr int kWords = BS / kWarpRows;
   const uint4* src = which ? a.v : a.k;
   const int c = lane & 15, odd = lane >> 4;
-  const int64_t blk = sl[0] >> kShift;
+  const int blk = sl[0].blk;
   int off = -1;
   if (lane < kWarpRows) {
-    const int64_t s = sl[w * kWarpRows + lane];
-    if (s >= 0 && (s >> kShift) == blk) off = static_cast<int>(s & (BS - 1));
+    const Slot s = sl[w * kWarpRows + lane];
+    if (s.blk == blk) off = s.off;
   }
   // (a token that goes elsewhere counts as the block's first one, which changes no extreme)
   uint4 x[8];
@@ -70,7 +74,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const int64_t*
     const int row = (live >> (2 * i)) & 1u ? w * kWarpRows + 2 * i + odd : 0;
     x[i] = src[static_cast<int64_t>(row) * a.num_kv_heads * 16];
   }
-  const int64_t bh = blk * a.num_kv_heads + h;
+  const int64_t bh = static_cast<int64_t>(blk) * a.num_kv_heads + h;
   float* scale_at = a.scales + bh * 2 + which;
   const float had = *scale_at;
   const bool bounded = a.bounds && which == 0;
@@ -149,43 +153,64 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, const int64_t*
   const float need = int8_scale(top);
   const float old = fresh ? 0.f : had;
   const float s = fresh ? need : int8_grown(need, old);
-  const float r = int8_inverse(s);
-  const float factor = old * r;   // <= 1; 0 for a fresh block and for NaN
+  const Int8Mover move(old * int8_inverse(s));   // nothing stays in a fresh block, or of a NaN
   uint8_t* block = (which ? a.v_cache : a.k_cache) + bh * (BS * 128);
   const bool moved = fresh || !(s == old);
   sync();   // every thread has read the scale
   if (w == 0 && lane == 0 && moved) *scale_at = s;
   // ---- the new rows ----
-  const Int8Quantiser codes(s);
+  const Int8Quantiser quant(s);
   uint2* rows = reinterpret_cast<uint2*>(block) + c;
+  if (quant.kind == 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int o = __shfl_sync(0xffffffffu, off, 2 * i + odd);
-    if (o >= 0) rows[o * 16] = codes(x[i]);
+    for (int i = 0; i < 8; ++i) {
+      const int o = __shfl_sync(0xffffffffu, off, 2 * i + odd);
+      if (o >= 0) rows[o * 16] = quant.codes<true>(x[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int o = __shfl_sync(0xffffffffu, off, 2 * i + odd);
+      if (o >= 0) rows[o * 16] = quant.codes(x[i]);
+    }
   }
   // ---- the block's other rows ----
-  if (moved) {
-    for (int row = 4 * w + (lane >> 3); row < BS; row += 4 * G) {
+  if (moved && !(kWords == 1 && written[0] == 0xffffu)) {
+    // 4 rows a warp, four times with the loads ahead of the first use
+    constexpr int kPass = 4 * G;
+    uint4* at = reinterpret_cast<uint4*>(block) + lane;   // (8 lanes a row)
+    auto mine = [&](int row) {
       const uint32_t word = kWords == 1 ? written[0] : sh.rows[row >> 4];
-      if ((word >> (row & 15)) & 1u) continue;
-      uint4* p = reinterpret_cast<uint4*>(block + row * 128) + (lane & 7);
-      uint4 u = make_uint4(kInt8Zeros, kInt8Zeros, kInt8Zeros, kInt8Zeros);
-      if (factor > 0.f) {
-        u = *p;
-        u = make_uint4(int8_rescaled(u.x, factor), int8_rescaled(u.y, factor),
-                       int8_rescaled(u.z, factor), int8_rescaled(u.w, factor));
+      return !((word >> (row & 15)) & 1u);
+    };
+    if (!move.none) {
+#pragma unroll 1
+      for (int r0 = 4 * w; r0 < BS; r0 += 4 * kPass) {
+        uint4 u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r0 + i * kPass < BS) u[i] = at[(r0 + i * kPass) * 8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = r0 + i * kPass;
+          if (row < BS && mine(row + (lane >> 3)))
+            at[row * 8] = move(u[i]);
+        }
       }
-      *p = u;
+    } else {
+      for (int row = 4 * w; row < BS; row += kPass)
+        if (mine(row + (lane >> 3)))
+          at[row * 8] = make_uint4(kInt8Zeros, kInt8Zeros, kInt8Zeros, kInt8Zeros);
     }
   }
   // ---- the keys' bounds: the least and the greatest new code are the codes of the least and
   // the greatest element ----
   if (bounded && w == 0) {
-    uint2 u = codes(ends);
+    uint2 u = quant.codes(ends);
     uint2* to = reinterpret_cast<uint2*>(a.bounds + bh * 256) + lane;   // least codes, then greatest
-    if (!fresh && r != 0.f) {
+    if (!fresh && s == s) {
       uint2 b = *to;
-      if (moved) b = make_uint2(int8_rescaled(b.x, factor), int8_rescaled(b.y, factor));
+      if (moved) b = make_uint2(move(b.x), move(b.y));
       u = odd ? make_uint2(__vmaxu4(u.x, b.x), __vmaxu4(u.y, b.y))
               : make_uint2(__vminu4(u.x, b.x), __vminu4(u.y, b.y));
     }
@@ -205,7 +230,7 @@ kv_append_int8_kernel(const AppendArgs a) {
   constexpr int kBs = W * kWarpRows;
   constexpr int kShift = W == 1 ? 4 : W == 2 ? 5 : W == 4 ? 6 : W == 8 ? 7 : 8;
   constexpr int kSlots = 3 * kBs - 2, kMasks = (kBs + 31) / 32;
-  __shared__ int64_t slots_s[kTeams][kSlots];   // the span's, kBs - 1 before it and behind it
+  __shared__ Slot slots_s[kTeams][kSlots];   // the span's, kBs - 1 before it and behind it
   __shared__ uint32_t first_s[kTeams][kMasks], wide_s[kTeams][kMasks];   // blocks' first tokens; for the team
   __shared__ Shared<1, kBs> warp_s[kTeams * W];
   __shared__ Shared<W, kBs> team_s[kTeams];
@@ -221,7 +246,12 @@ kv_append_int8_kernel(const AppendArgs a) {
     if (W == 1) __syncwarp();
     else named_barrier_sync(1 + team, W * 32);
   };
-  const int64_t* sl = slots_s[team];
+  const Slot* sl = slots_s[team];
+  // the span's rows start on their way while their slots are looked up (a row is two lines)
+  if (a.span > 1)
+    for (int i = t; i < 2 * a.span; i += W * 32)
+      if (first + (i >> 1) < a.num_tokens)
+        prefetch_l2((which ? a.v : a.k) + ((first + (i >> 1)) * a.num_kv_heads + h) * 16 + (i & 1) * 8);
   for (int i = t; i < 2 * (kBs - 1) + a.span; i += W * 32) {
     const int64_t at = first - (kBs - 1) + i;
     int64_t s = at >= 0 && at < a.num_tokens ? a.slots[at] : -1;
@@ -229,7 +259,8 @@ kv_append_int8_kernel(const AppendArgs a) {
       if (which == 0 && h == 0) atomicOr(a.err, PKV_DEVERR_SLOT);
       s = -1;
     }
-    slots_s[team][i] = s;
+    slots_s[team][i] = s < 0 ? Slot{-1, 0}
+                             : Slot{static_cast<int>(s >> kShift), static_cast<int>(s & (kBs - 1))};
   }
   if (t < kMasks) first_s[team][t] = wide_s[team][t] = 0u;
   team_sync();
@@ -237,22 +268,21 @@ kv_append_int8_kernel(const AppendArgs a) {
   for (int i0 = 0; i0 < a.span; i0 += 32) {
     bool cand = false;
     if (i0 + lane < a.span) {
-      const int64_t s = sl[kBs - 1 + i0 + lane], p = sl[kBs - 2 + i0 + lane];
-      cand = s >= 0 && (p < 0 || (s >> kShift) != (p >> kShift));
+      const int b = sl[kBs - 1 + i0 + lane].blk;
+      cand = b >= 0 && b != sl[kBs - 2 + i0 + lane].blk;
     }
     int turn = 0;
     for (unsigned m = __ballot_sync(0xffffffffu, cand); m; m &= m - 1, ++turn) {
       if (W > 1 && turn % W != w) continue;
       const int i = i0 + __ffs(m) - 1, at = kBs - 1 + i;
-      const int64_t blk = sl[at] >> kShift;
+      const int blk = sl[at].blk;
       bool before = false, far = false;
 #pragma unroll
       for (int j = 0; j < (kBs + 31) / 32; ++j) {
         const int d = 1 + 32 * j + lane;
         if (d < kBs) {
-          const int64_t p = sl[at - d], n = sl[at + d];
-          before |= p >= 0 && (p >> kShift) == blk;
-          far |= d >= kWarpRows && n >= 0 && (n >> kShift) == blk;
+          before |= sl[at - d].blk == blk;
+          far |= d >= kWarpRows && sl[at + d].blk == blk;
         }
       }
       before = __any_sync(0xffffffffu, before);

@@ -38,18 +38,11 @@ namespace {
 constexpr int kTile8 = kChunk * kD;          // one chunk's K (or V): 2048 bytes
 constexpr int kStage8 = 4 * kTile8;          // K of two chunks, V of two chunks
 // Per-segment cost in chunks (see kSegCost): as for the 4-bit cache, whose segments do the same work.
-#ifndef SEGC
-#define SEGC 8
-#endif
-constexpr int kSeg8 = SEGC;
+constexpr int kSeg8 = 8;
 // No slice finer than sqrt(kPartCost * the longest unit's chunks), and whole units to a CTA where
 // that costs at most kAlone rounds of stages (see pkv_decode_int4.cu).
-#ifndef PART
-#define PART 3
-#define ALONE 3
-#endif
-constexpr float kPartCost = PART;
-constexpr int kAlone = ALONE;
+constexpr float kPartCost = 3.f;
+constexpr int kAlone = 3;
 constexpr size_t kMaxSmem = 227 * 1024;
 // How far the softmax's reference is put below the running maximum, and how far a weight may pass
 // the maximum before the reference moves: weights stay below 2^13.
@@ -652,23 +645,25 @@ Variant variant8() {
                  (NCS * RS + 2) * 32, &Smem8<NCS, RS, RT, ND, SB>::bytes};
 }
 
-#ifndef V1
-#define V1 4, 1, 1, 2, 2, 2
-#endif
-#ifndef V2
-#define V2 8, 1, 2, 2, 1, 1
-#endif
-#ifndef V3
-#define V3 3, 3, 1, 2, 1, 1
-#endif
-#ifndef V4
-#define V4 3, 2, 2, 2, 1, 1
-#endif
-Variant choose8(int R) {
-  return R <= 8    ? variant8<V1>()
-         : R <= 16 ? variant8<V2>()
-         : R <= 24 ? variant8<V3>()
-                   : variant8<V4>();
+// The variant for R query rows. `few`: no more units than SMs. `wide`: tables for 4096 tokens and more
+// (the lengths are on the GPU; a table per head is as wide as its contexts are long, so it counts).
+// Measured against each other, us (a: 64 sequences of 16 to 2048 tokens, 2 kv heads; b: 16 of 4096, 8
+// kv heads; c: one of 65536; d: 32 of 50 to 8000; e: 512 of 20 to 200):
+//   to 8   <4, 1, 1, 2, 2, 2> a 13.5, b 25.1, c 34.5, d 52.6, e 42.0, 16 of 1024 in a table as long 13.1
+//          <8, 1, 1, 2, 1, 1>   15.9    22.6    28.1    55.6    79.5                                10.3
+//   to 16  <4, 1, 2, 2, 1, 2> a 17.7, b 33.5, c 49.4, d 60.0, e 72.9
+//          <8, 1, 2, 2, 1, 1>   21.2    32.1    37.0    72.2   137.8
+//   to 24  <3, 3, 1, 2, 1, 1> a 23.4, b 55.8, c 59.9, d 104
+//          <6, 1, 3, 2, 1, 1>   27.2    46.6    51.6     91
+//   to 32  <3, 2, 2, 2, 1, 1> a 27.0, b 61.2, c 68.9, d 115, e 145
+//          <4, 2, 2, 2, 1, 1>   29.9    54.8    59.8    112    172
+// Many warps in one CTA keep more in flight than two CTAs of four, but hand a segment over only once
+// per SM and merge more states for it; a warp with several row tiles widens the codes once for all.
+Variant choose8(int R, bool few, bool wide) {
+  return R <= 8    ? (few && wide ? variant8<8, 1, 1, 2, 1, 1>() : variant8<4, 1, 1, 2, 2, 2>())
+         : R <= 16 ? (few && wide ? variant8<8, 1, 2, 2, 1, 1>() : variant8<4, 1, 2, 2, 1, 2>())
+         : R <= 24 ? (wide ? variant8<6, 1, 3, 2, 1, 1>() : variant8<3, 3, 1, 2, 1, 1>())
+                   : (wide ? variant8<4, 2, 2, 2, 1, 1>() : variant8<3, 2, 2, 2, 1, 1>());
 }
 
 int launch_decode_int8(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -702,8 +697,12 @@ int launch_decode_int8(void* out, const void* q, const void* k_cache, const void
   const WsLayout ws = ws_layout(num_seqs, Hkv, R, workspace_bytes);
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
-  const Variant v = choose8(R);
-  const size_t smem = v.smem(R, num_seqs, 0);
+  Variant v = choose8(R, num_seqs * Hkv <= sm_count(), head_tables || max_ctx >= 4096);
+  size_t smem = v.smem(R, num_seqs, 0);
+  if (smem > kMaxSmem) {   // thousands of sequences with 17 and more rows each
+    v = variant8<3, 2, 2, 2, 1, 1>();
+    smem = v.smem(R, num_seqs, 0);
+  }
   if (smem > kMaxSmem) return PKV_EINVAL;
   int status = PKV_OK;
   const int grid = grid_size(v, smem, &status);

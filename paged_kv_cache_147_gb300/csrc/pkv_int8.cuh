@@ -22,9 +22,6 @@ namespace pkv {
 constexpr int kInt8Low = -30, kInt8High = 9;   // exponents of a scale
 constexpr uint32_t kInt8Zeros = 0x80808080u;   // four codes of zero
 constexpr uint32_t kNanBits = 0x7fffffffu;
-// 1.5 * 2^23 + 128: added to a number of at most 127 (in size) it leaves the code, ties to even, in
-// the sum's lowest byte.
-constexpr float kInt8Magic = 12582912.f + 128.f;
 
 // The least scale s with top <= 127 s (2^9 at most); NaN for a top that is NaN or infinite.
 __device__ __forceinline__ float int8_scale(float top) {
@@ -44,12 +41,6 @@ __device__ __forceinline__ float int8_grown(float need, float old) {
   return old != old ? old : (need != need ? need : fmaxf(need, old));
 }
 
-__device__ __forceinline__ uint32_t int8_pack(float a, float b, float c, float d) {
-  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
-  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
-  return __byte_perm(lo, hi, 0x5410);
-}
-
 // Quantises elements at one scale (a power of two, or NaN: all codes are zeros). x / s is a product
 // with 1 / s, and adding 1664 = 1.5 * 2^10 + 128 in the same packed operation rounds it to a whole
 // number, ties to even, and leaves the code in the sum's low byte: one rounding in all, as in 32 bits.
@@ -64,16 +55,18 @@ struct Int8Quantiser {
     r = __float2half2_rn(s != s ? 0.f
                                 : __uint_as_float(static_cast<uint32_t>(127 - e - (e < -15 ? 15 : 0)) << 23));
   }
-  __device__ __forceinline__ uint2 operator()(uint4 h) const {
-    if (kind == 3) return make_uint2(kInt8Zeros, kInt8Zeros);
+  // (PLAIN: for kind 0 only)
+  template <bool PLAIN = false>
+  __device__ __forceinline__ uint2 codes(uint4 h) const {
+    if (!PLAIN && kind == 3) return make_uint2(kInt8Zeros, kInt8Zeros);
     const __half2 magic = __half2half2(__ushort_as_half(0x6680));
     __half2* p = reinterpret_cast<__half2*>(&h);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (kind == 1) p[i] = __hmul2(p[i], up);   // (exact: below 2^-8 before)
+      if (!PLAIN && kind == 1) p[i] = __hmul2(p[i], up);   // (exact: below 2^-8 before)
       p[i] = __hfma2(p[i], r, magic);
       // only at the greatest scale can an element pass 127.5 steps
-      if (kind == 2)
+      if (!PLAIN && kind == 2)
         p[i] = __hmax2(__hmin2(p[i], __half2half2(__ushort_as_half(0x66ff))),
                        __half2half2(__ushort_as_half(0x6601)));
     }
@@ -87,10 +80,30 @@ __device__ __forceinline__ float int8_value(uint32_t w) {
   return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | I)) - (8388608.f + 128.f);
 }
 
-// Four codes on a grid 1 / f times as coarse (f <= 1, a power of two or 0).
-__device__ __forceinline__ uint32_t int8_rescaled(uint32_t w, float f) {
-  return int8_pack(fmaf(int8_value<0>(w), f, kInt8Magic), fmaf(int8_value<1>(w), f, kInt8Magic),
-                   fmaf(int8_value<2>(w), f, kInt8Magic), fmaf(int8_value<3>(w), f, kInt8Magic));
-}
+// Codes on a grid 1 / f times as coarse (f <= 1, a power of two or 0). 1024 + u is an fp16 number with
+// u as its lowest bits, and (1024 + u) f + (1664 - 1152 f) = 1664 + (u - 128) f, rounded once, leaves
+// the new code in its low byte; the constant is a whole number down to f = 2^-7, below which nothing
+// is left of a code.
+struct Int8Mover {
+  __half2 f, c;
+  bool none;
+
+  __device__ __forceinline__ explicit Int8Mover(float factor) : none(!(factor >= 0x1p-7f)) {
+    f = __float2half2_rn(none ? 0.f : factor);
+    c = __float2half2_rn(1664.f - (none ? 0.f : 1152.f * factor));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t w) const {
+    if (none) return kInt8Zeros;
+    uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 l2 = __hfma2(*reinterpret_cast<const __half2*>(&lo), f, c);
+    const __half2 h2 = __hfma2(*reinterpret_cast<const __half2*>(&hi), f, c);
+    lo = *reinterpret_cast<const uint32_t*>(&l2);
+    hi = *reinterpret_cast<const uint32_t*>(&h2);
+    return __byte_perm(lo, hi, 0x6420);
+  }
+  __device__ __forceinline__ uint4 operator()(const uint4& w) const {
+    return make_uint4((*this)(w.x), (*this)(w.y), (*this)(w.z), (*this)(w.w));
+  }
+};
 
 }  // namespace pkv

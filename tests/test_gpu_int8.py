@@ -262,6 +262,36 @@ def test_decode_of_long_and_of_many_contexts(lens, hq, hkv, q_len, bs):
     assert torch.equal(first, _decode(k, v, scales, tables, lens, q, SCALE))
 
 
+@pytest.mark.parametrize("hq,hkv,q_len", [(8, 1, 1), (8, 1, 2), (8, 1, 3), (8, 1, 4)])
+@pytest.mark.parametrize("width", [256, 8])
+def test_decode_of_every_row_count_in_wide_and_narrow_tables(hq, hkv, q_len, width):
+    # 8, 16, 24 and 32 rows; few long units, whole and split, against many short ones
+    for lens in ([4090, 700], [3000], [100] * 160 + [0, 1, 17]):
+        rng = np.random.default_rng(hq * q_len + len(lens))
+        if max(lens) > 16 * width:
+            continue
+        lens, tables, nb, _ = _tables(rng, lens, 16, width=width)
+        k, v, scales, _ = _cache(rng, nb, hkv, 16)
+        q = rng.standard_normal((len(lens), q_len, hq, 128)).astype(np.float16)
+        want, tol = int8.attention(q, k, v, scales, tables, lens, SCALE)
+        _close(_decode(k, v, scales, tables, lens, q, SCALE), want, tol)
+
+
+@pytest.mark.parametrize("q_len", [1, 3, 8, 12, 16, 24, 32])
+def test_decode_of_as_many_sequences_as_it_takes(q_len):
+    # shared blocks: each sequence reads its own part of a small pool
+    rng = np.random.default_rng(q_len)
+    B, nb = 4096, 40
+    k, v, scales, _ = _cache(rng, nb, 1, 16)
+    lens = rng.integers(0, 40, B).astype(np.int32)
+    tables = rng.integers(0, nb, (B, 256)).astype(np.int32)
+    q = rng.standard_normal((B, q_len, 1, 128)).astype(np.float16)
+    out = _decode(k, v, scales, tables, lens, q, SCALE)
+    pick = rng.choice(B, 60, replace=False)
+    want, tol = int8.attention(q[pick], k, v, scales, tables[pick], lens[pick], SCALE)
+    _close(out[torch.as_tensor(pick).to(DEV)], want, tol)
+
+
 @pytest.mark.parametrize("spread", [0, 9])
 @pytest.mark.parametrize("scale", [SCALE, -0.3, 0.0, 2.0])
 def test_decode_with_other_scales(scale, spread):
@@ -397,6 +427,23 @@ def test_selection_across_clusters_of_all_sizes(seqs, hkv, blocks, budget):
     scales = (2.0 ** rng.integers(-8, -5, (nb, hkv, 2))).astype(np.float32)
     q = rng.standard_normal((seqs, 1, hkv * 4, 128)).astype(np.float16)
     _select_both(q, scales, bounds, tables, lens, 16, budget, 1, 2)
+
+
+@pytest.mark.parametrize("blocks,budget,ties", [(20000, 64, False), (20000, 3000, True), (16384, 999, True),
+                                                (17000, 16999, True)])
+def test_selection_of_more_blocks_than_a_cta_holds(blocks, budget, ties):
+    rng = np.random.default_rng(budget)
+    nb = 50                                   # blocks that stand in the table many times: many ties
+    tables = rng.integers(0, nb, (2, blocks)).astype(np.int32)
+    lens = np.array([blocks * 16, blocks * 16 - 5000], np.int32)
+    bounds = np.sort(rng.integers(1, 256, (nb, 1, 2, 128)), axis=2).astype(np.uint8)
+    if not ties:
+        nb = blocks
+        tables = np.stack([rng.permutation(nb) for _ in range(2)]).astype(np.int32)
+        bounds = np.sort(rng.integers(1, 256, (nb, 1, 2, 128)), axis=2).astype(np.uint8)
+    scales = np.full((nb, 1, 2), 2.0 ** -6, np.float32)
+    q = rng.standard_normal((2, 2, 3, 128)).astype(np.float16)
+    _select_both(q, scales, bounds, tables, lens, 16, budget, 1, 1)
 
 
 def test_equal_scores_go_to_the_lower_block():
