@@ -27,6 +27,8 @@
 //    reaches the queries that see a row of its block.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "pkv_decode_common.cuh"
 #include "pkv_device.cuh"
 #include "pkv_int8.cuh"
@@ -72,8 +74,6 @@ struct Smem8 {
   __host__ static size_t bytes(int R, int B, int) {
     return 128 + static_cast<size_t>(seq_off(R)) + (2 * static_cast<size_t>(B) + 1) * 4;
   }
-  // the merge of split units stages at least two partials in the stage memory
-  static_assert(kQ >= 8 * RS * RT * ((kD + 8) * 4 + 2 * (kD + 4) * 4), "merge staging");
 };
 
 __device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
@@ -189,6 +189,166 @@ __device__ __forceinline__ float exponent_of(float s) {
   return s == s ? fmaxf(e, -60.f) : s;
 }
 
+// Merges a split unit: its partials of slices c0 .. cl, which hold per row their maximum m, their sum l
+// and their normalised output, into (m, l, o) of N items of the calling thread, item i the output dims
+// 4 (gi & 31) .. + 3 of row gi >> 5, gi = t + i NT, in slice order. All items' loads of a batch are in
+// flight at once, past L1, which is not coherent: by way of shared memory, with a barrier between the
+// steps, 10 partials of 8 rows took 4.5 us.
+template <int N, int NT>
+__device__ __forceinline__ void merge_partials(const DecodeArgs& a, int c0, int cl, int cf,
+                                               bool first_odd, int t, float (&m)[N], float (&l)[N],
+                                               float4 (&o)[N]) {
+  constexpr int kBatch = N == 1 ? 8 : N == 2 ? 4 : N == 3 ? 3 : 2;
+  const int items = a.R * 32;
+#pragma unroll 1
+  for (int c = c0; c <= cl; c += kBatch) {
+    float2 ml[N][kBatch];
+    float4 x[N][kBatch];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int gi = min(t + i * NT, items - 1);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        ml[i][j] = make_float2(kNegInf, 0.f);
+        x[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c + j <= cl) {
+          const int64_t row =
+              (2 * static_cast<int64_t>(c + j) + ((c + j == cf && first_odd) ? 1 : 0)) * a.R + (gi >> 5);
+          ml[i][j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row * 4));
+          x[i][j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * kD) + (gi & 31));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float M = m[i];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) M = fmaxf(M, ml[i][j].x);
+      // (o is normalised by l: what it stands for is l o 2^m)
+      float w = m[i] == kNegInf ? 0.f : l[i] * fast_exp2(m[i] - M);
+      float L = w;
+      float4 V = make_float4(w * o[i].x, w * o[i].y, w * o[i].z, w * o[i].w);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        w = ml[i][j].x == kNegInf ? 0.f : ml[i][j].y * fast_exp2(ml[i][j].x - M);
+        L += w;
+        V.x += w * x[i][j].x; V.y += w * x[i][j].y; V.z += w * x[i][j].z; V.w += w * x[i][j].w;
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      m[i] = M;
+      l[i] = L;
+      o[i] = make_float4(V.x * inv, V.y * inv, V.z * inv, V.w * inv);
+    }
+  }
+}
+
+// End of the slice (finish_slice's protocol: who merges a split unit, the bounded wait, the counters)
+// by the consumers and the epilogue warp, dense index t: each thread has 4 output dims of up to
+// kItems rows of the last segment in its registers from the warps' states to the output. ROWS: the
+// most rows the variant takes.
+template <int NCS, int WARPS, int SB, int ROWS>
+__device__ __forceinline__ void finish_slice8(const DecodeArgs& a, const LastSeg& ls, const int* pre,
+                                              int per, const float* stO, const float* stM,
+                                              const float* stL, int* npend_s, volatile int* fast_s,
+                                              int t) {
+  constexpr int kNE = (WARPS + 1) * 32;
+  constexpr int kItems = (ROWS * 32 + kNE - 1) / kNE;
+  const int items = a.R * 32;
+  named_barrier_sync(2, kNE);                  // last states written, earlier segments merged
+  const int sb = ls.k % SB;
+  float m[kItems], l[kItems];
+  float4 o[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int gi = t + i * kNE, r = min(gi, items - 1) >> 5, c4 = gi & 31;
+    float w[NCS];
+    row_weights<NCS>(stM + sb * NCS * a.R, stL + sb * NCS * a.R, a.R, r, w, m[i], l[i]);
+    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int ww = 0; ww < NCS; ++ww) {
+      const float4 v =
+          reinterpret_cast<const float4*>(stO + (static_cast<int64_t>(sb * NCS + ww) * a.R + r) * kSt)[c4];
+      o[i].x += w[ww] * v.x; o[i].y += w[ww] * v.y; o[i].z += w[ww] * v.z; o[i].w += w[ww] * v.w;
+    }
+  }
+  auto put = [&](int b, int h, int gi, float4 v) {
+    store_half4(out_row(a, b, h, gi >> 5) + (gi & 31) * 4, v);
+  };
+  // a unit's first and last slice, and whether its first part is that slice's second
+  auto slices = [&](int b, int h, int nb, int& cf, int& cl) {
+    const int ua = unit_first<kSeg8>(pre, a.Hkv, b, h, nb);
+    cf = ua / per;
+    cl = (ua + nb - 1) / per;
+    return cf * per < ua - kSeg8;
+  };
+  if (ls.complete) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+      if (t + i * kNE < items) put(ls.b, ls.h, t + i * kNE, o[i]);
+  } else {
+    int cf, cl;
+    const bool odd = slices(ls.b, ls.h, ls.nb, cf, cl);
+    int* counter = a.counters + ls.b * a.Hkv + ls.h;
+    bool merged = false;
+    if (ls.head) {
+      if (t == 0) {
+        const uint64_t t_end = global_time_ns() + kMergeWaitNs;
+        int ok = 0;
+        do {
+          if (ld_acquire_gpu(counter) == cl - cf) { ok = 1; break; }
+        } while (global_time_ns() < t_end);
+        *fast_s = ok;
+      }
+      named_barrier_sync(2, kNE);
+      merged = *fast_s;
+    }
+    if (merged) {
+      if (t == 0) *counter = 0;
+      merge_partials<kItems, kNE>(a, cf + 1, cl, cf, odd, t, m, l, o);   // (slice cf is this one)
+#pragma unroll
+      for (int i = 0; i < kItems; ++i)
+        if (t + i * kNE < items) put(ls.b, ls.h, t + i * kNE, o[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int gi = t + i * kNE;
+        if (gi >= items) continue;
+        const int64_t row = static_cast<int64_t>(ls.slot) * a.R + (gi >> 5);
+        reinterpret_cast<float4*>(a.part_o + row * kD)[gi & 31] = o[i];
+        if ((gi & 31) == 0)
+          *reinterpret_cast<float4*>(a.part_ml + row * 4) = make_float4(m[i], l[i], 0.f, 0.f);
+      }
+      named_barrier_sync(2, kNE);                // partial written by every thread
+      if (t == 0 && atomic_add_acq_rel(counter, 1) == cl - cf) {
+        const int n = *npend_s;
+        npend_s[1 + 3 * n] = ls.b;
+        npend_s[2 + 3 * n] = ls.h;
+        npend_s[3 + 3 * n] = ls.nb;
+        *npend_s = n + 1;
+      }
+    }
+  }
+  named_barrier_sync(2, kNE);
+  const int np = *npend_s;
+#pragma unroll 1
+  for (int n = 0; n < np; ++n) {   // units whose last partial arrived from this CTA
+    const int b = npend_s[1 + 3 * n], h = npend_s[2 + 3 * n];
+    int cf, cl;
+    const bool odd = slices(b, h, npend_s[3 + 3 * n], cf, cl);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      m[i] = kNegInf;
+      l[i] = 0.f;
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    merge_partials<kItems, kNE>(a, cf, cl, cf, odd, t, m, l, o);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+      if (t + i * kNE < items) put(b, h, t + i * kNE, o[i]);
+    if (t == 0) a.counters[b * a.Hkv + h] = 0;
+  }
+}
+
 // Warps 0 .. NCS RS - 1 consume; the next one prepares the queries, the last one is the epilogue
 // (merges each segment's per-warp states, writes outputs and split units' partials).
 template <int NCS, int RS, int RT, int ND, int SB, int MINB>
@@ -223,7 +383,7 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
   // ---- per-sequence lengths and chunk counts -------------------------------------------------
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar_qfull + s * 8, 1);
+      mbar_init(bar_qfull + s * 8, RS * RT > 1 ? 2 : 1);   // (see kHelpers)
       mbar_init(bar_qempty + s * 8, NCW);
     }
     for (int s = 0; s < SB; ++s) {
@@ -277,79 +437,92 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
                    s.c0 == 0 && s.c1 == s.nb, s.c0 == 0};
   };
 
+  // Queries of segment kk into buffer kk & 1 as the products' B operands, tiles `tile0`, tile0 + STEP, ..:
+  // for lane (g, t4), row g of a tile, the dims 16 p + 4 t4 .. + 3 of piece p, paired as the codes
+  // are ((0, 2) and (1, 3)). And per lane, for rows 2 t4 and 2 t4 + 1: what the codes' offset adds to a
+  // product (negative), and what makes scores of the products.
+  auto prepare = [&](const Seg& sg, int kk, int tile0, auto step) {
+    constexpr int STEP = decltype(step)::value, N = (RS * RT + STEP - 1) / STEP;
+    const uint32_t qb = sbase + L::kQ + (kk & 1) * L::kQBuf;
+    uint2 v[N][8];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int row = 8 * (tile0 + n * STEP) + g;
+      const int qi = row / a.G;
+      // a query before its sequence's first token sees nothing, whatever it holds: taken as zeros, it
+      // keeps a NaN from its scores, which are all masked
+      const bool sees = row < a.R && slen[sg.b] - a.q_len + qi >= 0;
+      const uint2* src = reinterpret_cast<const uint2*>(
+          x8.q +
+          ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) v[n][p] = sees ? src[4 * p + t4] : make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int tile = tile0 + n * STEP;
+      if (8 * tile >= a.R) break;
+      __half2 big = __half2half2(__ushort_as_half(0));
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[n][p].x)));
+        big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[n][p].y)));
+      }
+      big = __hmax2_nan(big, __lowhigh2highlow(big));
+      big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const float top = __low2float(big);
+      // 2^(10 - exponent of the row's largest), which comes to lie in [2^10, 2^11); a negative score
+      // scale turns the queries' signs instead, so that a larger product is a larger score
+      const int ex = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) : 127;
+      float f = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
+      // codes come in as u 2^-24; a NaN or an infinity among the queries makes the scores NaN
+      const float unit = top <= 65504.f
+                             ? fabsf(a.scale_log2) *
+                                   (0x1p24f * __uint_as_float(static_cast<uint32_t>(ex - 10) << 23))
+                             : __uint_as_float(kNanBits);
+      if (a.scale_log2 < 0.f) f = -f;
+      float sum = 0.f;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        float2 u = __half22float2(*reinterpret_cast<const __half2*>(&v[n][p].x));
+        float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[n][p].y));
+        u.x *= f; u.y *= f; y.x *= f; y.y *= f;
+        sum += (u.x + u.y) + (y.x + y.y);
+        v[n][p] = make_uint2(pack_half2(u.x, y.x), pack_half2(u.y, y.y));
+      }
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        st_shared_v4(qb + tile * L::kQTile + p * 512 + lane * 16,
+                     make_uint4(v[n][2 * p].x, v[n][2 * p].y, v[n][2 * p + 1].x, v[n][2 * p + 1].y));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const float o = sum * -0x1p-17f;   // 128 2^-24
+      const float o0 = __shfl_sync(0xffffffffu, o, 8 * t4), o1 = __shfl_sync(0xffffffffu, o, 8 * t4 + 4);
+      const float r0 = __shfl_sync(0xffffffffu, unit, 8 * t4);
+      const float r1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
+      st_shared_v4(qb + tile * L::kQTile + 2048 + lane * 16,
+                   make_uint4(__float_as_uint(o0), __float_as_uint(o1), __float_as_uint(r0),
+                              __float_as_uint(r1)));
+    }
+    __syncwarp();
+  };
+  // The first segment's queries, which everyone waits for, are shared between the two helper warps.
+  constexpr int kHelpers = RS * RT > 1 ? 2 : 1;
+
   if (warp == NCW) {
     // =================================== queries =============================================
-    // Queries of segment kk into buffer kk & 1 as the products' B operands: for lane (g, t4), row g
-    // of each tile, the dims 16 p + 4 t4 .. + 3 of piece p, paired as the codes are ((0, 2) and
-    // (1, 3)). And per lane, for rows 2 t4 and 2 t4 + 1: what the codes' offset adds to a product
-    // (negative), and what makes scores of the products.
-    auto prepare = [&](const Seg& sg, int kk) {
-      const uint32_t qb = sbase + L::kQ + (kk & 1) * L::kQBuf;
-#pragma unroll 1
-      for (int tile = 0; 8 * tile < a.R; ++tile) {
-        const int row = 8 * tile + g;
-        const int qi = row / a.G;
-        // a query before its sequence's first token sees nothing, whatever it holds: taken as zeros,
-        // it keeps a NaN from its scores, which are all masked
-        const bool sees = row < a.R && slen[sg.b] - a.q_len + qi >= 0;
-        const uint2* src = reinterpret_cast<const uint2*>(
-            x8.q +
-            ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
-        uint2 v[8];
-        __half2 big = __half2half2(__ushort_as_half(0));
-#pragma unroll
-        for (int p = 0; p < 8; ++p) v[p] = sees ? src[4 * p + t4] : make_uint2(0, 0);
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[p].x)));
-          big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[p].y)));
-        }
-        big = __hmax2_nan(big, __lowhigh2highlow(big));
-        big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const float top = __low2float(big);
-        // 2^(10 - exponent of the row's largest), which comes to lie in [2^10, 2^11); a negative
-        // score scale turns the queries' signs instead, so that a larger product is a larger score
-        const int ex = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) : 127;
-        float f = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
-        // codes come in as u 2^-24; a NaN or an infinity among the queries makes the scores NaN
-        const float unit = top <= 65504.f
-                               ? fabsf(a.scale_log2) *
-                                     (0x1p24f * __uint_as_float(static_cast<uint32_t>(ex - 10) << 23))
-                               : __uint_as_float(kNanBits);
-        if (a.scale_log2 < 0.f) f = -f;
-        float sum = 0.f;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          float2 u = __half22float2(*reinterpret_cast<const __half2*>(&v[p].x));
-          float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[p].y));
-          u.x *= f; u.y *= f; y.x *= f; y.y *= f;
-          sum += (u.x + u.y) + (y.x + y.y);
-          v[p] = make_uint2(pack_half2(u.x, y.x), pack_half2(u.y, y.y));
-        }
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-          st_shared_v4(qb + tile * L::kQTile + p * 512 + lane * 16,
-                       make_uint4(v[2 * p].x, v[2 * p].y, v[2 * p + 1].x, v[2 * p + 1].y));
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const float o = sum * -0x1p-17f;   // 128 2^-24
-        const float o0 = __shfl_sync(0xffffffffu, o, 8 * t4), o1 = __shfl_sync(0xffffffffu, o, 8 * t4 + 4);
-        const float r0 = __shfl_sync(0xffffffffu, unit, 8 * t4);
-        const float r1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
-        st_shared_v4(qb + tile * L::kQTile + 2048 + lane * 16,
-                     make_uint4(__float_as_uint(o0), __float_as_uint(o1), __float_as_uint(r0),
-                                __float_as_uint(r1)));
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_qfull + (kk & 1) * 8);
-    };
     Seg s;
     bool has = cur.first(begin, s);
     for (int k = 0; has; ++k) {
       if (k >= 2 && !mbar_wait(bar_qempty + (k & 1) * 8, ((k >> 1) - 1) & 1, abort))
         flag_timeout(a, abort);
-      prepare(s, k);
+      if (k == 0) prepare(s, k, 0, std::integral_constant<int, kHelpers>());
+      else prepare(s, k, 0, std::integral_constant<int, 1>());
+      if (lane == 0) {
+        mbar_arrive(bar_qfull + (k & 1) * 8);
+        if (kHelpers == 2 && k > 0) mbar_arrive(bar_qfull + (k & 1) * 8);
+      }
       has = cur.next(s);
     }
     // sequences without any chunk get zeros (their units are in no CTA's slice)
@@ -365,6 +538,10 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
     // =================================== epilogue ============================================
     Seg s;
     if (cur.first(begin, s)) {
+      if (kHelpers == 2) {
+        prepare(s, 0, 1, std::integral_constant<int, 2>());
+        if (lane == 0) mbar_arrive(bar_qfull);
+      }
       int npend = 0, k = 0;
       Seg nx = s;
       while (cur.next(nx)) {
@@ -632,8 +809,8 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
 
   // ---- end of the slice ----
   if (last.k >= 0)
-    finish_slice<NCS, kSeg8, NCW, SB>(a, last, pre, per, smem, L::kQ, stO, stM, stL, npend_s,
-                                      fast_s, warp < NCW ? tid : tid - 32);
+    finish_slice8<NCS, NCW, SB, 8 * RS * RT>(a, last, pre, per, stO, stM, stL, npend_s, fast_s,
+                                             warp < NCW ? tid : tid - 32);
 }
 
 // ---------------------------------------------------------------------------------------------
