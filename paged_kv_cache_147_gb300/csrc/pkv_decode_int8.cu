@@ -41,14 +41,22 @@ constexpr int kTile8 = kChunk * kD;          // one chunk's K (or V): 2048 bytes
 constexpr int kStage8 = 4 * kTile8;          // K of two chunks, V of two chunks
 // Per-segment cost in chunks (see kSegCost): as for the 4-bit cache, whose segments do the same work.
 constexpr int kSeg8 = 8;
-// No slice finer than sqrt(kPartCost * the longest unit's chunks), and whole units to a CTA where
-// that costs at most kAlone rounds of stages (see pkv_decode_int4.cu).
+// No slice finer than sqrt(kPartCost * the longest unit's chunks) (see pkv_decode_int4.cu). Where units
+// are few, whole or evenly divided ones to a CTA each, if that takes at most kAlone rounds of stages
+// more; parts of r rounds cost about r and as many partials as there are parts, kPartRounds of a round
+// each.
 constexpr float kPartCost = 3.f;
+constexpr float kPartRounds = 0.06f;
 constexpr int kAlone = 3;
 constexpr size_t kMaxSmem = 227 * 1024;
 // How far the softmax's reference is put below the running maximum, and how far a weight may pass
 // the maximum before the reference moves: weights stay below 2^13.
 constexpr float kShift = 11.f, kGrow = 2.f;
+
+// Units divided evenly: parts of `chunks` chunks, `parts` CTAs a unit (0: slices of the stream).
+struct Split {
+  int parts, chunks;
+};
 
 // What the kernel needs beside DecodeArgs.
 struct Int8Args {
@@ -248,9 +256,9 @@ __device__ __forceinline__ void merge_partials(const DecodeArgs& a, int c0, int 
 // most rows the variant takes.
 template <int NCS, int WARPS, int SB, int ROWS>
 __device__ __forceinline__ void finish_slice8(const DecodeArgs& a, const LastSeg& ls, const int* pre,
-                                              int per, const float* stO, const float* stM,
-                                              const float* stL, int* npend_s, volatile int* fast_s,
-                                              int t) {
+                                              int per, Split split, const float* stO,
+                                              const float* stM, const float* stL, int* npend_s,
+                                              volatile int* fast_s, int t) {
   constexpr int kNE = (WARPS + 1) * 32;
   constexpr int kItems = (ROWS * 32 + kNE - 1) / kNE;
   const int items = a.R * 32;
@@ -276,6 +284,11 @@ __device__ __forceinline__ void finish_slice8(const DecodeArgs& a, const LastSeg
   };
   // a unit's first and last slice, and whether its first part is that slice's second
   auto slices = [&](int b, int h, int nb, int& cf, int& cl) {
+    if (split.parts > 0) {
+      cf = (b * a.Hkv + h) * split.parts;
+      cl = cf + (nb - 1) / split.chunks;
+      return false;
+    }
     const int ua = unit_first<kSeg8>(pre, a.Hkv, b, h, nb);
     cf = ua / per;
     cl = (ua + nb - 1) / per;
@@ -419,11 +432,30 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
   const int per = max(static_cast<int>((total + gridDim.x - 1) / gridDim.x),
                       static_cast<int>(sqrtf(kPartCost * *longest_s)));
   int begin = blockIdx.x * per, end = min(total, begin + per);
-  if (B * a.Hkv <= gridDim.x && *longest_s <= 2 * NCS * ((per + 2 * NCS - 1) / (2 * NCS) + kAlone)) {
-    const int b = blockIdx.x / a.Hkv;
-    const int len = b < B ? pre[b + 1] - pre[b] : 0;
-    begin = len > 0 ? pre[b] * a.Hkv + (blockIdx.x - b * a.Hkv) * len : 0;
-    end = begin + len;
+  // Few units: CTA (u, i) takes the i-th of `split.parts` equal parts of unit u, in whole rounds of
+  // its warps (2 NCS chunks), where no unit takes more than kAlone rounds more than an equal share.
+  Split split{0, 0};
+  const int units = B * a.Hkv;
+  if (units <= static_cast<int>(gridDim.x)) {
+    constexpr int kRound = 2 * NCS;
+    const int longest = (*longest_s + kRound - 1) / kRound;
+    int rounds = 1, parts = 1;
+    if (longest > 1) {
+      const int most = gridDim.x / units;
+      rounds = max((longest + most - 1) / most, max(1, __float2int_rn(sqrtf(kPartRounds * longest))));
+      parts = (longest + rounds - 1) / rounds;
+    }
+    if (rounds <= (per + kRound - 1) / kRound + kAlone) {
+      split = Split{parts, rounds * kRound};
+      const int u = parts > 1 ? blockIdx.x / parts : blockIdx.x, b = u / a.Hkv;
+      const int len = b < B ? pre[b + 1] - pre[b] : 0;
+      begin = end = 0;
+      if (len > 0) {
+        const int first = unit_first<kSeg8>(pre, a.Hkv, b, u - b * a.Hkv, len - kSeg8);
+        begin = first + (blockIdx.x - u * parts) * split.chunks;
+        end = min(first + len - kSeg8, begin + split.chunks);
+      }
+    }
   }
   const CursorT<kSeg8> cur{pre, B, a.Hkv, end};
 
@@ -809,7 +841,8 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
 
   // ---- end of the slice ----
   if (last.k >= 0)
-    finish_slice8<NCS, NCW, SB, 8 * RS * RT>(a, last, pre, per, stO, stM, stL, npend_s, fast_s,
+    finish_slice8<NCS, NCW, SB, 8 * RS * RT>(a, last, pre, per, split, stO, stM, stL, npend_s,
+                                             fast_s,
                                              warp < NCW ? tid : tid - 32);
 }
 
