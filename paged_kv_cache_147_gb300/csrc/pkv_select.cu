@@ -35,7 +35,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = kThreads / 32;   // as many as rows in a tile of queries
 constexpr int kMaxCluster = 8;
 constexpr int kGather = 16384;    // blocks whose keys a CTA takes all of
 constexpr int kBinBits = 10, kBins = 1 << kBinBits;   // 4 a thread
@@ -181,7 +181,9 @@ select_blocks_kernel(const SelectArgs a) {
   const int head = a.keep_first;
   const int tail = nblk - max(a.keep_last, nblk - (max(ctx - a.q_len, 0) >> a.bs_shift));
   auto id_of = [&](int j) { return j < to ? table[j] : -1; };
-  int next[2] = {id_of(from + 16 * warp + g), id_of(from + 16 * warp + g + 8)};
+  constexpr int kStep = 16 * kWarps;
+  int j0 = from + 16 * warp;
+  int next[2] = {id_of(j0 + g), id_of(j0 + g + 8)};   // ids of the warp's next 16 blocks
 
   // ---- the queries: whole numbers as the products' B operands ----
   for (int i = tid; i < 2 * kBins; i += kThreads) hist[i] = 0u;
@@ -190,13 +192,21 @@ select_blocks_kernel(const SelectArgs a) {
     ends_s[1] = 0u;
     ncand_s = 0u;
   }
-  for (int r = warp; r < 8 * NT; r += kWarps) {
-    const int qi = r / a.G;
-    uint2 v = make_uint2(0u, 0u);
-    const bool sees = r < a.R && ctx - a.q_len + qi >= 0;
-    if (sees)
-      v = reinterpret_cast<const uint2*>(
+  // (a warp has row `warp` of each tile; all of its loads go out first)
+  uint2 qv[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + warp, qi = r / a.G;
+    qv[nt] = make_uint2(0u, 0u);
+    if (r < a.R && ctx - a.q_len + qi >= 0)
+      qv[nt] = reinterpret_cast<const uint2*>(
           a.q + ((static_cast<int64_t>(b) * a.q_len + qi) * a.Hq + h * a.G + r - qi * a.G) * kD)[lane];
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + warp;
+    const bool sees = r < a.R && ctx - a.q_len + r / a.G >= 0;
+    const uint2 v = qv[nt];
     const __half2 x = *reinterpret_cast<const __half2*>(&v.x);
     const __half2 y = *reinterpret_cast<const __half2*>(&v.y);
     __half2 big = __hmax2_nan(__habs2(x), __habs2(y));
@@ -215,11 +225,10 @@ select_blocks_kernel(const SelectArgs a) {
     }
     sum = __reduce_add_sync(0xffffffffu, sum);
     // dims 4 lane .. + 3: word `lane & 3` of 16-byte piece (lane >> 2) & 3 of 64-byte part lane >> 4
-    uint2* to = frag + (r >> 3) * 512 + ((lane >> 4) * 4 + (lane & 3)) * 32 + (r & 7) * 4 +
-                ((lane >> 2) & 3);
-    to[0] = make_uint2(pack_half2(fminf(p[0], 0.f), fminf(p[2], 0.f)),
+    uint2* at = frag + nt * 512 + ((lane >> 4) * 4 + (lane & 3)) * 32 + warp * 4 + ((lane >> 2) & 3);
+    at[0] = make_uint2(pack_half2(fminf(p[0], 0.f), fminf(p[2], 0.f)),
                        pack_half2(fminf(p[1], 0.f), fminf(p[3], 0.f)));
-    to[8 * 32] = make_uint2(pack_half2(fmaxf(p[0], 0.f), fmaxf(p[2], 0.f)),
+    at[8 * 32] = make_uint2(pack_half2(fmaxf(p[0], 0.f), fmaxf(p[2], 0.f)),
                             pack_half2(fmaxf(p[1], 0.f), fmaxf(p[3], 0.f)));
     if (lane == 0) {
       const bool counts = sees && s == s;
@@ -247,27 +256,37 @@ select_blocks_kernel(const SelectArgs a) {
       for (int i = 0; i < 4; ++i) t.w[o][i] = t.good[o] ? src[4 * i] : make_uint4(0, 0, 0, 0);
       t.sc[o] = t.good[o] ? a.scales[bh * 2] : 0.f;
       if (!t.good[o] && j0 + g + 8 * o < to && t4 == 0) atomicOr(a.err, PKV_DEVERR_BLOCK_ID);
-      next[o] = id_of(j0 + 16 * kWarps + g + 8 * o);
+      next[o] = id_of(j0 + kStep + g + 8 * o);
     }
   };
   auto score = [&](const Tile& t, int j0) {
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      acc[nt][0] = acc[nt][2] = col[8 * nt + 2 * t4].x;
+      acc[nt][1] = acc[nt][3] = col[8 * nt + 2 * t4 + 1].x;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t u0 = u4_word(t.w[0][i], e), u1 = u4_word(t.w[1][i], e);
+        const uint32_t l0 = u0 & 0x00ff00ffu, l1 = u1 & 0x00ff00ffu;
+        const uint32_t h0 = __byte_perm(u0, 0u, 0x4341), h1 = __byte_perm(u1, 0u, 0x4341);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 f = frag[nt * 512 + (4 * i + e) * 32 + lane];
+          mma_f16(acc[nt], l0, l1, h0, h1, f.x, f.y);
+        }
+      }
     float best[2] = {kNegInf, kNegInf};
-#pragma unroll(NT <= 2 ? NT : 1)
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float4 c0 = col[8 * nt + 2 * t4], c1 = col[8 * nt + 2 * t4 + 1];
-      float acc[4] = {c0.x, c1.x, c0.x, c1.x};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint2 f = frag[nt * 512 + (4 * i + e) * 32 + lane];
-          const uint32_t u0 = u4_word(t.w[0][i], e), u1 = u4_word(t.w[1][i], e);
-          mma_f16(acc, u0 & 0x00ff00ffu, u1 & 0x00ff00ffu, __byte_perm(u0, 0u, 0x4341),
-                  __byte_perm(u1, 0u, 0x4341), f.x, f.y);
-        }
 #pragma unroll
       for (int o = 0; o < 2; ++o)
-        best[o] = fmaxf(best[o], fmaxf(fmaf(acc[2 * o], c0.y, c0.z), fmaf(acc[2 * o + 1], c1.y, c1.z)));
+        best[o] = fmaxf(best[o], fmaxf(fmaf(acc[nt][2 * o], c0.y, c0.z),
+                                       fmaf(acc[nt][2 * o + 1], c1.y, c1.z)));
     }
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
@@ -287,8 +306,6 @@ select_blocks_kernel(const SelectArgs a) {
       }
     }
   };
-  constexpr int kStep = 16 * kWarps;
-  int j0 = from + 16 * warp;
   if constexpr (NT == 1) {
     // the next 16 blocks' bounds on the way (more rows leave no registers for that)
     Tile t[2];
