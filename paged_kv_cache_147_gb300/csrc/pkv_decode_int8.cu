@@ -27,8 +27,6 @@
 //    reaches the queries that see a row of its block.
 #include <cuda_fp16.h>
 
-#include <type_traits>
-
 #include "pkv_decode_common.cuh"
 #include "pkv_device.cuh"
 #include "pkv_int8.cuh"
@@ -53,6 +51,8 @@ constexpr size_t kMaxSmem = 227 * 1024;
 // the maximum before the reference moves: weights stay below 2^13.
 constexpr float kShift = 11.f, kGrow = 2.f;
 
+constexpr int kQTile8 = 5 * 512;   // a tile of 8 query rows: fragments of 8 pieces, constants
+
 // Units divided evenly: parts of `chunks` chunks, `parts` CTAs a unit (0: slices of the stream).
 struct Split {
   int parts, chunks;
@@ -70,7 +70,7 @@ struct Int8Args {
 // warp, SB: buffers of segment states.
 template <int NCS, int RS, int RT, int ND, int SB>
 struct Smem8 {
-  static constexpr int kQTile = 5 * 512;              // 8 rows: fragments of 8 pieces, constants
+  static constexpr int kQTile = kQTile8;
   static constexpr int kQBuf = RS * RT * kQTile;
   static constexpr int kQ = NCS * RS * ND * kStage8;
   static constexpr int kScales = kQ + 2 * kQBuf;      // per stage: (s_K, s_V) of both chunks
@@ -362,6 +362,84 @@ __device__ __forceinline__ void finish_slice8(const DecodeArgs& a, const LastSeg
   }
 }
 
+// A segment's queries, tiles `tile0`, tile0 + STEP, .. of TILES: for lane (g, t4), row g of a tile, the
+// dims 16 p + 4 t4 .. + 3 of piece p.
+template <int TILES, int STEP>
+__device__ __forceinline__ void fetch_queries(const DecodeArgs& a, const __half* q, const int* slen,
+                                              const Seg& sg, int tile0, int lane,
+                                              uint2 (&v)[TILES][8]) {
+  const int g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+  for (int n = 0; n * STEP < TILES; ++n) {
+    const int row = 8 * (tile0 + n * STEP) + g;
+    const int qi = row / a.G;
+    // a query before its sequence's first token sees nothing, whatever it holds: taken as zeros, it
+    // keeps a NaN from its scores, which are all masked
+    const bool sees = row < a.R && slen[sg.b] - a.q_len + qi >= 0;
+    const uint2* src = reinterpret_cast<const uint2*>(
+        q + ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) v[n][p] = sees ? src[4 * p + t4] : make_uint2(0, 0);
+  }
+}
+
+// Into the buffer at qb as the products' B operands, paired as the codes are ((0, 2) and (1, 3)). And
+// per lane, for rows 2 t4 and 2 t4 + 1: what the codes' offset adds to a product (negative), and what
+// makes scores of the products.
+template <int TILES, int STEP>
+__device__ __forceinline__ void put_queries(const DecodeArgs& a, uint32_t qb, int tile0, int lane,
+                                            uint2 (&v)[TILES][8]) {
+  const int t4 = lane & 3;
+#pragma unroll
+  for (int n = 0; n * STEP < TILES; ++n) {
+    const int tile = tile0 + n * STEP;
+    if (8 * tile >= a.R) break;
+    __half2 big = __half2half2(__ushort_as_half(0));
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[n][p].x)));
+      big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[n][p].y)));
+    }
+    big = __hmax2_nan(big, __lowhigh2highlow(big));
+    big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const float top = __low2float(big);
+    // 2^(10 - exponent of the row's largest), which comes to lie in [2^10, 2^11); a negative score
+    // scale turns the queries' signs instead, so that a larger product is a larger score
+    const int ex = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) : 127;
+    float f = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
+    // codes come in as u 2^-24; a NaN or an infinity among the queries makes the scores NaN
+    const float unit = top <= 65504.f
+                           ? fabsf(a.scale_log2) *
+                                 (0x1p24f * __uint_as_float(static_cast<uint32_t>(ex - 10) << 23))
+                           : __uint_as_float(kNanBits);
+    if (a.scale_log2 < 0.f) f = -f;
+    float sum = 0.f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      float2 u = __half22float2(*reinterpret_cast<const __half2*>(&v[n][p].x));
+      float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[n][p].y));
+      u.x *= f; u.y *= f; y.x *= f; y.y *= f;
+      sum += (u.x + u.y) + (y.x + y.y);
+      v[n][p] = make_uint2(pack_half2(u.x, y.x), pack_half2(u.y, y.y));
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      st_shared_v4(qb + tile * kQTile8 + p * 512 + lane * 16,
+                   make_uint4(v[n][2 * p].x, v[n][2 * p].y, v[n][2 * p + 1].x, v[n][2 * p + 1].y));
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const float o = sum * -0x1p-17f;   // 128 2^-24
+    const float o0 = __shfl_sync(0xffffffffu, o, 8 * t4), o1 = __shfl_sync(0xffffffffu, o, 8 * t4 + 4);
+    const float r0 = __shfl_sync(0xffffffffu, unit, 8 * t4);
+    const float r1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
+    st_shared_v4(qb + tile * kQTile8 + 2048 + lane * 16,
+                 make_uint4(__float_as_uint(o0), __float_as_uint(o1), __float_as_uint(r0),
+                            __float_as_uint(r1)));
+  }
+  __syncwarp();
+}
+
 // Warps 0 .. NCS RS - 1 consume; the next one prepares the queries, the last one is the epilogue
 // (merges each segment's per-warp states, writes outputs and split units' partials).
 template <int NCS, int RS, int RT, int ND, int SB, int MINB>
@@ -469,93 +547,32 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
                    s.c0 == 0 && s.c1 == s.nb, s.c0 == 0};
   };
 
-  // Queries of segment kk into buffer kk & 1 as the products' B operands, tiles `tile0`, tile0 + STEP, ..:
-  // for lane (g, t4), row g of a tile, the dims 16 p + 4 t4 .. + 3 of piece p, paired as the codes
-  // are ((0, 2) and (1, 3)). And per lane, for rows 2 t4 and 2 t4 + 1: what the codes' offset adds to a
-  // product (negative), and what makes scores of the products.
-  auto prepare = [&](const Seg& sg, int kk, int tile0, auto step) {
-    constexpr int STEP = decltype(step)::value, N = (RS * RT + STEP - 1) / STEP;
-    const uint32_t qb = sbase + L::kQ + (kk & 1) * L::kQBuf;
-    uint2 v[N][8];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int row = 8 * (tile0 + n * STEP) + g;
-      const int qi = row / a.G;
-      // a query before its sequence's first token sees nothing, whatever it holds: taken as zeros, it
-      // keeps a NaN from its scores, which are all masked
-      const bool sees = row < a.R && slen[sg.b] - a.q_len + qi >= 0;
-      const uint2* src = reinterpret_cast<const uint2*>(
-          x8.q +
-          ((static_cast<int64_t>(sg.b) * a.q_len + qi) * a.Hq + sg.h * a.G + row - qi * a.G) * kD);
-#pragma unroll
-      for (int p = 0; p < 8; ++p) v[n][p] = sees ? src[4 * p + t4] : make_uint2(0, 0);
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int tile = tile0 + n * STEP;
-      if (8 * tile >= a.R) break;
-      __half2 big = __half2half2(__ushort_as_half(0));
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[n][p].x)));
-        big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __half2*>(&v[n][p].y)));
-      }
-      big = __hmax2_nan(big, __lowhigh2highlow(big));
-      big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = __hmax2_nan(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      const float top = __low2float(big);
-      // 2^(10 - exponent of the row's largest), which comes to lie in [2^10, 2^11); a negative score
-      // scale turns the queries' signs instead, so that a larger product is a larger score
-      const int ex = top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) : 127;
-      float f = __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
-      // codes come in as u 2^-24; a NaN or an infinity among the queries makes the scores NaN
-      const float unit = top <= 65504.f
-                             ? fabsf(a.scale_log2) *
-                                   (0x1p24f * __uint_as_float(static_cast<uint32_t>(ex - 10) << 23))
-                             : __uint_as_float(kNanBits);
-      if (a.scale_log2 < 0.f) f = -f;
-      float sum = 0.f;
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        float2 u = __half22float2(*reinterpret_cast<const __half2*>(&v[n][p].x));
-        float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[n][p].y));
-        u.x *= f; u.y *= f; y.x *= f; y.y *= f;
-        sum += (u.x + u.y) + (y.x + y.y);
-        v[n][p] = make_uint2(pack_half2(u.x, y.x), pack_half2(u.y, y.y));
-      }
-#pragma unroll
-      for (int p = 0; p < 4; ++p)
-        st_shared_v4(qb + tile * L::kQTile + p * 512 + lane * 16,
-                     make_uint4(v[n][2 * p].x, v[n][2 * p].y, v[n][2 * p + 1].x, v[n][2 * p + 1].y));
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const float o = sum * -0x1p-17f;   // 128 2^-24
-      const float o0 = __shfl_sync(0xffffffffu, o, 8 * t4), o1 = __shfl_sync(0xffffffffu, o, 8 * t4 + 4);
-      const float r0 = __shfl_sync(0xffffffffu, unit, 8 * t4);
-      const float r1 = __shfl_sync(0xffffffffu, unit, 8 * t4 + 4);
-      st_shared_v4(qb + tile * L::kQTile + 2048 + lane * 16,
-                   make_uint4(__float_as_uint(o0), __float_as_uint(o1), __float_as_uint(r0),
-                              __float_as_uint(r1)));
-    }
-    __syncwarp();
-  };
   // The first segment's queries, which everyone waits for, are shared between the two helper warps.
-  constexpr int kHelpers = RS * RT > 1 ? 2 : 1;
+  constexpr int kTiles = RS * RT, kHelpers = kTiles > 1 ? 2 : 1;
 
   if (warp == NCW) {
     // =================================== queries =============================================
     Seg s;
     bool has = cur.first(begin, s);
-    for (int k = 0; has; ++k) {
-      if (k >= 2 && !mbar_wait(bar_qempty + (k & 1) * 8, ((k >> 1) - 1) & 1, abort))
-        flag_timeout(a, abort);
-      if (k == 0) prepare(s, k, 0, std::integral_constant<int, kHelpers>());
-      else prepare(s, k, 0, std::integral_constant<int, 1>());
-      if (lane == 0) {
-        mbar_arrive(bar_qfull + (k & 1) * 8);
-        if (kHelpers == 2 && k > 0) mbar_arrive(bar_qfull + (k & 1) * 8);
-      }
+    if (has) {
+      uint2 v0[kTiles][8];
+      fetch_queries<kTiles, kHelpers>(a, x8.q, slen, s, 0, lane, v0);
+      uint2 v[kTiles][8];
       has = cur.next(s);
+      if (has) fetch_queries<kTiles, 1>(a, x8.q, slen, s, 0, lane, v);   // the next segment's are on their way
+      put_queries<kTiles, kHelpers>(a, sbase + L::kQ, 0, lane, v0);
+      if (lane == 0) mbar_arrive(bar_qfull);
+      for (int k = 1; has; ++k) {
+        if (k >= 2 && !mbar_wait(bar_qempty + (k & 1) * 8, ((k >> 1) - 1) & 1, abort))
+          flag_timeout(a, abort);
+        put_queries<kTiles, 1>(a, sbase + L::kQ + (k & 1) * L::kQBuf, 0, lane, v);
+        if (lane == 0) {
+          mbar_arrive(bar_qfull + (k & 1) * 8);
+          if (kHelpers == 2) mbar_arrive(bar_qfull + (k & 1) * 8);
+        }
+        has = cur.next(s);
+        if (has) fetch_queries<kTiles, 1>(a, x8.q, slen, s, 0, lane, v);
+      }
     }
     // sequences without any chunk get zeros (their units are in no CTA's slice)
     for (int b = blockIdx.x; b < B; b += gridDim.x) {
@@ -571,7 +588,9 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
     Seg s;
     if (cur.first(begin, s)) {
       if (kHelpers == 2) {
-        prepare(s, 0, 1, std::integral_constant<int, 2>());
+        uint2 v[kTiles][8];
+        fetch_queries<kTiles, kHelpers>(a, x8.q, slen, s, 1, lane, v);
+        put_queries<kTiles, kHelpers>(a, sbase + L::kQ, 1, lane, v);
         if (lane == 0) mbar_arrive(bar_qfull);
       }
       int npend = 0, k = 0;
