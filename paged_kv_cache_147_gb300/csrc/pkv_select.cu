@@ -590,7 +590,8 @@ extern "C" int pkv_select_blocks(int32_t* tables_out, int32_t* lens_out, const v
   const int ends = std::max(keep_last, 1 + (q_len - 1 + block_size - 1) / block_size);
   if (static_cast<int64_t>(keep_first) + ends > budget) return PKV_EINVAL;
   if (num_seqs == 0) return PKV_OK;
-  if (!tables_out || !lens_out || !q || !kv_scales || !k_bounds || !block_tables || !context_lens)
+  if (!tables_out || !lens_out || !q || !kv_scales || !k_bounds || !context_lens ||
+      (!block_tables && max_blocks_per_seq > 0))   // (a table without columns has no address)
     return PKV_EINVAL;
   if (!aligned16(q) || !aligned16(k_bounds) || (reinterpret_cast<uintptr_t>(kv_scales) & 7u))
     return PKV_EINVAL;
