@@ -695,19 +695,28 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
           uint4 b[RT];
 #pragma unroll
           for (int t = 0; t < RT; ++t) b[t] = ld_shared_v4(qb + t * L::kQTile + i * 512);
+          uint32_t w[2][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w0, w1, w2, w3;
-            ldsm_x4(stK + h * kTile8 + lm_row + (((2 * i + lm_p) ^ lm_x) << 4), w0, w1, w2, w3);
-            const uint32_t l0 = w0 & 0x00ff00ffu, l1 = w1 & 0x00ff00ffu;
-            const uint32_t l2 = w2 & 0x00ff00ffu, l3 = w3 & 0x00ff00ffu;
-            const uint32_t u0 = __byte_perm(w0, 0u, 0x4341), u1 = __byte_perm(w1, 0u, 0x4341);
-            const uint32_t u2 = __byte_perm(w2, 0u, 0x4341), u3 = __byte_perm(w3, 0u, 0x4341);
+          for (int h = 0; h < 2; ++h)
+            ldsm_x4(stK + h * kTile8 + lm_row + (((2 * i + lm_p) ^ lm_x) << 4), w[h][0], w[h][1], w[h][2],
+                    w[h][3]);
+          // (products that do not wait on each other next to each other)
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-              mma_f16(x[t][h], l0, l1, u0, u1, b[t].x, b[t].y);
-              mma_f16(x[t][h], l2, l3, u2, u3, b[t].z, b[t].w);
-            }
+          for (int o = 0; o < 2; ++o) {
+            uint32_t lo[2][2], hi[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                lo[h][e] = w[h][2 * o + e] & 0x00ff00ffu;
+                hi[h][e] = __byte_perm(w[h][2 * o + e], 0u, 0x4341);
+              }
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                mma_f16(x[t][h], lo[h][0], lo[h][1], hi[h][0], hi[h][1], o ? b[t].z : b[t].x,
+                        o ? b[t].w : b[t].y);
           }
         }
 
@@ -720,6 +729,7 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
         for (int h = 0; h < 2; ++h)
           // (a NaN scale, or what lies behind the last chunk: only weights may carry it)
           iv[h] = ve[h] == ve[h] ? fast_exp2(-ve[h]) : 0.f;
+        bool move = false;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           const uint2 rc = ld_shared_v2(qb + t * L::kQTile + 2056);   // what makes scores of products
@@ -732,23 +742,29 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
               x[t][h][e] = fmaf(x[t][h][e], m, z);
               x[t][h][2 + e] = fmaf(x[t][h][2 + e], m, z);
             }
-          if (!full) {
+        }
+        if (!full) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int lim = h == 0 || two ? Lc - a.q_len + 1 - (c + h) * kChunk : -(1 << 30);
+          for (int h = 0; h < 2; ++h) {
+            const int lim = h == 0 || two ? Lc - a.q_len + 1 - (c + h) * kChunk : -(1 << 30);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
 #pragma unroll
               for (int o = 0; o < 2; ++o)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                   if (g + 8 * o >= lim + qi[t][e]) x[t][h][2 * o + e] = kNegInf;
-            }
           }
-          bool move = false;
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             move |= fmaxf(fmaxf(x[t][0][e], x[t][0][2 + e]), fmaxf(x[t][1][e], x[t][1][2 + e])) >
                     thr[t][e];
-          if (__any_sync(0xffffffffu, move)) {
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float mx = fmaxf(fmaxf(x[t][0][e], x[t][0][2 + e]), fmaxf(x[t][1][e], x[t][1][2 + e]));
@@ -779,9 +795,11 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
                 ot[t][p][2 + e] *= alpha;
               }
             }
-          }
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[t][h][e] = fast_exp2(x[t][h][e]);
             tl[t][0] = fmaf(x[t][h][0] + x[t][h][2], iv[h], tl[t][0]);
@@ -790,7 +808,6 @@ decode_int8_kernel(const DecodeArgs a, const Int8Args x8) {
             for (int o = 0; o < 2; ++o)
               pb[t][h][o] = movmatrix_trans(pack_half2(x[t][h][2 * o], x[t][h][2 * o + 1]));
           }
-        }
 
         // ---- O^T += V^T P^T: row g of tile p is dim 16 p + 2 g, row g + 8 dim 16 p + 2 g + 1 ----
         const __half2 kOff = __half2half2(__ushort_as_half(0x6480));   // 1152
