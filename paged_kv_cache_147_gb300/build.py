@@ -86,7 +86,7 @@ class _TorchBuild:
                "-isystem", os.path.join(root, "include"),
                "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
                os.path.join(CSRC, TORCH_SOURCE), "-o", self.tmp, f"-L{lib}", "-ltorch_python",
-               "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+               "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
         self.process = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
                                         text=True, start_new_session=True)
 

@@ -374,7 +374,7 @@ select_blocks_kernel(const SelectArgs a) {
   // ---- where the budget ends: keys above `edge` are taken, and the first `need` equal to it ----
   uint32_t need = n - min(head, nblk) - (nblk - tail);
   uint32_t edge = kAlways - 1;     // (nothing but the kept ones)
-  for (int round = 0; need > 0; ++round) {
+  for (int round = 0; need > 0 && round < 4; ++round) {   // (32 bits, 10 a round)
     const int shift = max(0, 32 - __clz(most - least) - kBinBits);
     uint32_t* hr = hist + (round & 1) * kBins;
 #pragma unroll 4
