@@ -42,9 +42,10 @@ constexpr int kSeg8 = 8;
 // No slice finer than sqrt(kPartCost * the longest unit's chunks) (see pkv_decode_int4.cu). Where units
 // are few, whole or evenly divided ones to a CTA each, if that takes at most kAlone rounds of stages
 // more; parts of r rounds cost about r and as many partials as there are parts, kPartRounds of a round
-// each.
+// each (0.06: one sequence of 2000 tokens, 64 heads over 8, 10.5 us, 0.15: 9.9, 0.4: 9.9; one of 30000,
+// 12 heads over 2, 2 tokens: 19.9, 19.8, 21.7).
 constexpr float kPartCost = 3.f;
-constexpr float kPartRounds = 0.06f;
+constexpr float kPartRounds = 0.15f;
 constexpr int kAlone = 3;
 constexpr size_t kMaxSmem = 227 * 1024;
 // How far the softmax's reference is put below the running maximum, and how far a weight may pass
@@ -201,12 +202,13 @@ __device__ __forceinline__ float exponent_of(float s) {
 // and their normalised output, into (m, l, o) of N items of the calling thread, item i the output dims
 // 4 (gi & 31) .. + 3 of row gi >> 5, gi = t + i NT, in slice order. All items' loads of a batch are in
 // flight at once, past L1, which is not coherent: by way of shared memory, with a barrier between the
-// steps, 10 partials of 8 rows took 4.5 us.
+// steps, 10 partials of 8 rows took 4.5 us. The batches are as large as the registers let them be: half
+// of them, and a sequence of 2000 tokens with 12 rows takes 18.8 us instead of 13.8.
 template <int N, int NT>
 __device__ __forceinline__ void merge_partials(const DecodeArgs& a, int c0, int cl, int cf,
                                                bool first_odd, int t, float (&m)[N], float (&l)[N],
                                                float4 (&o)[N]) {
-  constexpr int kBatch = N == 1 ? 8 : N == 2 ? 4 : N == 3 ? 3 : 2;
+  constexpr int kBatch = N <= 2 ? 8 : N == 3 ? 5 : N == 4 ? 4 : 3;
   const int items = a.R * 32;
 #pragma unroll 1
   for (int c = c0; c <= cl; c += kBatch) {
@@ -893,6 +895,9 @@ Variant variant8() {
 
 // The variant for R query rows. `few`: no more units than SMs. `wide`: tables for 4096 tokens and more
 // (the lengths are on the GPU; a table per head is as wide as its contexts are long, so it counts).
+// `lone`: a quarter as many units as SMs and tables for 512 tokens and more (8 rows, 4 of 500, 8 kv
+// heads: 9.4 us with 4 warps, 8.8 with 8; one of 2000: 9.8, 8.6; 16 rows, one of 2000, 2 kv heads 12.1,
+// 10.8; one of 101: 6.7, 7.1; 64 of 16 to 2048, 2 kv heads, 8 rows: 14.0, 16.1).
 // Measured against each other, us (a: 64 sequences of 16 to 2048 tokens, 2 kv heads; b: 16 of 4096, 8
 // kv heads; c: one of 65536; d: 32 of 50 to 8000; e: 512 of 20 to 200):
 //   to 8   <4, 1, 1, 2, 2, 2> a 13.5, b 25.1, c 34.5, d 52.6, e 42.0, 16 of 1024 in a table as long 13.1
@@ -905,9 +910,9 @@ Variant variant8() {
 //          <4, 2, 2, 2, 1, 1>   29.9    54.8    59.8    112    172
 // Many warps in one CTA keep more in flight than two CTAs of four, but hand a segment over only once
 // per SM and merge more states for it; a warp with several row tiles widens the codes once for all.
-Variant choose8(int R, bool few, bool wide) {
-  return R <= 8    ? (few && wide ? variant8<8, 1, 1, 2, 1, 1>() : variant8<4, 1, 1, 2, 2, 2>())
-         : R <= 16 ? (few && wide ? variant8<8, 1, 2, 2, 1, 1>() : variant8<4, 1, 2, 2, 1, 2>())
+Variant choose8(int R, bool few, bool wide, bool lone) {
+  return R <= 8    ? ((few && wide) || lone ? variant8<8, 1, 1, 2, 1, 1>() : variant8<4, 1, 1, 2, 2, 2>())
+         : R <= 16 ? ((few && wide) || lone ? variant8<8, 1, 2, 2, 1, 1>() : variant8<4, 1, 2, 2, 1, 2>())
          : R <= 24 ? (wide ? variant8<6, 1, 3, 2, 1, 1>() : variant8<3, 3, 1, 2, 1, 1>())
                    : (wide ? variant8<4, 2, 2, 2, 1, 1>() : variant8<3, 2, 2, 2, 1, 1>());
 }
@@ -943,7 +948,9 @@ int launch_decode_int8(void* out, const void* q, const void* k_cache, const void
   const WsLayout ws = ws_layout(num_seqs, Hkv, R, workspace_bytes);
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
-  Variant v = choose8(R, num_seqs * Hkv <= sm_count(), head_tables || max_ctx >= 4096);
+  const int64_t units = static_cast<int64_t>(num_seqs) * Hkv;
+  const int sms = sm_count();
+  Variant v = choose8(R, units <= sms, head_tables || max_ctx >= 4096, 4 * units <= sms && max_ctx >= 512);
   size_t smem = v.smem(R, num_seqs, 0);
   if (smem > kMaxSmem) {   // thousands of sequences with 17 and more rows each
     v = variant8<3, 2, 2, 2, 1, 1>();
