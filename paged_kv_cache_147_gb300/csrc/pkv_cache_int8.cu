@@ -3,7 +3,11 @@
 //
 // All move bytes. The append reads 256 and writes 128 per row; a block that rows are added to is
 // read and written again only when its scale grows (its largest element doubles, so a few times
-// in a block's life).
+// in a block's life). A scale needs all of a block's new rows before the first code, so that the rows
+// stay in registers between the two (16 rows a warp) and are read once: 8192 tokens of 8 heads in
+// 16-token blocks take 13.2 us (50 MB, 3.8 TB/s; first load to last store is one trip through memory
+// and nothing is left to overlap it with), 64 tokens of 2 heads 2.9 (a launch and three dependent
+// loads). Widening 8192 tokens: 9.6 us (5.3 TB/s).
 #include <algorithm>
 
 #include "pkv_int8.cuh"
@@ -423,7 +427,8 @@ int pkv_kv_append_int8(const void* k, const void* v, const int64_t* slot_mapping
       !aligned16(k_bounds) || (reinterpret_cast<uintptr_t>(kv_scales) & 7u))
     return PKV_EINVAL;
   // Few rows: a team for every token, so that a step's blocks are all taken at once. Many: as many tokens
-  // a team as leave about as many warps as are resident, a block's worth at most.
+  // a team as leave about as many warps as are resident, a block's worth at most (8192 tokens of 8 heads
+  // in blocks of 16: a token a team 19.8 us, this 13.2; half or twice as many warps change nothing).
   const int64_t halves = static_cast<int64_t>(num_kv_heads) * 2;   // K and V of a head
   const int64_t warps = num_tokens * halves * (block_size / 16);
   const int span = static_cast<int>(std::min<int64_t>(std::max<int64_t>(warps / 4096, 1), block_size));

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <new>
 #include <tuple>
 
 #include "pkv_device.cuh"
@@ -650,7 +651,10 @@ inline int grid_size(const Variant& v, size_t smem, int* status) {
   if (e != cudaSuccess) { *status = cuda_status(e); return 0; }
   if (occ < 1) { *status = PKV_EINVAL; return 0; }
   const int grid = sm_count() * std::min(occ, kMaxCtasPerSm);
-  cache[key] = grid;
+  try {
+    cache[key] = grid;
+  } catch (const std::bad_alloc&) {   // found again by the next call
+  }
   return grid;
 }
 

@@ -5,9 +5,15 @@
 // s_V (code_V - 128), (s_K, s_V) of the block and kv head that hold the row. With a table per kv head
 // it runs over that table's blocks as if they were the whole context.
 //
-// What bounds it: 256 bytes per (token, kv head). Stream, slices, split units and merges are those of
-// pkv_decode.cu (pkv_decode_common.cuh); the warps' own rings of cp.async stages, the transposed
-// tile, the query and the epilogue warp those of pkv_decode_int4.cu. What is its own:
+// What bounds it: 256 bytes per (token, kv head). 32 sequences of 16384 tokens, 8 kv heads, 8 query
+// rows each, take 160 us (1.07 GB at 6.7 TB/s, a copy's rate), 16 of 4096 24.4 (5.5 TB/s, with 4 us of
+// start and merge). Few or short contexts are bound by latency (one of 101 tokens 5.1 us), 9 rows and
+// more by the products' operands, which every 8 rows take again (16 of 4096: 16 rows 33 us, 24 rows 46,
+// 32 rows 54).
+//
+// Stream, slices, split units and merges are those of pkv_decode.cu (pkv_decode_common.cuh); the warps'
+// own rings of cp.async stages, the transposed tile, the query and the epilogue warp those of
+// pkv_decode_int4.cu. What is its own:
 //  * A stage is two 16-token chunks, K and V, 2048 contiguous bytes each, and the two chunks' scales
 //    (blocks are 16 tokens or more, so a chunk has one of each). 16-byte pieces are exchanged by row
 //    (piece p of row r lies at p ^ (r & 7)): ldmatrix then reads 8 rows without a bank conflict.
