@@ -277,6 +277,19 @@ def test_decode_of_every_row_count_in_wide_and_narrow_tables(hq, hkv, q_len, wid
         _close(_decode(k, v, scales, tables, lens, q, SCALE), want, tol)
 
 
+@pytest.mark.parametrize("rows", [1, 8, 12, 16, 24, 28, 32])
+@pytest.mark.parametrize("lens", [[505], [512, 100], [2000], [640, 0, 4095, 1]])
+def test_decode_of_few_sequences_in_many_parts(rows, lens):
+    # one kv head: units in parts of 1 to 3 rounds, up to 16 partials a unit; tables just below and
+    # above the widths at which eight warps take over
+    q_len = 1 if rows < 12 else rows // 4
+    k, v, scales, _, tables, lens, q = _case(lens, 16, rows // q_len, 1, q_len, seed=rows)
+    want, tol = int8.attention(q, k, v, scales, tables, lens, SCALE)
+    first = _decode(k, v, scales, tables, lens, q, SCALE)
+    _close(first, want, tol)
+    assert torch.equal(first, _decode(k, v, scales, tables, lens, q, SCALE))
+
+
 @pytest.mark.parametrize("q_len", [1, 3, 8, 12, 16, 24, 32])
 def test_decode_of_as_many_sequences_as_it_takes(q_len):
     # shared blocks: each sequence reads its own part of a small pool
