@@ -49,10 +49,11 @@ constexpr int kSeg8 = 8;
 // are few, whole or evenly divided ones to a CTA each, if that takes at most kAlone rounds of stages
 // more; parts of r rounds cost about r and as many partials as there are parts, kPartRounds of a round
 // each (0.06: one sequence of 2000 tokens, 64 heads over 8, 10.5 us, 0.15: 9.9, 0.4: 9.9; one of 30000,
-// 12 heads over 2, 2 tokens: 19.9, 19.8, 21.7).
+// 12 heads over 2, 2 tokens: 19.9, 19.8, 21.7). kAlone 3, 4, 5: 64 sequences of 16 to 2048 tokens, 2 kv
+// heads 16.0, 14.4, 14.4; 10 of 16 to 2000, 8 kv heads 13.0, 12.6, 13.4.
 constexpr float kPartCost = 3.f;
 constexpr float kPartRounds = 0.15f;
-constexpr int kAlone = 3;
+constexpr int kAlone = 4;
 constexpr size_t kMaxSmem = 227 * 1024;
 // How far the softmax's reference is put below the running maximum, and how far a weight may pass
 // the maximum before the reference moves: weights stay below 2^13.
@@ -899,26 +900,24 @@ Variant variant8() {
                  (NCS * RS + 2) * 32, &Smem8<NCS, RS, RT, ND, SB>::bytes};
 }
 
-// The variant for R query rows. `few`: no more units than SMs. `wide`: tables for 4096 tokens and more
-// (the lengths are on the GPU; a table per head is as wide as its contexts are long, so it counts).
-// `lone`: a quarter as many units as SMs and tables for 512 tokens and more (8 rows, 4 of 500, 8 kv
-// heads: 9.4 us with 4 warps, 8.8 with 8; one of 2000: 9.8, 8.6; 16 rows, one of 2000, 2 kv heads 12.1,
-// 10.8; one of 101: 6.7, 7.1; 64 of 16 to 2048, 2 kv heads, 8 rows: 14.0, 16.1).
-// Measured against each other, us (a: 64 sequences of 16 to 2048 tokens, 2 kv heads; b: 16 of 4096, 8
-// kv heads; c: one of 65536; d: 32 of 50 to 8000; e: 512 of 20 to 200):
-//   to 8   <4, 1, 1, 2, 2, 2> a 13.5, b 25.1, c 34.5, d 52.6, e 42.0, 16 of 1024 in a table as long 13.1
-//          <8, 1, 1, 2, 1, 1>   15.9    22.6    28.1    55.6    79.5                                10.3
-//   to 16  <4, 1, 2, 2, 1, 2> a 17.7, b 33.5, c 49.4, d 60.0, e 72.9
-//          <8, 1, 2, 2, 1, 1>   21.2    32.1    37.0    72.2   137.8
-//   to 24  <3, 3, 1, 2, 1, 1> a 23.4, b 55.8, c 59.9, d 104
-//          <6, 1, 3, 2, 1, 1>   27.2    46.6    51.6     91
-//   to 32  <3, 2, 2, 2, 1, 1> a 27.0, b 61.2, c 68.9, d 115, e 145
-//          <4, 2, 2, 2, 1, 1>   29.9    54.8    59.8    112    172
+// The variant for R query rows. `few`: no more units than SMs, and tables for more than 128 tokens (a
+// round of four warps). `wide`: tables for 4096 tokens and more (the lengths are on the GPU; a table per
+// head is as wide as its contexts are long, so it counts). Measured against each other, us (a: 64
+// sequences of 16 to 2048 tokens, 2 kv heads; b: 16 of 4096, 8 kv heads; c: one of 65536; d: 32 of 50 to
+// 8000; e: 512 of 20 to 200; f: 16 of 1000; g: 19 of 300; h: one of 101, 2 kv heads):
+//   to 8   <4, 1, 1, 2, 2, 2> a 14.0, b 25.1, c 34.5, d 48.4, e 42.0, f 13.8, g 10.4, h 5.1
+//          <8, 1, 1, 2, 1, 1>   14.4    24.4    27.7    55.6    79.5    10.7     7.7    5.1
+//   to 16  <4, 1, 2, 2, 1, 2> a 18.2, b 33.5, c 49.4, d 58.3, e 72.9, f 17.5, g 13.3, h 6.7
+//          <8, 1, 2, 2, 1, 1>   19.7    32.9    36.6    72.2   137.8    14.7    10.4    7.1
+//   to 24  <3, 3, 1, 2, 1, 1> a 23.5, b 55.8, c 59.9, d 104, one of 1000, 2 kv heads, 4 times 12.4
+//          <6, 1, 3, 2, 1, 1>   26.6    46.3    48.0     89                                    13.2
+//   to 32  <3, 2, 2, 2, 1, 1> a 26.7, b 61.2, c 68.9, d 115, e 145, two of 1000, 8 kv heads 14.4
+//          <4, 2, 2, 2, 1, 1>   29.9    54.4    57.4    110    172                          14.9
 // Many warps in one CTA keep more in flight than two CTAs of four, but hand a segment over only once
 // per SM and merge more states for it; a warp with several row tiles widens the codes once for all.
-Variant choose8(int R, bool few, bool wide, bool lone) {
-  return R <= 8    ? ((few && wide) || lone ? variant8<8, 1, 1, 2, 1, 1>() : variant8<4, 1, 1, 2, 2, 2>())
-         : R <= 16 ? ((few && wide) || lone ? variant8<8, 1, 2, 2, 1, 1>() : variant8<4, 1, 2, 2, 1, 2>())
+Variant choose8(int R, bool few, bool wide) {
+  return R <= 8    ? (few ? variant8<8, 1, 1, 2, 1, 1>() : variant8<4, 1, 1, 2, 2, 2>())
+         : R <= 16 ? (few ? variant8<8, 1, 2, 2, 1, 1>() : variant8<4, 1, 2, 2, 1, 2>())
          : R <= 24 ? (wide ? variant8<6, 1, 3, 2, 1, 1>() : variant8<3, 3, 1, 2, 1, 1>())
                    : (wide ? variant8<4, 2, 2, 2, 1, 1>() : variant8<3, 2, 2, 2, 1, 1>());
 }
@@ -954,9 +953,8 @@ int launch_decode_int8(void* out, const void* q, const void* k_cache, const void
   const WsLayout ws = ws_layout(num_seqs, Hkv, R, workspace_bytes);
   if (workspace_bytes < ws.total) return PKV_ENOSPC;
 
-  const int64_t units = static_cast<int64_t>(num_seqs) * Hkv;
-  const int sms = sm_count();
-  Variant v = choose8(R, units <= sms, head_tables || max_ctx >= 4096, 4 * units <= sms && max_ctx >= 512);
+  Variant v = choose8(R, static_cast<int64_t>(num_seqs) * Hkv <= sm_count() && max_ctx > 128,
+                      head_tables || max_ctx >= 4096);
   size_t smem = v.smem(R, num_seqs, 0);
   if (smem > kMaxSmem) {   // thousands of sequences with 17 and more rows each
     v = variant8<3, 2, 2, 2, 1, 1>();
