@@ -516,9 +516,6 @@ select_blocks_kernel(const SelectArgs a) {
     eq += __reduce_add_sync(0xffffffffu, before ? ld_cluster_u32(&taken_s[1], lane) : 0u);
     cluster_arrive();   // this CTA has read what the others counted
   }
-  // Only ids are left to write: the next kernel on the stream may take its places (16 sequences' sparse
-  // step 51.5 -> 51.0 us; earlier in the kernel gained nothing, or cost 3 %).
-  if (tid == 0) griddep_launch_dependents();
   const uint32_t below = (1u << lane) - 1u;
   for (int j = k0 + lane; j - lane < k1; j += 32) {
     const uint32_t key = j < k1 ? own[j] : 0u;
