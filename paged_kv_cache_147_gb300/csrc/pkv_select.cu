@@ -357,6 +357,7 @@ select_blocks_kernel(const SelectArgs a) {
     }
     cluster_arrive();   // this CTA has read the others' keys
   }
+  bool copying = gather;   // the others may still be reading this CTA's
   least = __reduce_min_sync(0xffffffffu, least);
   most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0 && least <= most) {
@@ -456,6 +457,10 @@ select_blocks_kernel(const SelectArgs a) {
         x = cand_s[tid];
       }
       all_s[tid] = x;
+      if (copying) {   // (the marks below go into this CTA's own keys, too)
+        cluster_wait();
+        copying = false;
+      }
       __syncthreads();
       if (static_cast<uint32_t>(tid) < inside && c == rank) {
         uint32_t better = 0;
@@ -528,7 +533,7 @@ select_blocks_kernel(const SelectArgs a) {
     gt += __popc(gts);
     eq += __popc(eqs);
   }
-  if (a.C > 1) cluster_wait();     // the others have read this CTA's
+  if (joint || copying) cluster_wait();   // the others have read this CTA's
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -1,0 +1,55 @@
+"""The block selection where a cluster of CTAs shares a head: with other work on the GPU, so that its
+CTAs run apart, and with guards around the outputs."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import int8
+from paged_kv_cache_147_gb300 import pkv
+
+from test_gpu_int8 import _dev, _tables
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+GUARD = -77777
+
+
+def _inputs(rng, seqs, hkv, blocks, q_len=1, group=2):
+    lens = rng.integers(blocks * 12, blocks * 16, seqs, endpoint=True)
+    lens, tables, nb, _ = _tables(rng, lens, 16, width=blocks)
+    bounds = np.sort(rng.integers(1, 256, (nb, hkv, 2, 128)), axis=2).astype(np.uint8)
+    scales = (2.0 ** rng.integers(-8, -5, (nb, hkv, 2))).astype(np.float32)
+    q = rng.standard_normal((seqs, q_len, hkv * group, 128)).astype(np.float16)
+    return q, scales, bounds, tables, lens
+
+
+@pytest.mark.parametrize("seqs,hkv,blocks,budget,q_len", [
+    (1, 8, 2048, 64, 1),        # eight CTAs a head
+    (2, 1, 1100, 300, 2), (8, 4, 700, 90, 1), (16, 8, 512, 64, 2), (3, 2, 16384, 1000, 1),
+    (1, 1, 16400, 2000, 1)])    # each CTA keeps its own keys
+def test_clusters_among_other_work_write_their_own_rows_only(seqs, hkv, blocks, budget, q_len):
+    rng = np.random.default_rng(blocks)
+    args = _inputs(rng, seqs, hkv, blocks, q_len)
+    want = int8.select(*args, 16, budget, 1, 2)
+    dev = [_dev(x) for x in args]
+    n = seqs * hkv * budget
+    load = torch.randn(512, 512, device=DEV)
+    busy = torch.empty_like(load)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(40):
+        with torch.cuda.stream(side):
+            torch.mm(load, load, out=busy)
+        room = torch.full((n + 2 * budget,), GUARD, dtype=torch.int32, device=DEV)
+        tables = room[budget:budget + n].view(seqs, hkv, budget)
+        lens = torch.full((seqs + 2,), GUARD, dtype=torch.int32, device=DEV)
+        pkv.select_blocks(*dev, 16, budget, 1, 2, tables, lens[1:-1])
+        runs.append((room, lens))
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == 0
+    for room, lens in runs:
+        assert (room[:budget] == GUARD).all() and (room[budget + n:] == GUARD).all()
+        assert lens[0] == GUARD and lens[-1] == GUARD
+        assert np.array_equal(room[budget:budget + n].view(seqs, hkv, budget).cpu().numpy(), want[0])
+        assert np.array_equal(lens[1:-1].cpu().numpy(), want[1])

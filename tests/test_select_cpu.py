@@ -1,0 +1,25 @@
+"""CPU pins of the block selection: the order of its cluster's accesses to shared memory, from the
+source."""
+import os
+import re
+
+from paged_kv_cache_147_gb300 import build
+
+
+def _code(source):
+    with open(os.path.join(build.CSRC, source)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+def test_keys_that_other_ctas_copy_are_not_written_before_they_have_read_them():
+    # every CTA of a cluster copies the others' keys, arrives at the cluster's barrier when it has, and
+    # later marks the chosen ones in its own: the barrier's wait lies between the two
+    code = _code("pkv_select.cu")
+    copied = code.index("ld_cluster_v4(keys")
+    arrived = code.index("cluster_arrive();", copied)
+    writes = [m.start() for m in re.finditer(r"\bkeys\[[^;]*?\]\s*=[^=]", code) if m.start() > arrived]
+    assert writes
+    for at in writes:
+        assert "cluster_wait();" in code[arrived:at]
+    # and a CTA does not leave while the others may still read its keys
+    assert code.index("cluster_wait();", writes[-1]) > writes[-1]
