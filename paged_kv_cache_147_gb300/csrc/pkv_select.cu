@@ -155,8 +155,8 @@ select_blocks_kernel(const SelectArgs a) {
   const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.max_blocks;
   int32_t* out = a.tables_out + static_cast<int64_t>(unit) * a.budget;
   if (h == 0 && rank == 0 && tid == 0) a.lens_out[b] = ctx - (nblk - n) * a.block_size;
-  // entries without a block, and all of a context within the budget
-  for (int i = rank * kThreads + tid; i < a.budget; i += a.C * kThreads) {
+  // entries without a block, and all of a context within the budget (which may be any int)
+  for (int64_t i = rank * kThreads + tid; i < a.budget; i += a.C * kThreads) {
     if (i >= n) out[i] = -1;
     else if (nblk == n) out[i] = table[i];
   }

@@ -1,5 +1,5 @@
 """The block selection where a cluster of CTAs shares a head: with other work on the GPU, so that its
-CTAs run apart, and with guards around the outputs."""
+CTAs run apart, and with guards around the outputs; the largest budget."""
 import numpy as np
 import pytest
 import torch
@@ -53,3 +53,21 @@ def test_clusters_among_other_work_write_their_own_rows_only(seqs, hkv, blocks, 
         assert lens[0] == GUARD and lens[-1] == GUARD
         assert np.array_equal(room[budget:budget + n].view(seqs, hkv, budget).cpu().numpy(), want[0])
         assert np.array_equal(lens[1:-1].cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("blocks", [5, 200])      # one CTA, and a cluster
+def test_the_largest_budget(blocks):
+    # 8.6 GB of places, nearly all of them without a block
+    rng = np.random.default_rng(blocks)
+    q, scales, bounds, tables, lens = _inputs(rng, 1, 1, blocks)
+    budget, pad = 2 ** 31 - 1, 4096
+    room = torch.full((pad + budget + pad,), GUARD, dtype=torch.int32, device=DEV)
+    out = room[pad:pad + budget].view(1, 1, budget)
+    _, taken = pkv.select_blocks(*(_dev(x) for x in (q, scales, bounds, tables, lens)), 16, budget, 1, 1, out)
+    torch.cuda.synchronize()
+    assert pkv.device_error(clear=True) == 0
+    n = -(-int(lens[0]) // 16)
+    assert int(taken[0]) == lens[0]
+    assert np.array_equal(out[0, 0, :n].cpu().numpy(), tables[0, :n])
+    assert out[0, 0, n:].amin() == -1 and out[0, 0, n:].amax() == -1
+    assert (room[:pad] == GUARD).all() and (room[-pad:] == GUARD).all()

@@ -1,5 +1,5 @@
-"""CPU pins of the block selection: the order of its cluster's accesses to shared memory, from the
-source."""
+"""CPU pins of the block selection, from the source: the order of its cluster's accesses to shared
+memory, and the width of what counts to the budget."""
 import os
 import re
 
@@ -23,3 +23,9 @@ def test_keys_that_other_ctas_copy_are_not_written_before_they_have_read_them():
         assert "cluster_wait();" in code[arrived:at]
     # and a CTA does not leave while the others may still read its keys
     assert code.index("cluster_wait();", writes[-1]) > writes[-1]
+
+
+def test_places_up_to_the_budget_are_counted_in_64_bits():
+    # a budget may be as large as an int; the loop's step past it may not
+    loops = re.findall(r"for \((\w+) \w+ = [^;]*; \w+ < a\.budget;", _code("pkv_select.cu"))
+    assert loops == ["int64_t"]
