@@ -457,9 +457,9 @@ int pkv_selected_attn_decode_int8(void* out, const void* q, const void* k_cache,
  * what the append would take for the row as a scale, (lo, hi) the block's bounds without the offset and
  * s_K its K scale. That is an upper bound of the rounded row's products with the block's keys (for a
  * positive score scale), exact in fp32. A row before its sequence's first token, or with a NaN or an
- * infinity, does not count; a block with a NaN scale comes before all others; one with an id outside
- * [0, num_blocks) comes last and sets PKV_DEVERR_BLOCK_ID (contexts within the budget are not scored,
- * and their ids not looked at).
+ * infinity, does not count (no row left: all scores are equal); a block with a NaN scale comes before
+ * all others, whatever the rows hold; one with an id outside [0, num_blocks) comes last and sets
+ * PKV_DEVERR_BLOCK_ID (contexts within the budget are not scored, and their ids not looked at).
  *   tables_out [num_seqs][num_kv_heads][budget]: the chosen blocks' ids in the order of the context,
  *     entries behind them -1;
  *   lens_out [num_seqs]: the tokens in them (the last block's part counts as in context_lens),

@@ -130,7 +130,8 @@ def attention(q, k_pool, v_pool, scales, tables, lens, scale):
 
 def bound_scores(q_rows, bounds, k_scale):
     """Scores of blocks with bounds [N, 2, 128] and scales [N], the greatest over the query rows
-    [R, 128] (a row with a NaN or an infinity does not count)."""
+    [R, 128] (a row with a NaN or an infinity does not count); NaN where the scale is, whatever the
+    rows hold."""
     lo, hi = (bounds[:, i].astype(np.int64) - 128 for i in (0, 1))
     best = np.full(len(bounds), -np.inf)
     for row in np.asarray(q_rows, np.float64):
@@ -140,7 +141,8 @@ def bound_scores(q_rows, bounds, k_scale):
         p = np.clip(np.rint(row / s), -127, 127).astype(np.int64)
         dot = np.maximum(p * lo, p * hi).sum(-1)
         best = np.maximum(best, dot * s)
-    return np.where(np.isneginf(best), -np.inf, best * np.where(np.isneginf(best), 1, k_scale))
+    none = np.isneginf(best)      # (the same for all blocks: no row counts)
+    return np.where(none & ~np.isnan(k_scale), -np.inf, np.where(none, 1, best) * k_scale)
 
 
 def select(q, scales, bounds, tables, lens, bs, budget, first, last):

@@ -296,8 +296,9 @@ select_blocks_kernel(const SelectArgs a) {
       best[o] = fmaxf(best[o], __shfl_xor_sync(0xffffffffu, best[o], 2));
       const int j = j0 + g + 8 * o;
       if (t4 == 0 && j < to) {
-        // (+ 0 turns -0 into 0; a scale of 0 must not meet -infinity)
-        float s = best[o] == kNegInf ? kNegInf : best[o] * t.sc[o] + 0.f;
+        // (+ 0 turns -0 into 0; a scale of 0 must not meet -infinity, which a NaN one outranks)
+        float s = best[o] * t.sc[o] + 0.f;
+        if (best[o] == kNegInf && t.sc[o] == t.sc[o]) s = kNegInf;
         if (!t.good[o]) s = kNegInf;
         const uint32_t key = j < head || j >= tail ? kAlways : key_of(s);
         if (key != kAlways) {

@@ -1,5 +1,5 @@
 """The block selection where a cluster of CTAs shares a head: with other work on the GPU, so that its
-CTAs run apart, and with guards around the outputs; the largest budget."""
+CTAs run apart, and with guards around the outputs; the largest budget; NaN scales where no query counts."""
 import numpy as np
 import pytest
 import torch
@@ -71,3 +71,25 @@ def test_the_largest_budget(blocks):
     assert np.array_equal(out[0, 0, :n].cpu().numpy(), tables[0, :n])
     assert out[0, 0, n:].amin() == -1 and out[0, 0, n:].amax() == -1
     assert (room[:pad] == GUARD).all() and (room[-pad:] == GUARD).all()
+
+
+@pytest.mark.parametrize("seqs,hkv,blocks,q_len", [(40, 4, 100, 1), (1, 2, 900, 2), (2, 1, 17000, 1)])
+def test_a_nan_scale_comes_first_whatever_the_queries_hold(seqs, hkv, blocks, q_len):
+    rng = np.random.default_rng(blocks + 1)
+    q, scales, bounds, tables, lens = _inputs(rng, seqs, hkv, blocks, q_len)
+    scales[tables[:, 5:blocks // 2:7].reshape(-1), :, 0] = np.nan
+    scales[tables[:, 8:blocks // 2:7].reshape(-1), :, 0] = 0
+    for x in (np.nan, np.inf, None):
+        if x is None:                          # a row that counts beside one that does not
+            q[:, 0, 1] = rng.standard_normal(128).astype(np.float16)
+        else:
+            q[:] = x
+        for budget in (9, blocks // 3):        # (fewer places than NaN scales, and more)
+            dev = [_dev(t) for t in (q, scales, bounds, tables, lens)]
+            got = pkv.select_blocks(*dev, 16, budget, 1, 2)
+            want = int8.select(q, scales, bounds, tables, lens, 16, budget, 1, 2)
+            torch.cuda.synchronize()
+            assert pkv.device_error(clear=True) == 0
+            assert np.array_equal(got[0].cpu().numpy(), want[0])
+            assert np.array_equal(got[1].cpu().numpy(), want[1])
+        assert budget <= 9 or np.isin(tables[0, 5:blocks // 2:7], want[0][0, 0]).all()

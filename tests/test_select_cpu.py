@@ -1,8 +1,11 @@
 """CPU pins of the block selection, from the source: the order of its cluster's accesses to shared
-memory, and the width of what counts to the budget."""
+memory, and the width of what counts to the budget; and of its oracle."""
 import os
 import re
 
+import numpy as np
+
+from oracle import int8
 from paged_kv_cache_147_gb300 import build
 
 
@@ -29,3 +32,14 @@ def test_places_up_to_the_budget_are_counted_in_64_bits():
     # a budget may be as large as an int; the loop's step past it may not
     loops = re.findall(r"for \((\w+) \w+ = [^;]*; \w+ < a\.budget;", _code("pkv_select.cu"))
     assert loops == ["int64_t"]
+
+
+def test_the_oracle_puts_a_nan_scale_first_whatever_the_queries_hold():
+    bounds = np.full((10, 1, 2, 128), 128, np.uint8)
+    scales = np.ones((10, 1, 2), np.float32)
+    scales[[3, 6], 0, 0] = np.nan
+    tables = np.arange(10, dtype=np.int32)[None]
+    for x in (1, np.nan, np.inf, 0):
+        q = np.full((1, 2, 1, 128), x, np.float16)
+        got, lens = int8.select(q, scales, bounds, tables, [160], 16, 5, 1, 1)
+        assert list(got[0, 0]) == [0, 1, 3, 6, 9] and lens[0] == 80
