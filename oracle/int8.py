@@ -170,10 +170,8 @@ def select(q, scales, bounds, tables, lens, bs, budget, first, last):
             s = bound_scores(np.array(rows).reshape(-1, D), bounds[safe, h],
                              scales[safe, h, 0].astype(np.float64))
             # kept blocks first, then NaN scales, then the scores, unknown blocks last
-            rank = np.where(np.isnan(s), 1, 0)
-            s = np.where(np.isnan(s), 0.0, s)
-            s = np.where(there, s, -np.inf)
-            rank = np.where(there, rank, 0)
+            rank = np.where(there, np.where(np.isnan(s), 1, 0), -1)
+            s = np.where(there & ~np.isnan(s), s, 0.0)
             rank[:first] = 2
             rank[count - max(last, own):] = 2
             s = np.where(rank == 2, 0.0, s)

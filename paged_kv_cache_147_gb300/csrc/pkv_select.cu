@@ -44,6 +44,7 @@ constexpr int kBinBits = 10, kBins = 1 << kBinBits;   // 4 a thread
 constexpr int kCands = kThreads;
 constexpr uint32_t kAlways = 0xffffffffu;     // key of a block that is kept whatever its score
 constexpr uint32_t kNanKey = 0xfffffffeu;     // a NaN scale: before every number
+constexpr uint32_t kUnknownKey = 1u;          // an id outside the pool: behind every number (0: not chosen)
 
 struct SelectArgs {
   const __half* q;
@@ -299,8 +300,7 @@ select_blocks_kernel(const SelectArgs a) {
         // (+ 0 turns -0 into 0; a scale of 0 must not meet -infinity, which a NaN one outranks)
         float s = best[o] * t.sc[o] + 0.f;
         if (best[o] == kNegInf && t.sc[o] == t.sc[o]) s = kNegInf;
-        if (!t.good[o]) s = kNegInf;
-        const uint32_t key = j < head || j >= tail ? kAlways : key_of(s);
+        const uint32_t key = j < head || j >= tail ? kAlways : t.good[o] ? key_of(s) : kUnknownKey;
         if (key != kAlways) {
           least = min(least, key);
           most = max(most, key);

@@ -1,5 +1,6 @@
 """The block selection where a cluster of CTAs shares a head: with other work on the GPU, so that its
-CTAs run apart, and with guards around the outputs; the largest budget; NaN scales where no query counts."""
+CTAs run apart, and with guards around the outputs; the largest budget; NaN scales and unknown
+blocks where no query counts."""
 import numpy as np
 import pytest
 import torch
@@ -93,3 +94,21 @@ def test_a_nan_scale_comes_first_whatever_the_queries_hold(seqs, hkv, blocks, q_
             assert np.array_equal(got[0].cpu().numpy(), want[0])
             assert np.array_equal(got[1].cpu().numpy(), want[1])
         assert budget <= 9 or np.isin(tables[0, 5:blocks // 2:7], want[0][0, 0]).all()
+
+
+@pytest.mark.parametrize("seqs,hkv,blocks", [(40, 4, 100), (1, 2, 900), (2, 1, 17000)])
+def test_unknown_blocks_come_last_whatever_the_queries_hold(seqs, hkv, blocks):
+    rng = np.random.default_rng(blocks + 2)
+    q, scales, bounds, tables, lens = _inputs(rng, seqs, hkv, blocks)
+    scales[tables[:, 5:blocks // 2:7].reshape(-1), :, 0] = np.nan
+    tables[:, 1:blocks // 2:5], tables[:, 2:blocks // 2:5] = -9, len(bounds)
+    for x in (np.nan, 1, 0):
+        q[:] = x
+        for budget in (9, blocks * 2 // 3, blocks * 4 // 5):   # (the last takes some unknown ones, too)
+            dev = [_dev(t) for t in (q, scales, bounds, tables, lens)]
+            got = pkv.select_blocks(*dev, 16, budget, 1, 2)
+            want = int8.select(q, scales, bounds, tables, lens, 16, budget, 1, 2)
+            torch.cuda.synchronize()
+            assert pkv.device_error(clear=True) == (pkv.DEVERR_BLOCK_ID if (lens > 16 * budget).any() else 0)
+            assert np.array_equal(got[0].cpu().numpy(), want[0])
+            assert np.array_equal(got[1].cpu().numpy(), want[1])

@@ -43,3 +43,17 @@ def test_the_oracle_puts_a_nan_scale_first_whatever_the_queries_hold():
         q = np.full((1, 2, 1, 128), x, np.float16)
         got, lens = int8.select(q, scales, bounds, tables, [160], 16, 5, 1, 1)
         assert list(got[0, 0]) == [0, 1, 3, 6, 9] and lens[0] == 80
+
+
+def test_the_oracle_puts_unknown_blocks_last_whatever_the_queries_hold():
+    bounds = np.full((10, 1, 2, 128), 128, np.uint8)
+    scales = np.ones((10, 1, 2), np.float32)
+    scales[5, 0, 0] = np.nan
+    tables = np.arange(10, dtype=np.int32)[None]
+    tables[0, [1, 2, 4]] = [-3, 10, 99]
+    for x in (1, np.nan, 0):
+        q = np.full((1, 1, 1, 128), x, np.float16)
+        got, _ = int8.select(q, scales, bounds, tables, [160], 16, 5, 1, 1)
+        assert list(got[0, 0]) == [0, 3, 5, 6, 9]
+        got, _ = int8.select(q, scales, bounds, tables, [160], 16, 8, 1, 1)
+        assert list(got[0, 0]) == [0, -3, 3, 5, 6, 7, 8, 9]
