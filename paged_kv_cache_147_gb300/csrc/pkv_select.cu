@@ -547,16 +547,23 @@ const void* kernel_for(int R) {
                    : reinterpret_cast<const void*>(&select_blocks_kernel<4>);
 }
 
-// CTAs per cluster: as many as are resident at once, with at least kMinBlocks blocks each (8 heads of
-// 2048 blocks: 1 CTA each 19.0 us, 2 13.5, 4 10.1, 8 8.0; 128 of up to 1024, 16 rows: 1 14.0, 2 13.1, 4
-// 17.8; 128 of up to 128: 1 4.7, 2 6.1).
+// CTAs per cluster: as many as are resident at once, with at least kMinBlocks columns of the table each
+// (the lengths are on the GPU), where the table has room for contexts that are worth it: a cluster costs
+// 1 us more than a CTA alone, its barriers and the copying of the keys. Measured with 1, 2, 4, 8 CTAs,
+// contexts as long as the table, us:
+//   8 heads     of 128 blocks 4.9, 5.7, 5.7, 5.8   of 256 6.1, 6.3, 5.9, 5.9   of 384 7.3, 7.0, 6.2, 6.1
+//               of 1024 12.4, 9.9, 7.7, 6.8        of 2048 19.5, 14.0, 10.3, 8.3
+//   64 heads    of 128 blocks 5.1, 6.2, 6.2        of 384 7.5, 7.2, 6.9        of 1024 12.7, 10.1, 8.9
+//   128 heads   of 128 blocks 5.1, 6.5             of 512 8.7, 8.8             of 1024 15.1, 13.1
+//   (16 rows)                 5.2, 6.7                    8.8, 9.3                     16.8, 14.4
 constexpr int kMinBlocks = 64;
+constexpr int kWide = 384, kWidePair = 768;   // columns from which on a cluster, and one of two, pays
 int cluster_for(int64_t units, int max_blocks) {
   int c = 1;
   while (c < kMaxCluster && units * 2 * c <= static_cast<int64_t>(kCtas) * sm_count() &&
          max_blocks >= 2 * c * kMinBlocks)
     c *= 2;
-  return c;
+  return max_blocks >= (c > 2 ? kWide : kWidePair) ? c : 1;
 }
 
 // Raises the limit of dynamic shared memory of the kernel for `nt` tiles to the device's, once per

@@ -112,3 +112,22 @@ def test_unknown_blocks_come_last_whatever_the_queries_hold(seqs, hkv, blocks):
             assert pkv.device_error(clear=True) == (pkv.DEVERR_BLOCK_ID if (lens > 16 * budget).any() else 0)
             assert np.array_equal(got[0].cpu().numpy(), want[0])
             assert np.array_equal(got[1].cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("seqs,hkv", [(1, 1), (4, 8), (9, 8), (16, 8)])
+def test_tables_around_the_widths_where_clusters_begin(seqs, hkv):
+    # 8, 4 and 2 CTAs a head, or one, by the table's columns; contexts of all lengths in them
+    rng = np.random.default_rng(seqs)
+    q, scales, bounds, tables, lens = _inputs(rng, seqs, hkv, 1024)
+    for width in (127, 128, 383, 384, 511, 512, 767, 768, 1023, 1024):
+        n = np.minimum(lens, width * 16).astype(np.int32)
+        n[::3] = rng.integers(0, width * 16, len(n[::3]))
+        args = q, scales, bounds, np.ascontiguousarray(tables[:, :width]), n
+        got = pkv.select_blocks(*(_dev(x) for x in args), 16, 50, 2, 1)
+        want = int8.select(*args, 16, 50, 2, 1)
+        torch.cuda.synchronize()
+        # (some of those lengths pass what their table holds: places without a block, which are scored)
+        holes = any(c > 800 and (t[:-(-c // 16)] < 0).any() for c, t in zip(n, args[3]))
+        assert pkv.device_error(clear=True) == (pkv.DEVERR_BLOCK_ID if holes else 0)
+        assert np.array_equal(got[0].cpu().numpy(), want[0])
+        assert np.array_equal(got[1].cpu().numpy(), want[1])
