@@ -5,9 +5,10 @@
 // read and written again only when its scale grows (its largest element doubles, so a few times
 // in a block's life). A scale needs all of a block's new rows before the first code, so that the rows
 // stay in registers between the two (16 rows a warp) and are read once: 8192 tokens of 8 heads in
-// 16-token blocks take 13.2 us (50 MB, 3.8 TB/s; first load to last store is one trip through memory
-// and nothing is left to overlap it with), 64 tokens of 2 heads 2.9 (a launch and three dependent
-// loads). Widening 8192 tokens: 9.6 us (5.3 TB/s).
+// 16-token blocks take 13.2 us (50 MB, 3.8 TB/s: two waves of warps, none of which loads its next
+// block's rows while it writes this one's codes), 64 tokens of 2 heads 2.9 (a launch and three
+// dependent loads). Widening 8192 tokens: 9.6 us (5.3 TB/s). Copying 64 blocks of 8 heads and 16 tokens
+// in each of 80 layers: 54 us (357 MB, 6.6 TB/s), 8 blocks of one layer 2.5 (a launch and two).
 #include <algorithm>
 
 #include "pkv_int8.cuh"
@@ -427,8 +428,11 @@ int pkv_kv_append_int8(const void* k, const void* v, const int64_t* slot_mapping
       !aligned16(k_bounds) || (reinterpret_cast<uintptr_t>(kv_scales) & 7u))
     return PKV_EINVAL;
   // Few rows: a team for every token, so that a step's blocks are all taken at once. Many: as many tokens
-  // a team as leave about as many warps as are resident, a block's worth at most (8192 tokens of 8 heads
-  // in blocks of 16: a token a team 19.8 us, this 13.2; half or twice as many warps change nothing).
+  // a team as leave 4096 warps, about as many as are resident, but a block's worth at most, so that
+  // calls of 32768 tokens times heads and more have more than one wave. Measured, us: 8192 tokens of 8
+  // heads in blocks of 16 with 1, 4, 8, 16 tokens a team 40.4, 17.9, 14.3, 13.2; 2048 tokens with 1, 4, 8,
+  // 16: 10.0, 6.4, 5.2, 5.2; those in blocks of 256 with 64, 128, 256: 14.8, 12.5, 15.8; single tokens of
+  // 512 sequences, blocks of 16, with 1, 2, 4: 7.4, 6.7, 8.5.
   const int64_t halves = static_cast<int64_t>(num_kv_heads) * 2;   // K and V of a head
   const int64_t warps = num_tokens * halves * (block_size / 16);
   const int span = static_cast<int>(std::min<int64_t>(std::max<int64_t>(warps / 4096, 1), block_size));

@@ -6,10 +6,10 @@
 // it runs over that table's blocks as if they were the whole context.
 //
 // What bounds it: 256 bytes per (token, kv head). 32 sequences of 16384 tokens, 8 kv heads, 8 query
-// rows each, take 160 us (1.07 GB at 6.7 TB/s, a copy's rate), 16 of 4096 24.4 (5.5 TB/s, with 4 us of
-// start and merge). Few or short contexts are bound by latency (one of 101 tokens 5.1 us), 9 rows and
-// more by the products' operands, which every 8 rows take again (16 of 4096: 16 rows 33 us, 24 rows 46,
-// 32 rows 54).
+// rows each, take 161 us (1.07 GB at 6.7 TB/s, a copy's rate), 16 of 4096 24.5 (5.5 TB/s, with 4 us of
+// start and merge). Few or short contexts are bound by latency (one of 101 tokens 5.3 us), 9 rows and
+// more by a warp's chain per stage, in which every 8 rows add their products, and where RS > 1 by as
+// many fetches of each stage from L2 (16 of 4096: 16 rows 33 us, 24 rows 46, 32 rows 55).
 //
 // Stream, slices, split units and merges are those of pkv_decode.cu (pkv_decode_common.cuh); the warps'
 // own rings of cp.async stages, the transposed tile, the query and the epilogue warp those of
@@ -28,7 +28,11 @@
 //    - M), x the score in powers of two, M the reference that follows the largest x + e_V (lazily, kept
 //    kShift below it, so that w fills fp16's range upwards and small weights keep their bits). The sum
 //    of the softmax weights takes w 2^-e_V. O = sum w code and that sum share the reference M, so the
-//    merges of warps and slices are those of the other caches.
+//    merges of warps and slices are those of the other caches. For the product w is rounded once to
+//    fp16, as in every decode here: the tensor cores take both operands in one type, and codes are
+//    exact in it. That moves an output by 0.6e-4 to 1.8e-4 of its row, the more the fewer tokens carry
+//    the weights; against exact results its error is 2.0e-4 to 2.3e-4, with fp32 weights 2.0e-4 to
+//    2.2e-4, nearly all of it the output's own rounding to fp16.
 //  * Codes are never NaN or infinite, whatever a masked row holds: only a scale can be. A NaN scale
 //    reaches the queries that see a row of its block.
 #include <cuda_fp16.h>
@@ -914,7 +918,10 @@ Variant variant8() {
 //   to 32  <3, 2, 2, 2, 1, 1> a 26.7, b 61.2, c 68.9, d 115, e 145, two of 1000, 8 kv heads 14.4
 //          <4, 2, 2, 2, 1, 1>   29.9    54.4    57.4    110    172                          14.9
 // Many warps in one CTA keep more in flight than two CTAs of four, but hand a segment over only once
-// per SM and merge more states for it; a warp with several row tiles widens the codes once for all.
+// per SM and merge more states for it; a warp with several row tiles widens the codes once for all, at
+// the price of registers: <8, 1, 2>, <4, 2, 2>, <4, 1, 2> and <6, 1, 3> spill 140, 132, 60 and 56
+// bytes a thread. Above 16 rows the table's width alone decides: short contexts in wide tables take the
+// wide variant's time (e: 172 us instead of 145).
 Variant choose8(int R, bool few, bool wide) {
   return R <= 8    ? (few ? variant8<8, 1, 1, 2, 1, 1>() : variant8<4, 1, 1, 2, 2, 2>())
          : R <= 16 ? (few ? variant8<8, 1, 2, 2, 1, 1>() : variant8<4, 1, 2, 2, 1, 2>())

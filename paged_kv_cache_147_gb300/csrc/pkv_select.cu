@@ -20,9 +20,10 @@
 // intervals between the least and the greatest, the CTAs' counts added up through distributed
 // shared memory; the few scores in the interval where the budget ends are compared with each other
 // one by one (more of them: counted again in finer intervals). One launch, no workspace.
-// Measured: 256 heads of 1024 blocks 19.1 us (67 MB of bounds at 3.6 TB/s: a gather of 256-byte pieces
-// behind a table; its start and the choice, about 5 us, are not hidden), 8 heads of 2048 blocks 8.0,
-// 128 heads of up to 128 blocks 4.8.
+// Measured: 256 heads of 1024 blocks 19.2 us (67 MB of bounds at 3.5 TB/s: a gather of 256-byte pieces
+// behind a table; its start and the choice, about 5 us, are not hidden), 8 heads of 2048 blocks 8.2,
+// 128 heads of up to 128 blocks 4.9, with 16 rows of 512 to 1024 blocks 12.9 (above 8 rows no next
+// bounds are on their way while a tile is scored).
 #include <cuda_fp16.h>
 
 #include <algorithm>
