@@ -209,16 +209,31 @@ __device__ __forceinline__ float exponent_of(float s) {
   return s == s ? fmaxf(e, -60.f) : s;
 }
 
-// Merges a split unit: its partials of slices c0 .. cl, which hold per row their maximum m, their sum l
-// and their normalised output, into (m, l, o) of N items of the calling thread, item i the output dims
-// 4 (gi & 31) .. + 3 of row gi >> 5, gi = t + i NT, in slice order. All items' loads of a batch are in
+// A partial's row of slot `slot`, items as below, into (m, l, o).
+template <int N, int NT>
+__device__ __forceinline__ void load_partial(const DecodeArgs& a, int64_t slot, int t, float (&m)[N],
+                                             float (&l)[N], float4 (&o)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int gi = min(t + i * NT, a.R * 32 - 1);
+    const int64_t row = slot * a.R + (gi >> 5);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row * 4));
+    m[i] = ml.x;
+    l[i] = ml.y;
+    o[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * kD) + (gi & 31));
+  }
+}
+
+// Merges a split unit: its first partial, which is (m, l, o), and those of slices c0 .. cl behind it, which
+// hold per row their maximum m, their sum l and their normalised output, into (m, l, o) of N items of the
+// calling thread, item i the output dims 4 (gi & 31) .. + 3 of row gi >> 5, gi = t + i NT, in slice order
+// (in the same batches whoever merges, so that the bits are the same). All items' loads of a batch are in
 // flight at once, past L1, which is not coherent: by way of shared memory, with a barrier between the
 // steps, 10 partials of 8 rows took 4.5 us. The batches are as large as the registers let them be: half
 // of them, and a sequence of 2000 tokens with 12 rows takes 18.8 us instead of 13.8.
 template <int N, int NT>
-__device__ __forceinline__ void merge_partials(const DecodeArgs& a, int c0, int cl, int cf,
-                                               bool first_odd, int t, float (&m)[N], float (&l)[N],
-                                               float4 (&o)[N]) {
+__device__ __forceinline__ void merge_partials(const DecodeArgs& a, int c0, int cl, int t,
+                                               float (&m)[N], float (&l)[N], float4 (&o)[N]) {
   constexpr int kBatch = N <= 2 ? 8 : N == 3 ? 5 : N == 4 ? 4 : 3;
   const int items = a.R * 32;
 #pragma unroll 1
@@ -233,8 +248,8 @@ __device__ __forceinline__ void merge_partials(const DecodeArgs& a, int c0, int 
         ml[i][j] = make_float2(kNegInf, 0.f);
         x[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c + j <= cl) {
-          const int64_t row =
-              (2 * static_cast<int64_t>(c + j) + ((c + j == cf && first_odd) ? 1 : 0)) * a.R + (gi >> 5);
+          // (the first segment of its slice: a unit begins before its second slice)
+          const int64_t row = 2 * static_cast<int64_t>(c + j) * a.R + (gi >> 5);
           ml[i][j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + row * 4));
           x[i][j] = __ldcg(reinterpret_cast<const float4*>(a.part_o + row * kD) + (gi & 31));
         }
@@ -313,7 +328,7 @@ __device__ __forceinline__ void finish_slice8(const DecodeArgs& a, const LastSeg
       if (t + i * kNE < items) put(ls.b, ls.h, t + i * kNE, o[i]);
   } else {
     int cf, cl;
-    const bool odd = slices(ls.b, ls.h, ls.nb, cf, cl);
+    slices(ls.b, ls.h, ls.nb, cf, cl);
     int* counter = a.counters + ls.b * a.Hkv + ls.h;
     bool merged = false;
     if (ls.head) {
@@ -330,7 +345,7 @@ __device__ __forceinline__ void finish_slice8(const DecodeArgs& a, const LastSeg
     }
     if (merged) {
       if (t == 0) *counter = 0;
-      merge_partials<kItems, kNE>(a, cf + 1, cl, cf, odd, t, m, l, o);   // (slice cf is this one)
+      merge_partials<kItems, kNE>(a, cf + 1, cl, t, m, l, o);   // (slice cf is this one)
 #pragma unroll
       for (int i = 0; i < kItems; ++i)
         if (t + i * kNE < items) put(ls.b, ls.h, t + i * kNE, o[i]);
@@ -361,13 +376,8 @@ __device__ __forceinline__ void finish_slice8(const DecodeArgs& a, const LastSeg
     const int b = npend_s[1 + 3 * n], h = npend_s[2 + 3 * n];
     int cf, cl;
     const bool odd = slices(b, h, npend_s[3 + 3 * n], cf, cl);
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      m[i] = kNegInf;
-      l[i] = 0.f;
-      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    merge_partials<kItems, kNE>(a, cf, cl, cf, odd, t, m, l, o);
+    load_partial<kItems, kNE>(a, 2 * static_cast<int64_t>(cf) + (odd ? 1 : 0), t, m, l, o);
+    merge_partials<kItems, kNE>(a, cf + 1, cl, t, m, l, o);
 #pragma unroll
     for (int i = 0; i < kItems; ++i)
       if (t + i * kNE < items) put(b, h, t + i * kNE, o[i]);
