@@ -10,7 +10,8 @@
  *     cached K/V, read indirectly through its block table, with GQA head groups;
  *   - sink + ring decode attention with RoPE applied at read time;
  * and around it: an FP8 (E4M3), a 4-bit and an 8-bit block-scaled form of the cache with their
- * appends and decodes, attention over the blocks of a long context that a score selects, the per-head norm and rotation of queries and keys before them, verification of speculative drafts
+ * appends and decodes, attention over the blocks of a long context that a score selects, the
+ * per-head norm and rotation of queries and keys before them, verification of speculative drafts
  * (accept/reject, next token), block tables and slot maps kept on the device, and a host block
  * pool that hands out the block tables (prefix sharing, reference counts, copy-on-write pairs).
  *

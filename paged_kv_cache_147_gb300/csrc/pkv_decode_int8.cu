@@ -30,8 +30,8 @@
 //    of the softmax weights takes w 2^-e_V. O = sum w code and that sum share the reference M, so the
 //    merges of warps and slices are those of the other caches. For the product w is rounded once to
 //    fp16, as in every decode here: the tensor cores take both operands in one type, and codes are
-//    exact in it. That moves an output by 0.6e-4 to 1.8e-4 of its row, the more the fewer tokens carry
-//    the weights; against exact results its error is 2.0e-4 to 2.3e-4, with fp32 weights 2.0e-4 to
+//    exact in it. That moves outputs by 0.3e-4 to 1.8e-4 of their norm, the more the fewer tokens carry
+//    the weights; against exact results the error is 2.0e-4 to 2.4e-4, with fp32 weights 2.0e-4 to
 //    2.2e-4, nearly all of it the output's own rounding to fp16.
 //  * Codes are never NaN or infinite, whatever a masked row holds: only a scale can be. A NaN scale
 //    reaches the queries that see a row of its block.
